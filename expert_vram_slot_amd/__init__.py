@@ -60,6 +60,7 @@ def lib():
             raise ImportError(f"{LIB_PATH} is missing: run __graft_entry__.build() (hipcc for gfx950) first")
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        i64 = ctypes.c_int64
         sig = {
             "moe_abi_version": (i32, []),
             "moe_last_error": (ctypes.c_char_p, []),
@@ -92,6 +93,12 @@ def lib():
             "moe_step_set_stream_threshold": (i32, [vp, i32]),
             "moe_step_last_host_mode": (i32, [vp]),
             "moe_fused_spin_limit": (ctypes.c_int64, [ctypes.c_int64]),
+            "moe_linear_q4": (i32, [vp, i32, i64, vp, vp, i32, vp, i32, i32, i32, vp, i32, i64, vp]),
+            "moe_sample_workspace_bytes": (sz, [i32, i32]),
+            "moe_sample": (i32, [vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "moe_balance_workspace_bytes": (sz, [i32, i32]),
+            "moe_balance_loss": (i32, [vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "moe_balance_loss_bwd": (i32, [vp, i32, vp, vp, vp, vp, vp, i32, i32, vp, vp]),
             "moe_host_alloc": (vp, [sz]),
             "moe_host_free": (i32, [vp]),
         }
@@ -242,6 +249,37 @@ def moe_combine(y, y_add, T, H, stream=None):
 
 def moe_residual(x, x_dtype, y, x_out, T, H, stream=None):
     return _check("moe_residual", lib().moe_residual(_p(x), x_dtype, _p(y), _p(x_out), T, H, _stream(stream)))
+
+
+def moe_linear_q4(x, x_dtype, ldx, wq, scales, group, bias, T, N, K, y, y_dtype, ldy, stream=None):
+    return _check("moe_linear_q4", lib().moe_linear_q4(_p(x), x_dtype, ldx, _p(wq), _p(scales), group, _p(bias), T, N,
+                                                       K, _p(y), y_dtype, ldy, _stream(stream)))
+
+
+def moe_sample_workspace_bytes(T, V) -> int:
+    return int(lib().moe_sample_workspace_bytes(T, V))
+
+
+def moe_sample(logits, l_dtype, ldl, T, V, temperature, min_p, top_k, top_p, u, ids, prob, ws, ws_bytes, stream=None):
+    return _check("moe_sample", lib().moe_sample(_p(logits), l_dtype, ldl, T, V, _p(temperature), _p(min_p), _p(top_k),
+                                                 _p(top_p), _p(u), _p(ids), _p(prob), _p(ws), ws_bytes,
+                                                 _stream(stream)))
+
+
+def moe_balance_workspace_bytes(T, E) -> int:
+    return int(lib().moe_balance_workspace_bytes(T, E))
+
+
+def moe_balance_loss(z, z_dtype, ids, mask, T, E, k, counts, totals, share, lse, loss, ws, ws_bytes, stream=None):
+    return _check("moe_balance_loss", lib().moe_balance_loss(_p(z), z_dtype, _p(ids), _p(mask), T, E, k, _p(counts),
+                                                             _p(totals), _p(share), _p(lse), _p(loss), _p(ws),
+                                                             ws_bytes, _stream(stream)))
+
+
+def moe_balance_loss_bwd(z, z_dtype, lse, mask, counts, totals, dloss, T, E, dz, stream=None):
+    return _check("moe_balance_loss_bwd", lib().moe_balance_loss_bwd(_p(z), z_dtype, _p(lse), _p(mask), _p(counts),
+                                                                     _p(totals), _p(dloss), T, E, _p(dz),
+                                                                     _stream(stream)))
 
 
 def moe_step_create(T_max, E, k, H, I, S, w_type):

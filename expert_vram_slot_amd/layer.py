@@ -26,9 +26,11 @@ import os
 import torch
 
 from . import (MOE_W_F32, MOE_X_BF16, MOE_X_F32, POLICIES, LayerDesc, cache_gather, cache_init, cache_manage,
-               cache_state, moe_combine, moe_ffn_host_misses, moe_ffn_slots, moe_ffn_workspace_bytes, moe_layer_step,
-               moe_residual, moe_route_ex, moe_slab_layout, moe_stack_step, moe_step_create,
-               moe_step_destroy, moe_step_last_host_mode, moe_step_set_stream_threshold, moe_step_stats)
+               cache_state, moe_balance_loss, moe_balance_loss_bwd, moe_balance_workspace_bytes, moe_combine,
+               moe_ffn_host_misses, moe_ffn_slots, moe_ffn_workspace_bytes, moe_layer_step, moe_linear_q4,
+               moe_residual, moe_route_ex, moe_sample, moe_sample_workspace_bytes, moe_slab_layout, moe_stack_step,
+               moe_step_create, moe_step_destroy, moe_step_last_host_mode, moe_step_set_stream_threshold,
+               moe_step_stats)
 
 
 def host_threads() -> int:
@@ -89,6 +91,7 @@ class SlotLayer:
         self.ffn_events = None     # (start, end) torch events recorded around moe_ffn_slots when set
         self.gather_events = None  # (start, end) torch events recorded around cache_gather when set
         self.route_flags = 0       # moe_route_ex flags (MOE_ROUTE_DAMPED)
+        self.stats_out = None      # moe_balance_loss's outputs and workspace, made by the first balance()
 
     def init_cache(self, resident=None):
         cache_init(self.st, resident)
@@ -154,6 +157,37 @@ class SlotLayer:
             self.y_host_dev[:T * self.H].copy_(self.h_y[:T * self.H], non_blocking=True)
             moe_combine(self.y, self.y_host_dev, T, self.H, cur)
         return self.y[:T * self.H].view(T, self.H)
+
+
+    def balance(self, T, mask=None):
+        """Router statistics of the last step's T tokens (moe_balance_loss on
+        its logits and picks; mask: device uint8 [T], 0 = padding).  Returns
+        a dict of counts [E], totals [2], share [E] (double: the brightness
+        moe_bias_table takes), lse [T] and loss [2], views of buffers the next
+        call overwrites."""
+        assert T <= self.T_max
+        o = self.stats_out
+        if o is None:
+            dev = self.ids.device
+            n = moe_balance_workspace_bytes(self.T_max, self.E)
+            o = self.stats_out = dict(counts=torch.empty(self.E, dtype=torch.int32, device=dev),
+                                      totals=torch.empty(2, dtype=torch.int32, device=dev),
+                                      share=torch.empty(self.E, dtype=torch.float64, device=dev),
+                                      lse=torch.empty(self.T_max, dtype=torch.float32, device=dev),
+                                      loss=torch.empty(2, dtype=torch.float32, device=dev),
+                                      ws=torch.empty(n, dtype=torch.uint8, device=dev), ws_bytes=n)
+        moe_balance_loss(self.logits, MOE_X_F32, self.ids, mask, T, self.E, self.k, o["counts"], o["totals"],
+                         o["share"], o["lse"], o["loss"], o["ws"], o["ws_bytes"], torch.cuda.current_stream())
+        return dict(counts=o["counts"], totals=o["totals"], share=o["share"], lse=o["lse"][:T], loss=o["loss"])
+
+    def balance_grad(self, T, dloss, mask=None):
+        """Gradient of the last balance()'s losses (weights dloss: device
+        float [2]; same T and mask) to the last step's logits, [T][E] fp32."""
+        o = self.stats_out
+        dz = torch.empty(T, self.E, dtype=torch.float32, device=self.ids.device)
+        moe_balance_loss_bwd(self.logits, MOE_X_F32, o["lse"], mask, o["counts"], o["totals"], dloss, T, self.E, dz,
+                             torch.cuda.current_stream())
+        return dz
 
 
 class SlotStack:
@@ -305,3 +339,37 @@ class NativeStack:
         except Exception:
             pass
 
+
+class DecodeHead:
+    """The end of a decode step behind a stack: the 4-bit output head's
+    logits and the token drawn from them.
+
+    wq: device uint8 [V][H/2], scales: device fp16 [V][H/group] (the layout of
+    moe_linear_q4); bias: device float [V] or None.  x_dtype is the stack's
+    activation format.
+    """
+
+    def __init__(self, *, H, V, wq, scales, group, T_max, x_dtype=MOE_X_BF16, bias=None, device="cuda"):
+        dev = torch.device(device)
+        self.H, self.V, self.T_max, self.x_dtype = H, V, T_max, x_dtype
+        self.wq, self.scales, self.group, self.bias = wq, scales, group, bias
+        self.logits_buf = torch.empty(T_max, V, dtype=torch.float32, device=dev)
+        self.ids = torch.empty(T_max, dtype=torch.int32, device=dev)
+        self.prob = torch.empty(T_max, dtype=torch.float32, device=dev)
+        self.ws_bytes = moe_sample_workspace_bytes(T_max, V)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
+
+    def logits(self, x, T):
+        """Logits [T][V] fp32 of x (device [T][H] in x_dtype): a view of this object's buffer."""
+        assert T <= self.T_max
+        moe_linear_q4(x, self.x_dtype, self.H, self.wq, self.scales, self.group, self.bias, T, self.V, self.H,
+                      self.logits_buf, MOE_X_F32, self.V, torch.cuda.current_stream())
+        return self.logits_buf[:T]
+
+    def step(self, x, T, u, temperature=None, min_p=None, top_k=None, top_p=None):
+        """The next token of each of T rows of x: (ids [T], prob [T]), views of
+        this object's buffers.  u and the settings as moe_sample takes them."""
+        self.logits(x, T)
+        moe_sample(self.logits_buf, MOE_X_F32, self.V, T, self.V, temperature, min_p, top_k, top_p, u, self.ids,
+                   self.prob, self.ws, self.ws_bytes, torch.cuda.current_stream())
+        return self.ids[:T], self.prob[:T]

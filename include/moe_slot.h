@@ -14,6 +14,13 @@
  *   moe_ffn_host_misses  the same FFN on CPU threads for the picks that are not
  *                        resident; summed in with moe_combine
  *
+ * and around stacks of such layers:
+ *
+ *   moe_linear_q4        dense products with 4-bit weights (projections, head)
+ *   moe_sample           a token id from each row of the head's logits
+ *   moe_balance_loss     picks and router mass per expert, balance and z loss
+ *                        (moe_balance_loss_bwd: their gradient)
+ *
  * Sources (web pages, by title and section):
  *   [BEL] the Betelgeuse engine post: an in-stream kernel resolves expert hits
  *         on the device and rings a mapped host doorbell only on a miss.
@@ -402,6 +409,108 @@ int moe_combine(float* y, const float* y_add, int T, int H, hipStream_t stream);
  * bf16: x_out = RNE_bf16(fl32(x + y)); fp32: x_out = fl32(x + y).
  * Errors: ARG, DTYPE, HIP. */
 int moe_residual(const void* x, int x_dtype, const float* y, void* x_out, int T, int H, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Around the stack: dense 4-bit products, the draw of a token, and the
+ * router's statistics.
+ */
+
+/* Dense product with 4-bit weights and group scales: the projections and the
+ * output head of a model whose experts are MOE_W_Q4B32.
+ *   x       device [T][ldx] in x_dtype, K inputs a row
+ *   wq      device [N][K/2]: codes in blocks of 32 inputs as in a slab's
+ *           Q4B32 plane (byte j of a block: input j low, input j+16 high)
+ *   scales  device fp16 [N][K/group]; group 32 (a slab's planes), 64 or 128
+ *   bias    device float[N] or NULL
+ *   y       device [T][ldy] in y_dtype (MOE_X_F32 or MOE_X_BF16) out:
+ *           y[t][n] = bias[n] + sum over k of x[t][k] * (scales[n][k/group] *
+ *           (code[n][k] - 8)), summed in fp32 (bf16: rounded once, RNE).
+ *           Columns from N to ldy are left as they are; y must not overlap
+ *           the inputs.
+ * fp32 activations keep their 24 bits.  A token whose x or bias holds an
+ * infinity or a NaN gets non-finite outputs; other tokens are not touched by
+ * it.  A token's bits do not depend on the other tokens' values.
+ * T = 0 does nothing (x and y may be NULL).
+ * Errors: ARG (null, sizes, ldx < K, ldy < N), DTYPE, SHAPE (group, K not a
+ * multiple of it, the limits below), ALIGN (x, its rows and wq on 16 bytes;
+ * scales, bias and y on their elements), HIP. */
+#define MOE_LINEAR_MAX_T (1 << 20)
+#define MOE_LINEAR_MAX_NK (1 << 22)
+#define MOE_LINEAR_MAX_LD ((int64_t)1 << 40)
+int moe_linear_q4(const void* x, int x_dtype, int64_t ldx, const void* wq, const void* scales, int group,
+                  const float* bias, int T, int N, int K, void* y, int y_dtype, int64_t ldy, hipStream_t stream);
+
+/* One token id for each row of logits, drawn with a given random number.
+ *   logits       device [T][ldl] in l_dtype, V a row; -inf and NaN are never
+ *                drawn; +inf outweighs every finite logit (several share)
+ *   temperature  device float[T] or NULL (1).  Not above 0, or NaN: greedy,
+ *                the largest logit, ties to the lower id
+ *   min_p        device float[T] or NULL.  Above 0: keep ids whose weight
+ *                w = exp((l - max) / temperature) is at least it (1 at most)
+ *   top_k        device int32[T] or NULL.  Above 0: keep the first top_k of
+ *                what min-p left, by falling logit, ties to the lower id
+ *   top_p        device float[T] or NULL.  Below 1: keep the shortest prefix
+ *                (same order) of what is left with at least top_p of its mass;
+ *                never less than one id
+ *   u            device float[T] in [0, 1) (values outside are taken as the
+ *                nearest end, NaN as 0): the draw is the first kept id, in
+ *                ascending id, whose running mass exceeds u times the kept
+ *                mass
+ *   ids          device int32[T] out; -1 where no logit is above -inf
+ *   prob         device float[T] out or NULL: the drawn id's share of the
+ *                kept mass (greedy 1; 0 where ids is -1)
+ *   ws           device workspace of >= moe_sample_workspace_bytes(T, V)
+ *                bytes; need not be cleared; calls that may overlap need one
+ *                each
+ * Weights are computed in double and summed as whole multiples of 2^-S, with
+ * S = 62 - ceil(log2 V) (45 at V = 131072): the result does not depend on any
+ * order of summation.  T = 0 does nothing.
+ * Errors: ARG (null, sizes, ldl < V, workspace too small), DTYPE, SHAPE (the
+ * limits below), ALIGN (logits on their elements, ws on 16 bytes), HIP. */
+#define MOE_SAMPLE_MAX_T 65535
+#define MOE_SAMPLE_MAX_V (1 << 20)
+#define MOE_SAMPLE_MAX_LD ((int64_t)1 << 40)
+size_t moe_sample_workspace_bytes(int T, int V);
+int moe_sample(const void* logits, int l_dtype, int64_t ldl, int T, int V, const float* temperature,
+               const float* min_p, const int32_t* top_k, const float* top_p, const float* u, int32_t* ids, float* prob,
+               void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Router statistics and losses of a batch, from the logits and picks of
+ * moe_route.  With p = softmax(z) of a token's logits, c_e the picks of
+ * expert e, f_e = c_e / sum c and P_e the mean of p_e over the n counted
+ * tokens:
+ *   z       device [T][E] in z_dtype, finite or -inf
+ *   ids     device int32[T][k]; ids outside [0, E) are not counted
+ *   mask    device uint8[T] or NULL: tokens with 0 (padding) are left out and
+ *           their logits not read.  So are tokens none of whose logits is
+ *           above -inf
+ *   counts  device int32[E] out: c
+ *   totals  device int32[2] out: n, and sum c
+ *   share   device double[E] out: P, the brightness moe_bias_table takes ("share
+ *           of router mass"; [PGO] "The method in five lines")
+ *   lse     device float[T] out: log sum exp z (0 for a token left out)
+ *   loss    device float[2] out: the balance loss E * sum f_e P_e (1 when
+ *           either is uniform) and the z loss, the mean of lse^2; 0 where
+ *           nothing is counted
+ *   ws      device workspace of >= moe_balance_workspace_bytes(T, E) bytes;
+ *           need not be cleared; calls that may overlap need one each
+ * The softmax and the sums run in double, in a fixed order.
+ * Errors: ARG, DTYPE, SHAPE (E > MOE_MAX_E, k > E, k > MOE_MAX_K, T beyond
+ * the limit), ALIGN (z, share and ws on 16 bytes), HIP. */
+#define MOE_BALANCE_MAX_T (1 << 24)
+size_t moe_balance_workspace_bytes(int T, int E);
+int moe_balance_loss(const void* z, int z_dtype, const int32_t* ids, const uint8_t* mask, int T, int E, int k,
+                     int32_t* counts, int32_t* totals, double* share, float* lse, float* loss, void* ws,
+                     size_t ws_bytes, hipStream_t stream);
+
+/* Gradient of the two losses to the logits (counts carry none):
+ *   dz[t][e] = p_te * (g_b * E * (f_e - sum_e' f_e' p_te') + 2 g_z lse_t) / n
+ * with g_b, g_z = dloss[0..1] (device float[2], the losses' own gradients or
+ * weights).  z, mask: as given to moe_balance_loss; lse, counts, totals: its
+ * outputs.  dz: device [T][E] in z_dtype out (overwritten; may alias z), 0 for
+ * tokens left out.  Errors: as moe_balance_loss. */
+int moe_balance_loss_bwd(const void* z, int z_dtype, const float* lse, const uint8_t* mask, const int32_t* counts,
+                         const int32_t* totals, const float* dloss, int T, int E, void* dz, hipStream_t stream);
 
 /* Pinned, device-mapped host memory for the host expert store. */
 void* moe_host_alloc(size_t bytes);

@@ -1,0 +1,220 @@
+"""moe_linear_q4, moe_sample and moe_balance_loss without a GPU: refusals and
+workspace sizes (nothing is launched on those paths), and the references of
+the GPU tests against brute force, closed forms and differences."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import ops_reference as ref
+import synth
+
+
+@pytest.fixture(scope="module")
+def mlib():
+    import os
+
+    from expert_vram_slot_amd import build as b
+    if not os.path.exists(b.LIB):
+        b.build()
+    import expert_vram_slot_amd as m
+    m.lib()
+    return m
+
+
+# ------------------------------------------------------------- refusals
+
+LINEAR = dict(x=16, x_dtype=1, ldx=64, wq=16, scales=16, group=32, bias=None, T=4, N=8, K=64, y=16, y_dtype=0, ldy=8)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(x=None), "ARG"), (dict(wq=None), "ARG"), (dict(scales=None), "ARG"), (dict(y=None), "ARG"),
+    (dict(T=-1), "ARG"), (dict(N=0), "ARG"), (dict(K=0), "ARG"), (dict(ldx=63), "ARG"), (dict(ldy=7), "ARG"),
+    (dict(ldx=-64), "ARG"),
+    (dict(x_dtype=2), "DTYPE"), (dict(y_dtype=-1), "DTYPE"),
+    (dict(group=16), "SHAPE"), (dict(group=0), "SHAPE"), (dict(group=48), "SHAPE"), (dict(K=48, ldx=48), "SHAPE"),
+    (dict(K=96, ldx=96, group=64), "SHAPE"), (dict(T=(1 << 20) + 1), "SHAPE"), (dict(N=(1 << 22) + 1, ldy=1 << 23), "SHAPE"),
+    (dict(ldx=1 << 41), "SHAPE"), (dict(ldy=1 << 41), "SHAPE"),
+    (dict(x=24), "ALIGN"), (dict(wq=8), "ALIGN"), (dict(ldx=68), "ALIGN"), (dict(scales=17), "ALIGN"),
+    (dict(bias=18), "ALIGN"), (dict(y=18), "ALIGN"), (dict(y=17, y_dtype=1), "ALIGN"),
+])
+def test_linear_q4_refuses(mlib, change, code):
+    a = dict(LINEAR, **change)
+    rc = mlib.lib().moe_linear_q4(*[a[n] for n in LINEAR], None)
+    assert rc == getattr(mlib, "MOE_E_" + code), mlib.moe_last_error()
+    assert mlib.moe_last_error().startswith("moe_linear_q4:")
+
+
+def test_linear_q4_of_no_tokens(mlib):
+    a = dict(LINEAR, T=0, x=None, y=None)
+    assert mlib.lib().moe_linear_q4(*[a[n] for n in LINEAR], None) == mlib.MOE_OK
+
+
+SAMPLE = dict(logits=16, l_dtype=0, ldl=100, T=4, V=100, temperature=None, min_p=None, top_k=None, top_p=None, u=16,
+              ids=16, prob=None, ws=16, ws_bytes=1 << 30)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(logits=None), "ARG"), (dict(u=None), "ARG"), (dict(ids=None), "ARG"), (dict(ws=None), "ARG"),
+    (dict(T=-1), "ARG"), (dict(V=0), "ARG"), (dict(ldl=99), "ARG"), (dict(ws_bytes=0), "ARG"),
+    (dict(l_dtype=3), "DTYPE"), (dict(T=65536), "SHAPE"), (dict(V=(1 << 20) + 1, ldl=1 << 21), "SHAPE"),
+    (dict(logits=18), "ALIGN"), (dict(logits=17, l_dtype=1), "ALIGN"), (dict(ws=8), "ALIGN"),
+])
+def test_sample_refuses(mlib, change, code):
+    a = dict(SAMPLE, **change)
+    rc = mlib.lib().moe_sample(*[a[n] for n in SAMPLE], None)
+    assert rc == getattr(mlib, "MOE_E_" + code), mlib.moe_last_error()
+    assert mlib.moe_last_error().startswith("moe_sample:")
+
+
+def test_sample_of_no_rows_and_workspace(mlib):
+    a = dict(SAMPLE, T=0, logits=None, u=None, ids=None, ws=None, ws_bytes=1 << 30)
+    assert mlib.lib().moe_sample(*[a[n] for n in SAMPLE], None) == mlib.MOE_OK
+    assert mlib.moe_sample_workspace_bytes(1, 1) > 0
+    assert mlib.moe_sample_workspace_bytes(64, 131072) >= mlib.moe_sample_workspace_bytes(1, 131072)
+    assert mlib.moe_sample_workspace_bytes(1, 0) == mlib.moe_sample_workspace_bytes(70000, 5) == 0
+
+
+BALANCE = dict(z=16, z_dtype=0, ids=16, mask=None, T=4, E=8, k=2, counts=16, totals=16, share=16, lse=16, loss=16,
+               ws=16, ws_bytes=1 << 30)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(z=None), "ARG"), (dict(ids=None), "ARG"), (dict(counts=None), "ARG"), (dict(totals=None), "ARG"),
+    (dict(share=None), "ARG"), (dict(lse=None), "ARG"), (dict(loss=None), "ARG"), (dict(ws=None), "ARG"),
+    (dict(T=-1), "ARG"), (dict(E=0), "ARG"), (dict(k=0), "ARG"), (dict(ws_bytes=8), "ARG"),
+    (dict(z_dtype=5), "DTYPE"), (dict(E=4097), "SHAPE"), (dict(k=9), "SHAPE"), (dict(E=64, k=33), "SHAPE"),
+    (dict(T=(1 << 24) + 1), "SHAPE"), (dict(z=20), "ALIGN"), (dict(ws=8), "ALIGN"), (dict(share=20), "ALIGN"),
+])
+def test_balance_refuses(mlib, change, code):
+    a = dict(BALANCE, **change)
+    rc = mlib.lib().moe_balance_loss(*[a[n] for n in BALANCE], None)
+    assert rc == getattr(mlib, "MOE_E_" + code), mlib.moe_last_error()
+    assert mlib.moe_last_error().startswith("moe_balance_loss:")
+
+
+GRAD = dict(z=16, z_dtype=0, lse=16, mask=None, counts=16, totals=16, dloss=16, T=4, E=8, dz=16)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(z=None), "ARG"), (dict(lse=None), "ARG"), (dict(counts=None), "ARG"), (dict(totals=None), "ARG"),
+    (dict(dloss=None), "ARG"), (dict(dz=None), "ARG"), (dict(T=-1), "ARG"), (dict(E=0), "ARG"),
+    (dict(z_dtype=2), "DTYPE"), (dict(E=4097), "SHAPE"), (dict(T=(1 << 24) + 1), "SHAPE"), (dict(z=20), "ALIGN"),
+    (dict(dz=8), "ALIGN"),
+])
+def test_balance_grad_refuses(mlib, change, code):
+    a = dict(GRAD, **change)
+    rc = mlib.lib().moe_balance_loss_bwd(*[a[n] for n in GRAD], None)
+    assert rc == getattr(mlib, "MOE_E_" + code), mlib.moe_last_error()
+    assert mlib.moe_last_error().startswith("moe_balance_loss_bwd:")
+
+
+def test_balance_workspace(mlib):
+    assert mlib.moe_balance_workspace_bytes(0, 1) > 0
+    assert mlib.moe_balance_workspace_bytes(4096, 512) >= mlib.moe_balance_workspace_bytes(1, 512)
+    assert mlib.moe_balance_workspace_bytes(1, 4097) == mlib.moe_balance_workspace_bytes(-1, 8) == 0
+
+
+def test_binding_raises_with_the_reason(mlib):
+    with pytest.raises(mlib.MoeError) as e:
+        mlib.moe_linear_q4(16, 1, 64, 16, 16, 7, None, 1, 8, 64, 16, 0, 8, stream=0)
+    assert e.value.code == mlib.MOE_E_SHAPE and "groups of 7" in str(e.value)
+    with pytest.raises(mlib.MoeError):
+        mlib.moe_sample(None, 0, 8, 1, 8, None, None, None, None, 16, 16, None, 16, 1 << 20, stream=0)
+    with pytest.raises(mlib.MoeError):
+        mlib.moe_balance_loss(16, 0, 16, None, 1, 8, 9, 16, 16, 16, 16, 16, 16, 1 << 20, stream=0)
+    with pytest.raises(mlib.MoeError):
+        mlib.moe_balance_loss_bwd(None, 0, 16, None, 16, 16, 16, 1, 8, 16, stream=0)
+
+
+# ------------------------------------------------------------ references
+
+
+def test_reference_codes_are_the_slab_planes():
+    """The nibble order is a Q4B32 slab's: decoding the generator's gate plane gives the oracle's weights."""
+    import oracle
+    H, I = 64, 32
+    rng = np.random.default_rng(0)
+    w = [rng.normal(0, 1, s).astype(np.float32) for s in ((I, H), (I, H), (H, I))]
+    slab = synth.encode_slab(synth.W_Q4B32, H, I, *w)
+    wq = slab[:I * H // 2].reshape(I, H // 2)
+    d = slab[I * H // 2:I * H // 2 + I * H // 16].view(np.float16).reshape(I, H // 32)
+    got = (ref.codes(wq).astype(np.float64) - 8) * np.repeat(d.astype(np.float64), 32, axis=1)
+    want = oracle.decode_expert(synth.W_Q4B32, slab, H, I)[0]
+    np.testing.assert_array_equal(got, np.asarray(want, np.float64).reshape(I, H))
+
+
+def test_reference_sample_hand_cases():
+    l = np.log(np.array([1.0, 4.0, 2.0, 1.0]))
+    # masses 1 4 2 1 of 8, ascending ids: 0 [0, 1/8), 1 [1/8, 5/8), 2 [5/8, 7/8), 3 [7/8, 1)
+    for u, want, prob in ((0.0, 0, .125), (0.124, 0, .125), (0.2, 1, .5), (0.7, 2, .25), (0.9, 3, .125), (1.0, 3, .125)):
+        assert ref.sample_row(l, u)[:2] == pytest.approx((want, prob))
+    assert list(ref.sample_row(l, 0.5, top_k=2)[2]) == [1, 2]
+    assert list(ref.sample_row(l, 0.5, top_k=3)[2]) == [0, 1, 2]  # of two equal logits the lower id
+    assert list(ref.sample_row(l, 0.5, top_p=0.49)[2]) == [1]
+    assert list(ref.sample_row(l, 0.5, top_p=0.51)[2]) == [1, 2]
+    assert list(ref.sample_row(l, 0.5, min_p=0.3)[2]) == [1, 2]
+    assert list(ref.sample_row(l, 0.5, top_k=2, top_p=0.66)[2]) == [1]  # 4 of the 6 that top-k left
+    assert ref.sample_row(l, 0.9, temperature=0.0)[:2] == (1, 1.0)
+    assert ref.sample_row(np.full(3, -np.inf), 0.5)[0] == -1
+    # temperature 1/2 squares the masses: 1 16 4 1 of 22
+    assert ref.sample_row(l, 0.5, temperature=0.5)[1] == pytest.approx(16 / 22)
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_reference_sample_against_brute_force(seed):
+    """Each cut against its definition over every prefix of a small row."""
+    rng = np.random.default_rng(seed)
+    V = int(rng.integers(1, 9))
+    l = rng.integers(-3, 4, V).astype(np.float64)  # ties are common
+    temperature, min_p = float(rng.uniform(0.5, 2)), float(rng.choice([0, 0.05, 0.3]))
+    top_k, top_p, u = int(rng.integers(0, V + 2)), float(rng.uniform(0, 1.1)), float(rng.uniform())
+    order = sorted(range(V), key=lambda i: (-l[i], i))
+    w = {i: np.exp((l[i] - l.max()) / temperature) for i in range(V)}
+    left = [i for i in order if w[i] >= min_p]
+    if top_k > 0:
+        left = left[:top_k]
+    if top_p < 1:
+        total = sum(w[i] for i in left)
+        left = next(left[:n] for n in range(1, len(left) + 1) if sum(w[i] for i in left[:n]) >= top_p * total * (1 - 1e-15))
+    got, prob, kept = ref.sample_row(l, u, temperature, min_p, top_k, top_p)
+    assert sorted(left) == list(kept)
+    total, run = sum(w[i] for i in left), 0.0
+    for i in sorted(left):
+        run += w[i]
+        if run > u * total:
+            break
+    assert got == i and prob == pytest.approx(w[i] / total)
+
+
+def test_reference_balance_closed_forms():
+    # uniform logits and even picks: loss 1; every pick and all mass on one expert: loss E
+    z, ids = np.zeros((8, 4)), np.arange(8, dtype=np.int32).reshape(8, 1) % 4
+    o = ref.balance(z, ids)
+    assert o["loss"][0] == pytest.approx(1.0) and o["loss"][1] == pytest.approx(np.log(4) ** 2)
+    np.testing.assert_array_equal(o["counts"], [2, 2, 2, 2])
+    z = np.full((3, 4), -np.inf)
+    z[:, 2] = 5.0
+    o = ref.balance(z, np.full((3, 1), 2, np.int32))
+    assert o["loss"][0] == 4.0 and o["loss"][1] == 25.0
+    np.testing.assert_array_equal(o["share"], [0, 0, 1, 0])
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_reference_balance_gradient_against_differences(seed):
+    rng = np.random.default_rng(seed)
+    T, E, k = 5, 6, 2
+    z = rng.normal(0, 1.5, (T, E))
+    ids = np.argsort(-z, axis=1)[:, :k].astype(np.int32)
+    mask = np.array([1, 0, 1, 1, 1], np.uint8) if seed % 2 else None
+    dloss = np.array([0.7, -0.3])
+    g = ref.balance_grad(z, ids, dloss, mask)
+    h = 1e-6
+    for t in range(T):
+        for e in range(E):
+            up, dn = z.copy(), z.copy()
+            up[t, e] += h
+            dn[t, e] -= h
+            d = dloss @ (ref.balance(up, ids, mask)["loss"] - ref.balance(dn, ids, mask)["loss"]) / (2 * h)
+            # central differences: truncation h^2 (1e-12), rounding 2^-52 * loss / h (loss below 50)
+            assert abs(g[t, e] - d) < 2e-8
