@@ -14,172 +14,304 @@
 // l, l + 64, ...).
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.hpp"
+#include "exp64.hpp"
+#include "wave.hpp"
 
 namespace {
 
-constexpr int BAL_THREADS = 256;
-constexpr int BAL_WAVES = BAL_THREADS / 64;
-constexpr int BAL_MAX_BLOCKS = 512;
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-template <int ZD>
-__device__ __forceinline__ float load_z(const void* p, int64_t i) {
-    if constexpr (ZD == MOE_X_F32) return reinterpret_cast<const float*>(p)[i];
-    else return moe::bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]);
-}
+constexpr int BAL_MAX_BLOCKS = 512;   // of the row kernel: two a CU
+constexpr int BAL_ONE = 128;          // batches of up to this many tokens: one workgroup does it all
+constexpr int SUM_E = 16;             // experts of a workgroup of the second pass
+constexpr int SUM_THREADS = 1024;
 
-__device__ __forceinline__ float wave_max(float v) {
+// Waves of a row-kernel workgroup: sixteen where it is the only one, eight, or
+// four where a lane's experts fill its registers.
+constexpr int bal_waves(int NE, bool one) { return NE > 8 ? 4 : one ? 16 : 8; }
+
+// Lane l holds experts (l + 64 j) * VEC + v of a row in v[j * VEC + v]: single
+// fp32 logits (no lane idles on a row of, say, 288 but in its last group), or
+// bf16 pairs.  Past the row: -inf.
+template <int ZD, int VEC, int NE>
+__device__ __forceinline__ void load_row(const void* z, int64_t t, int E, int lane, float (&v)[NE]) {
 #pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor(v, s, moe::WAVE));
-    return v;
+    for (int j = 0; j < NE / VEC; ++j) {
+        const int e = (lane + 64 * j) * VEC;
+        const int64_t at = t * E + e;
+        if constexpr (ZD == MOE_X_F32) {
+            v[j] = e < E ? reinterpret_cast<const float*>(z)[at] : -INFINITY;
+        } else if constexpr (VEC == 1) {
+            v[j] = e < E ? moe::bf16_to_f32(reinterpret_cast<const uint16_t*>(z)[at]) : -INFINITY;
+        } else {
+            const uint32_t p = e < E ? *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(z) + at)
+                                     : 0xFF80FF80u;
+            v[2 * j] = moe::bf16_lo(p);
+            v[2 * j + 1] = moe::bf16_hi(p);
+        }
+    }
 }
 
-// Workspace: per block, the sums of p per expert, the sum of lse^2, the picks
-// per expert and the counted tokens.
+// Workspace: per block of the row kernel the sums of p per expert, the sum of
+// lse^2, the picks per expert and the counted tokens; per block of the second
+// pass its part of sum_e c_e P_e and of sum_e c_e.
 struct BalWs {
     double* share;   // [blocks][E]
     double* lse2;    // [blocks]
+    double* dot;     // [parts]
     int32_t* picks;  // [blocks][E]
     int32_t* toks;   // [blocks]
+    int32_t* sum;    // [parts]
 };
 
-__host__ __device__ inline size_t bal_bytes(int blocks, int E) { return (size_t)blocks * (12 * (size_t)E + 12); }
+inline int bal_blocks(int T, int waves) {
+    const int64_t b = ((int64_t)T + waves - 1) / waves;
+    return T <= BAL_ONE ? 1 : b < BAL_MAX_BLOCKS ? (int)b : BAL_MAX_BLOCKS;
+}
 
-inline int bal_blocks(int T) {
-    const int b = (T + BAL_WAVES - 1) / BAL_WAVES;
-    return b < 1 ? 1 : b < BAL_MAX_BLOCKS ? b : BAL_MAX_BLOCKS;
+inline int bal_parts(int E) { return (E + SUM_E - 1) / SUM_E; }
+
+inline size_t bal_bytes(int blocks, int E) {
+    return (size_t)blocks * (12 * (size_t)E + 12) + (size_t)bal_parts(E) * 12;
 }
 
 inline BalWs bal_ws(void* ws, int blocks, int E) {
     BalWs w;
     w.share = reinterpret_cast<double*>(ws);
     w.lse2 = w.share + (size_t)blocks * E;
-    w.picks = reinterpret_cast<int32_t*>(w.lse2 + blocks);
+    w.dot = w.lse2 + blocks;
+    w.picks = reinterpret_cast<int32_t*>(w.dot + bal_parts(E));
     w.toks = w.picks + (size_t)blocks * E;
+    w.sum = w.toks + blocks;
     return w;
 }
 
-template <int ZD, int NE>
-__global__ void __launch_bounds__(BAL_THREADS) k_balance(const void* __restrict__ z, const int32_t* __restrict__ ids,
-                                                         const uint8_t* __restrict__ mask, int T, int E, int k,
-                                                         float* __restrict__ lse, BalWs ws) {
+// Rows of per-expert sums in LDS: one a wave of half the workgroup, or one.
+constexpr int share_rows(int NE, bool one) { return NE <= 8 ? bal_waves(NE, one) / 2 : 1; }
+
+struct BalOut {
+    int32_t* counts;
+    int32_t* totals;
+    double* share;
+    float* loss;
+};
+
+__device__ __forceinline__ void write_totals(const BalOut& o, int E, int n, int picks, double dot, double lse2) {
+    o.totals[0] = n;
+    o.totals[1] = picks;
+    o.loss[0] = picks > 0 && n > 0 ? (float)(E * dot / (double)picks) : 0.0f;
+    o.loss[1] = n > 0 ? (float)(lse2 / n) : 0.0f;
+}
+
+// A wave takes `per` tokens in a row, 64 at a time: one after the other for the
+// softmax (all lanes on one token), then side by side (a lane a token) for the
+// logarithm, lse and the picks.  ONE: a single workgroup, which also writes the
+// outputs.
+template <int ZD, int VEC, int NE, bool ONE>
+__global__ void __launch_bounds__(64 * bal_waves(NE, ONE)) k_balance(const void* __restrict__ z,
+                                                                     const int32_t* __restrict__ ids,
+                                                                     const uint8_t* __restrict__ mask, int T, int E,
+                                                                     int k, int per, float* __restrict__ lse, BalWs ws,
+                                                                     BalOut o) {
+    constexpr int NW = bal_waves(NE, ONE);
     extern __shared__ __align__(16) unsigned char smem[];
-    double* s_share = reinterpret_cast<double*>(smem);                 // [E]
-    double* s_lse2 = s_share + E;                                      // [BAL_WAVES]
-    int32_t* s_picks = reinterpret_cast<int32_t*>(s_lse2 + BAL_WAVES);  // [E]
-    int32_t* s_toks = s_picks + E;                                     // [BAL_WAVES]
+    double* s_share = reinterpret_cast<double*>(smem);            // [share_rows(NE, ONE)][E]
+    double* s_lse2 = s_share + (size_t)share_rows(NE, ONE) * E;   // [NW]
+    int32_t* s_picks = reinterpret_cast<int32_t*>(s_lse2 + NW);    // [E]
+    int32_t* s_toks = s_picks + E;                                // [NW]
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-    for (int e = threadIdx.x; e < E; e += BAL_THREADS) s_picks[e] = 0;
+    for (int e = threadIdx.x; e < E; e += 64 * NW) s_picks[e] = 0;
     __syncthreads();
     double acc[NE] = {}, lse2 = 0.0;
     int toks = 0;
-    for (int64_t t = (int64_t)blockIdx.x * BAL_WAVES + wid; t < T; t += (int64_t)gridDim.x * BAL_WAVES) {
-        bool live = !mask || mask[t];
-        float v[NE], m = -INFINITY;
-        if (live) {
+    const int64_t first = ((int64_t)blockIdx.x * NW + wid) * per;
+    const int64_t end = first + per < T ? first + per : T;
+    for (int64_t t0 = first; t0 < end; t0 += 64) {
+        const int n = end - t0 < 64 ? (int)(end - t0) : 64;
+        const unsigned long long todo = __ballot(lane < n && (!mask || mask[t0 + lane]));
+        float v[NE], my_m = 0.0f;
+        double my_sum = 0.0;  // of token t0 + lane; 0: left out
+        if (todo & 1) load_row<ZD, VEC, NE>(z, t0, E, lane, v);
+        for (int i = 0; i < n; ++i) {
+            float cur[NE], m = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < NE; ++j) {
-                const int e = lane + 64 * j;
-                v[j] = e < E ? load_z<ZD>(z, t * E + e) : -INFINITY;
-                m = fmaxf(m, v[j]);
-            }
-            m = wave_max(m);  // NaN loses every comparison: looked for where nothing else is left
-            bool nan = false;
+            for (int j = 0; j < NE; ++j) cur[j] = v[j];
+            // the next token's logits, while this one's are summed
+            if (i + 1 < n && (todo >> (i + 1)) & 1) load_row<ZD, VEC, NE>(z, t0 + i + 1, E, lane, v);
+            if (!((todo >> i) & 1)) continue;
+#pragma unroll
+            for (int j = 0; j < NE; ++j) m = fmaxf(m, cur[j]);
+            m = moe::wave_all_max(m);  // NaN loses every comparison: looked for where nothing else is left
             if (m == -INFINITY) {
+                bool nan = false;
 #pragma unroll
-                for (int j = 0; j < NE; ++j) nan |= v[j] != v[j];
+                for (int j = 0; j < NE; ++j) nan |= cur[j] != cur[j];
+                if (!__any(nan)) continue;
             }
-            live = m > -INFINITY || __any(nan);
-        }
-        float out = 0.0f;
-        if (live) {
             double p[NE], sum = 0.0;
 #pragma unroll
-            for (int j = 0; j < NE; ++j) sum += p[j] = exp((double)v[j] - (double)m);
-            sum = moe::wave_sum(sum);
-            const double r = 1.0 / sum, l = (double)m + log(sum);
+            for (int j = 0; j < NE; ++j) sum += p[j] = moe::exp64((double)cur[j] - (double)m);
+            sum = moe::wave_all_sum(sum);
+            // 1 / sum: the hardware's estimate and two Newton steps (sum lies in [1, E])
+            double r = __builtin_amdgcn_rcp(sum);
+            r = fma(fma(-sum, r, 1.0), r, r);
+            r = fma(fma(-sum, r, 1.0), r, r);
 #pragma unroll
-            for (int j = 0; j < NE; ++j) acc[j] += p[j] * r;
-            lse2 += l * l;
-            out = (float)l;
-            ++toks;
-            for (int j = lane; j < k; j += 64) {
-                const int e = ids[t * k + j];
-                if (e >= 0 && e < E) atomicAdd(&s_picks[e], 1);
-            }
+            for (int j = 0; j < NE; ++j) acc[j] = fma(p[j], r, acc[j]);
+            if (lane == i) my_m = m, my_sum = sum;
         }
-        if (lane == 0) lse[t] = out;
+        const bool live = my_sum != 0.0;
+        const double l = live ? (double)my_m + log(my_sum) : 0.0;
+        if (lane < n) lse[t0 + lane] = (float)l;
+        lse2 += l * l;
+        toks += live;
+        const unsigned long long counted = __ballot(live);
+        for (int i = lane; i < n * k; i += 64) {
+            const int e = ids[t0 * k + i];
+            if (((counted >> (i / k)) & 1) && e >= 0 && e < E) atomicAdd(&s_picks[e], 1);
+        }
     }
-    for (int w = 0; w < BAL_WAVES; ++w) {
-        if (wid == w) {
+    lse2 = moe::wave_all_sum(lse2);
+    toks = moe::wave_all_sum(toks);
+    if (lane == 0) s_lse2[wid] = lse2, s_toks[wid] = toks;
+    // the waves' sums, in an order of their own: halves, quarters, ... (or one
+    // after the other where LDS has room for one row)
+    const auto at = [&](int j) { return (lane + 64 * (j / VEC)) * VEC + j % VEC; };
+    if constexpr (share_rows(NE, ONE) > 1) {
 #pragma unroll
-            for (int j = 0; j < NE; ++j) {
-                const int e = lane + 64 * j;
-                if (e < E) s_share[e] = w ? s_share[e] + acc[j] : acc[j];
+        for (int h = NW / 2; h >= 1; h >>= 1) {
+            if (wid >= h && wid < 2 * h) {
+#pragma unroll
+                for (int j = 0; j < NE; ++j)
+                    if (at(j) < E) s_share[(size_t)(wid - h) * E + at(j)] = acc[j];
             }
-            if (lane == 0) s_lse2[w] = lse2, s_toks[w] = toks;
+            __syncthreads();
+            if (wid < h) {
+#pragma unroll
+                for (int j = 0; j < NE; ++j)
+                    if (at(j) < E) acc[j] += s_share[(size_t)wid * E + at(j)];
+            }
+            __syncthreads();
+        }
+        if (wid == 0) {
+#pragma unroll
+            for (int j = 0; j < NE; ++j)
+                if (at(j) < E) s_share[at(j)] = acc[j];
         }
         __syncthreads();
+    } else {
+        for (int w = 0; w < NW; ++w) {
+            if (wid == w) {
+#pragma unroll
+                for (int j = 0; j < NE; ++j)
+                    if (at(j) < E) s_share[at(j)] = w ? s_share[at(j)] + acc[j] : acc[j];
+            }
+            __syncthreads();
+        }
     }
-    for (int e = threadIdx.x; e < E; e += BAL_THREADS) {
-        ws.share[(int64_t)blockIdx.x * E + e] = s_share[e];
-        ws.picks[(int64_t)blockIdx.x * E + e] = s_picks[e];
-    }
-    if (threadIdx.x == 0) {
-        double l = 0.0;
-        int n = 0;
-        for (int w = 0; w < BAL_WAVES; ++w) l += s_lse2[w], n += s_toks[w];
-        ws.lse2[blockIdx.x] = l;
-        ws.toks[blockIdx.x] = n;
+    double l2 = 0.0;
+    int n = 0;
+    for (int w = 0; w < NW; ++w) l2 += s_lse2[w], n += s_toks[w];
+    if constexpr (!ONE) {
+        for (int e = threadIdx.x; e < E; e += 64 * NW) {
+            ws.share[(int64_t)blockIdx.x * E + e] = s_share[e];
+            ws.picks[(int64_t)blockIdx.x * E + e] = s_picks[e];
+        }
+        if (threadIdx.x == 0) ws.lse2[blockIdx.x] = l2, ws.toks[blockIdx.x] = n;
+    } else {
+        double dot = 0.0;
+        int picks = 0;
+        for (int e = threadIdx.x; e < E; e += 64 * NW) {
+            const double s = n > 0 ? s_share[e] / n : 0.0;
+            o.share[e] = s;
+            o.counts[e] = s_picks[e];
+            dot += s * s_picks[e];
+            picks += s_picks[e];
+        }
+        dot = moe::wave_all_sum(dot);
+        picks = moe::wave_all_sum(picks);
+        __syncthreads();  // every thread has read s_lse2 and s_toks
+        if (lane == 0) s_lse2[wid] = dot, s_toks[wid] = picks;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            dot = 0.0;
+            picks = 0;
+            for (int w = 0; w < NW; ++w) dot += s_lse2[w], picks += s_toks[w];
+            write_totals(o, E, n, picks, dot, l2);
+        }
     }
 }
 
-__global__ void __launch_bounds__(1024) k_balance_final(BalWs ws, int blocks, int E, int32_t* __restrict__ counts,
-                                                        int32_t* __restrict__ totals, double* __restrict__ share,
-                                                        float* __restrict__ loss) {
-    __shared__ double s_dot[16];
-    __shared__ int64_t s_picks[16];
+// Second pass: SUM_E experts a workgroup, 64 groups of threads each adding up
+// every 64th block, then the groups in order.
+__global__ void __launch_bounds__(SUM_THREADS) k_balance_sum(BalWs ws, int blocks, int E, BalOut o) {
+    __shared__ double s_share[SUM_THREADS];
+    __shared__ int s_picks[SUM_THREADS], s_n[SUM_THREADS / 64];
+    const int tid = threadIdx.x, e = blockIdx.x * SUM_E + tid % SUM_E;
     int n = 0;
-    double l2 = 0.0;
-    for (int b = 0; b < blocks; ++b) n += ws.toks[b], l2 += ws.lse2[b];
-    const double inv = n > 0 ? 1.0 / n : 0.0;
-    double dot = 0.0;
-    int64_t picks = 0;
-    for (int e = threadIdx.x; e < E; e += 1024) {
-        double s = 0.0;
-        int c = 0;
-        for (int b = 0; b < blocks; ++b) s += ws.share[(int64_t)b * E + e], c += ws.picks[(int64_t)b * E + e];
-        s *= inv;
-        counts[e] = c;
-        share[e] = s;
-        dot += s * c;
-        picks += c;
-    }
-    dot = moe::wave_sum(dot);
-    picks = moe::wave_sum((long long)picks);
-    if ((threadIdx.x & 63) == 0) s_dot[threadIdx.x >> 6] = dot, s_picks[threadIdx.x >> 6] = picks;
+    for (int b = tid; b < blocks; b += SUM_THREADS) n += ws.toks[b];
+    n = moe::wave_all_sum(n);
+    if ((tid & 63) == 0) s_n[tid >> 6] = n;
+    double s = 0.0;
+    int c = 0;
+    if (e < E)
+        for (int b = tid / SUM_E; b < blocks; b += SUM_THREADS / SUM_E)
+            s += ws.share[(int64_t)b * E + e], c += ws.picks[(int64_t)b * E + e];
+    s_share[tid] = s;
+    s_picks[tid] = c;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        dot = 0.0;
-        picks = 0;
-        for (int w = 0; w < 16; ++w) dot += s_dot[w], picks += s_picks[w];
-        totals[0] = n;
-        totals[1] = (int32_t)picks;
-        loss[0] = picks > 0 ? (float)(E * dot / (double)picks) : 0.0f;
-        loss[1] = (float)(l2 * inv);
+    if (tid >= 64) return;
+    n = 0;
+    for (int w = 0; w < SUM_THREADS / 64; ++w) n += s_n[w];
+    // a wave holds four of the 64 groups: each lane adds every fourth, then the four
+    s = 0.0;
+    c = 0;
+    for (int g = tid; g < SUM_THREADS; g += 64) s += s_share[g], c += s_picks[g];
+    s += __shfl_xor(s, 16, moe::WAVE);
+    s += __shfl_xor(s, 32, moe::WAVE);
+    c += __shfl_xor(c, 16, moe::WAVE);
+    c += __shfl_xor(c, 32, moe::WAVE);
+    s = n > 0 ? s / n : 0.0;
+    const bool mine = tid < SUM_E && e < E;
+    if (mine) o.share[e] = s, o.counts[e] = c;
+    const double dot = moe::wave_sum(mine ? s * c : 0.0);
+    const int picks = moe::wave_sum(mine ? c : 0);
+    if (tid == 0) ws.dot[blockIdx.x] = dot, ws.sum[blockIdx.x] = picks;
+}
+
+__global__ void __launch_bounds__(256) k_balance_loss(BalWs ws, int blocks, int parts, int E, BalOut o) {
+    __shared__ double s_dot[4], s_l2[4];
+    __shared__ int s_picks[4], s_n[4];
+    const int tid = threadIdx.x;
+    double dot = 0.0, l2 = 0.0;
+    int picks = 0, n = 0;
+    for (int p = tid; p < parts; p += 256) dot += ws.dot[p], picks += ws.sum[p];
+    for (int b = tid; b < blocks; b += 256) l2 += ws.lse2[b], n += ws.toks[b];
+    dot = moe::wave_sum(dot);
+    l2 = moe::wave_sum(l2);
+    picks = moe::wave_sum(picks);
+    n = moe::wave_sum(n);
+    if ((tid & 63) == 0) s_dot[tid >> 6] = dot, s_l2[tid >> 6] = l2, s_picks[tid >> 6] = picks, s_n[tid >> 6] = n;
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < 4; ++w) dot += s_dot[w], l2 += s_l2[w], picks += s_picks[w], n += s_n[w];
+        write_totals(o, E, n, picks, dot, l2);
     }
 }
 
 // f is taken less its mean 1/E, as whole numbers over whole numbers: the
 // subtraction f_e - sum f p of nearly equal numbers (a balanced router) then
 // costs no digits, since sum p = 1.
-template <int ZD, int NE>
-__global__ void __launch_bounds__(BAL_THREADS) k_balance_bwd(const void* __restrict__ z, const float* __restrict__ lse,
-                                                             const uint8_t* __restrict__ mask,
-                                                             const int32_t* __restrict__ counts,
-                                                             const int32_t* __restrict__ totals,
-                                                             const float* __restrict__ dloss, int T, int E,
-                                                             void* __restrict__ dz) {
+template <int ZD, int VEC, int NE>
+__global__ void __launch_bounds__(256) k_balance_bwd(const void* z, const float* __restrict__ lse,
+                                                     const uint8_t* __restrict__ mask,
+                                                     const int32_t* __restrict__ counts,
+                                                     const int32_t* __restrict__ totals,
+                                                     const float* __restrict__ dloss, int T, int E, void* dz) {
+    constexpr int NW = 4;
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
     const int n = totals[0], picks = totals[1];
     const double rn = n > 0 ? 1.0 / n : 0.0;
@@ -188,60 +320,66 @@ __global__ void __launch_bounds__(BAL_THREADS) k_balance_bwd(const void* __restr
     float f[NE];  // g_b E (f_e - 1/E) / n
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
-        const int e = lane + 64 * j;
+        const int e = (lane + 64 * (j / VEC)) * VEC + j % VEC;
         f[j] = e < E ? (float)((double)((int64_t)counts[e] * E - picks) * gb) : 0.0f;
     }
-    for (int64_t t = (int64_t)blockIdx.x * BAL_WAVES + wid; t < T; t += (int64_t)gridDim.x * BAL_WAVES) {
+    for (int64_t t = (int64_t)blockIdx.x * NW + wid; t < T; t += (int64_t)gridDim.x * NW) {
         const bool live = !mask || mask[t];
-        float p[NE], dot = 0.0f;
-        const float l = lse[t];
+        float p[NE], dot = 0.0f, l = 0.0f;
+        if (live) {
+            l = lse[t];
+            load_row<ZD, VEC, NE>(z, t, E, lane, p);
 #pragma unroll
-        for (int j = 0; j < NE; ++j) {
-            const int e = lane + 64 * j;
-            p[j] = live && e < E ? expf(load_z<ZD>(z, t * E + e) - l) : 0.0f;
-            dot = fmaf(p[j], f[j], dot);
+            for (int j = 0; j < NE; ++j) {
+                p[j] = expf(p[j] - l);
+                dot = fmaf(p[j], f[j], dot);
+            }
         }
-        dot = moe::wave_sum(dot);
+        dot = moe::wave_all_sum(dot);
         const float c = gz * l - dot;
 #pragma unroll
-        for (int j = 0; j < NE; ++j) {
-            const int e = lane + 64 * j;
+        for (int j = 0; j < NE / VEC; ++j) {
+            const int e = (lane + 64 * j) * VEC;
             if (e >= E) continue;
-            const float d = live ? p[j] * (f[j] + c) : 0.0f;
-            if constexpr (ZD == MOE_X_F32) reinterpret_cast<float*>(dz)[t * E + e] = d;
-            else reinterpret_cast<__bf16*>(dz)[t * E + e] = (__bf16)d;
+            const float d = live ? p[VEC * j] * (f[VEC * j] + c) : 0.0f;
+            if constexpr (ZD == MOE_X_F32) {
+                reinterpret_cast<float*>(dz)[t * E + e] = d;
+            } else if constexpr (VEC == 1) {
+                reinterpret_cast<__bf16*>(dz)[t * E + e] = (__bf16)d;
+            } else {
+                const float d1 = live ? p[VEC * j + 1] * (f[VEC * j + 1] + c) : 0.0f;
+                reinterpret_cast<bf16x2*>(dz)[(t * E + e) / 2] = bf16x2{(__bf16)d, (__bf16)d1};
+            }
         }
     }
 }
 
-template <int ZD>
-void launch_rows(int blocks, size_t lds, hipStream_t st, const void* z, const int32_t* ids, const uint8_t* mask, int T,
-                 int E, int k, float* lse, BalWs ws) {
-    const auto go = [&](auto kern) {
-        hipLaunchKernelGGL(kern, dim3(blocks), dim3(BAL_THREADS), lds, st, z, ids, mask, T, E, k, lse, ws);
-    };
-    if (E <= 64) go(k_balance<ZD, 1>);
-    else if (E <= 128) go(k_balance<ZD, 2>);
-    else if (E <= 256) go(k_balance<ZD, 4>);
-    else if (E <= 512) go(k_balance<ZD, 8>);
-    else if (E <= 1024) go(k_balance<ZD, 16>);
-    else if (E <= 2048) go(k_balance<ZD, 32>);
-    else go(k_balance<ZD, 64>);
+// Calls go with the number of experts a lane holds: one number for each group
+// of 64 (64 pairs) up to eight, then 16, 32, 64.
+template <int VEC, typename Go>
+void by_experts(int E, const Go& go) {
+    const int j = (E + 64 * VEC - 1) / (64 * VEC);
+    if (j <= 1) go(std::integral_constant<int, VEC>{});
+    else if (j <= 2) go(std::integral_constant<int, 2 * VEC>{});
+    else if (j <= 3) go(std::integral_constant<int, 3 * VEC>{});
+    else if (j <= 4) go(std::integral_constant<int, 4 * VEC>{});
+    else if (j * VEC <= 6 && VEC == 1) go(std::integral_constant<int, 6>{});
+    else if (j * VEC <= 8) go(std::integral_constant<int, 8>{});
+    else if (j * VEC <= 16) go(std::integral_constant<int, 16>{});
+    else if (j * VEC <= 32) go(std::integral_constant<int, 32>{});
+    else go(std::integral_constant<int, 64>{});
 }
 
-template <int ZD>
-void launch_bwd(int blocks, hipStream_t st, const void* z, const float* lse, const uint8_t* mask,
-                const int32_t* counts, const int32_t* totals, const float* dloss, int T, int E, void* dz) {
-    const auto go = [&](auto kern) {
-        hipLaunchKernelGGL(kern, dim3(blocks), dim3(BAL_THREADS), 0, st, z, lse, mask, counts, totals, dloss, T, E, dz);
-    };
-    if (E <= 64) go(k_balance_bwd<ZD, 1>);
-    else if (E <= 128) go(k_balance_bwd<ZD, 2>);
-    else if (E <= 256) go(k_balance_bwd<ZD, 4>);
-    else if (E <= 512) go(k_balance_bwd<ZD, 8>);
-    else if (E <= 1024) go(k_balance_bwd<ZD, 16>);
-    else if (E <= 2048) go(k_balance_bwd<ZD, 32>);
-    else go(k_balance_bwd<ZD, 64>);
+// Format and pairs: bf16 rows of an even length are read in pairs.
+template <typename Go>
+void by_format(int z_dtype, int E, const Go& go) {
+    using std::integral_constant;
+    if (z_dtype == MOE_X_F32)
+        by_experts<1>(E, [&](auto ne) { go(integral_constant<int, MOE_X_F32>{}, integral_constant<int, 1>{}, ne); });
+    else if (E % 2)
+        by_experts<1>(E, [&](auto ne) { go(integral_constant<int, MOE_X_BF16>{}, integral_constant<int, 1>{}, ne); });
+    else
+        by_experts<2>(E, [&](auto ne) { go(integral_constant<int, MOE_X_BF16>{}, integral_constant<int, 2>{}, ne); });
 }
 
 }  // namespace
@@ -250,7 +388,7 @@ extern "C" {
 
 size_t moe_balance_workspace_bytes(int T, int E) {
     if (T < 0 || T > MOE_BALANCE_MAX_T || E < 1 || E > MOE_MAX_E) return 0;
-    return (bal_bytes(bal_blocks(T), E) + 15) & ~(size_t)15;
+    return (bal_bytes(bal_blocks(T, 4), E) + 15) & ~(size_t)15;
 }
 
 int moe_balance_loss(const void* z, int z_dtype, const int32_t* ids, const uint8_t* mask, int T, int E, int k,
@@ -267,14 +405,32 @@ int moe_balance_loss(const void* z, int z_dtype, const int32_t* ids, const uint8
                 "moe_balance_loss: z, share and ws must start on 16 bytes");
     MOE_REQUIRE(ws_bytes >= moe_balance_workspace_bytes(T, E), MOE_E_ARG,
                 "moe_balance_loss: workspace of %zu bytes, %zu needed", ws_bytes, moe_balance_workspace_bytes(T, E));
-    const int blocks = bal_blocks(T);
-    const BalWs w = bal_ws(ws, blocks, E);
-    const size_t lds = 12 * (size_t)E + 12 * BAL_WAVES;
-    if (z_dtype == MOE_X_F32) launch_rows<MOE_X_F32>(blocks, lds, stream, z, ids, mask, T, E, k, lse, w);
-    else launch_rows<MOE_X_BF16>(blocks, lds, stream, z, ids, mask, T, E, k, lse, w);
+    const BalOut o{counts, totals, share, loss};
+    int blocks = 0;
+    BalWs w{};
+    by_format(z_dtype, E, [&](auto zd, auto vec, auto ne) {
+        constexpr int ZD = decltype(zd)::value, VEC = decltype(vec)::value, NE = decltype(ne)::value;
+        const auto launch = [&](auto one) {
+            constexpr bool ONE = decltype(one)::value;
+            constexpr int NW = bal_waves(NE, ONE);
+            blocks = ONE ? 1 : bal_blocks(T, NW);
+            w = bal_ws(ws, blocks, E);
+            const int64_t waves = (int64_t)blocks * NW;
+            const int per = (int)((T + waves - 1) / waves);
+            const size_t lds = (size_t)E * (8 * share_rows(NE, ONE) + 4) + 12 * NW;
+            hipLaunchKernelGGL((k_balance<ZD, VEC, NE, ONE>), dim3(blocks), dim3(64 * NW), lds, stream, z, ids, mask, T,
+                               E, k, per, lse, w, o);
+        };
+        if (T <= BAL_ONE) launch(std::true_type{});
+        else launch(std::false_type{});
+    });
     if (int rc = moe_check_launch("moe_balance_loss")) return rc;
-    hipLaunchKernelGGL(k_balance_final, dim3(1), dim3(1024), 0, stream, w, blocks, E, counts, totals, share, loss);
-    return moe_check_launch("moe_balance_loss/final");
+    if (T <= BAL_ONE) return moe_ok();
+    const int parts = bal_parts(E);
+    hipLaunchKernelGGL(k_balance_sum, dim3(parts), dim3(SUM_THREADS), 0, stream, w, blocks, E, o);
+    if (int rc = moe_check_launch("moe_balance_loss/sum")) return rc;
+    hipLaunchKernelGGL(k_balance_loss, dim3(1), dim3(256), 0, stream, w, blocks, parts, E, o);
+    return moe_check_launch("moe_balance_loss/loss");
 }
 
 int moe_balance_loss_bwd(const void* z, int z_dtype, const float* lse, const uint8_t* mask, const int32_t* counts,
@@ -289,9 +445,11 @@ int moe_balance_loss_bwd(const void* z, int z_dtype, const float* lse, const uin
     MOE_REQUIRE(moe_aligned16(z) && moe_aligned16(dz), MOE_E_ALIGN,
                 "moe_balance_loss_bwd: z and dz must start on 16 bytes");
     if (T == 0) return moe_ok();
-    const int blocks = (T + BAL_WAVES - 1) / BAL_WAVES < 2048 ? (T + BAL_WAVES - 1) / BAL_WAVES : 2048;
-    if (z_dtype == MOE_X_F32) launch_bwd<MOE_X_F32>(blocks, stream, z, lse, mask, counts, totals, dloss, T, E, dz);
-    else launch_bwd<MOE_X_BF16>(blocks, stream, z, lse, mask, counts, totals, dloss, T, E, dz);
+    const int blocks = (T + 3) / 4 < 2048 ? (T + 3) / 4 : 2048;
+    by_format(z_dtype, E, [&](auto zd, auto vec, auto ne) {
+        hipLaunchKernelGGL((k_balance_bwd<decltype(zd)::value, decltype(vec)::value, decltype(ne)::value>),
+                           dim3(blocks), dim3(256), 0, stream, z, lse, mask, counts, totals, dloss, T, E, dz);
+    });
     return moe_check_launch("moe_balance_loss_bwd");
 }
 
