@@ -11,15 +11,15 @@
 // mass exceeds u times the kept mass Z.
 //
 // Masses are whole numbers: w_i, computed in double, rounded to a multiple of
-// 2^-S with S = 62 - ceil(log2 V), so a row's mass stays below 2^63.  Sums of
-// whole numbers do not depend on their order: the result is one of the inputs
-// alone, with integer atomics wherever they are handy.
+// 2^-S with S = 62 - ceil(log2 V) (51 at most), so a row's mass stays below
+// 2^63.  Sums of whole numbers do not depend on their order: the result is one
+// of the inputs alone, with integer atomics wherever they are handy.
 //
 // What is kept is always a prefix, so one pair (key, id) says it, and no row
 // is ever sorted.  A row is cut into BINS of equal width in the logit (over
 // the span where masses are not 0); counts and masses per bin tell in which
 // bin a cut falls, and only the ids of those bins (a few hundred, whatever the
-// row) are listed, sorted and summed to find where.
+// row) are listed and searched for the place.
 //   rows of up to ROW_MAX ids   one workgroup a row, logits in registers
 //   longer rows                 k_top (largest and smallest candidate of each
 //                               chunk) -> k_bins (counts and masses per bin)
@@ -31,8 +31,11 @@
 // bits of the logit's key a pass over the whole row: slower, the same result.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "exp64.hpp"
+#include "wave.hpp"
 
 namespace {
 
@@ -42,11 +45,10 @@ using v2u = uint32_t __attribute__((ext_vector_type(2)));
 
 constexpr int BINS = 1024;
 constexpr int LIST = 2048;
-constexpr int CHUNK = 4096;          // ids of a workgroup of k_top .. k_list
-constexpr int CHUNK_THREADS = 256;
-constexpr int ROW_THREADS = 1024;
-constexpr int ROW_MAX = 16384;       // ids a workgroup's registers hold
-constexpr int MAX_CHUNKS = MOE_SAMPLE_MAX_V / CHUNK;
+constexpr int PER = 16;               // ids a thread holds
+constexpr int GROUPS = PER / 4;       // in groups of four
+constexpr int ROW_MAX = 1024 * PER;   // ids of a row one workgroup holds
+constexpr int MAX_CHUNKS = MOE_SAMPLE_MAX_V / (256 * PER);
 
 // Rising with the value; -inf and NaN give 0 (not a candidate).  -0 counts as +0.
 __device__ __forceinline__ uint32_t key_of(float l) {
@@ -73,31 +75,48 @@ struct SmpArgs {
     int vec;  // rows start on four logits
 };
 
+// Where the cuts fall.  Ids of bins below `sure` are kept whatever happens
+// inside the cut bins: bins p0 .. p1 (top-p; the last one is open as long as
+// the mass that top-k leaves is) and bin `bk` (top-k).
+struct Cuts {
+    int sure, p0, p1, bk;
+    u64 rank, mass_bk;  // ids of bin bk that top-k keeps; mass above bin bk (no such bin: the row's)
+    __device__ __forceinline__ bool lists(int b) const { return (b >= p0 && b <= p1) || b == bk; }
+    __device__ __forceinline__ bool any() const { return sure < BINS; }
+};
+
 // Per row of the workspace (longer rows).
+struct Head {
+    Cuts cuts;
+    uint32_t kmax, kmin;  // keys of the row's largest and smallest candidate; kmax 0: none
+    uint32_t listed, pad;
+};
+
 struct RowWs {
+    Head* head;
     u64* bin_mass;       // [BINS]
     u64* list;           // [LIST] key << 32 | ~id
     u64* chunk_mass;     // [chunks] mass of the chunk's ids above the cut bins
     uint32_t* bin_count;  // [BINS]
     uint32_t* chunk_max;  // [chunks] keys
     uint32_t* chunk_min;  // [chunks]
-    uint32_t* listed;    // [1]
 
     static __host__ __device__ size_t bytes(int chunks) {
-        return (size_t)BINS * 12 + (size_t)LIST * 8 + (size_t)((chunks + 1) & ~1) * 16 + 16;
+        return sizeof(Head) + (size_t)BINS * 12 + (size_t)LIST * 8 + (size_t)((chunks + 1) & ~1) * 16;
     }
     __host__ __device__ RowWs(void* ws, int64_t row, int chunks) {
         const int c = (chunks + 1) & ~1;
         char* p = reinterpret_cast<char*>(ws) + row * bytes(chunks);
-        bin_mass = reinterpret_cast<u64*>(p);
+        head = reinterpret_cast<Head*>(p);
+        bin_mass = reinterpret_cast<u64*>(p + sizeof(Head));
         list = bin_mass + BINS;
         chunk_mass = list + LIST;
         bin_count = reinterpret_cast<uint32_t*>(chunk_mass + c);
         chunk_max = bin_count + BINS;
         chunk_min = chunk_max + c;
-        listed = chunk_min + c;
     }
 };
+static_assert(sizeof(Head) % 16 == 0, "rows of the workspace start on 16 bytes");
 
 template <int LD>
 __device__ __forceinline__ uint32_t load_key(const SmpArgs& a, int row, int i) {
@@ -146,7 +165,7 @@ struct Row {
         top = topf;
         rtemp = 1.0 / (double)temp;
         min_p = a.min_p ? (double)a.min_p[row] : 0.0;
-        if (!(min_p > 0.0)) min_p = 0.0;
+        min_p = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
         one = ldexp(1.0, a.S);
         k = a.top_k ? a.top_k[row] : 0;
         p = a.top_p ? a.top_p[row] : 1.0f;
@@ -159,9 +178,11 @@ struct Row {
     // of a candidate; 0 also for one that min-p drops
     __device__ __forceinline__ u64 mass(uint32_t key) const {
 #pragma clang fp contract(off)
-        if (key == kmax) return (u64)one;
-        const double w = moe::exp64(((double)value_of(key) - top) * rtemp);
-        return w >= min_p ? (u64)rint(w * one) : 0;
+        double w = moe::exp64(((double)value_of(key) - top) * rtemp);
+        w = key == kmax ? 1.0 : w;
+        // added to 2^52 the product, at most 2^51, is rounded into the low bits
+        const u64 m = __builtin_bit_cast(u64, fma(w, one, 0x1p52)) & ((1ull << 52) - 1);
+        return w >= min_p ? m : 0;
     }
     // never falls as the key falls: each step rounds monotonically
     __device__ __forceinline__ int bin(uint32_t key) const {
@@ -178,11 +199,12 @@ struct Row {
 
 // ------------------------------------------------------------- block helpers
 
+// Over the block, for every thread.  scratch: NT / 64 entries, free again once
+// the block has met another barrier.
 template <int NT, typename T, typename Op>
 __device__ __forceinline__ T block_reduce(T v, u64* scratch_, Op op) {
     T* scratch = reinterpret_cast<T*>(scratch_);
-#pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) v = op(v, __shfl_xor(v, s, moe::WAVE));
+    v = moe::wave_all(v, op);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -192,21 +214,11 @@ __device__ __forceinline__ T block_reduce(T v, u64* scratch_, Op op) {
     return v;
 }
 
-__device__ __forceinline__ u64 wave_scan(u64 v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        const u64 o = __shfl_up(v, s, moe::WAVE);
-        if (lane >= s) v += o;
-    }
-    return v;
-}
-
 // Inclusive sum over the block's threads, in thread order; *total the sum of all.
 template <int NT>
 __device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
     const int wid = threadIdx.x >> 6;
-    v = wave_scan(v);
+    v = moe::wave_upto(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 63) scratch[wid] = v;
     __syncthreads();
@@ -222,7 +234,11 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
 
 struct UMax { __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; } };
 struct UMin { __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a < b ? a : b; } };
-struct Add { __device__ u64 operator()(u64 a, u64 b) const { return a + b; } };
+struct Add {
+    __device__ u64 operator()(u64 a, u64 b) const { return a + b; }
+};
+struct U64Max { __device__ u64 operator()(u64 a, u64 b) const { return a > b ? a : b; } };
+struct U64Min { __device__ u64 operator()(u64 a, u64 b) const { return a < b ? a : b; } };
 
 __device__ __forceinline__ void finish(const SmpArgs& a, int row, int id, u64 w, u64 z) {
     a.ids[row] = id;
@@ -238,43 +254,33 @@ __device__ __forceinline__ u64 draw_at(const SmpArgs& a, int row, u64 z) {
 
 // ------------------------------------------------------ cuts: bins, then ids
 
-// Where the cuts fall.  Ids of bins below `sure` are kept whatever happens
-// inside the cut bins: bins p0 .. p1 (top-p; the last one is open as long as
-// the mass that top-k leaves is) and bin `bk` (top-k).
-struct Cuts {
-    int sure, p0, p1, bk;
-    u64 rank, mass_bk;  // ids of bin bk that top-k keeps; mass above bin bk
-    __device__ __forceinline__ bool lists(int b) const { return (b >= p0 && b <= p1) || b == bk; }
-    __device__ __forceinline__ bool any() const { return sure < BINS; }
-};
-
 // From the row's counts and masses per bin (counts only where top-k cuts,
 // masses only where top-p does).  s_cuts and scratch in LDS.
 template <int NT>
 __device__ __forceinline__ void find_cuts(const Row& r, const uint32_t* count, const u64* mass, Cuts* s_cuts,
                                           u64* s_z, u64* scratch) {
-    constexpr int PER = BINS / NT;
-    const int b0 = threadIdx.x * PER;
+    constexpr int NB = BINS / NT;
+    const int b0 = threadIdx.x * NB;
     if (threadIdx.x == 0) {
         s_cuts->sure = BINS, s_cuts->p0 = BINS, s_cuts->p1 = -1, s_cuts->bk = -1;
         s_cuts->rank = 0, s_cuts->mass_bk = 0;
     }
-    u64 m[PER], before = 0, total = 0;
+    u64 m[NB], before = 0, total = 0;
     if (r.cut_p) {
         u64 sum = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sum += m[i] = mass[b0 + i];
+        for (int i = 0; i < NB; ++i) sum += m[i] = mass[b0 + i];
         before = block_scan<NT>(sum, scratch, &total) - sum;
     }
     if (threadIdx.x == 0) s_z[0] = s_z[1] = total;  // the mass that top-k leaves lies between the two
     __syncthreads();
     if (r.cut_k) {
-        u64 c[PER], sum = 0, all;
+        u64 c[NB], sum = 0, all;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sum += c[i] = count[b0 + i];
+        for (int i = 0; i < NB; ++i) sum += c[i] = count[b0 + i];
         u64 at = block_scan<NT>(sum, scratch, &all) - sum, mb = before;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
+        for (int i = 0; i < NB; ++i) {
             if (all > (u64)r.k && at < (u64)r.k && at + c[i] >= (u64)r.k) {
                 s_cuts->bk = s_cuts->sure = b0 + i;
                 s_cuts->rank = (u64)r.k - at;
@@ -290,7 +296,7 @@ __device__ __forceinline__ void find_cuts(const Row& r, const uint32_t* count, c
         const u64 lo = r.want(s_z[0] ? s_z[0] : 1), hi = r.want(s_z[1]);
         u64 mb = before;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
+        for (int i = 0; i < NB; ++i) {
             if (mb < lo && mb + m[i] >= lo) s_cuts->p0 = s_cuts->sure = b0 + i;
             if (mb < hi && mb + m[i] >= hi) s_cuts->p1 = b0 + i;
             mb += m[i];
@@ -299,59 +305,109 @@ __device__ __forceinline__ void find_cuts(const Row& r, const uint32_t* count, c
     }
 }
 
-// Sorts list[0 .. n) falling (n at most LIST) and finds the last kept entry.
-// Returns its position; cum[i] is the mass of entries 0 .. i.
-template <int NT>
-__device__ __forceinline__ int resolve(const Row& r, const Cuts& c, u64 sure_mass, int n, u64* list, u64* cum,
-                                       u64* scratch, int* s_at) {
-    int size = 2;
-    while (size < n) size <<= 1;
-    for (int i = n + threadIdx.x; i < size; i += NT) list[i] = 0;
-    __syncthreads();
-    for (int w = 2; w <= size; w <<= 1)
-        for (int s = w >> 1; s >= 1; s >>= 1) {
-            for (int h = threadIdx.x; h < size >> 1; h += NT) {
-                const int i = 2 * h - (h & (s - 1)), j = i + s;
-                const u64 x = list[i], y = list[j];
-                if ((x < y) == ((i & w) == 0)) list[i] = y, list[j] = x;
+// The entry of list[0 .. n) that ends the shortest prefix (falling order, all
+// entries different) whose weight reaches `want` (at least 1, at most all of
+// it); entries of weight 0 are not there.  weight(i): entry i's, of any thread.
+// The span of the entries is cut into 256 by its leading bits, again and again,
+// until a wave can hold what is left: a lane an entry, each summing the weights
+// of the entries at least as large.
+template <int NT, typename W>
+__device__ __forceinline__ u64 select_list(const u64* list, int n, const W& weight, u64 want, u64* hist, u64* few,
+                                           u64* scratch, u64* s_out, int* s_n) {
+    u64 lo = ~0ull, hi = 0;
+    for (int i = threadIdx.x; i < n; i += NT)
+        if (weight(i)) lo = list[i] < lo ? list[i] : lo, hi = list[i] > hi ? list[i] : hi;
+    if (n > 64) {
+        lo = block_reduce<NT>(lo, scratch, U64Min());
+        hi = block_reduce<NT>(hi, scratch, U64Max());
+        int left = n;
+        while (left > 64 && lo < hi) {
+            const int top = 63 - __clzll((long long)(lo ^ hi));
+            const int shift = top > 7 ? top - 7 : 0;
+            const u64 base = lo >> shift & ~255ull;  // the bits above the digit, the same in all
+            __syncthreads();
+            for (int i = threadIdx.x; i < 256; i += NT) hist[i] = 0;
+            __syncthreads();
+            for (int i = threadIdx.x; i < n; i += NT) {
+                const u64 v = list[i], w = weight(i);
+                if (w && v >= lo && v <= hi) atomicAdd(&hist[v >> shift & 255], w);
             }
             __syncthreads();
+            if (threadIdx.x < 64) {  // falling digits: four a lane
+                u64 h[4], sum = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum += h[i] = hist[255 - 4 * threadIdx.x - i];
+                u64 before = moe::wave_upto(sum) - sum;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (before < want && before + h[i] >= want) s_out[0] = 255 - 4 * threadIdx.x - i, s_out[1] = want - before;
+                    before += h[i];
+                }
+            }
+            if (threadIdx.x == 0) *s_n = 0;
+            __syncthreads();
+            lo = (base | s_out[0]) << shift;
+            hi = lo | ((1ull << shift) - 1);
+            want = s_out[1];
+            int mine = 0;
+            u64 l = ~0ull, h = 0;
+            for (int i = threadIdx.x; i < n; i += NT) {
+                const u64 v = list[i];
+                if (v >= lo && v <= hi && weight(i)) ++mine, l = v < l ? v : l, h = v > h ? v : h;
+            }
+            if (mine) atomicAdd(s_n, mine);
+            lo = block_reduce<NT>(l, scratch, U64Min());
+            hi = block_reduce<NT>(h, scratch, U64Max());
+            left = *s_n;
         }
-    u64 base = 0;
-    for (int i0 = 0; i0 < n; i0 += NT) {
-        const int i = i0 + threadIdx.x;
-        u64 total;
-        const u64 v = block_scan<NT>(i < n ? r.mass((uint32_t)(list[i] >> 32)) : 0, scratch, &total);
-        if (i < n) cum[i] = base + v;
-        base += total;
-    }
-    if (threadIdx.x == 0) *s_at = n - 1;
-    __syncthreads();
-    u64 z = 0;  // the mass that top-k leaves
-    int last = n - 1;
-    if (c.bk >= 0) {
-        // entries of bins above bk come first
+        __syncthreads();
+        if (threadIdx.x == 0) *s_n = 0;
+        __syncthreads();
         for (int i = threadIdx.x; i < n; i += NT) {
-            const bool in = r.bin((uint32_t)(list[i] >> 32)) >= c.bk;
-            if (in && (i == 0 || r.bin((uint32_t)(list[i - 1] >> 32)) < c.bk)) *s_at = i + (int)c.rank - 1;
+            const u64 v = list[i], w = weight(i);
+            if (w && v >= lo && v <= hi) {
+                const int at = atomicAdd(s_n, 1);
+                if (at < 64) few[at] = v, few[64 + at] = w;
+            }
         }
         __syncthreads();
-        last = *s_at < n ? *s_at : n - 1;
-        const int first = last - (int)c.rank + 1;
-        z = c.mass_bk + cum[last] - (first > 0 ? cum[first - 1] : 0);
-    }
-    if (r.cut_p) {
-        if (c.bk < 0) z = c.mass_bk;
-        const u64 want = r.want(z);
+        n = *s_n < 64 ? *s_n : 64;
+    } else {
         __syncthreads();
-        for (int i = threadIdx.x; i <= last; i += NT) {
-            const u64 prev = sure_mass + (i > 0 ? cum[i - 1] : 0);
-            if (sure_mass + cum[i] >= want && prev < want) *s_at = i;
-        }
+        for (int i = threadIdx.x; i < n; i += NT) few[i] = list[i], few[64 + i] = weight(i);
         __syncthreads();
-        last = *s_at;
     }
-    return last;
+    if (threadIdx.x < 64) {
+        const u64 v = (int)threadIdx.x < n ? few[threadIdx.x] : 0, w = (int)threadIdx.x < n ? few[64 + threadIdx.x] : 0;
+        u64 cum = 0;
+        for (int i = 0; i < n; ++i) cum += few[i] >= v ? few[64 + i] : 0;
+        if (w && cum >= want && cum - w < want) s_out[0] = v;
+    }
+    __syncthreads();
+    const u64 out = s_out[0];
+    __syncthreads();
+    return out;
+}
+
+// The last kept entry of a row whose cut bins' ids are list[0 .. n), with their
+// masses beside them; sure_mass: of the bins above.
+template <int NT>
+__device__ __forceinline__ u64 resolve(const Row& r, const Cuts& c, u64 sure_mass, int n, const u64* list,
+                                       const u64* mass, u64* hist, u64* few, u64* scratch, u64* s_out, int* s_n) {
+    u64 bound = 0, z = c.mass_bk;  // the mass that top-k leaves
+    const auto in_bk = [&](int i) { return r.bin((uint32_t)(list[i] >> 32)) == c.bk; };
+    if (c.bk >= 0) {
+        bound = select_list<NT>(list, n, [&](int i) { return (u64)(in_bk(i) ? 1 : 0); }, c.rank, hist, few, scratch,
+                                s_out, s_n);
+        if (!r.cut_p) return bound;
+        u64 part = 0;
+        for (int i = threadIdx.x; i < n; i += NT)
+            if (list[i] >= bound && in_bk(i)) part += mass[i];
+        z += block_reduce<NT>(part, scratch, Add());
+    }
+    const u64 want = r.want(z);
+    return select_list<NT>(list, n, [&](int i) { return list[i] >= bound ? mass[i] : 0; },
+                           want > sure_mass ? want - sure_mass : 1, hist, few, scratch, s_out, s_n);
 }
 
 // ------------------------------------------------ the whole row, bit by bit
@@ -446,325 +502,352 @@ __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row
 // ------------------------------------------------------------ the draw
 
 // Thread's keys of group j are those of ids i0 + (j * NT + thread) * 4 .. + 3;
-// a segment is a wave's part of a group: 256 ids in a row.  Writes the result
-// of the id where the running mass passes `target`; z < 0: z is the mass of
-// these ids and target is drawn from it.  seg: J * NT / 64 u64.
-template <int NT, int J, bool WHOLE>
-__device__ __forceinline__ void draw(const SmpArgs& a, const Row& r, int row, int i0, const v4u (&key)[J], u64 bound,
-                                     u64 z, u64 target, u64* seg) {
+// a segment is a wave's part of a group: 256 ids in a row.  Finishes the row
+// with the id where the running mass of the kept ids (entries from `bound` on)
+// passes `target`.  WHOLE: these ids are the row; their mass is z, and the
+// target is drawn from it.  seg: GROUPS * NT / 64 entries.
+template <int NT, bool WHOLE>
+__device__ __forceinline__ void draw(const SmpArgs& a, const Row& r, int row, int i0, const v4u (&key)[GROUPS],
+                                     u64 bound, u64 z, u64 target, u64* seg) {
     constexpr int NW = NT / 64;
     const int wid = threadIdx.x >> 6;
-    u64 m[J][4], sum[J];
+    const auto mass = [&](int j, int v) {
+        const uint32_t kk = key[j][v];
+        const u64 at = ((u64)kk << 32) | (uint32_t)~(i0 + (j * NT + (int)threadIdx.x) * 4 + v);
+        return kk && at >= bound ? r.mass(kk) : 0;
+    };
+    u64 sum[GROUPS];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
+    for (int j = 0; j < GROUPS; ++j) {
         sum[j] = 0;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const uint32_t kk = key[j][v];
-            const u64 at = ((u64)kk << 32) | (uint32_t)~(i0 + (j * NT + (int)threadIdx.x) * 4 + v);
-            m[j][v] = kk && at >= bound ? r.mass(kk) : 0;
-            sum[j] += m[j][v];
-        }
-        const u64 all = moe::wave_sum(sum[j]);
+        for (int v = 0; v < 4; ++v) sum[j] += mass(j, v);
+        const u64 all = moe::wave_all_sum(sum[j]);
         if ((threadIdx.x & 63) == 0) seg[j * NW + wid] = all;
     }
     __syncthreads();
+    // segments are at most 64: a lane each
+    const int lane = threadIdx.x & 63;
+    const u64 mine = lane < GROUPS * NW ? seg[lane] : 0;
+    const u64 upto = moe::wave_upto(mine);
     if constexpr (WHOLE) {
-        z = 0;
-        for (int s = 0; s < J * NW; ++s) z += seg[s];
+        z = __shfl(upto, 63, moe::WAVE);
         target = draw_at(a, row, z);
     }
-    u64 before = 0;
-    int s = 0;
-    while (s < J * NW - 1 && before + seg[s] <= target) before += seg[s++];
+    const unsigned long long hit = __ballot(mine && upto > target);
+    const int s = hit ? __ffsll(hit) - 1 : 0;
+    const u64 before = __shfl(upto - mine, s, moe::WAVE);
     if (s % NW != wid) return;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
+    for (int j = 0; j < GROUPS; ++j) {
         if (j != s / NW) continue;
-        u64 at = before + wave_scan(sum[j]) - sum[j];
+        u64 at = before + moe::wave_upto(sum[j]) - sum[j];
+        if (at > target || at + sum[j] <= target) continue;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            if (m[j][v] && at <= target && at + m[j][v] > target)
-                finish(a, row, i0 + (j * NT + (int)threadIdx.x) * 4 + v, m[j][v], z);
-            at += m[j][v];
+            const u64 m = mass(j, v);
+            if (m && at <= target && at + m > target)
+                finish(a, row, i0 + (j * NT + (int)threadIdx.x) * 4 + v, m, z);
+            at += m;
         }
     }
 }
 
-// -------------------------------------------------- rows in one workgroup
-
-template <int LD>
-__global__ void __launch_bounds__(ROW_THREADS) k_row(SmpArgs a) {
-    constexpr int NT = ROW_THREADS, J = ROW_MAX / (4 * NT);
-    __shared__ u64 bin_mass[BINS];
-    __shared__ uint32_t bin_count[BINS];
-    __shared__ u64 list[LIST], cum[LIST];
-    __shared__ u64 scratch[NT / 64], s_z[2], seg[J * NT / 64];
-    __shared__ Cuts cuts;
-    __shared__ uint32_t s_key, s_n;
-    __shared__ int s_at;
-    const int row = blockIdx.x, tid = threadIdx.x;
-    v4u key[J];
-    uint32_t kmax = 0, kmin = 0xFFFFFFFFu;
+// A thread's share of a chunk of NT * PER ids from i0 on.
+template <int LD, int NT>
+__device__ __forceinline__ void load_ids(const SmpArgs& a, int row, int i0, v4u (&key)[GROUPS]) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        key[j] = load_keys<LD>(a, row, (j * NT + tid) * 4);
+    for (int j = 0; j < GROUPS; ++j) key[j] = load_keys<LD>(a, row, i0 + (j * NT + (int)threadIdx.x) * 4);
+}
+
+__device__ __forceinline__ void ends(const v4u (&key)[GROUPS], uint32_t& kmax, uint32_t& kmin) {
+    kmax = 0, kmin = 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             kmax = key[j][v] > kmax ? key[j][v] : kmax;
             kmin = key[j][v] && key[j][v] < kmin ? key[j][v] : kmin;
         }
-    }
-    for (int i = tid; i < BINS; i += NT) bin_mass[i] = 0, bin_count[i] = 0;
-    if (tid == 0) s_n = 0, s_at = a.V;
-    kmax = block_reduce<NT>(kmax, scratch, UMax());
-    if (kmax == 0) {
-        if (tid == 0) finish(a, row, -1, 0, 0);
-        return;
-    }
-    kmin = block_reduce<NT>(kmin, scratch, UMin());
-    const Row r(a, row, kmax, kmin);
-    if (r.greedy) {
-        int at = a.V;
-#pragma unroll
-        for (int j = J - 1; j >= 0; --j)
-#pragma unroll
-            for (int v = 3; v >= 0; --v)
-                if (key[j][v] == kmax) at = (j * NT + tid) * 4 + v;
-        if (at < a.V) atomicMin(&s_at, at);
-        __syncthreads();
-        if (tid == 0) finish(a, row, s_at, 1, 1);
-        return;
-    }
-    u64 bound = 0;
-    if (r.cut_k || r.cut_p) {
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const uint32_t kk = key[j][v];
-                const u64 w = kk ? r.mass(kk) : 0;
-                if (w) {
-                    const int b = r.bin(kk);
-                    if (r.cut_k) atomicAdd(&bin_count[b], 1u);
-                    if (r.cut_p) atomicAdd(&bin_mass[b], w);
-                }
-            }
-        __syncthreads();
-        find_cuts<NT>(r, bin_count, bin_mass, &cuts, s_z, scratch);
-        const Cuts c = cuts;
-        if (c.any()) {
-            u64 sure = 0;
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const uint32_t kk = key[j][v];
-                    const int b = kk ? r.bin(kk) : BINS;
-                    if (b < c.sure && r.cut_p) sure += r.mass(kk);
-                    if (kk && c.lists(b) && r.mass(kk)) {
-                        const uint32_t at = atomicAdd(&s_n, 1u);
-                        if (at < LIST) list[at] = ((u64)kk << 32) | (uint32_t)~((j * NT + tid) * 4 + v);
-                    }
-                }
-            sure = block_reduce<NT>(sure, scratch, Add());
-            Cuts cc = c;
-            if (c.bk < 0) cc.mass_bk = s_z[1];
-            if (s_n > LIST) {
-                select_row<LD, NT>(a, r, row, list, scratch, s_z, &s_key, &s_at);
-                return;
-            }
-            const int last = resolve<NT>(r, cc, sure, s_n, list, cum, scratch, &s_at);
-            bound = list[last];
-        }
-    }
-    draw<NT, J, true>(a, r, row, 0, key, bound, 0, 0, seg);
 }
 
-// -------------------------------------------------------------- longer rows
-
-template <int LD>
-__device__ __forceinline__ void load_chunk(const SmpArgs& a, int row, int chunk, v4u (&key)[CHUNK / 4 / CHUNK_THREADS]) {
+// The lowest of a thread's ids that holds kmax (~0: none).
+template <int NT>
+__device__ __forceinline__ uint32_t first_top(const v4u (&key)[GROUPS], int i0, uint32_t kmax) {
+    uint32_t id = ~0u;
 #pragma unroll
-    for (int j = 0; j < CHUNK / 4 / CHUNK_THREADS; ++j)
-        key[j] = load_keys<LD>(a, row, chunk * CHUNK + (j * CHUNK_THREADS + (int)threadIdx.x) * 4);
+    for (int j = GROUPS - 1; j >= 0; --j)
+#pragma unroll
+        for (int v = 3; v >= 0; --v)
+            if (key[j][v] == kmax) id = i0 + (j * NT + (int)threadIdx.x) * 4 + v;
+    return id;
 }
 
-template <int LD>
-__global__ void __launch_bounds__(CHUNK_THREADS) k_top(SmpArgs a, void* ws) {
-    constexpr int NT = CHUNK_THREADS, J = CHUNK / 4 / NT;
-    __shared__ u64 scratch[NT / 64];
-    const int row = blockIdx.y, chunk = blockIdx.x;
-    const RowWs w(ws, row, a.chunks);
-    v4u key[J];
-    load_chunk<LD>(a, row, chunk, key);
-    for (int i = chunk * NT + threadIdx.x; i < BINS; i += a.chunks * NT) w.bin_mass[i] = 0, w.bin_count[i] = 0;
-    if (chunk == 0 && threadIdx.x == 0) *w.listed = 0;
-    uint32_t kmax = 0, kmin = 0xFFFFFFFFu;
+// Counts and masses of a thread's ids into the bins.
+__device__ __forceinline__ void fill_bins(const Row& r, const v4u (&key)[GROUPS], uint32_t* count, u64* mass) {
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            kmax = key[j][v] > kmax ? key[j][v] : kmax;
-            kmin = key[j][v] && key[j][v] < kmin ? key[j][v] : kmin;
-        }
-    kmax = block_reduce<NT>(kmax, scratch, UMax());
-    kmin = block_reduce<NT>(kmin, scratch, UMin());
-    if (threadIdx.x == 0) w.chunk_max[chunk] = kmax, w.chunk_min[chunk] = kmin;
-}
-
-// The row's largest and smallest candidate (kmax 0: none).
-__device__ __forceinline__ void row_ends(const SmpArgs& a, const RowWs& w, u64* scratch, uint32_t& kmax,
-                                         uint32_t& kmin) {
-    static_assert(MAX_CHUNKS <= CHUNK_THREADS, "one chunk a thread");
-    const bool in = (int)threadIdx.x < a.chunks;
-    kmax = block_reduce<CHUNK_THREADS>(in ? w.chunk_max[threadIdx.x] : 0u, scratch, UMax());
-    kmin = block_reduce<CHUNK_THREADS>(in ? w.chunk_min[threadIdx.x] : 0xFFFFFFFFu, scratch, UMin());
-}
-
-template <int LD>
-__global__ void __launch_bounds__(CHUNK_THREADS) k_bins(SmpArgs a, void* ws) {
-    constexpr int NT = CHUNK_THREADS, J = CHUNK / 4 / NT;
-    __shared__ u64 bin_mass[BINS];
-    __shared__ uint32_t bin_count[BINS];
-    __shared__ u64 scratch[NT / 64];
-    const int row = blockIdx.y, chunk = blockIdx.x;
-    const RowWs w(ws, row, a.chunks);
-    v4u key[J];
-    load_chunk<LD>(a, row, chunk, key);
-    uint32_t kmax, kmin;
-    row_ends(a, w, scratch, kmax, kmin);
-    if (kmax == 0) return;
-    const Row r(a, row, kmax, kmin);
-    if (r.greedy) return;
-    if (!r.cut_k && !r.cut_p) {
-        u64 sum = 0;
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) sum += key[j][v] ? r.mass(key[j][v]) : 0;
-        sum = block_reduce<NT>(sum, scratch, Add());
-        if (threadIdx.x == 0) w.chunk_mass[chunk] = sum;
-        return;
-    }
-    for (int i = threadIdx.x; i < BINS; i += NT) bin_mass[i] = 0, bin_count[i] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < J; ++j)
+    for (int j = 0; j < GROUPS; ++j)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const uint32_t kk = key[j][v];
             const u64 m = kk ? r.mass(kk) : 0;
             if (m) {
                 const int b = r.bin(kk);
-                if (r.cut_k) atomicAdd(&bin_count[b], 1u);
-                if (r.cut_p) atomicAdd(&bin_mass[b], m);
+                if (r.cut_k) atomicAdd(&count[b], 1u);
+                if (r.cut_p) atomicAdd(&mass[b], m);
             }
         }
+}
+
+// Lists a thread's ids of the cut bins, and returns the mass of those above.
+template <int NT>
+__device__ __forceinline__ u64 fill_list(const Row& r, const Cuts& c, const v4u (&key)[GROUPS], int i0, u64* list,
+                                         uint32_t* listed) {
+    u64 sure = 0;
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const uint32_t kk = key[j][v];
+            const int b = kk ? r.bin(kk) : BINS;
+            if (b >= c.sure && !c.lists(b)) continue;
+            const u64 m = kk ? r.mass(kk) : 0;
+            if (b < c.sure) {
+                sure += m;
+            } else if (m) {
+                const uint32_t at = atomicAdd(listed, 1u);
+                if (at < LIST) list[at] = ((u64)kk << 32) | (uint32_t)~(i0 + (j * NT + (int)threadIdx.x) * 4 + v);
+            }
+        }
+    return sure;
+}
+
+// -------------------------------------------------- rows in one workgroup
+
+template <int LD, int NT>
+__global__ void __launch_bounds__(NT) k_row(SmpArgs a) {
+    __shared__ u64 bin_mass[BINS];
+    __shared__ uint32_t bin_count[BINS];
+    __shared__ u64 list[LIST], list_mass[LIST], hist[256], few[128];
+    __shared__ u64 scratch[NT / 64], s_z[2], seg[GROUPS * NT / 64];
+    __shared__ Cuts cuts;
+    __shared__ uint32_t s_key, s_listed;
+    __shared__ int s_at;
+    const int row = blockIdx.x, tid = threadIdx.x;
+    v4u key[GROUPS];
+    load_ids<LD, NT>(a, row, 0, key);
+    for (int i = tid; i < BINS; i += NT) bin_mass[i] = 0, bin_count[i] = 0;
+    if (tid == 0) s_listed = 0;
+    uint32_t kmax, kmin;
+    ends(key, kmax, kmin);
+    kmax = block_reduce<NT>(kmax, scratch, UMax());
+    if (kmax == 0) {
+        if (tid == 0) finish(a, row, -1, 0, 0);
+        return;
+    }
+    kmin = block_reduce<NT>(kmin, scratch, UMin());
+    const Row r(a, row, kmax, kmin);
+    if (r.greedy) {
+        const uint32_t id = block_reduce<NT>(first_top<NT>(key, 0, kmax), scratch, UMin());
+        if (tid == 0) finish(a, row, (int)id, 1, 1);
+        return;
+    }
+    u64 bound = 0;
+    if (r.cut_k || r.cut_p) {
+        fill_bins(r, key, bin_count, bin_mass);
+        __syncthreads();
+        find_cuts<NT>(r, bin_count, bin_mass, &cuts, s_z, scratch);
+        Cuts c = cuts;
+        if (c.any()) {
+            if (c.bk < 0) c.mass_bk = s_z[1];
+            const u64 sure = block_reduce<NT>(fill_list<NT>(r, c, key, 0, list, &s_listed), scratch, Add());
+            const uint32_t n = s_listed;
+            if (n > LIST) {
+                select_row<LD, NT>(a, r, row, hist, scratch, s_z, &s_key, &s_at);
+                return;
+            }
+            for (int i = tid; i < (int)n; i += NT) list_mass[i] = r.mass((uint32_t)(list[i] >> 32));
+            __syncthreads();
+            bound = resolve<NT>(r, c, sure, (int)n, list, list_mass, hist, few, scratch, s_z, &s_at);
+        }
+    }
+    draw<NT, true>(a, r, row, 0, key, bound, 0, 0, seg);
+}
+
+// -------------------------------------------------------------- longer rows
+
+template <int LD, int NT>
+__global__ void __launch_bounds__(NT) k_top(SmpArgs a, void* ws) {
+    __shared__ u64 scratch[NT / 64];
+    const int row = blockIdx.y, chunk = blockIdx.x;
+    const RowWs w(ws, row, a.chunks);
+    v4u key[GROUPS];
+    load_ids<LD, NT>(a, row, chunk * NT * PER, key);
+    for (int i = chunk * NT + threadIdx.x; i < BINS; i += a.chunks * NT) w.bin_mass[i] = 0, w.bin_count[i] = 0;
+    if (chunk == 0 && threadIdx.x == 0) w.head->listed = 0;
+    uint32_t kmax, kmin;
+    ends(key, kmax, kmin);
+    kmax = block_reduce<NT>(kmax, scratch, UMax());
+    kmin = block_reduce<NT>(kmin, scratch, UMin());
+    if (threadIdx.x == 0) w.chunk_max[chunk] = kmax, w.chunk_min[chunk] = kmin;
+}
+
+template <int LD, int NT>
+__global__ void __launch_bounds__(NT) k_bins(SmpArgs a, void* ws) {
+    static_assert(MAX_CHUNKS <= 256, "one chunk a thread");
+    __shared__ u64 bin_mass[BINS];
+    __shared__ uint32_t bin_count[BINS];
+    __shared__ u64 scratch[NT / 64];
+    const int row = blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x;
+    const RowWs w(ws, row, a.chunks);
+    v4u key[GROUPS];
+    load_ids<LD, NT>(a, row, chunk * NT * PER, key);
+    for (int i = tid; i < BINS; i += NT) bin_mass[i] = 0, bin_count[i] = 0;
+    const bool in = tid < a.chunks;
+    const uint32_t kmax = block_reduce<NT>(in ? w.chunk_max[tid] : 0u, scratch, UMax());
+    const uint32_t kmin = block_reduce<NT>(in ? w.chunk_min[tid] : 0xFFFFFFFFu, scratch, UMin());
+    if (chunk == 0 && tid == 0) w.head->kmax = kmax, w.head->kmin = kmin;
+    if (kmax == 0) return;
+    const Row r(a, row, kmax, kmin);
+    if (r.greedy) return;
+    if (!r.cut_k && !r.cut_p) {
+        u64 sum = 0;
+#pragma unroll
+        for (int j = 0; j < GROUPS; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) sum += key[j][v] ? r.mass(key[j][v]) : 0;
+        sum = block_reduce<NT>(sum, scratch, Add());
+        if (tid == 0) w.chunk_mass[chunk] = sum;
+        return;
+    }
+    fill_bins(r, key, bin_count, bin_mass);
     __syncthreads();
-    for (int i = threadIdx.x; i < BINS; i += NT) {
+    for (int i = tid; i < BINS; i += NT) {
         if (r.cut_k && bin_count[i]) atomicAdd(&w.bin_count[i], bin_count[i]);
         if (r.cut_p && bin_mass[i]) atomicAdd(&w.bin_mass[i], bin_mass[i]);
     }
 }
 
-template <int LD>
-__global__ void __launch_bounds__(CHUNK_THREADS) k_list(SmpArgs a, void* ws) {
-    constexpr int NT = CHUNK_THREADS, J = CHUNK / 4 / NT;
+template <int LD, int NT>
+__global__ void __launch_bounds__(NT) k_list(SmpArgs a, void* ws) {
     __shared__ u64 scratch[NT / 64], s_z[2];
     __shared__ Cuts cuts;
     const int row = blockIdx.y, chunk = blockIdx.x;
     const RowWs w(ws, row, a.chunks);
-    v4u key[J];
-    load_chunk<LD>(a, row, chunk, key);
-    uint32_t kmax, kmin;
-    row_ends(a, w, scratch, kmax, kmin);
-    if (kmax == 0) return;
-    const Row r(a, row, kmax, kmin);
+    if (w.head->kmax == 0) return;
+    const Row r(a, row, w.head->kmax, w.head->kmin);
     if (r.greedy || (!r.cut_k && !r.cut_p)) return;
+    v4u key[GROUPS];
+    load_ids<LD, NT>(a, row, chunk * NT * PER, key);
     find_cuts<NT>(r, w.bin_count, w.bin_mass, &cuts, s_z, scratch);
-    const Cuts c = cuts;
-    u64 sure = 0;
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const uint32_t kk = key[j][v];
-            const int b = kk ? r.bin(kk) : BINS;
-            if (b < c.sure) sure += r.mass(kk);
-            if (kk && c.lists(b) && r.mass(kk)) {
-                const uint32_t at = atomicAdd(w.listed, 1u);
-                if (at < LIST) w.list[at] = ((u64)kk << 32) | (uint32_t)~(chunk * CHUNK + (j * NT + (int)threadIdx.x) * 4 + v);
-            }
-        }
-    sure = block_reduce<NT>(sure, scratch, Add());
+    Cuts c = cuts;
+    if (c.bk < 0) c.mass_bk = s_z[1];
+    if (chunk == 0 && threadIdx.x == 0) w.head->cuts = c;
+    const u64 sure = block_reduce<NT>(fill_list<NT>(r, c, key, chunk * NT * PER, w.list, &w.head->listed), scratch, Add());
     if (threadIdx.x == 0) w.chunk_mass[chunk] = sure;
 }
 
-template <int LD>
-__global__ void __launch_bounds__(CHUNK_THREADS) k_draw(SmpArgs a, void* ws) {
-    constexpr int NT = CHUNK_THREADS, J = CHUNK / 4 / NT;
-    __shared__ u64 list[LIST], cum[LIST];
+template <int LD, int NT>
+__global__ void __launch_bounds__(NT) k_draw(SmpArgs a, void* ws) {
+    constexpr int CHUNK = NT * PER;
+    __shared__ u64 list[LIST], list_mass[LIST], hist[256], few[128];
     __shared__ u64 chunk_mass[MAX_CHUNKS];
-    __shared__ u64 scratch[NT / 64], s_z[2], seg[J * NT / 64];
-    __shared__ Cuts cuts;
+    __shared__ u64 scratch[NT / 64], s_z[2], seg[GROUPS * NT / 64], s_target;
     __shared__ uint32_t s_key;
     __shared__ int s_at;
     const int row = blockIdx.x, tid = threadIdx.x;
     const RowWs w(ws, row, a.chunks);
-    uint32_t kmax, kmin;
-    row_ends(a, w, scratch, kmax, kmin);
+    const uint32_t kmax = w.head->kmax;
     if (kmax == 0) {
         if (tid == 0) finish(a, row, -1, 0, 0);
         return;
     }
-    const Row r(a, row, kmax, kmin);
+    const Row r(a, row, kmax, w.head->kmin);
+    v4u key[GROUPS];
     if (r.greedy) {
         // the first chunk that holds the largest, and the first id there
         const uint32_t at = block_reduce<NT>(tid < a.chunks && w.chunk_max[tid] == kmax ? (uint32_t)tid : ~0u, scratch, UMin());
-        v4u key[J];
-        load_chunk<LD>(a, row, (int)at, key);
-        uint32_t id = ~0u;
-#pragma unroll
-        for (int j = J - 1; j >= 0; --j)
-#pragma unroll
-            for (int v = 3; v >= 0; --v)
-                if (key[j][v] == kmax) id = at * CHUNK + (j * NT + tid) * 4 + v;
-        id = block_reduce<NT>(id, scratch, UMin());
+        load_ids<LD, NT>(a, row, (int)at * CHUNK, key);
+        const uint32_t id = block_reduce<NT>(first_top<NT>(key, (int)at * CHUNK, kmax), scratch, UMin());
         if (tid == 0) finish(a, row, (int)id, 1, 1);
         return;
     }
     u64 mass = tid < a.chunks ? w.chunk_mass[tid] : 0;
-    chunk_mass[tid] = mass;
     u64 bound = 0;
     if (r.cut_k || r.cut_p) {
-        find_cuts<NT>(r, w.bin_count, w.bin_mass, &cuts, s_z, scratch);
-        Cuts c = cuts;
+        const Cuts c = w.head->cuts;
         if (c.any()) {
-            const uint32_t n = *w.listed;
+            const uint32_t n = w.head->listed;
             if (n > LIST) {
-                select_row<LD, NT>(a, r, row, list, scratch, s_z, &s_key, &s_at);
+                select_row<LD, NT>(a, r, row, hist, scratch, s_z, &s_key, &s_at);
                 return;
             }
-            for (int i = tid; i < (int)n; i += NT) list[i] = w.list[i];
+            if (tid < MAX_CHUNKS) chunk_mass[tid] = mass;
+            for (int i = tid; i < (int)n; i += NT) {
+                const u64 e = w.list[i];
+                list[i] = e;
+                list_mass[i] = r.mass((uint32_t)(e >> 32));
+            }
             const u64 sure = block_reduce<NT>(mass, scratch, Add());
-            if (c.bk < 0) c.mass_bk = s_z[1];
-            const int last = resolve<NT>(r, c, sure, (int)n, list, cum, scratch, &s_at);
-            bound = list[last];
-            for (int i = tid; i <= last; i += NT)
-                atomicAdd(&chunk_mass[(uint32_t)~(uint32_t)list[i] / CHUNK], cum[i] - (i > 0 ? cum[i - 1] : 0));
+            bound = resolve<NT>(r, c, sure, (int)n, list, list_mass, hist, few, scratch, s_z, &s_at);
+            for (int i = tid; i < (int)n; i += NT)
+                if (list[i] >= bound) atomicAdd(&chunk_mass[(uint32_t)~(uint32_t)list[i] / CHUNK], list_mass[i]);
             __syncthreads();
-            mass = chunk_mass[tid];
+            if (tid < MAX_CHUNKS) mass = chunk_mass[tid];
         }
     }
     u64 z;
     const u64 upto = block_scan<NT>(mass, scratch, &z);
     const u64 target = draw_at(a, row, z);
-    if (mass && upto > target && upto - mass <= target) s_at = tid, s_z[0] = target - (upto - mass);
+    if (mass && upto > target && upto - mass <= target) s_at = tid, s_target = target - (upto - mass);
     __syncthreads();
-    v4u key[J];
-    load_chunk<LD>(a, row, s_at, key);
-    draw<NT, J, false>(a, r, row, s_at * CHUNK, key, bound, z, s_z[0], seg);
+    const int i0 = s_at * CHUNK;
+    const u64 rest = s_target;
+    load_ids<LD, NT>(a, row, i0, key);
+    draw<NT, false>(a, r, row, i0, key, bound, z, rest, seg);
+}
+
+// Threads of a chunk's workgroup: few rows go to many small workgroups, many
+// rows to large ones, which read a row's bins and ends once for four times the
+// ids.
+inline int chunk_threads(int T, int V) {
+    return (int64_t)T * ((V + 256 * PER - 1) / (256 * PER)) > 1024 ? 1024 : 256;
+}
+
+inline int chunks_of(int T, int V) {
+    const int ids = chunk_threads(T, V) * PER;
+    return (V + ids - 1) / ids;
+}
+
+template <int LD, int NT>
+int run_long(SmpArgs a, void* ws, hipStream_t st) {
+    const dim3 grid(a.chunks, a.T), block(NT);
+    hipLaunchKernelGGL((k_top<LD, NT>), grid, block, 0, st, a, ws);
+    if (int rc = moe_check_launch("moe_sample/top")) return rc;
+    hipLaunchKernelGGL((k_bins<LD, NT>), grid, block, 0, st, a, ws);
+    if (int rc = moe_check_launch("moe_sample/bins")) return rc;
+    if (a.top_k || a.top_p) {
+        hipLaunchKernelGGL((k_list<LD, NT>), grid, block, 0, st, a, ws);
+        if (int rc = moe_check_launch("moe_sample/list")) return rc;
+    }
+    hipLaunchKernelGGL((k_draw<LD, NT>), dim3(a.T), block, 0, st, a, ws);
+    return moe_check_launch("moe_sample/draw");
+}
+
+template <int LD>
+int run(SmpArgs a, void* ws, hipStream_t st) {
+    if (a.V <= ROW_MAX) {
+        const auto go = [&](auto nt) {
+            constexpr int NT = decltype(nt)::value;
+            hipLaunchKernelGGL((k_row<LD, NT>), dim3(a.T), dim3(NT), 0, st, a);
+        };
+        if (a.V <= 256 * PER) go(std::integral_constant<int, 256>{});
+        else if (a.V <= 512 * PER) go(std::integral_constant<int, 512>{});
+        else go(std::integral_constant<int, 1024>{});
+        return moe_check_launch("moe_sample");
+    }
+    a.chunks = chunks_of(a.T, a.V);
+    return chunk_threads(a.T, a.V) == 256 ? run_long<LD, 256>(a, ws, st) : run_long<LD, 1024>(a, ws, st);
 }
 
 }  // namespace
@@ -774,7 +857,7 @@ extern "C" {
 size_t moe_sample_workspace_bytes(int T, int V) {
     if (T < 0 || T > MOE_SAMPLE_MAX_T || V < 1 || V > MOE_SAMPLE_MAX_V) return 0;
     if (T == 0 || V <= ROW_MAX) return 16;
-    return (size_t)T * RowWs::bytes((V + CHUNK - 1) / CHUNK);
+    return (size_t)T * RowWs::bytes(chunks_of(T, V));
 }
 
 int moe_sample(const void* logits, int l_dtype, int64_t ldl, int T, int V, const float* temperature,
@@ -793,25 +876,10 @@ int moe_sample(const void* logits, int l_dtype, int64_t ldl, int T, int V, const
     MOE_REQUIRE(ws_bytes >= moe_sample_workspace_bytes(T, V), MOE_E_ARG, "moe_sample: workspace of %zu bytes, %zu needed",
                 ws_bytes, moe_sample_workspace_bytes(T, V));
     if (T == 0) return moe_ok();
-    SmpArgs a{logits, ldl, T, V, 62, (V + CHUNK - 1) / CHUNK, temperature, min_p, top_k, top_p, u, ids, prob, 0};
-    while ((1 << (62 - a.S)) < V) --a.S;
+    SmpArgs a{logits, ldl, T, V, 51, 0, temperature, min_p, top_k, top_p, u, ids, prob, 0};
+    while (((int64_t)1 << (62 - a.S)) < V) --a.S;
     a.vec = reinterpret_cast<uintptr_t>(logits) % (4 * el) == 0 && (T == 1 || ldl % 4 == 0);
-    const bool f32 = l_dtype == MOE_X_F32;
-    if (V <= ROW_MAX) {
-        hipLaunchKernelGGL(f32 ? k_row<MOE_X_F32> : k_row<MOE_X_BF16>, dim3(T), dim3(ROW_THREADS), 0, stream, a);
-        return moe_check_launch("moe_sample");
-    }
-    const dim3 grid(a.chunks, T), block(CHUNK_THREADS);
-    hipLaunchKernelGGL(f32 ? k_top<MOE_X_F32> : k_top<MOE_X_BF16>, grid, block, 0, stream, a, ws);
-    if (int rc = moe_check_launch("moe_sample/top")) return rc;
-    hipLaunchKernelGGL(f32 ? k_bins<MOE_X_F32> : k_bins<MOE_X_BF16>, grid, block, 0, stream, a, ws);
-    if (int rc = moe_check_launch("moe_sample/bins")) return rc;
-    if (top_k || top_p) {
-        hipLaunchKernelGGL(f32 ? k_list<MOE_X_F32> : k_list<MOE_X_BF16>, grid, block, 0, stream, a, ws);
-        if (int rc = moe_check_launch("moe_sample/list")) return rc;
-    }
-    hipLaunchKernelGGL(f32 ? k_draw<MOE_X_F32> : k_draw<MOE_X_BF16>, dim3(T), block, 0, stream, a, ws);
-    return moe_check_launch("moe_sample/draw");
+    return l_dtype == MOE_X_F32 ? run<MOE_X_F32>(a, ws, stream) : run<MOE_X_BF16>(a, ws, stream);
 }
 
 }  // extern "C"

@@ -70,6 +70,30 @@ __device__ __forceinline__ T wave_all_sum(T v) {
     return wave_all(v, [](T a, T b) { return a + b; });
 }
 
+// v of the lane that CTRL names, in the rows of the mask ROWS; 0 where there is none.
+template <int CTRL, int ROWS, typename T>
+__device__ __forceinline__ T dpp_or_0(T v) {
+    const auto move = [](uint32_t w) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, CTRL, ROWS, 0xF, false); };
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, move(__builtin_bit_cast(uint32_t, v)));
+    } else {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        return __builtin_bit_cast(T, (uint64_t)move((uint32_t)b) | ((uint64_t)move((uint32_t)(b >> 32)) << 32));
+    }
+}
+
+// Inclusive sum over the lanes up to this one.
+template <typename T>
+__device__ __forceinline__ T wave_upto(T v) {
+    v += dpp_or_0<0x111, 0xF>(v);  // from 1, 2, 4, 8 lanes below in the row of 16
+    v += dpp_or_0<0x112, 0xF>(v);
+    v += dpp_or_0<0x114, 0xF>(v);
+    v += dpp_or_0<0x118, 0xF>(v);
+    v += dpp_or_0<0x142, 0xA>(v);  // lane 15 of rows 0 and 2 to rows 1 and 3
+    v += dpp_or_0<0x143, 0xC>(v);  // lane 31 to rows 2 and 3
+    return v;
+}
+
 __device__ __forceinline__ float wave_all_max(float v) {
     return wave_all(v, [](float a, float b) { return fmaxf(a, b); });
 }

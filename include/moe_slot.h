@@ -463,8 +463,8 @@ int moe_linear_q4(const void* x, int x_dtype, int64_t ldx, const void* wq, const
  *                bytes; need not be cleared; calls that may overlap need one
  *                each
  * Weights are computed in double and summed as whole multiples of 2^-S, with
- * S = 62 - ceil(log2 V) (45 at V = 131072): the result does not depend on any
- * order of summation.  T = 0 does nothing.
+ * S = 62 - ceil(log2 V) (45 at V = 131072; 51 at most): the result does not
+ * depend on any order of summation.  T = 0 does nothing.
  * Errors: ARG (null, sizes, ldl < V, workspace too small), DTYPE, SHAPE (the
  * limits below), ALIGN (logits on their elements, ws on 16 bytes), HIP. */
 #define MOE_SAMPLE_MAX_T 65535

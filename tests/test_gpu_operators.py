@@ -190,8 +190,9 @@ def check_draw(m, l, u, temperature=None, min_p=None, top_k=None, top_p=None, ld
         a = [d if o is None else o[t] for o, d in zip(opt, (1.0, 0.0, 0, 1.0))]
         want, p, _ = ref.sample_row(lh[t], uh[t], a[0], a[1], int(a[2]), a[3])
         assert ids[t] == want, f"row {t}: {ids[t]}, not {want} ({a}, u {uh[t]})"
-        # rounding to fp32, and whole multiples of 2^-S (S = 62 - ceil(log2 V)), half a step for each id of a mass of 1 or more
-        assert abs(prob[t] - p) <= 2.0 ** -24 * p + V * 2.0 ** -(62 - max(V - 1, 0).bit_length()) + 1e-38
+        # rounding to fp32, and whole multiples of 2^-S (S = 62 - ceil(log2 V), 51 at most), half a step for each id of a
+        # mass of 1 or more
+        assert abs(prob[t] - p) <= 2.0 ** -24 * p + V * 2.0 ** -min(51, 62 - max(V - 1, 0).bit_length()) + 1e-38
 
 
 def settings(T, g, kind, V):
