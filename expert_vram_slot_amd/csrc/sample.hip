@@ -20,12 +20,13 @@
 // the span where masses are not 0); counts and masses per bin tell in which
 // bin a cut falls, and only the ids of those bins (a few hundred, whatever the
 // row) are listed and searched for the place.
-//   rows of up to ROW_MAX ids   one workgroup a row, logits in registers
+//   rows of up to ROW_MAX ids   one workgroup a row, keys in LDS
 //   longer rows                 k_top (largest and smallest candidate of each
-//                               chunk) -> k_bins (counts and masses per bin)
-//                               -> k_list (ids of the cut bins, mass of each
-//                               chunk above them) -> k_draw (one workgroup a
-//                               row: the cuts, the draw's chunk, the draw)
+//                               segment of 1024 ids) -> k_bins (counts and
+//                               masses per bin) -> k_list (ids of the cut bins,
+//                               mass of each segment above them) -> k_draw (one
+//                               workgroup a row: the cuts, the draw's segment,
+//                               the draw)
 // A row whose cut bins hold more than LIST ids (many equal logits, or one far
 // outlier under a high temperature) takes a radix selection instead, eight
 // bits of the logit's key a pass over the whole row: slower, the same result.
@@ -43,12 +44,16 @@ using u64 = unsigned long long;
 using v4u = uint32_t __attribute__((ext_vector_type(4)));
 using v2u = uint32_t __attribute__((ext_vector_type(2)));
 
+constexpr int NT = 256;               // threads of every workgroup
+constexpr int NW = NT / 64;
 constexpr int BINS = 1024;
-constexpr int LIST = 2048;
-constexpr int PER = 16;               // ids a thread holds
-constexpr int GROUPS = PER / 4;       // in groups of four
-constexpr int ROW_MAX = 1024 * PER;   // ids of a row one workgroup holds
-constexpr int MAX_CHUNKS = MOE_SAMPLE_MAX_V / (256 * PER);
+constexpr int NB = BINS / NT;         // bins a thread looks after
+constexpr int LIST = 2048;            // listed ids of a longer row
+constexpr int ROW_LIST = 1024;        // and of a short one
+constexpr int SEG = 1024;             // ids a wave takes at a time: four groups of 64 x 4
+constexpr int GROUPS = SEG / 256;
+constexpr int ROW_MAX = 8 * SEG;      // ids of a row one workgroup holds
+constexpr int MAX_SEGS = MOE_SAMPLE_MAX_V / SEG;
 
 // Rising with the value; -inf and NaN give 0 (not a candidate).  -0 counts as +0.
 __device__ __forceinline__ uint32_t key_of(float l) {
@@ -57,6 +62,7 @@ __device__ __forceinline__ uint32_t key_of(float l) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// Of a key; NaN of 0.
 __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
@@ -64,7 +70,9 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 struct SmpArgs {
     const void* logits;
     int64_t ldl;
-    int T, V, S, chunks;
+    int T, V, S;
+    int segs;   // segments of a row
+    int share;  // segments of a wave (longer rows)
     const float* temperature;
     const float* min_p;
     const int32_t* top_k;
@@ -72,7 +80,6 @@ struct SmpArgs {
     const float* u;
     int32_t* ids;
     float* prob;
-    int vec;  // rows start on four logits
 };
 
 // Where the cuts fall.  Ids of bins below `sure` are kept whatever happens
@@ -81,6 +88,8 @@ struct SmpArgs {
 struct Cuts {
     int sure, p0, p1, bk;
     u64 rank, mass_bk;  // ids of bin bk that top-k keeps; mass above bin bk (no such bin: the row's)
+    u64 mass_sure;      // mass above bin p0
+    u64 pad;
     __device__ __forceinline__ bool lists(int b) const { return (b >= p0 && b <= p1) || b == bk; }
     __device__ __forceinline__ bool any() const { return sure < BINS; }
 };
@@ -96,24 +105,24 @@ struct RowWs {
     Head* head;
     u64* bin_mass;       // [BINS]
     u64* list;           // [LIST] key << 32 | ~id
-    u64* chunk_mass;     // [chunks] mass of the chunk's ids above the cut bins
+    u64* seg_mass;       // [segs] mass of the segment's ids above the cut bins
     uint32_t* bin_count;  // [BINS]
-    uint32_t* chunk_max;  // [chunks] keys
-    uint32_t* chunk_min;  // [chunks]
+    uint32_t* seg_max;   // [segs] keys
+    uint32_t* seg_min;   // [segs]
 
-    static __host__ __device__ size_t bytes(int chunks) {
-        return sizeof(Head) + (size_t)BINS * 12 + (size_t)LIST * 8 + (size_t)((chunks + 1) & ~1) * 16;
+    static __host__ __device__ size_t bytes(int segs) {
+        return sizeof(Head) + (size_t)BINS * 12 + (size_t)LIST * 8 + (size_t)((segs + 1) & ~1) * 16;
     }
-    __host__ __device__ RowWs(void* ws, int64_t row, int chunks) {
-        const int c = (chunks + 1) & ~1;
-        char* p = reinterpret_cast<char*>(ws) + row * bytes(chunks);
+    __host__ __device__ RowWs(void* ws, int64_t row, int segs) {
+        const int c = (segs + 1) & ~1;
+        char* p = reinterpret_cast<char*>(ws) + row * bytes(segs);
         head = reinterpret_cast<Head*>(p);
         bin_mass = reinterpret_cast<u64*>(p + sizeof(Head));
         list = bin_mass + BINS;
-        chunk_mass = list + LIST;
-        bin_count = reinterpret_cast<uint32_t*>(chunk_mass + c);
-        chunk_max = bin_count + BINS;
-        chunk_min = chunk_max + c;
+        seg_mass = list + LIST;
+        bin_count = reinterpret_cast<uint32_t*>(seg_mass + c);
+        seg_max = bin_count + BINS;
+        seg_min = seg_max + c;
     }
 };
 static_assert(sizeof(Head) % 16 == 0, "rows of the workspace start on 16 bytes");
@@ -125,57 +134,87 @@ __device__ __forceinline__ uint32_t load_key(const SmpArgs& a, int row, int i) {
     else return key_of(moe::bf16_to_f32(reinterpret_cast<const uint16_t*>(a.logits)[at]));
 }
 
-// Keys of ids i .. i + 3 (0 past the row).
+// Four logits of a row as they lie in memory: rows start on any logit, which
+// the wide loads allow.
+template <int LD>
+struct Raw {
+    using U = std::conditional_t<LD == MOE_X_F32, v4u, v2u>;
+    typedef U Loose __attribute__((aligned(LD == MOE_X_F32 ? 4 : 2)));
+    U v;
+    // Of ids i .. i + 3; past V - 4 the row's last four (V at least 4).
+    __device__ __forceinline__ void load(const SmpArgs& a, int row, int i) {
+        const int64_t at = (int64_t)row * a.ldl + (i < a.V - 4 ? i : a.V - 4);
+        v = *reinterpret_cast<const Loose*>(reinterpret_cast<const char*>(a.logits) + at * (LD == MOE_X_F32 ? 4 : 2));
+    }
+    // Their keys; 0 from the row's end on.
+    __device__ __forceinline__ v4u keys(const SmpArgs& a, int i) const {
+        v4u k;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (LD == MOE_X_F32) k[j] = key_of(__uint_as_float(v[j]));
+            else k[j] = key_of(j & 1 ? moe::bf16_hi(v[j >> 1]) : moe::bf16_lo(v[j >> 1]));
+        }
+        const int over = i - (a.V - 4);  // ids that the load went back by
+        if (over > 0) k = over == 1 ? v4u{k[1], k[2], k[3], 0} : over == 2 ? v4u{k[2], k[3], 0, 0}
+                        : over == 3 ? v4u{k[3], 0, 0, 0} : v4u{0, 0, 0, 0};
+        return k;
+    }
+};
+
+// Keys of ids i .. i + 3 (0 from the row's end on).
 template <int LD>
 __device__ __forceinline__ v4u load_keys(const SmpArgs& a, int row, int i) {
-    v4u k = {0, 0, 0, 0};
-    if (a.vec && i + 3 < a.V) {
-        const int64_t at = (int64_t)row * a.ldl + i;
-        if constexpr (LD == MOE_X_F32) {
-            const v4u v = *reinterpret_cast<const v4u*>(reinterpret_cast<const float*>(a.logits) + at);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) k[j] = key_of(__uint_as_float(v[j]));
-        } else {
-            const v2u v = *reinterpret_cast<const v2u*>(reinterpret_cast<const uint16_t*>(a.logits) + at);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) k[j] = key_of(j & 1 ? moe::bf16_hi(v[j >> 1]) : moe::bf16_lo(v[j >> 1]));
-        }
-    } else {
-#pragma unroll
+    if (a.V < 4) {
+        v4u k = {0, 0, 0, 0};
         for (int j = 0; j < 4; ++j)
             if (i + j < a.V) k[j] = load_key<LD>(a, row, i + j);
+        return k;
     }
-    return k;
+    Raw<LD> r;
+    r.load(a, row, i);
+    return r.keys(a, i);
 }
 
-// A row's settings, and the mass and the bin of a key under them.
+// A row's settings as they lie in memory: fetched at once, before anything waits.
+struct Settings {
+    float temperature, min_p, top_p, u;
+    int k;
+    __device__ __forceinline__ Settings(const SmpArgs& a, int row) {
+        temperature = a.temperature ? a.temperature[row] : 1.0f;
+        min_p = a.min_p ? a.min_p[row] : 0.0f;
+        k = a.top_k ? a.top_k[row] : 0;
+        top_p = a.top_p ? a.top_p[row] : 1.0f;
+        u = a.u[row];
+    }
+};
+
+// The mass and the bin of a key under a row's settings.
 struct Row {
     double top, rtemp, min_p, one;
     float topf, width;  // width: bins per unit of the logit
-    float p;
+    float p, u;
     uint32_t kmax;
     int k;
     bool greedy, cut_k, cut_p;
 
-    __device__ __forceinline__ Row(const SmpArgs& a, int row, uint32_t kmax_, uint32_t kmin) {
+    __device__ __forceinline__ Row(const SmpArgs& a, const Settings& s, uint32_t kmax_, uint32_t kmin) {
         kmax = kmax_;
-        const float temp = a.temperature ? a.temperature[row] : 1.0f;
-        greedy = !(temp > 0.0f);
+        greedy = !(s.temperature > 0.0f);
         topf = value_of(kmax);
         top = topf;
-        rtemp = 1.0 / (double)temp;
-        min_p = a.min_p ? (double)a.min_p[row] : 0.0;
-        min_p = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
+        rtemp = 1.0 / (double)s.temperature;
+        min_p = s.min_p > 0.0f ? (s.min_p < 1.0f ? s.min_p : 1.0f) : 0.0f;
         one = ldexp(1.0, a.S);
-        k = a.top_k ? a.top_k[row] : 0;
-        p = a.top_p ? a.top_p[row] : 1.0f;
+        k = s.k;
+        p = s.top_p;
+        u = s.u;
         cut_k = k > 0 && k < a.V;
         cut_p = p < 1.0f;
         // masses are 0 from (S + 1) ln 2 temperatures below the top on
-        const float span = fminf(topf - value_of(kmin), temp * ((float)(a.S + 1) * 0.6932f));
+        const float span = fminf(topf - value_of(kmin), s.temperature * ((float)(a.S + 1) * 0.6932f));
         width = span > 0.0f ? (float)BINS / span : 0.0f;
     }
-    // of a candidate; 0 also for one that min-p drops
+    // 0 for what is no candidate (key 0 stands for a NaN) or min-p drops
     __device__ __forceinline__ u64 mass(uint32_t key) const {
 #pragma clang fp contract(off)
         double w = moe::exp64(((double)value_of(key) - top) * rtemp);
@@ -195,13 +234,19 @@ struct Row {
         const double w = ceil((double)(p > 0.0f ? p : 0.0f) * (double)z);
         return w < 1.0 ? 1 : (u64)w < z ? (u64)w : z;
     }
+    // where the draw falls in a kept mass z
+    __device__ __forceinline__ u64 target(u64 z) const {
+        const double f = u > 0.0f ? u < 1.0f ? u : 1.0f : 0.0f;
+        const u64 t = (u64)(f * (double)z);
+        return t < z ? t : z - 1;
+    }
 };
 
 // ------------------------------------------------------------- block helpers
 
-// Over the block, for every thread.  scratch: NT / 64 entries, free again once
+// Over the block, for every thread.  scratch: NW entries, free again once
 // the block has met another barrier.
-template <int NT, typename T, typename Op>
+template <typename T, typename Op>
 __device__ __forceinline__ T block_reduce(T v, u64* scratch_, Op op) {
     T* scratch = reinterpret_cast<T*>(scratch_);
     v = moe::wave_all(v, op);
@@ -210,12 +255,11 @@ __device__ __forceinline__ T block_reduce(T v, u64* scratch_, Op op) {
     __syncthreads();
     v = scratch[0];
 #pragma unroll
-    for (int w = 1; w < NT / 64; ++w) v = op(v, scratch[w]);
+    for (int w = 1; w < NW; ++w) v = op(v, scratch[w]);
     return v;
 }
 
 // Inclusive sum over the block's threads, in thread order; *total the sum of all.
-template <int NT>
 __device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
     const int wid = threadIdx.x >> 6;
     v = moe::wave_upto(v);
@@ -224,7 +268,7 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
     __syncthreads();
     u64 all = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 64; ++w) {
+    for (int w = 0; w < NW; ++w) {
         if (w == wid) v += all;
         all += scratch[w];
     }
@@ -245,40 +289,31 @@ __device__ __forceinline__ void finish(const SmpArgs& a, int row, int id, u64 w,
     if (a.prob) a.prob[row] = z ? (float)((double)w / (double)z) : 0.0f;
 }
 
-__device__ __forceinline__ u64 draw_at(const SmpArgs& a, int row, u64 z) {
-    double u = a.u[row];
-    u = u > 0.0 ? u < 1.0 ? u : 1.0 : 0.0;
-    const u64 t = (u64)(u * (double)z);
-    return t < z ? t : z - 1;
-}
-
 // ------------------------------------------------------ cuts: bins, then ids
 
 // From the row's counts and masses per bin (counts only where top-k cuts,
 // masses only where top-p does).  s_cuts and scratch in LDS.
-template <int NT>
 __device__ __forceinline__ void find_cuts(const Row& r, const uint32_t* count, const u64* mass, Cuts* s_cuts,
                                           u64* s_z, u64* scratch) {
-    constexpr int NB = BINS / NT;
     const int b0 = threadIdx.x * NB;
     if (threadIdx.x == 0) {
         s_cuts->sure = BINS, s_cuts->p0 = BINS, s_cuts->p1 = -1, s_cuts->bk = -1;
-        s_cuts->rank = 0, s_cuts->mass_bk = 0;
+        s_cuts->rank = 0, s_cuts->mass_bk = 0, s_cuts->mass_sure = 0;
     }
     u64 m[NB], before = 0, total = 0;
     if (r.cut_p) {
         u64 sum = 0;
 #pragma unroll
         for (int i = 0; i < NB; ++i) sum += m[i] = mass[b0 + i];
-        before = block_scan<NT>(sum, scratch, &total) - sum;
+        before = block_scan(sum, scratch, &total) - sum;
     }
-    if (threadIdx.x == 0) s_z[0] = s_z[1] = total;  // the mass that top-k leaves lies between the two
+    if (threadIdx.x == 0) s_z[0] = s_z[1] = s_cuts->mass_bk = total;  // the mass that top-k leaves lies between the two
     __syncthreads();
     if (r.cut_k) {
         u64 c[NB], sum = 0, all;
 #pragma unroll
         for (int i = 0; i < NB; ++i) sum += c[i] = count[b0 + i];
-        u64 at = block_scan<NT>(sum, scratch, &all) - sum, mb = before;
+        u64 at = block_scan(sum, scratch, &all) - sum, mb = before;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             if (all > (u64)r.k && at < (u64)r.k && at + c[i] >= (u64)r.k) {
@@ -297,7 +332,7 @@ __device__ __forceinline__ void find_cuts(const Row& r, const uint32_t* count, c
         u64 mb = before;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            if (mb < lo && mb + m[i] >= lo) s_cuts->p0 = s_cuts->sure = b0 + i;
+            if (mb < lo && mb + m[i] >= lo) s_cuts->p0 = s_cuts->sure = b0 + i, s_cuts->mass_sure = mb;
             if (mb < hi && mb + m[i] >= hi) s_cuts->p1 = b0 + i;
             mb += m[i];
         }
@@ -311,15 +346,15 @@ __device__ __forceinline__ void find_cuts(const Row& r, const uint32_t* count, c
 // The span of the entries is cut into 256 by its leading bits, again and again,
 // until a wave can hold what is left: a lane an entry, each summing the weights
 // of the entries at least as large.
-template <int NT, typename W>
+template <typename W>
 __device__ __forceinline__ u64 select_list(const u64* list, int n, const W& weight, u64 want, u64* hist, u64* few,
                                            u64* scratch, u64* s_out, int* s_n) {
     u64 lo = ~0ull, hi = 0;
     for (int i = threadIdx.x; i < n; i += NT)
         if (weight(i)) lo = list[i] < lo ? list[i] : lo, hi = list[i] > hi ? list[i] : hi;
     if (n > 64) {
-        lo = block_reduce<NT>(lo, scratch, U64Min());
-        hi = block_reduce<NT>(hi, scratch, U64Max());
+        lo = block_reduce(lo, scratch, U64Min());
+        hi = block_reduce(hi, scratch, U64Max());
         int left = n;
         while (left > 64 && lo < hi) {
             const int top = 63 - __clzll((long long)(lo ^ hi));
@@ -356,8 +391,8 @@ __device__ __forceinline__ u64 select_list(const u64* list, int n, const W& weig
                 if (v >= lo && v <= hi && weight(i)) ++mine, l = v < l ? v : l, h = v > h ? v : h;
             }
             if (mine) atomicAdd(s_n, mine);
-            lo = block_reduce<NT>(l, scratch, U64Min());
-            hi = block_reduce<NT>(h, scratch, U64Max());
+            lo = block_reduce(l, scratch, U64Min());
+            hi = block_reduce(h, scratch, U64Max());
             left = *s_n;
         }
         __syncthreads();
@@ -390,31 +425,30 @@ __device__ __forceinline__ u64 select_list(const u64* list, int n, const W& weig
 }
 
 // The last kept entry of a row whose cut bins' ids are list[0 .. n), with their
-// masses beside them; sure_mass: of the bins above.
-template <int NT>
-__device__ __forceinline__ u64 resolve(const Row& r, const Cuts& c, u64 sure_mass, int n, const u64* list,
+// masses beside them.
+__device__ __forceinline__ u64 resolve(const Row& r, const Cuts& c, int n, const u64* list,
                                        const u64* mass, u64* hist, u64* few, u64* scratch, u64* s_out, int* s_n) {
     u64 bound = 0, z = c.mass_bk;  // the mass that top-k leaves
     const auto in_bk = [&](int i) { return r.bin((uint32_t)(list[i] >> 32)) == c.bk; };
     if (c.bk >= 0) {
-        bound = select_list<NT>(list, n, [&](int i) { return (u64)(in_bk(i) ? 1 : 0); }, c.rank, hist, few, scratch,
+        bound = select_list(list, n, [&](int i) { return (u64)(in_bk(i) ? 1 : 0); }, c.rank, hist, few, scratch,
                                 s_out, s_n);
         if (!r.cut_p) return bound;
         u64 part = 0;
         for (int i = threadIdx.x; i < n; i += NT)
             if (list[i] >= bound && in_bk(i)) part += mass[i];
-        z += block_reduce<NT>(part, scratch, Add());
+        z += block_reduce(part, scratch, Add());
     }
     const u64 want = r.want(z);
-    return select_list<NT>(list, n, [&](int i) { return list[i] >= bound ? mass[i] : 0; },
-                           want > sure_mass ? want - sure_mass : 1, hist, few, scratch, s_out, s_n);
+    return select_list(list, n, [&](int i) { return list[i] >= bound ? mass[i] : 0; },
+                           want > c.mass_sure ? want - c.mass_sure : 1, hist, few, scratch, s_out, s_n);
 }
 
 // ------------------------------------------------ the whole row, bit by bit
 
 // Radix selection over the row in memory: for rows whose cut bins hold more
 // ids than a list.  hist: 256 u64.
-template <int LD, int NT>
+template <int LD>
 __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row& r, int row, u64* hist, u64* scratch,
                                                      u64* s_left, uint32_t* s_key, int* s_at) {
     const int tid = threadIdx.x, V = a.V;
@@ -427,7 +461,7 @@ __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row
             const uint32_t kk = load_key<LD>(a, row, i);
             if (kk && kept(kk, i)) v += weight(kk);
         }
-        return block_reduce<NT>(v, scratch, Add());
+        return block_reduce(v, scratch, Add());
     };
     // the shortest prefix whose weight reaches `want` (at least 1, at most all of it)
     const auto select = [&](auto weight, u64 want) {
@@ -463,7 +497,7 @@ __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row
             const uint32_t kk = i < V ? load_key<LD>(a, row, i) : 0;
             const bool is = kk == prefix && kept(kk, i);
             u64 total;
-            const u64 at = block_scan<NT>(is ? 1 : 0, scratch, &total);
+            const u64 at = block_scan(is ? 1 : 0, scratch, &total);
             if (tid == 0) *s_at = V;
             __syncthreads();
             if (is && at == need) *s_at = i;
@@ -486,241 +520,303 @@ __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row
         select(mass, r.want(z));
         z = total_of(mass);
     }
-    u64 target = draw_at(a, row, z);
+    u64 target = r.target(z);
     for (int i0 = 0; i0 < V; i0 += NT) {
         const int i = i0 + tid;
         const uint32_t kk = i < V ? load_key<LD>(a, row, i) : 0;
         const u64 w = kk && kept(kk, i) ? r.mass(kk) : 0;
         u64 total;
-        const u64 cum = block_scan<NT>(w, scratch, &total);
+        const u64 cum = block_scan(w, scratch, &total);
         if (w && cum > target && cum - w <= target) finish(a, row, i, w, z);
         if (total > target) break;
         target -= total;
     }
 }
 
-// ------------------------------------------------------------ the draw
+// ------------------------------------------------------------ segments
 
-// Thread's keys of group j are those of ids i0 + (j * NT + thread) * 4 .. + 3;
-// a segment is a wave's part of a group: 256 ids in a row.  Finishes the row
-// with the id where the running mass of the kept ids (entries from `bound` on)
-// passes `target`.  WHOLE: these ids are the row; their mass is z, and the
-// target is drawn from it.  seg: GROUPS * NT / 64 entries.
-template <int NT, bool WHOLE>
-__device__ __forceinline__ void draw(const SmpArgs& a, const Row& r, int row, int i0, const v4u (&key)[GROUPS],
-                                     u64 bound, u64 z, u64 target, u64* seg) {
-    constexpr int NW = NT / 64;
-    const int wid = threadIdx.x >> 6;
-    const auto mass = [&](int j, int v) {
-        const uint32_t kk = key[j][v];
-        const u64 at = ((u64)kk << 32) | (uint32_t)~(i0 + (j * NT + (int)threadIdx.x) * 4 + v);
-        return kk && at >= bound ? r.mass(kk) : 0;
-    };
-    u64 sum[GROUPS];
+// Where a wave's segments come from.  Lane l holds ids seg * SEG + g * 256 +
+// 4 l .. + 3 of group g.
+template <int LD>
+struct FromRow {
+    using Held = Raw<LD>;
+    const SmpArgs& a;
+    int row;
+    __device__ __forceinline__ static int id(int seg, int g) { return seg * SEG + g * 256 + 4 * (int)(threadIdx.x & 63); }
+    __device__ __forceinline__ void load(int seg, Held (&h)[GROUPS]) const {
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-        sum[j] = 0;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) sum[j] += mass(j, v);
-        const u64 all = moe::wave_all_sum(sum[j]);
-        if ((threadIdx.x & 63) == 0) seg[j * NW + wid] = all;
+        for (int g = 0; g < GROUPS; ++g) h[g].load(a, row, id(seg, g));
     }
-    __syncthreads();
-    // segments are at most 64: a lane each
-    const int lane = threadIdx.x & 63;
-    const u64 mine = lane < GROUPS * NW ? seg[lane] : 0;
-    const u64 upto = moe::wave_upto(mine);
-    if constexpr (WHOLE) {
-        z = __shfl(upto, 63, moe::WAVE);
-        target = draw_at(a, row, z);
+    __device__ __forceinline__ v4u keys(const Held& h, int id) const { return h.keys(a, id); }
+};
+
+struct FromLds {
+    using Held = v4u;
+    const v4u* at;
+    __device__ __forceinline__ void load(int seg, v4u (&h)[GROUPS]) const {
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) h[g] = at[seg * (SEG / 4) + g * 64 + (threadIdx.x & 63)];
     }
-    const unsigned long long hit = __ballot(mine && upto > target);
-    const int s = hit ? __ffsll(hit) - 1 : 0;
-    const u64 before = __shfl(upto - mine, s, moe::WAVE);
-    if (s % NW != wid) return;
+    __device__ __forceinline__ v4u keys(const v4u& h, int) const { return h; }
+};
+
+// f(seg, id of the first, four keys, group) over the groups of segments first,
+// first + step, ... below end, of this wave; a segment is fetched while the one
+// before is worked on.  What is held moves through one register group, so f's
+// code is there once.
+template <typename From, typename F>
+__device__ __forceinline__ void each_group(int first, int step, int end, const From& from, const F& f) {
+    if (first >= end) return;
+    typename From::Held next[GROUPS];
+    from.load(first, next);
+    for (int seg = first; seg < end; seg += step) {
+        typename From::Held held[GROUPS];
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-        if (j != s / NW) continue;
-        u64 at = before + moe::wave_upto(sum[j]) - sum[j];
-        if (at > target || at + sum[j] <= target) continue;
+        for (int g = 0; g < GROUPS; ++g) held[g] = next[g];
+        if (seg + step < end) from.load(seg + step, next);
+#pragma unroll 1
+        for (int g = 0; g < GROUPS; ++g) {
+            const int id = seg * SEG + g * 256 + 4 * (int)(threadIdx.x & 63);
+            const v4u key = from.keys(held[0], id);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const u64 m = mass(j, v);
-            if (m && at <= target && at + m > target)
-                finish(a, row, i0 + (j * NT + (int)threadIdx.x) * 4 + v, m, z);
-            at += m;
+            for (int i = 0; i + 1 < GROUPS; ++i) held[i] = held[i + 1];
+            f(seg, id, key, g);
         }
     }
 }
 
-// A thread's share of a chunk of NT * PER ids from i0 on.
-template <int LD, int NT>
-__device__ __forceinline__ void load_ids(const SmpArgs& a, int row, int i0, v4u (&key)[GROUPS]) {
+__device__ __forceinline__ void ends(const v4u& key, uint32_t& kmax, uint32_t& kmin) {
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j) key[j] = load_keys<LD>(a, row, i0 + (j * NT + (int)threadIdx.x) * 4);
+    for (int v = 0; v < 4; ++v) {
+        kmax = key[v] > kmax ? key[v] : kmax;
+        kmin = key[v] && key[v] < kmin ? key[v] : kmin;
+    }
 }
 
-__device__ __forceinline__ void ends(const v4u (&key)[GROUPS], uint32_t& kmax, uint32_t& kmin) {
-    kmax = 0, kmin = 0xFFFFFFFFu;
+// Counts and masses into the bins.
+__device__ __forceinline__ void to_bins(const Row& r, const v4u& key, uint32_t* count, u64* mass) {
+    u64 m[4];
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j)
+    for (int v = 0; v < 4; ++v) m[v] = r.mass(key[v]);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            kmax = key[j][v] > kmax ? key[j][v] : kmax;
-            kmin = key[j][v] && key[j][v] < kmin ? key[j][v] : kmin;
+    for (int v = 0; v < 4; ++v) {
+        if (m[v]) {
+            const int b = r.bin(key[v]);
+            if (r.cut_k) atomicAdd(&count[b], 1u);
+            if (r.cut_p) atomicAdd(&mass[b], m[v]);
         }
+    }
 }
 
-// The lowest of a thread's ids that holds kmax (~0: none).
-template <int NT>
-__device__ __forceinline__ uint32_t first_top(const v4u (&key)[GROUPS], int i0, uint32_t kmax) {
-    uint32_t id = ~0u;
-#pragma unroll
-    for (int j = GROUPS - 1; j >= 0; --j)
-#pragma unroll
-        for (int v = 3; v >= 0; --v)
-            if (key[j][v] == kmax) id = i0 + (j * NT + (int)threadIdx.x) * 4 + v;
-    return id;
-}
-
-// Counts and masses of a thread's ids into the bins.
-__device__ __forceinline__ void fill_bins(const Row& r, const v4u (&key)[GROUPS], uint32_t* count, u64* mass) {
-#pragma unroll
-    for (int j = 0; j < GROUPS; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const uint32_t kk = key[j][v];
-            const u64 m = kk ? r.mass(kk) : 0;
-            if (m) {
-                const int b = r.bin(kk);
-                if (r.cut_k) atomicAdd(&count[b], 1u);
-                if (r.cut_p) atomicAdd(&mass[b], m);
-            }
-        }
-}
-
-// Lists a thread's ids of the cut bins, and returns the mass of those above.
-template <int NT>
-__device__ __forceinline__ u64 fill_list(const Row& r, const Cuts& c, const v4u (&key)[GROUPS], int i0, u64* list,
-                                         uint32_t* listed) {
+// Entries of the cut bins into a list of `room`; SURE: returns the mass of the
+// ids above them.
+template <bool SURE>
+__device__ __forceinline__ u64 to_list(const Row& r, const Cuts& c, const v4u& key, int id, u64* list, int room,
+                                       uint32_t* listed) {
     u64 sure = 0;
+    int bin[4];
+    bool any = false;
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j)
+    for (int v = 0; v < 4; ++v) {
+        bin[v] = key[v] ? r.bin(key[v]) : BINS;
+        any |= c.lists(bin[v]) || (SURE && bin[v] < c.sure);
+    }
+    if (!__any(any)) return 0;
+    u64 m[4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const uint32_t kk = key[j][v];
-            const int b = kk ? r.bin(kk) : BINS;
-            if (b >= c.sure && !c.lists(b)) continue;
-            const u64 m = kk ? r.mass(kk) : 0;
-            if (b < c.sure) {
-                sure += m;
-            } else if (m) {
-                const uint32_t at = atomicAdd(listed, 1u);
-                if (at < LIST) list[at] = ((u64)kk << 32) | (uint32_t)~(i0 + (j * NT + (int)threadIdx.x) * 4 + v);
-            }
+    for (int v = 0; v < 4; ++v) m[v] = r.mass(key[v]);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        if (bin[v] < c.sure) {
+            sure += m[v];
+        } else if (m[v] && c.lists(bin[v])) {
+            const uint32_t at = atomicAdd(listed, 1u);
+            if (at < (uint32_t)room) list[at] = ((u64)key[v] << 32) | (uint32_t)~(id + v);
         }
+    }
     return sure;
+}
+
+// Masses of the kept of four ids (entries from `bound` on), and their sum.
+__device__ __forceinline__ u64 kept_masses(const Row& r, const v4u& key, int id, u64 bound, u64 (&m)[4]) {
+    bool in[4], any = false;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        in[v] = key[v] && (((u64)key[v] << 32) | (uint32_t)~(id + v)) >= bound;
+        any |= in[v];
+        m[v] = 0;
+    }
+    if (!__any(any)) return 0;
+    u64 sum = 0;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        m[v] = r.mass(key[v]);
+        m[v] = in[v] ? m[v] : 0;
+        sum += m[v];
+    }
+    return sum;
+}
+
+// The wave's lane whose ids hold the target finishes the row.
+__device__ __forceinline__ void pick(const SmpArgs& a, const Row& r, int row, const v4u& key, int id, u64 bound, u64 z,
+                                     u64 target) {
+    u64 m[4];
+    const u64 sum = kept_masses(r, key, id, bound, m);
+    u64 at = moe::wave_upto(sum) - sum;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        if (m[v] && at <= target && at + m[v] > target) finish(a, row, id + v, m[v], z);
+        at += m[v];
+    }
 }
 
 // -------------------------------------------------- rows in one workgroup
 
-template <int LD, int NT>
+template <int LD>
 __global__ void __launch_bounds__(NT) k_row(SmpArgs a) {
-    __shared__ u64 bin_mass[BINS];
-    __shared__ uint32_t bin_count[BINS];
-    __shared__ u64 list[LIST], list_mass[LIST], hist[256], few[128];
-    __shared__ u64 scratch[NT / 64], s_z[2], seg[GROUPS * NT / 64];
+    __shared__ v4u keys[ROW_MAX / 4];
+    __shared__ u64 bin_mass[BINS];        // then the listed masses
+    __shared__ uint32_t bin_count[BINS];  // then the search's bins and its last few
+    __shared__ u64 list[ROW_LIST];
+    __shared__ u64 scratch[NW], s_z[2], group_mass[ROW_MAX / 256];
     __shared__ Cuts cuts;
     __shared__ uint32_t s_key, s_listed;
     __shared__ int s_at;
-    const int row = blockIdx.x, tid = threadIdx.x;
-    v4u key[GROUPS];
-    load_ids<LD, NT>(a, row, 0, key);
+    static_assert(ROW_LIST <= BINS && (256 + 128) * 8 <= BINS * 4, "the list's arrays fit where the bins were");
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+    const Settings set(a, row);
+    uint32_t kmax = 0, kmin = 0xFFFFFFFFu;
     for (int i = tid; i < BINS; i += NT) bin_mass[i] = 0, bin_count[i] = 0;
+    for (int i = tid; i < ROW_MAX / 256; i += NT) group_mass[i] = 0;
     if (tid == 0) s_listed = 0;
-    uint32_t kmax, kmin;
-    ends(key, kmax, kmin);
-    kmax = block_reduce<NT>(kmax, scratch, UMax());
+    const FromLds from_lds{keys};
+    const auto take = [&](int, int id, const v4u& k, int) {
+        keys[id / 4] = k;
+        ends(k, kmax, kmin);
+    };
+    if (a.V >= 4) {
+        each_group(wid, NW, a.segs, FromRow<LD>{a, row}, take);
+    } else if (wid == 0) {
+        for (int g = 0; g < GROUPS; ++g) take(0, g * 256 + 4 * lane, load_keys<LD>(a, row, g * 256 + 4 * lane), g);
+    }
+    kmax = block_reduce(kmax, scratch, UMax());
     if (kmax == 0) {
         if (tid == 0) finish(a, row, -1, 0, 0);
         return;
     }
-    kmin = block_reduce<NT>(kmin, scratch, UMin());
-    const Row r(a, row, kmax, kmin);
+    kmin = block_reduce(kmin, scratch, UMin());
+    const Row r(a, set, kmax, kmin);
     if (r.greedy) {
-        const uint32_t id = block_reduce<NT>(first_top<NT>(key, 0, kmax), scratch, UMin());
-        if (tid == 0) finish(a, row, (int)id, 1, 1);
+        uint32_t first = ~0u;
+        each_group(wid, NW, a.segs, from_lds, [&](int, int id, const v4u& k, int) {
+#pragma unroll
+            for (int v = 3; v >= 0; --v)
+                if (k[v] == kmax && (uint32_t)(id + v) < first) first = id + v;
+        });
+        first = block_reduce(first, scratch, UMin());
+        if (tid == 0) finish(a, row, (int)first, 1, 1);
         return;
     }
     u64 bound = 0;
     if (r.cut_k || r.cut_p) {
-        fill_bins(r, key, bin_count, bin_mass);
+        each_group(wid, NW, a.segs, from_lds, [&](int, int, const v4u& k, int) { to_bins(r, k, bin_count, bin_mass); });
         __syncthreads();
-        find_cuts<NT>(r, bin_count, bin_mass, &cuts, s_z, scratch);
-        Cuts c = cuts;
+        find_cuts(r, bin_count, bin_mass, &cuts, s_z, scratch);
+        const Cuts c = cuts;
         if (c.any()) {
-            if (c.bk < 0) c.mass_bk = s_z[1];
-            const u64 sure = block_reduce<NT>(fill_list<NT>(r, c, key, 0, list, &s_listed), scratch, Add());
-            const uint32_t n = s_listed;
-            if (n > LIST) {
-                select_row<LD, NT>(a, r, row, hist, scratch, s_z, &s_key, &s_at);
+            each_group(wid, NW, a.segs, from_lds, [&](int, int id, const v4u& k, int) {
+                to_list<false>(r, c, k, id, list, ROW_LIST, &s_listed);
+            });
+            __syncthreads();
+            const int n = (int)s_listed;
+            u64* hist = reinterpret_cast<u64*>(bin_count);
+            if (n > ROW_LIST) {
+                select_row<LD>(a, r, row, hist, scratch, s_z, &s_key, &s_at);
                 return;
             }
-            for (int i = tid; i < (int)n; i += NT) list_mass[i] = r.mass((uint32_t)(list[i] >> 32));
+            for (int i = tid; i < n; i += NT) bin_mass[i] = r.mass((uint32_t)(list[i] >> 32));
             __syncthreads();
-            bound = resolve<NT>(r, c, sure, (int)n, list, list_mass, hist, few, scratch, s_z, &s_at);
+            bound = resolve(r, c, n, list, bin_mass, hist, hist + 256, scratch, s_z, &s_at);
         }
     }
-    draw<NT, true>(a, r, row, 0, key, bound, 0, 0, seg);
+    each_group(wid, NW, a.segs, from_lds, [&](int, int id, const v4u& k, int) {
+        u64 m[4];
+        const u64 all = moe::wave_all_sum(kept_masses(r, k, id, bound, m));
+        if (lane == 0) group_mass[id / 256] = all;
+    });
+    __syncthreads();
+    static_assert(ROW_MAX / 256 <= 64, "a lane a group");
+    const u64 mine = lane < ROW_MAX / 256 ? group_mass[lane] : 0;
+    const u64 upto = moe::wave_upto(mine), z = __shfl(upto, 63, moe::WAVE), target = r.target(z);
+    const unsigned long long hit = __ballot(mine && upto > target);
+    const int g = hit ? __ffsll(hit) - 1 : 0;
+    const u64 before = __shfl(upto - mine, g, moe::WAVE);
+    if (wid == 0) pick(a, r, row, keys[g * 64 + lane], g * 256 + 4 * lane, bound, z, target - before);
 }
 
 // -------------------------------------------------------------- longer rows
 
-template <int LD, int NT>
-__global__ void __launch_bounds__(NT) k_top(SmpArgs a, void* ws) {
-    __shared__ u64 scratch[NT / 64];
-    const int row = blockIdx.y, chunk = blockIdx.x;
-    const RowWs w(ws, row, a.chunks);
-    v4u key[GROUPS];
-    load_ids<LD, NT>(a, row, chunk * NT * PER, key);
-    for (int i = chunk * NT + threadIdx.x; i < BINS; i += a.chunks * NT) w.bin_mass[i] = 0, w.bin_count[i] = 0;
-    if (chunk == 0 && threadIdx.x == 0) w.head->listed = 0;
-    uint32_t kmax, kmin;
-    ends(key, kmax, kmin);
-    kmax = block_reduce<NT>(kmax, scratch, UMax());
-    kmin = block_reduce<NT>(kmin, scratch, UMin());
-    if (threadIdx.x == 0) w.chunk_max[chunk] = kmax, w.chunk_min[chunk] = kmin;
+// This wave's segments.
+__device__ __forceinline__ int first_seg(const SmpArgs& a) {
+    return ((int)blockIdx.x * NW + (int)(threadIdx.x >> 6)) * a.share;
+}
+__device__ __forceinline__ int end_seg(const SmpArgs& a) {
+    const int e = first_seg(a) + a.share;
+    return e < a.segs ? e : a.segs;
 }
 
-template <int LD, int NT>
+template <int LD>
+__global__ void __launch_bounds__(NT) k_top(SmpArgs a, void* ws) {
+    const int row = blockIdx.y, lane = threadIdx.x & 63;
+    const RowWs w(ws, row, a.segs);
+    for (int i = blockIdx.x * NT + threadIdx.x; i < BINS; i += gridDim.x * NT) w.bin_mass[i] = 0, w.bin_count[i] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) w.head->listed = 0;
+    uint32_t kmax = 0, kmin = 0xFFFFFFFFu;
+    each_group(first_seg(a), 1, end_seg(a), FromRow<LD>{a, row},
+               [&](int seg, int, const v4u& k, int g) {
+                   ends(k, kmax, kmin);
+                   if (g + 1 < GROUPS) return;
+                   const uint32_t hi = moe::wave_all(kmax, UMax()), lo = moe::wave_all(kmin, UMin());
+                   if (lane == 0) w.seg_max[seg] = hi, w.seg_min[seg] = lo;
+                   kmax = 0, kmin = 0xFFFFFFFFu;
+               });
+}
+
+template <int LD>
 __global__ void __launch_bounds__(NT) k_bins(SmpArgs a, void* ws) {
-    static_assert(MAX_CHUNKS <= 256, "one chunk a thread");
     __shared__ u64 bin_mass[BINS];
     __shared__ uint32_t bin_count[BINS];
-    __shared__ u64 scratch[NT / 64];
-    const int row = blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x;
-    const RowWs w(ws, row, a.chunks);
-    v4u key[GROUPS];
-    load_ids<LD, NT>(a, row, chunk * NT * PER, key);
+    __shared__ u64 scratch[NW];
+    const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+    const RowWs w(ws, row, a.segs);
+    const Settings set(a, row);
+    const FromRow<LD> load{a, row};
     for (int i = tid; i < BINS; i += NT) bin_mass[i] = 0, bin_count[i] = 0;
-    const bool in = tid < a.chunks;
-    const uint32_t kmax = block_reduce<NT>(in ? w.chunk_max[tid] : 0u, scratch, UMax());
-    const uint32_t kmin = block_reduce<NT>(in ? w.chunk_min[tid] : 0xFFFFFFFFu, scratch, UMin());
-    if (chunk == 0 && tid == 0) w.head->kmax = kmax, w.head->kmin = kmin;
+    uint32_t kmax = 0, kmin = 0xFFFFFFFFu;
+    for (int i = tid; i < a.segs; i += NT) {
+        const uint32_t hi = w.seg_max[i], lo = w.seg_min[i];
+        kmax = hi > kmax ? hi : kmax;
+        kmin = lo < kmin ? lo : kmin;
+    }
+    kmax = block_reduce(kmax, scratch, UMax());
+    kmin = block_reduce(kmin, scratch, UMin());
+    if (blockIdx.x == 0 && tid == 0) w.head->kmax = kmax, w.head->kmin = kmin;
     if (kmax == 0) return;
-    const Row r(a, row, kmax, kmin);
+    const Row r(a, set, kmax, kmin);
     if (r.greedy) return;
     if (!r.cut_k && !r.cut_p) {
         u64 sum = 0;
+        each_group(first_seg(a), 1, end_seg(a), load, [&](int seg, int, const v4u& k, int g) {
 #pragma unroll
-        for (int j = 0; j < GROUPS; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) sum += key[j][v] ? r.mass(key[j][v]) : 0;
-        sum = block_reduce<NT>(sum, scratch, Add());
-        if (tid == 0) w.chunk_mass[chunk] = sum;
+            for (int v = 0; v < 4; ++v) sum += r.mass(k[v]);
+            if (g + 1 < GROUPS) return;
+            sum = moe::wave_all_sum(sum);
+            if (lane == 0) w.seg_mass[seg] = sum;
+            sum = 0;
+        });
         return;
     }
-    fill_bins(r, key, bin_count, bin_mass);
+    each_group(first_seg(a), 1, end_seg(a), load, [&](int, int, const v4u& k, int) { to_bins(r, k, bin_count, bin_mass); });
     __syncthreads();
     for (int i = tid; i < BINS; i += NT) {
         if (r.cut_k && bin_count[i]) atomicAdd(&w.bin_count[i], bin_count[i]);
@@ -728,126 +824,155 @@ __global__ void __launch_bounds__(NT) k_bins(SmpArgs a, void* ws) {
     }
 }
 
-template <int LD, int NT>
+template <int LD>
 __global__ void __launch_bounds__(NT) k_list(SmpArgs a, void* ws) {
-    __shared__ u64 scratch[NT / 64], s_z[2];
+    __shared__ u64 list[LIST];
+    __shared__ u64 scratch[NW], s_z[2];
     __shared__ Cuts cuts;
-    const int row = blockIdx.y, chunk = blockIdx.x;
-    const RowWs w(ws, row, a.chunks);
-    if (w.head->kmax == 0) return;
-    const Row r(a, row, w.head->kmax, w.head->kmin);
+    __shared__ uint32_t s_listed, s_first;
+    const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+    const RowWs w(ws, row, a.segs);
+    const Settings set(a, row);
+    const uint32_t kmax = w.head->kmax, kmin = w.head->kmin;
+    if (tid == 0) s_listed = 0;
+    if (kmax == 0) return;
+    const Row r(a, set, kmax, kmin);
     if (r.greedy || (!r.cut_k && !r.cut_p)) return;
-    v4u key[GROUPS];
-    load_ids<LD, NT>(a, row, chunk * NT * PER, key);
-    find_cuts<NT>(r, w.bin_count, w.bin_mass, &cuts, s_z, scratch);
-    Cuts c = cuts;
-    if (c.bk < 0) c.mass_bk = s_z[1];
-    if (chunk == 0 && threadIdx.x == 0) w.head->cuts = c;
-    const u64 sure = block_reduce<NT>(fill_list<NT>(r, c, key, chunk * NT * PER, w.list, &w.head->listed), scratch, Add());
-    if (threadIdx.x == 0) w.chunk_mass[chunk] = sure;
+    find_cuts(r, w.bin_count, w.bin_mass, &cuts, s_z, scratch);
+    const Cuts c = cuts;
+    if (blockIdx.x == 0 && tid == 0) w.head->cuts = c;
+    u64 sure = 0;
+    each_group(first_seg(a), 1, end_seg(a), FromRow<LD>{a, row},
+               [&](int seg, int id, const v4u& k, int g) {
+                   sure += to_list<true>(r, c, k, id, list, LIST, &s_listed);
+                   if (g + 1 < GROUPS) return;
+                   sure = moe::wave_all_sum(sure);
+                   if (lane == 0) w.seg_mass[seg] = sure;
+                   sure = 0;
+               });
+    __syncthreads();
+    const uint32_t n = s_listed;
+    if (n == 0) return;
+    if (tid == 0) s_first = atomicAdd(&w.head->listed, n);  // a place for all of the workgroup's
+    __syncthreads();
+    if (n > LIST) return;  // too many: the count says so
+    const uint32_t first = s_first;
+    for (uint32_t i = tid; i < n; i += NT)
+        if (first + i < LIST) w.list[first + i] = list[i];
 }
 
-template <int LD, int NT>
+template <int LD>
 __global__ void __launch_bounds__(NT) k_draw(SmpArgs a, void* ws) {
-    constexpr int CHUNK = NT * PER;
+    constexpr int MINE = MAX_SEGS / NT;  // segments a thread looks after
     __shared__ u64 list[LIST], list_mass[LIST], hist[256], few[128];
-    __shared__ u64 chunk_mass[MAX_CHUNKS];
-    __shared__ u64 scratch[NT / 64], s_z[2], seg[GROUPS * NT / 64], s_target;
+    __shared__ u64 seg_mass[MAX_SEGS];
+    __shared__ u64 scratch[NW], s_z[2], group_mass[GROUPS], s_target;
     __shared__ uint32_t s_key;
     __shared__ int s_at;
-    const int row = blockIdx.x, tid = threadIdx.x;
-    const RowWs w(ws, row, a.chunks);
-    const uint32_t kmax = w.head->kmax;
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+    const RowWs w(ws, row, a.segs);
+    const Settings set(a, row);
+    const Head head = *w.head;
+    const uint32_t kmax = head.kmax;
+    const int s0 = tid * MINE;
+    u64 mass[MINE];
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) mass[i] = s0 + i < a.segs ? w.seg_mass[s0 + i] : 0;
+    const u64 entry = w.list[tid];  // the list's first, before its length is known
     if (kmax == 0) {
         if (tid == 0) finish(a, row, -1, 0, 0);
         return;
     }
-    const Row r(a, row, kmax, w.head->kmin);
-    v4u key[GROUPS];
+    const Row r(a, set, kmax, head.kmin);
     if (r.greedy) {
-        // the first chunk that holds the largest, and the first id there
-        const uint32_t at = block_reduce<NT>(tid < a.chunks && w.chunk_max[tid] == kmax ? (uint32_t)tid : ~0u, scratch, UMin());
-        load_ids<LD, NT>(a, row, (int)at * CHUNK, key);
-        const uint32_t id = block_reduce<NT>(first_top<NT>(key, (int)at * CHUNK, kmax), scratch, UMin());
-        if (tid == 0) finish(a, row, (int)id, 1, 1);
+        // the first segment that holds the largest, and the first id there
+        uint32_t at = ~0u;
+#pragma unroll
+        for (int i = MINE - 1; i >= 0; --i)
+            if (s0 + i < a.segs && w.seg_max[s0 + i] == kmax) at = s0 + i;
+        at = block_reduce(at, scratch, UMin());
+        const int id = (int)at * SEG + 4 * tid;
+        const v4u k = load_keys<LD>(a, row, id);
+        uint32_t first = ~0u;
+#pragma unroll
+        for (int v = 3; v >= 0; --v)
+            if (k[v] == kmax) first = id + v;
+        first = block_reduce(first, scratch, UMin());
+        if (tid == 0) finish(a, row, (int)first, 1, 1);
         return;
     }
-    u64 mass = tid < a.chunks ? w.chunk_mass[tid] : 0;
     u64 bound = 0;
-    if (r.cut_k || r.cut_p) {
-        const Cuts c = w.head->cuts;
-        if (c.any()) {
-            const uint32_t n = w.head->listed;
-            if (n > LIST) {
-                select_row<LD, NT>(a, r, row, hist, scratch, s_z, &s_key, &s_at);
-                return;
-            }
-            if (tid < MAX_CHUNKS) chunk_mass[tid] = mass;
-            for (int i = tid; i < (int)n; i += NT) {
-                const u64 e = w.list[i];
-                list[i] = e;
-                list_mass[i] = r.mass((uint32_t)(e >> 32));
-            }
-            const u64 sure = block_reduce<NT>(mass, scratch, Add());
-            bound = resolve<NT>(r, c, sure, (int)n, list, list_mass, hist, few, scratch, s_z, &s_at);
-            for (int i = tid; i < (int)n; i += NT)
-                if (list[i] >= bound) atomicAdd(&chunk_mass[(uint32_t)~(uint32_t)list[i] / CHUNK], list_mass[i]);
-            __syncthreads();
-            if (tid < MAX_CHUNKS) mass = chunk_mass[tid];
+    if ((r.cut_k || r.cut_p) && head.cuts.any()) {
+        const int n = (int)head.listed;
+        if (n > LIST) {
+            select_row<LD>(a, r, row, hist, scratch, s_z, &s_key, &s_at);
+            return;
         }
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) seg_mass[s0 + i] = mass[i];
+        for (int i = tid; i < n; i += NT) {
+            const u64 e = i < NT ? entry : w.list[i];
+            list[i] = e;
+            list_mass[i] = r.mass((uint32_t)(e >> 32));
+        }
+        __syncthreads();
+        bound = resolve(r, head.cuts, n, list, list_mass, hist, few, scratch, s_z, &s_at);
+        for (int i = tid; i < n; i += NT)
+            if (list[i] >= bound) atomicAdd(&seg_mass[(uint32_t)~(uint32_t)list[i] / SEG], list_mass[i]);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) mass[i] = seg_mass[s0 + i];
     }
-    u64 z;
-    const u64 upto = block_scan<NT>(mass, scratch, &z);
-    const u64 target = draw_at(a, row, z);
-    if (mass && upto > target && upto - mass <= target) s_at = tid, s_target = target - (upto - mass);
+    u64 sum = 0, z;
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) sum += mass[i];
+    u64 at = block_scan(sum, scratch, &z) - sum;
+    const u64 target = r.target(z);
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        if (mass[i] && at <= target && at + mass[i] > target) s_at = s0 + i, s_target = target - at;
+        at += mass[i];
+    }
     __syncthreads();
-    const int i0 = s_at * CHUNK;
+    // the segment's groups, a wave each
+    static_assert(GROUPS == NW, "a wave a group");
+    const int id = s_at * SEG + 4 * tid;
     const u64 rest = s_target;
-    load_ids<LD, NT>(a, row, i0, key);
-    draw<NT, false>(a, r, row, i0, key, bound, z, rest, seg);
+    const v4u k = load_keys<LD>(a, row, id);
+    u64 m[4];
+    const u64 all = moe::wave_all_sum(kept_masses(r, k, id, bound, m));
+    if (lane == 0) group_mass[wid] = all;
+    __syncthreads();
+    u64 before = 0;
+    for (int g = 0; g < wid; ++g) before += group_mass[g];
+    if (before <= rest && before + all > rest) pick(a, r, row, k, id, bound, z, rest - before);
 }
 
-// Threads of a chunk's workgroup: few rows go to many small workgroups, many
-// rows to large ones, which read a row's bins and ends once for four times the
-// ids.
-inline int chunk_threads(int T, int V) {
-    return (int64_t)T * ((V + 256 * PER - 1) / (256 * PER)) > 1024 ? 1024 : 256;
-}
-
-inline int chunks_of(int T, int V) {
-    const int ids = chunk_threads(T, V) * PER;
-    return (V + ids - 1) / ids;
-}
-
-template <int LD, int NT>
-int run_long(SmpArgs a, void* ws, hipStream_t st) {
-    const dim3 grid(a.chunks, a.T), block(NT);
-    hipLaunchKernelGGL((k_top<LD, NT>), grid, block, 0, st, a, ws);
-    if (int rc = moe_check_launch("moe_sample/top")) return rc;
-    hipLaunchKernelGGL((k_bins<LD, NT>), grid, block, 0, st, a, ws);
-    if (int rc = moe_check_launch("moe_sample/bins")) return rc;
-    if (a.top_k || a.top_p) {
-        hipLaunchKernelGGL((k_list<LD, NT>), grid, block, 0, st, a, ws);
-        if (int rc = moe_check_launch("moe_sample/list")) return rc;
-    }
-    hipLaunchKernelGGL((k_draw<LD, NT>), dim3(a.T), block, 0, st, a, ws);
-    return moe_check_launch("moe_sample/draw");
-}
+inline int segs_of(int V) { return (V + SEG - 1) / SEG; }
 
 template <int LD>
 int run(SmpArgs a, void* ws, hipStream_t st) {
+    a.segs = segs_of(a.V);
     if (a.V <= ROW_MAX) {
-        const auto go = [&](auto nt) {
-            constexpr int NT = decltype(nt)::value;
-            hipLaunchKernelGGL((k_row<LD, NT>), dim3(a.T), dim3(NT), 0, st, a);
-        };
-        if (a.V <= 256 * PER) go(std::integral_constant<int, 256>{});
-        else if (a.V <= 512 * PER) go(std::integral_constant<int, 512>{});
-        else go(std::integral_constant<int, 1024>{});
+        hipLaunchKernelGGL(k_row<LD>, dim3(a.T), dim3(NT), 0, st, a);
         return moe_check_launch("moe_sample");
     }
-    a.chunks = chunks_of(a.T, a.V);
-    return chunk_threads(a.T, a.V) == 256 ? run_long<LD, 256>(a, ws, st) : run_long<LD, 1024>(a, ws, st);
+    // one segment a wave where rows are few; from about four workgroups a CU
+    // on a wave takes several, so that a row's bins are gathered fewer times
+    const int64_t all = (int64_t)a.T * a.segs;
+    const int64_t share = (all + 4096 - 1) / 4096;
+    a.share = share < a.segs ? (int)share : a.segs;
+    const dim3 grid((a.segs + NW * a.share - 1) / (NW * a.share), a.T), block(NT);
+    hipLaunchKernelGGL(k_top<LD>, grid, block, 0, st, a, ws);
+    if (int rc = moe_check_launch("moe_sample/top")) return rc;
+    hipLaunchKernelGGL(k_bins<LD>, grid, block, 0, st, a, ws);
+    if (int rc = moe_check_launch("moe_sample/bins")) return rc;
+    if (a.top_k || a.top_p) {
+        hipLaunchKernelGGL(k_list<LD>, grid, block, 0, st, a, ws);
+        if (int rc = moe_check_launch("moe_sample/list")) return rc;
+    }
+    hipLaunchKernelGGL(k_draw<LD>, dim3(a.T), block, 0, st, a, ws);
+    return moe_check_launch("moe_sample/draw");
 }
 
 }  // namespace
@@ -857,7 +982,7 @@ extern "C" {
 size_t moe_sample_workspace_bytes(int T, int V) {
     if (T < 0 || T > MOE_SAMPLE_MAX_T || V < 1 || V > MOE_SAMPLE_MAX_V) return 0;
     if (T == 0 || V <= ROW_MAX) return 16;
-    return (size_t)T * RowWs::bytes(chunks_of(T, V));
+    return (size_t)T * RowWs::bytes(segs_of(V));
 }
 
 int moe_sample(const void* logits, int l_dtype, int64_t ldl, int T, int V, const float* temperature,
@@ -876,9 +1001,8 @@ int moe_sample(const void* logits, int l_dtype, int64_t ldl, int T, int V, const
     MOE_REQUIRE(ws_bytes >= moe_sample_workspace_bytes(T, V), MOE_E_ARG, "moe_sample: workspace of %zu bytes, %zu needed",
                 ws_bytes, moe_sample_workspace_bytes(T, V));
     if (T == 0) return moe_ok();
-    SmpArgs a{logits, ldl, T, V, 51, 0, temperature, min_p, top_k, top_p, u, ids, prob, 0};
+    SmpArgs a{logits, ldl, T, V, 51, 0, 0, temperature, min_p, top_k, top_p, u, ids, prob};
     while (((int64_t)1 << (62 - a.S)) < V) --a.S;
-    a.vec = reinterpret_cast<uintptr_t>(logits) % (4 * el) == 0 && (T == 1 || ldl % 4 == 0);
     return l_dtype == MOE_X_F32 ? run<MOE_X_F32>(a, ws, stream) : run<MOE_X_BF16>(a, ws, stream);
 }
 
