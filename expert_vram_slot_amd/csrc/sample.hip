@@ -20,7 +20,7 @@
 // the span where masses are not 0); counts and masses per bin tell in which
 // bin a cut falls, and only the ids of those bins (a few hundred, whatever the
 // row) are listed and searched for the place.
-//   rows of up to ROW_MAX ids   one workgroup a row, keys in LDS
+//   rows of up to ROW_MAX ids   one workgroup a row, the row in LDS
 //   longer rows                 k_top (largest and smallest candidate of each
 //                               segment of 1024 ids) -> k_bins (counts and
 //                               masses per bin) -> k_list (ids of the cut bins,
@@ -55,17 +55,25 @@ constexpr int GROUPS = SEG / 256;
 constexpr int ROW_MAX = 8 * SEG;      // ids of a row one workgroup holds
 constexpr int MAX_SEGS = MOE_SAMPLE_MAX_V / SEG;
 
-// Rising with the value; -inf and NaN give 0 (not a candidate).  -0 counts as +0.
+// A logit as the kernels hold it: -inf for NaN and past a row's end.
+using v4f = float __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float held(float l) { return fmaxf(l, -INFINITY); }
+
+// Rising with the value; -0 and +0 alike.  Not of -inf.
 __device__ __forceinline__ uint32_t key_of(float l) {
-    if (!(l > -INFINITY)) return 0;
     const uint32_t b = __float_as_uint(l + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Of a key; NaN of 0.
 __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
+
+// An id in the order of the cuts: larger comes first.
+__device__ __forceinline__ u64 entry_of(float l, int id) { return ((u64)key_of(l) << 32) | (uint32_t)~id; }
+__device__ __forceinline__ float entry_value(u64 e) { return value_of((uint32_t)(e >> 32)); }
+__device__ __forceinline__ int entry_id(u64 e) { return (int)~(uint32_t)e; }
 
 struct SmpArgs {
     const void* logits;
@@ -97,18 +105,18 @@ struct Cuts {
 // Per row of the workspace (longer rows).
 struct Head {
     Cuts cuts;
-    uint32_t kmax, kmin;  // keys of the row's largest and smallest candidate; kmax 0: none
+    float top, low;  // the row's largest and smallest candidate; top -inf: none
     uint32_t listed, pad;
 };
 
 struct RowWs {
     Head* head;
     u64* bin_mass;       // [BINS]
-    u64* list;           // [LIST] key << 32 | ~id
+    u64* list;           // [LIST] entries
     u64* seg_mass;       // [segs] mass of the segment's ids above the cut bins
     uint32_t* bin_count;  // [BINS]
-    uint32_t* seg_max;   // [segs] keys
-    uint32_t* seg_min;   // [segs]
+    float* seg_max;      // [segs] largest and smallest candidate
+    float* seg_min;      // [segs]
 
     static __host__ __device__ size_t bytes(int segs) {
         return sizeof(Head) + (size_t)BINS * 12 + (size_t)LIST * 8 + (size_t)((segs + 1) & ~1) * 16;
@@ -121,17 +129,17 @@ struct RowWs {
         list = bin_mass + BINS;
         seg_mass = list + LIST;
         bin_count = reinterpret_cast<uint32_t*>(seg_mass + c);
-        seg_max = bin_count + BINS;
+        seg_max = reinterpret_cast<float*>(bin_count + BINS);
         seg_min = seg_max + c;
     }
 };
 static_assert(sizeof(Head) % 16 == 0, "rows of the workspace start on 16 bytes");
 
 template <int LD>
-__device__ __forceinline__ uint32_t load_key(const SmpArgs& a, int row, int i) {
+__device__ __forceinline__ float load_one(const SmpArgs& a, int row, int i) {
     const int64_t at = (int64_t)row * a.ldl + i;
-    if constexpr (LD == MOE_X_F32) return key_of(reinterpret_cast<const float*>(a.logits)[at]);
-    else return key_of(moe::bf16_to_f32(reinterpret_cast<const uint16_t*>(a.logits)[at]));
+    if constexpr (LD == MOE_X_F32) return held(reinterpret_cast<const float*>(a.logits)[at]);
+    else return held(moe::bf16_to_f32(reinterpret_cast<const uint16_t*>(a.logits)[at]));
 }
 
 // Four logits of a row as they lie in memory: rows start on any logit, which
@@ -146,33 +154,34 @@ struct Raw {
         const int64_t at = (int64_t)row * a.ldl + (i < a.V - 4 ? i : a.V - 4);
         v = *reinterpret_cast<const Loose*>(reinterpret_cast<const char*>(a.logits) + at * (LD == MOE_X_F32 ? 4 : 2));
     }
-    // Their keys; 0 from the row's end on.
-    __device__ __forceinline__ v4u keys(const SmpArgs& a, int i) const {
-        v4u k;
+    // Those of ids i .. i + 3; -inf from the row's end on.
+    __device__ __forceinline__ v4f logits(const SmpArgs& a, int i) const {
+        v4f k;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if constexpr (LD == MOE_X_F32) k[j] = key_of(__uint_as_float(v[j]));
-            else k[j] = key_of(j & 1 ? moe::bf16_hi(v[j >> 1]) : moe::bf16_lo(v[j >> 1]));
+            if constexpr (LD == MOE_X_F32) k[j] = held(__uint_as_float(v[j]));
+            else k[j] = held(j & 1 ? moe::bf16_hi(v[j >> 1]) : moe::bf16_lo(v[j >> 1]));
         }
         const int over = i - (a.V - 4);  // ids that the load went back by
-        if (over > 0) k = over == 1 ? v4u{k[1], k[2], k[3], 0} : over == 2 ? v4u{k[2], k[3], 0, 0}
-                        : over == 3 ? v4u{k[3], 0, 0, 0} : v4u{0, 0, 0, 0};
+        const float no = -INFINITY;
+        if (over > 0) k = over == 1 ? v4f{k[1], k[2], k[3], no} : over == 2 ? v4f{k[2], k[3], no, no}
+                        : over == 3 ? v4f{k[3], no, no, no} : v4f{no, no, no, no};
         return k;
     }
 };
 
-// Keys of ids i .. i + 3 (0 from the row's end on).
+// Logits of ids i .. i + 3 (-inf from the row's end on).
 template <int LD>
-__device__ __forceinline__ v4u load_keys(const SmpArgs& a, int row, int i) {
+__device__ __forceinline__ v4f load_four(const SmpArgs& a, int row, int i) {
     if (a.V < 4) {
-        v4u k = {0, 0, 0, 0};
+        v4f k = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         for (int j = 0; j < 4; ++j)
-            if (i + j < a.V) k[j] = load_key<LD>(a, row, i + j);
+            if (i + j < a.V) k[j] = load_one<LD>(a, row, i + j);
         return k;
     }
     Raw<LD> r;
     r.load(a, row, i);
-    return r.keys(a, i);
+    return r.logits(a, i);
 }
 
 // A row's settings as they lie in memory: fetched at once, before anything waits.
@@ -188,45 +197,66 @@ struct Settings {
     }
 };
 
-// The mass and the bin of a key under a row's settings.
+// The mass and the bin of a logit under a row's settings.
 struct Row {
-    double top, rtemp, min_p, one;
+    double top, least, scale, shift;
     float topf, width;  // width: bins per unit of the logit
     float p, u;
-    uint32_t kmax;
     int k;
-    bool greedy, cut_k, cut_p;
+    bool greedy, cut_k, cut_p, inf;
 
-    __device__ __forceinline__ Row(const SmpArgs& a, const Settings& s, uint32_t kmax_, uint32_t kmin) {
-        kmax = kmax_;
+    __device__ __forceinline__ Row(const SmpArgs& a, const Settings& s, float top_, float low) {
         greedy = !(s.temperature > 0.0f);
-        topf = value_of(kmax);
+        // a row with +inf: those alone, as if they were 0
+        inf = top_ == INFINITY;
+        topf = inf ? 0.0f : top_;
         top = topf;
-        rtemp = 1.0 / (double)s.temperature;
-        min_p = s.min_p > 0.0f ? (s.min_p < 1.0f ? s.min_p : 1.0f) : 0.0f;
-        one = ldexp(1.0, a.S);
+        const double t = s.temperature;
+        scale = 1.4426950408889634 / t;  // 1 / ln 2
+        shift = 0x1.8p52 + a.S;
+        // min-p's cut as a logit; masses are 0 from (S + 1) ln 2 temperatures below the top on
+        const double cut = (s.min_p > 0.0f ? log(s.min_p < 1.0f ? (double)s.min_p : 1.0) : -1000.0) * t;
+        const double zero = -(a.S + 1) * 0.6931471805599454 * t;
+        least = fmax(fmax(cut, zero), -0x1p1000);
         k = s.k;
         p = s.top_p;
         u = s.u;
         cut_k = k > 0 && k < a.V;
         cut_p = p < 1.0f;
-        // masses are 0 from (S + 1) ln 2 temperatures below the top on
-        const float span = fminf(topf - value_of(kmin), s.temperature * ((float)(a.S + 1) * 0.6932f));
+        const float span = inf ? 0.0f : fminf(topf - low, -(float)zero);
         width = span > 0.0f ? (float)BINS / span : 0.0f;
     }
-    // 0 for what is no candidate (key 0 stands for a NaN) or min-p drops
-    __device__ __forceinline__ u64 mass(uint32_t key) const {
+    __device__ __forceinline__ float norm(float l) const { return inf ? (l == INFINITY ? 0.0f : -INFINITY) : l; }
+    // 2^S exp((l - top) / temperature) to the nearest whole number; 0 for what
+    // is no candidate or min-p drops.  2^y, y = n + r with |r| <= 1/2: the
+    // polynomial of degree 10 through 2^r's values at the 11 Chebyshev nodes
+    // (relative error below 2^-51.6, 1 at 0), with n + S, from the low word of
+    // y + 1.5 * 2^52 + S, added to its exponent; added to 2^52 the result is
+    // rounded into the low bits.
+    __device__ __forceinline__ u64 mass(float l) const {
 #pragma clang fp contract(off)
-        double w = moe::exp64(((double)value_of(key) - top) * rtemp);
-        w = key == kmax ? 1.0 : w;
-        // added to 2^52 the product, at most 2^51, is rounded into the low bits
-        const u64 m = __builtin_bit_cast(u64, fma(w, one, 0x1p52)) & ((1ull << 52) - 1);
-        return w >= min_p ? m : 0;
+        const double d = (double)norm(l) - top;
+        const double t = fma(d, scale, shift);
+        const double r = fma(d, scale, shift - t);
+        double p = moe::fma_s(0x1.e6063f7a40c36p-28, r, 0x1.b675bcadc429ap-24);
+        p = moe::fma_s(p, r, 0x1.62bfd4776f20bp-20);
+        p = moe::fma_s(p, r, 0x1.ffcb540625945p-17);
+        p = moe::fma_s(p, r, 0x1.430913096fdb5p-13);
+        p = moe::fma_s(p, r, 0x1.5d87fe9d7a5b2p-10);
+        p = moe::fma_s(p, r, 0x1.3b2ab6fba1ddap-7);
+        p = moe::fma_s(p, r, 0x1.c6b08d703ce48p-5);
+        p = moe::fma_s(p, r, 0x1.ebfbdff82c598p-3);
+        p = moe::fma_s(p, r, 0x1.62e42fefa3a19p-1);
+        p = fma(p, r, 1.0);
+        const u64 b = __builtin_bit_cast(u64, p);
+        const uint32_t hi = (uint32_t)(b >> 32) + ((uint32_t)__builtin_bit_cast(u64, t) << 20);
+        const double w = __builtin_bit_cast(double, (u64)(uint32_t)b | ((u64)hi << 32));
+        const u64 m = __builtin_bit_cast(u64, w + 0x1p52) & ((1ull << 52) - 1);
+        return d >= least ? m : 0;
     }
-    // never falls as the key falls: each step rounds monotonically
-    __device__ __forceinline__ int bin(uint32_t key) const {
-        if (key == kmax) return 0;
-        const float b = (topf - value_of(key)) * width;
+    // of a candidate; never falls as the logit falls: each step rounds monotonically
+    __device__ __forceinline__ int bin(float l) const {
+        const float b = (topf - norm(l)) * width;
         return b < (float)(BINS - 1) ? (int)b : BINS - 1;
     }
     // the mass a prefix must reach, of a mass z that is left
@@ -276,7 +306,8 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
     return v;
 }
 
-struct UMax { __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; } };
+struct FMax { __device__ float operator()(float a, float b) const { return fmaxf(a, b); } };
+struct FMin { __device__ float operator()(float a, float b) const { return fminf(a, b); } };
 struct UMin { __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a < b ? a : b; } };
 struct Add {
     __device__ u64 operator()(u64 a, u64 b) const { return a + b; }
@@ -429,7 +460,7 @@ __device__ __forceinline__ u64 select_list(const u64* list, int n, const W& weig
 __device__ __forceinline__ u64 resolve(const Row& r, const Cuts& c, int n, const u64* list,
                                        const u64* mass, u64* hist, u64* few, u64* scratch, u64* s_out, int* s_n) {
     u64 bound = 0, z = c.mass_bk;  // the mass that top-k leaves
-    const auto in_bk = [&](int i) { return r.bin((uint32_t)(list[i] >> 32)) == c.bk; };
+    const auto in_bk = [&](int i) { return r.bin(entry_value(list[i])) == c.bk; };
     if (c.bk >= 0) {
         bound = select_list(list, n, [&](int i) { return (u64)(in_bk(i) ? 1 : 0); }, c.rank, hist, few, scratch,
                                 s_out, s_n);
@@ -452,14 +483,19 @@ template <int LD>
 __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row& r, int row, u64* hist, u64* scratch,
                                                      u64* s_left, uint32_t* s_key, int* s_at) {
     const int tid = threadIdx.x, V = a.V;
+    // 0: no candidate
+    const auto key_at = [&](int i) {
+        const float l = load_one<LD>(a, row, i);
+        return l > -INFINITY ? key_of(l) : 0u;
+    };
     uint32_t tkey = 0;
     int last = V;  // kept: key > tkey, or key == tkey and id <= last
     const auto kept = [&](uint32_t kk, int i) { return kk > tkey || (kk == tkey && i <= last); };
     const auto total_of = [&](auto weight) {
         u64 v = 0;
         for (int i = tid; i < V; i += NT) {
-            const uint32_t kk = load_key<LD>(a, row, i);
-            if (kk && kept(kk, i)) v += weight(kk);
+            const uint32_t kk = key_at(i);
+            if (kk && kept(kk, i)) v += weight(value_of(kk));
         }
         return block_reduce(v, scratch, Add());
     };
@@ -470,10 +506,10 @@ __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row
             for (int i = tid; i < 256; i += NT) hist[i] = 0;
             __syncthreads();
             for (int i = tid; i < V; i += NT) {
-                const uint32_t kk = load_key<LD>(a, row, i);
+                const uint32_t kk = key_at(i);
                 if (kk == 0 || !kept(kk, i)) continue;
                 if (shift < 24 && (kk >> (shift + 8)) != (prefix >> (shift + 8))) continue;
-                const u64 w = weight(kk);
+                const u64 w = weight(value_of(kk));
                 if (w) atomicAdd(&hist[(kk >> shift) & 255], w);
             }
             __syncthreads();
@@ -489,12 +525,12 @@ __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row
             __syncthreads();
         }
         // how many of the equal ones: all weigh the same
-        const u64 each = weight(prefix);
+        const u64 each = weight(value_of(prefix));
         u64 need = each ? (want + each - 1) / each : 0;
         int found = V;
         for (int i0 = 0; i0 < V; i0 += NT) {
             const int i = i0 + tid;
-            const uint32_t kk = i < V ? load_key<LD>(a, row, i) : 0;
+            const uint32_t kk = i < V ? key_at(i) : 0;
             const bool is = kk == prefix && kept(kk, i);
             u64 total;
             const u64 at = block_scan(is ? 1 : 0, scratch, &total);
@@ -512,8 +548,8 @@ __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row
         last = found;
         __syncthreads();
     };
-    const auto mass = [&](uint32_t kk) { return r.mass(kk); };
-    const auto count = [&](uint32_t kk) { return (u64)(r.mass(kk) ? 1 : 0); };
+    const auto mass = [&](float l) { return r.mass(l); };
+    const auto count = [&](float l) { return (u64)(r.mass(l) ? 1 : 0); };
     if (r.cut_k && total_of(count) > (u64)r.k) select(count, (u64)r.k);
     u64 z = total_of(mass);
     if (r.cut_p) {
@@ -523,8 +559,8 @@ __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row
     u64 target = r.target(z);
     for (int i0 = 0; i0 < V; i0 += NT) {
         const int i = i0 + tid;
-        const uint32_t kk = i < V ? load_key<LD>(a, row, i) : 0;
-        const u64 w = kk && kept(kk, i) ? r.mass(kk) : 0;
+        const uint32_t kk = i < V ? key_at(i) : 0;
+        const u64 w = kk && kept(kk, i) ? r.mass(value_of(kk)) : 0;
         u64 total;
         const u64 cum = block_scan(w, scratch, &total);
         if (w && cum > target && cum - w <= target) finish(a, row, i, w, z);
@@ -547,20 +583,20 @@ struct FromRow {
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) h[g].load(a, row, id(seg, g));
     }
-    __device__ __forceinline__ v4u keys(const Held& h, int id) const { return h.keys(a, id); }
+    __device__ __forceinline__ v4f logits(const Held& h, int id) const { return h.logits(a, id); }
 };
 
 struct FromLds {
-    using Held = v4u;
-    const v4u* at;
-    __device__ __forceinline__ void load(int seg, v4u (&h)[GROUPS]) const {
+    using Held = v4f;
+    const v4f* at;
+    __device__ __forceinline__ void load(int seg, v4f (&h)[GROUPS]) const {
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) h[g] = at[seg * (SEG / 4) + g * 64 + (threadIdx.x & 63)];
     }
-    __device__ __forceinline__ v4u keys(const v4u& h, int) const { return h; }
+    __device__ __forceinline__ v4f logits(const v4f& h, int) const { return h; }
 };
 
-// f(seg, id of the first, four keys, group) over the groups of segments first,
+// f(seg, id of the first, four logits, group) over the groups of segments first,
 // first + step, ... below end, of this wave; a segment is fetched while the one
 // before is worked on.  What is held moves through one register group, so f's
 // code is there once.
@@ -577,31 +613,31 @@ __device__ __forceinline__ void each_group(int first, int step, int end, const F
 #pragma unroll 1
         for (int g = 0; g < GROUPS; ++g) {
             const int id = seg * SEG + g * 256 + 4 * (int)(threadIdx.x & 63);
-            const v4u key = from.keys(held[0], id);
+            const v4f l = from.logits(held[0], id);
 #pragma unroll
             for (int i = 0; i + 1 < GROUPS; ++i) held[i] = held[i + 1];
-            f(seg, id, key, g);
+            f(seg, id, l, g);
         }
     }
 }
 
-__device__ __forceinline__ void ends(const v4u& key, uint32_t& kmax, uint32_t& kmin) {
+__device__ __forceinline__ void ends(const v4f& l, float& top, float& low) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-        kmax = key[v] > kmax ? key[v] : kmax;
-        kmin = key[v] && key[v] < kmin ? key[v] : kmin;
+        top = fmaxf(top, l[v]);
+        low = fminf(low, l[v] > -INFINITY ? l[v] : INFINITY);
     }
 }
 
 // Counts and masses into the bins.
-__device__ __forceinline__ void to_bins(const Row& r, const v4u& key, uint32_t* count, u64* mass) {
+__device__ __forceinline__ void to_bins(const Row& r, const v4f& l, uint32_t* count, u64* mass) {
     u64 m[4];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) m[v] = r.mass(key[v]);
+    for (int v = 0; v < 4; ++v) m[v] = r.mass(l[v]);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
         if (m[v]) {
-            const int b = r.bin(key[v]);
+            const int b = r.bin(l[v]);
             if (r.cut_k) atomicAdd(&count[b], 1u);
             if (r.cut_p) atomicAdd(&mass[b], m[v]);
         }
@@ -611,38 +647,47 @@ __device__ __forceinline__ void to_bins(const Row& r, const v4u& key, uint32_t* 
 // Entries of the cut bins into a list of `room`; SURE: returns the mass of the
 // ids above them.
 template <bool SURE>
-__device__ __forceinline__ u64 to_list(const Row& r, const Cuts& c, const v4u& key, int id, u64* list, int room,
+__device__ __forceinline__ u64 to_list(const Row& r, const Cuts& c, const v4f& l, int id, u64* list, int room,
                                        uint32_t* listed) {
     u64 sure = 0;
     int bin[4];
     bool any = false;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-        bin[v] = key[v] ? r.bin(key[v]) : BINS;
+        bin[v] = r.bin(l[v]);
         any |= c.lists(bin[v]) || (SURE && bin[v] < c.sure);
     }
     if (!__any(any)) return 0;
     u64 m[4];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) m[v] = r.mass(key[v]);
+    for (int v = 0; v < 4; ++v) m[v] = r.mass(l[v]);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
         if (bin[v] < c.sure) {
             sure += m[v];
         } else if (m[v] && c.lists(bin[v])) {
             const uint32_t at = atomicAdd(listed, 1u);
-            if (at < (uint32_t)room) list[at] = ((u64)key[v] << 32) | (uint32_t)~(id + v);
+            if (at < (uint32_t)room) list[at] = entry_of(l[v], id + v);
         }
     }
     return sure;
 }
 
-// Masses of the kept of four ids (entries from `bound` on), and their sum.
-__device__ __forceinline__ u64 kept_masses(const Row& r, const v4u& key, int id, u64 bound, u64 (&m)[4]) {
+// The last kept id and its logit; id past the row and -inf: all are kept.
+struct Bound {
+    float value;
+    int id;
+    __device__ __forceinline__ explicit Bound(const SmpArgs& a) : value(-INFINITY), id(a.V) {}
+    __device__ __forceinline__ explicit Bound(u64 entry) : value(entry_value(entry)), id(entry_id(entry)) {}
+    __device__ __forceinline__ bool keeps(float l, int i) const { return l > value || (l == value && i <= id); }
+};
+
+// Masses of the kept of four ids, and their sum.
+__device__ __forceinline__ u64 kept_masses(const Row& r, const v4f& l, int id, const Bound& bound, u64 (&m)[4]) {
     bool in[4], any = false;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-        in[v] = key[v] && (((u64)key[v] << 32) | (uint32_t)~(id + v)) >= bound;
+        in[v] = bound.keeps(l[v], id + v);
         any |= in[v];
         m[v] = 0;
     }
@@ -650,7 +695,7 @@ __device__ __forceinline__ u64 kept_masses(const Row& r, const v4u& key, int id,
     u64 sum = 0;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-        m[v] = r.mass(key[v]);
+        m[v] = r.mass(l[v]);
         m[v] = in[v] ? m[v] : 0;
         sum += m[v];
     }
@@ -658,10 +703,10 @@ __device__ __forceinline__ u64 kept_masses(const Row& r, const v4u& key, int id,
 }
 
 // The wave's lane whose ids hold the target finishes the row.
-__device__ __forceinline__ void pick(const SmpArgs& a, const Row& r, int row, const v4u& key, int id, u64 bound, u64 z,
-                                     u64 target) {
+__device__ __forceinline__ void pick(const SmpArgs& a, const Row& r, int row, const v4f& l, int id, const Bound& bound,
+                                     u64 z, u64 target) {
     u64 m[4];
-    const u64 sum = kept_masses(r, key, id, bound, m);
+    const u64 sum = kept_masses(r, l, id, bound, m);
     u64 at = moe::wave_upto(sum) - sum;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
@@ -674,7 +719,7 @@ __device__ __forceinline__ void pick(const SmpArgs& a, const Row& r, int row, co
 
 template <int LD>
 __global__ void __launch_bounds__(NT) k_row(SmpArgs a) {
-    __shared__ v4u keys[ROW_MAX / 4];
+    __shared__ v4f logits[ROW_MAX / 4];
     __shared__ u64 bin_mass[BINS];        // then the listed masses
     __shared__ uint32_t bin_count[BINS];  // then the search's bins and its last few
     __shared__ u64 list[ROW_LIST];
@@ -685,47 +730,47 @@ __global__ void __launch_bounds__(NT) k_row(SmpArgs a) {
     static_assert(ROW_LIST <= BINS && (256 + 128) * 8 <= BINS * 4, "the list's arrays fit where the bins were");
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
     const Settings set(a, row);
-    uint32_t kmax = 0, kmin = 0xFFFFFFFFu;
+    float top = -INFINITY, low = INFINITY;
     for (int i = tid; i < BINS; i += NT) bin_mass[i] = 0, bin_count[i] = 0;
     for (int i = tid; i < ROW_MAX / 256; i += NT) group_mass[i] = 0;
     if (tid == 0) s_listed = 0;
-    const FromLds from_lds{keys};
-    const auto take = [&](int, int id, const v4u& k, int) {
-        keys[id / 4] = k;
-        ends(k, kmax, kmin);
+    const FromLds lds{logits};
+    const auto take = [&](int, int id, const v4f& l, int) {
+        logits[id / 4] = l;
+        ends(l, top, low);
     };
     if (a.V >= 4) {
         each_group(wid, NW, a.segs, FromRow<LD>{a, row}, take);
     } else if (wid == 0) {
-        for (int g = 0; g < GROUPS; ++g) take(0, g * 256 + 4 * lane, load_keys<LD>(a, row, g * 256 + 4 * lane), g);
+        for (int g = 0; g < GROUPS; ++g) take(0, g * 256 + 4 * lane, load_four<LD>(a, row, g * 256 + 4 * lane), g);
     }
-    kmax = block_reduce(kmax, scratch, UMax());
-    if (kmax == 0) {
+    top = block_reduce(top, scratch, FMax());
+    if (top == -INFINITY) {
         if (tid == 0) finish(a, row, -1, 0, 0);
         return;
     }
-    kmin = block_reduce(kmin, scratch, UMin());
-    const Row r(a, set, kmax, kmin);
+    low = block_reduce(low, scratch, FMin());
+    const Row r(a, set, top, low);
     if (r.greedy) {
         uint32_t first = ~0u;
-        each_group(wid, NW, a.segs, from_lds, [&](int, int id, const v4u& k, int) {
+        each_group(wid, NW, a.segs, lds, [&](int, int id, const v4f& l, int) {
 #pragma unroll
             for (int v = 3; v >= 0; --v)
-                if (k[v] == kmax && (uint32_t)(id + v) < first) first = id + v;
+                if (l[v] == top && (uint32_t)(id + v) < first) first = id + v;
         });
         first = block_reduce(first, scratch, UMin());
         if (tid == 0) finish(a, row, (int)first, 1, 1);
         return;
     }
-    u64 bound = 0;
+    Bound bound(a);
     if (r.cut_k || r.cut_p) {
-        each_group(wid, NW, a.segs, from_lds, [&](int, int, const v4u& k, int) { to_bins(r, k, bin_count, bin_mass); });
+        each_group(wid, NW, a.segs, lds, [&](int, int, const v4f& l, int) { to_bins(r, l, bin_count, bin_mass); });
         __syncthreads();
         find_cuts(r, bin_count, bin_mass, &cuts, s_z, scratch);
         const Cuts c = cuts;
         if (c.any()) {
-            each_group(wid, NW, a.segs, from_lds, [&](int, int id, const v4u& k, int) {
-                to_list<false>(r, c, k, id, list, ROW_LIST, &s_listed);
+            each_group(wid, NW, a.segs, lds, [&](int, int id, const v4f& l, int) {
+                to_list<false>(r, c, l, id, list, ROW_LIST, &s_listed);
             });
             __syncthreads();
             const int n = (int)s_listed;
@@ -734,14 +779,14 @@ __global__ void __launch_bounds__(NT) k_row(SmpArgs a) {
                 select_row<LD>(a, r, row, hist, scratch, s_z, &s_key, &s_at);
                 return;
             }
-            for (int i = tid; i < n; i += NT) bin_mass[i] = r.mass((uint32_t)(list[i] >> 32));
+            for (int i = tid; i < n; i += NT) bin_mass[i] = r.mass(entry_value(list[i]));
             __syncthreads();
-            bound = resolve(r, c, n, list, bin_mass, hist, hist + 256, scratch, s_z, &s_at);
+            bound = Bound(resolve(r, c, n, list, bin_mass, hist, hist + 256, scratch, s_z, &s_at));
         }
     }
-    each_group(wid, NW, a.segs, from_lds, [&](int, int id, const v4u& k, int) {
+    each_group(wid, NW, a.segs, lds, [&](int, int id, const v4f& l, int) {
         u64 m[4];
-        const u64 all = moe::wave_all_sum(kept_masses(r, k, id, bound, m));
+        const u64 all = moe::wave_all_sum(kept_masses(r, l, id, bound, m));
         if (lane == 0) group_mass[id / 256] = all;
     });
     __syncthreads();
@@ -751,7 +796,7 @@ __global__ void __launch_bounds__(NT) k_row(SmpArgs a) {
     const unsigned long long hit = __ballot(mine && upto > target);
     const int g = hit ? __ffsll(hit) - 1 : 0;
     const u64 before = __shfl(upto - mine, g, moe::WAVE);
-    if (wid == 0) pick(a, r, row, keys[g * 64 + lane], g * 256 + 4 * lane, bound, z, target - before);
+    if (wid == 0) pick(a, r, row, logits[g * 64 + lane], g * 256 + 4 * lane, bound, z, target - before);
 }
 
 // -------------------------------------------------------------- longer rows
@@ -771,15 +816,15 @@ __global__ void __launch_bounds__(NT) k_top(SmpArgs a, void* ws) {
     const RowWs w(ws, row, a.segs);
     for (int i = blockIdx.x * NT + threadIdx.x; i < BINS; i += gridDim.x * NT) w.bin_mass[i] = 0, w.bin_count[i] = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) w.head->listed = 0;
-    uint32_t kmax = 0, kmin = 0xFFFFFFFFu;
-    each_group(first_seg(a), 1, end_seg(a), FromRow<LD>{a, row},
-               [&](int seg, int, const v4u& k, int g) {
-                   ends(k, kmax, kmin);
-                   if (g + 1 < GROUPS) return;
-                   const uint32_t hi = moe::wave_all(kmax, UMax()), lo = moe::wave_all(kmin, UMin());
-                   if (lane == 0) w.seg_max[seg] = hi, w.seg_min[seg] = lo;
-                   kmax = 0, kmin = 0xFFFFFFFFu;
-               });
+    float top = -INFINITY, low = INFINITY;
+    each_group(first_seg(a), 1, end_seg(a), FromRow<LD>{a, row}, [&](int seg, int, const v4f& l, int g) {
+        ends(l, top, low);
+        if (g + 1 < GROUPS) return;
+        top = moe::wave_all(top, FMax());
+        low = moe::wave_all(low, FMin());
+        if (lane == 0) w.seg_max[seg] = top, w.seg_min[seg] = low;
+        top = -INFINITY, low = INFINITY;
+    });
 }
 
 template <int LD>
@@ -792,23 +837,19 @@ __global__ void __launch_bounds__(NT) k_bins(SmpArgs a, void* ws) {
     const Settings set(a, row);
     const FromRow<LD> load{a, row};
     for (int i = tid; i < BINS; i += NT) bin_mass[i] = 0, bin_count[i] = 0;
-    uint32_t kmax = 0, kmin = 0xFFFFFFFFu;
-    for (int i = tid; i < a.segs; i += NT) {
-        const uint32_t hi = w.seg_max[i], lo = w.seg_min[i];
-        kmax = hi > kmax ? hi : kmax;
-        kmin = lo < kmin ? lo : kmin;
-    }
-    kmax = block_reduce(kmax, scratch, UMax());
-    kmin = block_reduce(kmin, scratch, UMin());
-    if (blockIdx.x == 0 && tid == 0) w.head->kmax = kmax, w.head->kmin = kmin;
-    if (kmax == 0) return;
-    const Row r(a, set, kmax, kmin);
+    float top = -INFINITY, low = INFINITY;
+    for (int i = tid; i < a.segs; i += NT) top = fmaxf(top, w.seg_max[i]), low = fminf(low, w.seg_min[i]);
+    top = block_reduce(top, scratch, FMax());
+    low = block_reduce(low, scratch, FMin());
+    if (blockIdx.x == 0 && tid == 0) w.head->top = top, w.head->low = low;
+    if (top == -INFINITY) return;
+    const Row r(a, set, top, low);
     if (r.greedy) return;
     if (!r.cut_k && !r.cut_p) {
         u64 sum = 0;
-        each_group(first_seg(a), 1, end_seg(a), load, [&](int seg, int, const v4u& k, int g) {
+        each_group(first_seg(a), 1, end_seg(a), load, [&](int seg, int, const v4f& l, int g) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) sum += r.mass(k[v]);
+            for (int v = 0; v < 4; ++v) sum += r.mass(l[v]);
             if (g + 1 < GROUPS) return;
             sum = moe::wave_all_sum(sum);
             if (lane == 0) w.seg_mass[seg] = sum;
@@ -816,7 +857,7 @@ __global__ void __launch_bounds__(NT) k_bins(SmpArgs a, void* ws) {
         });
         return;
     }
-    each_group(first_seg(a), 1, end_seg(a), load, [&](int, int, const v4u& k, int) { to_bins(r, k, bin_count, bin_mass); });
+    each_group(first_seg(a), 1, end_seg(a), load, [&](int, int, const v4f& l, int) { to_bins(r, l, bin_count, bin_mass); });
     __syncthreads();
     for (int i = tid; i < BINS; i += NT) {
         if (r.cut_k && bin_count[i]) atomicAdd(&w.bin_count[i], bin_count[i]);
@@ -833,18 +874,18 @@ __global__ void __launch_bounds__(NT) k_list(SmpArgs a, void* ws) {
     const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
     const RowWs w(ws, row, a.segs);
     const Settings set(a, row);
-    const uint32_t kmax = w.head->kmax, kmin = w.head->kmin;
+    const float top = w.head->top, low = w.head->low;
     if (tid == 0) s_listed = 0;
-    if (kmax == 0) return;
-    const Row r(a, set, kmax, kmin);
+    if (top == -INFINITY) return;
+    const Row r(a, set, top, low);
     if (r.greedy || (!r.cut_k && !r.cut_p)) return;
     find_cuts(r, w.bin_count, w.bin_mass, &cuts, s_z, scratch);
     const Cuts c = cuts;
     if (blockIdx.x == 0 && tid == 0) w.head->cuts = c;
     u64 sure = 0;
     each_group(first_seg(a), 1, end_seg(a), FromRow<LD>{a, row},
-               [&](int seg, int id, const v4u& k, int g) {
-                   sure += to_list<true>(r, c, k, id, list, LIST, &s_listed);
+               [&](int seg, int id, const v4f& l, int g) {
+                   sure += to_list<true>(r, c, l, id, list, LIST, &s_listed);
                    if (g + 1 < GROUPS) return;
                    sure = moe::wave_all_sum(sure);
                    if (lane == 0) w.seg_mass[seg] = sure;
@@ -873,35 +914,34 @@ __global__ void __launch_bounds__(NT) k_draw(SmpArgs a, void* ws) {
     const RowWs w(ws, row, a.segs);
     const Settings set(a, row);
     const Head head = *w.head;
-    const uint32_t kmax = head.kmax;
     const int s0 = tid * MINE;
     u64 mass[MINE];
 #pragma unroll
     for (int i = 0; i < MINE; ++i) mass[i] = s0 + i < a.segs ? w.seg_mass[s0 + i] : 0;
     const u64 entry = w.list[tid];  // the list's first, before its length is known
-    if (kmax == 0) {
+    if (head.top == -INFINITY) {
         if (tid == 0) finish(a, row, -1, 0, 0);
         return;
     }
-    const Row r(a, set, kmax, head.kmin);
+    const Row r(a, set, head.top, head.low);
     if (r.greedy) {
         // the first segment that holds the largest, and the first id there
         uint32_t at = ~0u;
 #pragma unroll
         for (int i = MINE - 1; i >= 0; --i)
-            if (s0 + i < a.segs && w.seg_max[s0 + i] == kmax) at = s0 + i;
+            if (s0 + i < a.segs && w.seg_max[s0 + i] == head.top) at = s0 + i;
         at = block_reduce(at, scratch, UMin());
         const int id = (int)at * SEG + 4 * tid;
-        const v4u k = load_keys<LD>(a, row, id);
+        const v4f l = load_four<LD>(a, row, id);
         uint32_t first = ~0u;
 #pragma unroll
         for (int v = 3; v >= 0; --v)
-            if (k[v] == kmax) first = id + v;
+            if (l[v] == head.top) first = id + v;
         first = block_reduce(first, scratch, UMin());
         if (tid == 0) finish(a, row, (int)first, 1, 1);
         return;
     }
-    u64 bound = 0;
+    Bound bound(a);
     if ((r.cut_k || r.cut_p) && head.cuts.any()) {
         const int n = (int)head.listed;
         if (n > LIST) {
@@ -913,12 +953,13 @@ __global__ void __launch_bounds__(NT) k_draw(SmpArgs a, void* ws) {
         for (int i = tid; i < n; i += NT) {
             const u64 e = i < NT ? entry : w.list[i];
             list[i] = e;
-            list_mass[i] = r.mass((uint32_t)(e >> 32));
+            list_mass[i] = r.mass(entry_value(e));
         }
         __syncthreads();
-        bound = resolve(r, head.cuts, n, list, list_mass, hist, few, scratch, s_z, &s_at);
+        const u64 last = resolve(r, head.cuts, n, list, list_mass, hist, few, scratch, s_z, &s_at);
+        bound = Bound(last);
         for (int i = tid; i < n; i += NT)
-            if (list[i] >= bound) atomicAdd(&seg_mass[(uint32_t)~(uint32_t)list[i] / SEG], list_mass[i]);
+            if (list[i] >= last) atomicAdd(&seg_mass[entry_id(list[i]) / SEG], list_mass[i]);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < MINE; ++i) mass[i] = seg_mass[s0 + i];
@@ -938,14 +979,14 @@ __global__ void __launch_bounds__(NT) k_draw(SmpArgs a, void* ws) {
     static_assert(GROUPS == NW, "a wave a group");
     const int id = s_at * SEG + 4 * tid;
     const u64 rest = s_target;
-    const v4u k = load_keys<LD>(a, row, id);
+    const v4f l = load_four<LD>(a, row, id);
     u64 m[4];
-    const u64 all = moe::wave_all_sum(kept_masses(r, k, id, bound, m));
+    const u64 all = moe::wave_all_sum(kept_masses(r, l, id, bound, m));
     if (lane == 0) group_mass[wid] = all;
     __syncthreads();
     u64 before = 0;
     for (int g = 0; g < wid; ++g) before += group_mass[g];
-    if (before <= rest && before + all > rest) pick(a, r, row, k, id, bound, z, rest - before);
+    if (before <= rest && before + all > rest) pick(a, r, row, l, id, bound, z, rest - before);
 }
 
 inline int segs_of(int V) { return (V + SEG - 1) / SEG; }
