@@ -44,10 +44,10 @@ using u64 = unsigned long long;
 using v4u = uint32_t __attribute__((ext_vector_type(4)));
 using v2u = uint32_t __attribute__((ext_vector_type(2)));
 
-constexpr int NT = 256;               // threads of every workgroup
-constexpr int NW = NT / 64;
+constexpr int CHUNK_NT = 256;         // threads of a workgroup of k_top, k_bins and k_list
+constexpr int ROW_NT = 1024;          // of k_row: two groups a wave at most, and nothing of a row waits for much
+constexpr int DRAW_NT = 256;          // of k_draw
 constexpr int BINS = 1024;
-constexpr int NB = BINS / NT;         // bins a thread looks after
 constexpr int LIST = 2048;            // listed ids of a longer row
 constexpr int ROW_LIST = 1024;        // and of a short one
 constexpr int SEG = 1024;             // ids a wave takes at a time: four groups of 64 x 4
@@ -215,7 +215,8 @@ struct Row {
         scale = 1.4426950408889634 / t;  // 1 / ln 2
         shift = 0x1.8p52 + a.S;
         // min-p's cut as a logit; masses are 0 from (S + 1) ln 2 temperatures below the top on
-        const double cut = (s.min_p > 0.0f ? log(s.min_p < 1.0f ? (double)s.min_p : 1.0) : -1000.0) * t;
+        double cut = -1000.0 * t;
+        if (s.min_p > 0.0f) cut = log(s.min_p < 1.0f ? (double)s.min_p : 1.0) * t;
         const double zero = -(a.S + 1) * 0.6931471805599454 * t;
         least = fmax(fmax(cut, zero), -0x1p1000);
         k = s.k;
@@ -274,44 +275,84 @@ struct Row {
 
 // ------------------------------------------------------------- block helpers
 
-// Over the block, for every thread.  scratch: NW entries, free again once
-// the block has met another barrier.
-template <typename T, typename Op>
-__device__ __forceinline__ T block_reduce(T v, u64* scratch_, Op op) {
-    T* scratch = reinterpret_cast<T*>(scratch_);
-    v = moe::wave_all(v, op);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = scratch[0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) v = op(v, scratch[w]);
-    return v;
+__device__ __forceinline__ u64 lane_value(u64 v, int lane) {  // lane: the same in the wave
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane), hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
+    return lo | ((u64)hi << 32);
 }
 
-// Inclusive sum over the block's threads, in thread order; *total the sum of all.
-__device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
-    const int wid = threadIdx.x >> 6;
-    v = moe::wave_upto(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 63) scratch[wid] = v;
-    __syncthreads();
-    u64 all = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        if (w == wid) v += all;
-        all += scratch[w];
+// Reductions and running sums over a workgroup of NT threads, one barrier
+// each: they write to two halves of `at` in turn, so a half is free again once
+// the other has had its barrier.
+template <int NT>
+struct Block {
+    static constexpr int NW = NT / 64;
+    u64* at;  // LDS, [2 * NW]
+    int half;
+
+    __device__ __forceinline__ explicit Block(u64* scratch) : at(scratch), half(0) {}
+    __device__ __forceinline__ u64* next() {
+        half ^= NW;
+        return at + half;
     }
-    *total = all;
-    return v;
-}
-
-struct FMax { __device__ float operator()(float a, float b) const { return fmaxf(a, b); } };
-struct FMin { __device__ float operator()(float a, float b) const { return fminf(a, b); } };
-struct UMin { __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a < b ? a : b; } };
-struct Add {
-    __device__ u64 operator()(u64 a, u64 b) const { return a + b; }
+    // op(v, v) is v: a largest or smallest
+    template <typename T, typename Op>
+    __device__ __forceinline__ T reduce(T v, Op op) {
+        T* s = reinterpret_cast<T*>(next());
+        v = moe::wave_all(v, op);
+        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+        __syncthreads();
+        if constexpr (NW <= 4) {
+            v = s[0];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) v = op(v, s[w]);
+            return v;
+        } else {
+            return moe::wave_all(s[(threadIdx.x & 63) % NW], op);
+        }
+    }
+    __device__ __forceinline__ u64 sum(u64 v) {
+        u64* s = next();
+        const int lane = threadIdx.x & 63;
+        v = moe::wave_all_sum(v);
+        if (lane == 0) s[threadIdx.x >> 6] = v;
+        __syncthreads();
+        return moe::wave_all_sum(lane < NW ? s[lane] : 0);
+    }
+    // the largest of a and the smallest of b
+    __device__ __forceinline__ void ends(float& a, float& b) {
+        float* s = reinterpret_cast<float*>(next());
+        a = moe::wave_all_max(a);
+        b = moe::wave_all_max(-b);
+        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = a, s[NW + (threadIdx.x >> 6)] = b;
+        __syncthreads();
+        a = moe::wave_all_max(s[(threadIdx.x & 63) % NW]);
+        b = -moe::wave_all_max(s[NW + (threadIdx.x & 63) % NW]);
+    }
+    // inclusive, in thread order; total: of all threads
+    __device__ __forceinline__ u64 scan(u64 v, u64& total) {
+        u64* s = next();
+        const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        v = moe::wave_upto(v);
+        if (lane == 63) s[wid] = v;
+        __syncthreads();
+        if constexpr (NW <= 4) {
+            u64 all = 0;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                if (w == wid) v += all;
+                all += s[w];
+            }
+            total = all;
+            return v;
+        } else {
+            const u64 mine = lane < NW ? s[lane] : 0, upto = moe::wave_upto(mine);
+            total = lane_value(upto, 63);
+            return v + lane_value(upto - mine, wid);
+        }
+    }
 };
+
+struct UMin { __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a < b ? a : b; } };
 struct U64Max { __device__ u64 operator()(u64 a, u64 b) const { return a > b ? a : b; } };
 struct U64Min { __device__ u64 operator()(u64 a, u64 b) const { return a < b ? a : b; } };
 
@@ -324,8 +365,10 @@ __device__ __forceinline__ void finish(const SmpArgs& a, int row, int id, u64 w,
 
 // From the row's counts and masses per bin (counts only where top-k cuts,
 // masses only where top-p does).  s_cuts and scratch in LDS.
+template <int NT>
 __device__ __forceinline__ void find_cuts(const Row& r, const uint32_t* count, const u64* mass, Cuts* s_cuts,
-                                          u64* s_z, u64* scratch) {
+                                          u64* s_z, Block<NT>& block) {
+    constexpr int NB = BINS / NT;  // bins a thread looks after
     const int b0 = threadIdx.x * NB;
     if (threadIdx.x == 0) {
         s_cuts->sure = BINS, s_cuts->p0 = BINS, s_cuts->p1 = -1, s_cuts->bk = -1;
@@ -336,7 +379,7 @@ __device__ __forceinline__ void find_cuts(const Row& r, const uint32_t* count, c
         u64 sum = 0;
 #pragma unroll
         for (int i = 0; i < NB; ++i) sum += m[i] = mass[b0 + i];
-        before = block_scan(sum, scratch, &total) - sum;
+        before = block.scan(sum, total) - sum;
     }
     if (threadIdx.x == 0) s_z[0] = s_z[1] = s_cuts->mass_bk = total;  // the mass that top-k leaves lies between the two
     __syncthreads();
@@ -344,7 +387,8 @@ __device__ __forceinline__ void find_cuts(const Row& r, const uint32_t* count, c
         u64 c[NB], sum = 0, all;
 #pragma unroll
         for (int i = 0; i < NB; ++i) sum += c[i] = count[b0 + i];
-        u64 at = block_scan(sum, scratch, &all) - sum, mb = before;
+        const u64 upto = block.scan(sum, all);
+        u64 at = upto - sum, mb = before;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             if (all > (u64)r.k && at < (u64)r.k && at + c[i] >= (u64)r.k) {
@@ -371,117 +415,132 @@ __device__ __forceinline__ void find_cuts(const Row& r, const uint32_t* count, c
     }
 }
 
+// Of a wave's n entries (falling order, all different), the one that ends the
+// shortest prefix whose weight reaches `want`; entries of weight 0 are not there.
+__device__ __forceinline__ u64 select_lanes(u64 entry, u64 weight, int n, u64 want) {
+    u64 cum = 0;
+    for (int i = 0; i < n; ++i) {
+        const u64 e = lane_value(entry, i), w = lane_value(weight, i);
+        cum += e >= entry ? w : 0;
+    }
+    const unsigned long long hit = __ballot(weight && cum >= want && cum - weight < want);
+    return lane_value(entry, hit ? __ffsll(hit) - 1 : 0);
+}
+
 // The entry of list[0 .. n) that ends the shortest prefix (falling order, all
 // entries different) whose weight reaches `want` (at least 1, at most all of
 // it); entries of weight 0 are not there.  weight(i): entry i's, of any thread.
 // The span of the entries is cut into 256 by its leading bits, again and again,
 // until a wave can hold what is left: a lane an entry, each summing the weights
 // of the entries at least as large.
-template <typename W>
+template <int NT, typename W>
 __device__ __forceinline__ u64 select_list(const u64* list, int n, const W& weight, u64 want, u64* hist, u64* few,
-                                           u64* scratch, u64* s_out, int* s_n) {
+                                           Block<NT>& block, u64* s_out, int* s_n) {
     u64 lo = ~0ull, hi = 0;
     for (int i = threadIdx.x; i < n; i += NT)
         if (weight(i)) lo = list[i] < lo ? list[i] : lo, hi = list[i] > hi ? list[i] : hi;
-    if (n > 64) {
-        lo = block_reduce(lo, scratch, U64Min());
-        hi = block_reduce(hi, scratch, U64Max());
-        int left = n;
-        while (left > 64 && lo < hi) {
-            const int top = 63 - __clzll((long long)(lo ^ hi));
-            const int shift = top > 7 ? top - 7 : 0;
-            const u64 base = lo >> shift & ~255ull;  // the bits above the digit, the same in all
-            __syncthreads();
-            for (int i = threadIdx.x; i < 256; i += NT) hist[i] = 0;
-            __syncthreads();
-            for (int i = threadIdx.x; i < n; i += NT) {
-                const u64 v = list[i], w = weight(i);
-                if (w && v >= lo && v <= hi) atomicAdd(&hist[v >> shift & 255], w);
-            }
-            __syncthreads();
-            if (threadIdx.x < 64) {  // falling digits: four a lane
-                u64 h[4], sum = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sum += h[i] = hist[255 - 4 * threadIdx.x - i];
-                u64 before = moe::wave_upto(sum) - sum;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (before < want && before + h[i] >= want) s_out[0] = 255 - 4 * threadIdx.x - i, s_out[1] = want - before;
-                    before += h[i];
-                }
-            }
-            if (threadIdx.x == 0) *s_n = 0;
-            __syncthreads();
-            lo = (base | s_out[0]) << shift;
-            hi = lo | ((1ull << shift) - 1);
-            want = s_out[1];
-            int mine = 0;
-            u64 l = ~0ull, h = 0;
-            for (int i = threadIdx.x; i < n; i += NT) {
-                const u64 v = list[i];
-                if (v >= lo && v <= hi && weight(i)) ++mine, l = v < l ? v : l, h = v > h ? v : h;
-            }
-            if (mine) atomicAdd(s_n, mine);
-            lo = block_reduce(l, scratch, U64Min());
-            hi = block_reduce(h, scratch, U64Max());
-            left = *s_n;
-        }
+    lo = block.reduce(lo, U64Min());
+    hi = block.reduce(hi, U64Max());
+    int left = n;
+    while (left > 64 && lo < hi) {
+        const int top = 63 - __clzll((long long)(lo ^ hi));
+        const int shift = top > 7 ? top - 7 : 0;
+        const u64 base = lo >> shift & ~255ull;  // the bits above the digit, the same in all
         __syncthreads();
-        if (threadIdx.x == 0) *s_n = 0;
+        for (int i = threadIdx.x; i < 256; i += NT) hist[i] = 0;
         __syncthreads();
         for (int i = threadIdx.x; i < n; i += NT) {
             const u64 v = list[i], w = weight(i);
-            if (w && v >= lo && v <= hi) {
-                const int at = atomicAdd(s_n, 1);
-                if (at < 64) few[at] = v, few[64 + at] = w;
-            }
+            if (w && v >= lo && v <= hi) atomicAdd(&hist[v >> shift & 255], w);
         }
         __syncthreads();
-        n = *s_n < 64 ? *s_n : 64;
-    } else {
+        if (threadIdx.x < 64) {  // falling digits: four a lane
+            u64 h[4], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += h[i] = hist[255 - 4 * threadIdx.x - i];
+            u64 before = moe::wave_upto(sum) - sum;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (before < want && before + h[i] >= want) s_out[0] = 255 - 4 * threadIdx.x - i, s_out[1] = want - before;
+                before += h[i];
+            }
+        }
+        if (threadIdx.x == 0) *s_n = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < n; i += NT) few[i] = list[i], few[64 + i] = weight(i);
-        __syncthreads();
-    }
-    if (threadIdx.x < 64) {
-        const u64 v = (int)threadIdx.x < n ? few[threadIdx.x] : 0, w = (int)threadIdx.x < n ? few[64 + threadIdx.x] : 0;
-        u64 cum = 0;
-        for (int i = 0; i < n; ++i) cum += few[i] >= v ? few[64 + i] : 0;
-        if (w && cum >= want && cum - w < want) s_out[0] = v;
+        lo = (base | s_out[0]) << shift;
+        hi = lo | ((1ull << shift) - 1);
+        want = s_out[1];
+        int mine = 0;
+        u64 l = ~0ull, h = 0;
+        for (int i = threadIdx.x; i < n; i += NT) {
+            const u64 v = list[i];
+            if (v >= lo && v <= hi && weight(i)) ++mine, l = v < l ? v : l, h = v > h ? v : h;
+        }
+        if (mine) atomicAdd(s_n, mine);
+        lo = block.reduce(l, U64Min());
+        hi = block.reduce(h, U64Max());
+        left = *s_n;
     }
     __syncthreads();
-    const u64 out = s_out[0];
+    if (threadIdx.x == 0) *s_n = 0;
     __syncthreads();
-    return out;
+    for (int i = threadIdx.x; i < n; i += NT) {
+        const u64 v = list[i], w = weight(i);
+        if (w && v >= lo && v <= hi) {
+            const int at = atomicAdd(s_n, 1);
+            if (at < 64) few[at] = v, few[64 + at] = w;
+        }
+    }
+    __syncthreads();
+    n = *s_n < 64 ? *s_n : 64;
+    const int lane = threadIdx.x & 63;
+    return select_lanes(lane < n ? few[lane] : 0, lane < n ? few[64 + lane] : 0, n, want);
 }
 
 // The last kept entry of a row whose cut bins' ids are list[0 .. n), with their
-// masses beside them.
+// masses beside them.  Where a wave holds them all, each wave works it out for
+// itself.
+template <int NT>
 __device__ __forceinline__ u64 resolve(const Row& r, const Cuts& c, int n, const u64* list,
-                                       const u64* mass, u64* hist, u64* few, u64* scratch, u64* s_out, int* s_n) {
+                                       const u64* mass, u64* hist, u64* few, Block<NT>& block, u64* s_out, int* s_n) {
     u64 bound = 0, z = c.mass_bk;  // the mass that top-k leaves
-    const auto in_bk = [&](int i) { return r.bin(entry_value(list[i])) == c.bk; };
+    const auto in_bk = [&](u64 e) { return r.bin(entry_value(e)) == c.bk; };
+    const auto left = [&](u64 want) { return want > c.mass_sure ? want - c.mass_sure : 1; };
+    if (n <= 64) {
+        const int lane = threadIdx.x & 63;
+        const u64 e = lane < n ? list[lane] : 0;
+        u64 m = lane < n ? mass[lane] : 0;
+        if (c.bk >= 0) {
+            const bool in = lane < n && in_bk(e);
+            bound = select_lanes(e, in ? 1 : 0, n, c.rank);
+            if (!r.cut_p) return bound;
+            z += moe::wave_all_sum(in && e >= bound ? m : 0);
+        }
+        m = e >= bound ? m : 0;
+        return select_lanes(e, m, n, left(r.want(z)));
+    }
     if (c.bk >= 0) {
-        bound = select_list(list, n, [&](int i) { return (u64)(in_bk(i) ? 1 : 0); }, c.rank, hist, few, scratch,
+        bound = select_list<NT>(list, n, [&](int i) { return (u64)(in_bk(list[i]) ? 1 : 0); }, c.rank, hist, few, block,
                                 s_out, s_n);
         if (!r.cut_p) return bound;
         u64 part = 0;
         for (int i = threadIdx.x; i < n; i += NT)
-            if (list[i] >= bound && in_bk(i)) part += mass[i];
-        z += block_reduce(part, scratch, Add());
+            if (list[i] >= bound && in_bk(list[i])) part += mass[i];
+        z += block.sum(part);
     }
-    const u64 want = r.want(z);
-    return select_list(list, n, [&](int i) { return list[i] >= bound ? mass[i] : 0; },
-                           want > c.mass_sure ? want - c.mass_sure : 1, hist, few, scratch, s_out, s_n);
+    return select_list<NT>(list, n, [&](int i) { return list[i] >= bound ? mass[i] : 0; }, left(r.want(z)), hist, few,
+                           block, s_out, s_n);
 }
 
 // ------------------------------------------------ the whole row, bit by bit
 
 // Radix selection over the row in memory: for rows whose cut bins hold more
 // ids than a list.  hist: 256 u64.
-template <int LD>
+template <int LD, int NT>
 __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row& r, int row, u64* hist, u64* scratch,
                                                      u64* s_left, uint32_t* s_key, int* s_at) {
+    Block<NT> block(scratch);
+    __syncthreads();
     const int tid = threadIdx.x, V = a.V;
     // 0: no candidate
     const auto key_at = [&](int i) {
@@ -497,7 +556,7 @@ __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row
             const uint32_t kk = key_at(i);
             if (kk && kept(kk, i)) v += weight(value_of(kk));
         }
-        return block_reduce(v, scratch, Add());
+        return block.sum(v);
     };
     // the shortest prefix whose weight reaches `want` (at least 1, at most all of it)
     const auto select = [&](auto weight, u64 want) {
@@ -533,7 +592,7 @@ __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row
             const uint32_t kk = i < V ? key_at(i) : 0;
             const bool is = kk == prefix && kept(kk, i);
             u64 total;
-            const u64 at = block_scan(is ? 1 : 0, scratch, &total);
+            const u64 at = block.scan(is ? 1 : 0, total);
             if (tid == 0) *s_at = V;
             __syncthreads();
             if (is && at == need) *s_at = i;
@@ -562,7 +621,7 @@ __device__ __attribute__((noinline)) void select_row(const SmpArgs& a, const Row
         const uint32_t kk = i < V ? key_at(i) : 0;
         const u64 w = kk && kept(kk, i) ? r.mass(value_of(kk)) : 0;
         u64 total;
-        const u64 cum = block_scan(w, scratch, &total);
+        const u64 cum = block.scan(w, total);
         if (w && cum > target && cum - w <= target) finish(a, row, i, w, z);
         if (total > target) break;
         target -= total;
@@ -584,16 +643,6 @@ struct FromRow {
         for (int g = 0; g < GROUPS; ++g) h[g].load(a, row, id(seg, g));
     }
     __device__ __forceinline__ v4f logits(const Held& h, int id) const { return h.logits(a, id); }
-};
-
-struct FromLds {
-    using Held = v4f;
-    const v4f* at;
-    __device__ __forceinline__ void load(int seg, v4f (&h)[GROUPS]) const {
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) h[g] = at[seg * (SEG / 4) + g * 64 + (threadIdx.x & 63)];
-    }
-    __device__ __forceinline__ v4f logits(const v4f& h, int) const { return h; }
 };
 
 // f(seg, id of the first, four logits, group) over the groups of segments first,
@@ -718,73 +767,79 @@ __device__ __forceinline__ void pick(const SmpArgs& a, const Row& r, int row, co
 // -------------------------------------------------- rows in one workgroup
 
 template <int LD>
-__global__ void __launch_bounds__(NT) k_row(SmpArgs a) {
+__global__ void __launch_bounds__(ROW_NT) k_row(SmpArgs a) {
+    constexpr int NT = ROW_NT;
     __shared__ v4f logits[ROW_MAX / 4];
     __shared__ u64 bin_mass[BINS];        // then the listed masses
     __shared__ uint32_t bin_count[BINS];  // then the search's bins and its last few
     __shared__ u64 list[ROW_LIST];
-    __shared__ u64 scratch[NW], s_z[2], group_mass[ROW_MAX / 256];
+    __shared__ u64 scratch[2 * NT / 64], s_z[2], group_mass[ROW_MAX / 256];
     __shared__ Cuts cuts;
     __shared__ uint32_t s_key, s_listed;
     __shared__ int s_at;
     static_assert(ROW_LIST <= BINS && (256 + 128) * 8 <= BINS * 4, "the list's arrays fit where the bins were");
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+    Block<NT> block(scratch);
     const Settings set(a, row);
     float top = -INFINITY, low = INFINITY;
     for (int i = tid; i < BINS; i += NT) bin_mass[i] = 0, bin_count[i] = 0;
     for (int i = tid; i < ROW_MAX / 256; i += NT) group_mass[i] = 0;
     if (tid == 0) s_listed = 0;
-    const FromLds lds{logits};
-    const auto take = [&](int, int id, const v4f& l, int) {
-        logits[id / 4] = l;
-        ends(l, top, low);
+    // f(id of the first, four logits) for each group of 256 ids of this wave
+    const auto groups = [&](const auto& f) {
+#pragma unroll 1
+        for (int i = tid; 4 * i - 4 * lane < a.V; i += NT) f(4 * i, logits[i]);
     };
-    if (a.V >= 4) {
-        each_group(wid, NW, a.segs, FromRow<LD>{a, row}, take);
-    } else if (wid == 0) {
-        for (int g = 0; g < GROUPS; ++g) take(0, g * 256 + 4 * lane, load_four<LD>(a, row, g * 256 + 4 * lane), g);
-    }
-    top = block_reduce(top, scratch, FMax());
+    v4f held_[ROW_MAX / 4 / NT];
+#pragma unroll
+    for (int i = 0; i < ROW_MAX / 4 / NT; ++i)
+        if (4 * (i * NT + tid - lane) < a.V) held_[i] = load_four<LD>(a, row, 4 * (i * NT + tid));
+#pragma unroll
+    for (int i = 0; i < ROW_MAX / 4 / NT; ++i)
+        if (4 * (i * NT + tid - lane) < a.V) {
+            logits[i * NT + tid] = held_[i];
+            ends(held_[i], top, low);
+        }
+    block.ends(top, low);
     if (top == -INFINITY) {
         if (tid == 0) finish(a, row, -1, 0, 0);
         return;
     }
-    low = block_reduce(low, scratch, FMin());
     const Row r(a, set, top, low);
     if (r.greedy) {
         uint32_t first = ~0u;
-        each_group(wid, NW, a.segs, lds, [&](int, int id, const v4f& l, int) {
+        groups([&](int id, const v4f& l) {
 #pragma unroll
             for (int v = 3; v >= 0; --v)
                 if (l[v] == top && (uint32_t)(id + v) < first) first = id + v;
         });
-        first = block_reduce(first, scratch, UMin());
+        first = block.reduce(first, UMin());
         if (tid == 0) finish(a, row, (int)first, 1, 1);
         return;
     }
     Bound bound(a);
     if (r.cut_k || r.cut_p) {
-        each_group(wid, NW, a.segs, lds, [&](int, int, const v4f& l, int) { to_bins(r, l, bin_count, bin_mass); });
+        groups([&](int, const v4f& l) { to_bins(r, l, bin_count, bin_mass); });
         __syncthreads();
-        find_cuts(r, bin_count, bin_mass, &cuts, s_z, scratch);
+        find_cuts<NT>(r, bin_count, bin_mass, &cuts, s_z, block);
         const Cuts c = cuts;
         if (c.any()) {
-            each_group(wid, NW, a.segs, lds, [&](int, int id, const v4f& l, int) {
+            groups([&](int id, const v4f& l) {
                 to_list<false>(r, c, l, id, list, ROW_LIST, &s_listed);
             });
             __syncthreads();
             const int n = (int)s_listed;
             u64* hist = reinterpret_cast<u64*>(bin_count);
             if (n > ROW_LIST) {
-                select_row<LD>(a, r, row, hist, scratch, s_z, &s_key, &s_at);
+                select_row<LD, NT>(a, r, row, hist, scratch, s_z, &s_key, &s_at);
                 return;
             }
             for (int i = tid; i < n; i += NT) bin_mass[i] = r.mass(entry_value(list[i]));
             __syncthreads();
-            bound = Bound(resolve(r, c, n, list, bin_mass, hist, hist + 256, scratch, s_z, &s_at));
+            bound = Bound(resolve<NT>(r, c, n, list, bin_mass, hist, hist + 256, block, s_z, &s_at));
         }
     }
-    each_group(wid, NW, a.segs, lds, [&](int, int id, const v4f& l, int) {
+    groups([&](int id, const v4f& l) {
         u64 m[4];
         const u64 all = moe::wave_all_sum(kept_masses(r, l, id, bound, m));
         if (lane == 0) group_mass[id / 256] = all;
@@ -803,7 +858,7 @@ __global__ void __launch_bounds__(NT) k_row(SmpArgs a) {
 
 // This wave's segments.
 __device__ __forceinline__ int first_seg(const SmpArgs& a) {
-    return ((int)blockIdx.x * NW + (int)(threadIdx.x >> 6)) * a.share;
+    return ((int)blockIdx.x * (CHUNK_NT / 64) + (int)(threadIdx.x >> 6)) * a.share;
 }
 __device__ __forceinline__ int end_seg(const SmpArgs& a) {
     const int e = first_seg(a) + a.share;
@@ -811,36 +866,37 @@ __device__ __forceinline__ int end_seg(const SmpArgs& a) {
 }
 
 template <int LD>
-__global__ void __launch_bounds__(NT) k_top(SmpArgs a, void* ws) {
+__global__ void __launch_bounds__(CHUNK_NT) k_top(SmpArgs a, void* ws) {
     const int row = blockIdx.y, lane = threadIdx.x & 63;
     const RowWs w(ws, row, a.segs);
-    for (int i = blockIdx.x * NT + threadIdx.x; i < BINS; i += gridDim.x * NT) w.bin_mass[i] = 0, w.bin_count[i] = 0;
+    for (int i = blockIdx.x * CHUNK_NT + threadIdx.x; i < BINS; i += gridDim.x * CHUNK_NT) w.bin_mass[i] = 0, w.bin_count[i] = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) w.head->listed = 0;
     float top = -INFINITY, low = INFINITY;
     each_group(first_seg(a), 1, end_seg(a), FromRow<LD>{a, row}, [&](int seg, int, const v4f& l, int g) {
         ends(l, top, low);
         if (g + 1 < GROUPS) return;
-        top = moe::wave_all(top, FMax());
-        low = moe::wave_all(low, FMin());
+        top = moe::wave_all_max(top);
+        low = -moe::wave_all_max(-low);
         if (lane == 0) w.seg_max[seg] = top, w.seg_min[seg] = low;
         top = -INFINITY, low = INFINITY;
     });
 }
 
 template <int LD>
-__global__ void __launch_bounds__(NT) k_bins(SmpArgs a, void* ws) {
+__global__ void __launch_bounds__(CHUNK_NT) k_bins(SmpArgs a, void* ws) {
+    constexpr int NT = CHUNK_NT;
     __shared__ u64 bin_mass[BINS];
     __shared__ uint32_t bin_count[BINS];
-    __shared__ u64 scratch[NW];
+    __shared__ u64 scratch[2 * NT / 64];
     const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
     const RowWs w(ws, row, a.segs);
+    Block<NT> block(scratch);
     const Settings set(a, row);
     const FromRow<LD> load{a, row};
     for (int i = tid; i < BINS; i += NT) bin_mass[i] = 0, bin_count[i] = 0;
     float top = -INFINITY, low = INFINITY;
     for (int i = tid; i < a.segs; i += NT) top = fmaxf(top, w.seg_max[i]), low = fminf(low, w.seg_min[i]);
-    top = block_reduce(top, scratch, FMax());
-    low = block_reduce(low, scratch, FMin());
+    block.ends(top, low);
     if (blockIdx.x == 0 && tid == 0) w.head->top = top, w.head->low = low;
     if (top == -INFINITY) return;
     const Row r(a, set, top, low);
@@ -866,20 +922,22 @@ __global__ void __launch_bounds__(NT) k_bins(SmpArgs a, void* ws) {
 }
 
 template <int LD>
-__global__ void __launch_bounds__(NT) k_list(SmpArgs a, void* ws) {
+__global__ void __launch_bounds__(CHUNK_NT) k_list(SmpArgs a, void* ws) {
+    constexpr int NT = CHUNK_NT;
     __shared__ u64 list[LIST];
-    __shared__ u64 scratch[NW], s_z[2];
+    __shared__ u64 scratch[2 * NT / 64], s_z[2];
     __shared__ Cuts cuts;
     __shared__ uint32_t s_listed, s_first;
     const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
     const RowWs w(ws, row, a.segs);
+    Block<NT> block(scratch);
     const Settings set(a, row);
     const float top = w.head->top, low = w.head->low;
     if (tid == 0) s_listed = 0;
     if (top == -INFINITY) return;
     const Row r(a, set, top, low);
     if (r.greedy || (!r.cut_k && !r.cut_p)) return;
-    find_cuts(r, w.bin_count, w.bin_mass, &cuts, s_z, scratch);
+    find_cuts<NT>(r, w.bin_count, w.bin_mass, &cuts, s_z, block);
     const Cuts c = cuts;
     if (blockIdx.x == 0 && tid == 0) w.head->cuts = c;
     u64 sure = 0;
@@ -903,15 +961,16 @@ __global__ void __launch_bounds__(NT) k_list(SmpArgs a, void* ws) {
 }
 
 template <int LD>
-__global__ void __launch_bounds__(NT) k_draw(SmpArgs a, void* ws) {
-    constexpr int MINE = MAX_SEGS / NT;  // segments a thread looks after
+__global__ void __launch_bounds__(DRAW_NT) k_draw(SmpArgs a, void* ws) {
+    constexpr int NT = DRAW_NT, MINE = MAX_SEGS / NT;  // segments a thread looks after
     __shared__ u64 list[LIST], list_mass[LIST], hist[256], few[128];
     __shared__ u64 seg_mass[MAX_SEGS];
-    __shared__ u64 scratch[NW], s_z[2], group_mass[GROUPS], s_target;
+    __shared__ u64 scratch[2 * NT / 64], s_z[2], group_mass[GROUPS], s_target;
     __shared__ uint32_t s_key;
     __shared__ int s_at;
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
     const RowWs w(ws, row, a.segs);
+    Block<NT> block(scratch);
     const Settings set(a, row);
     const Head head = *w.head;
     const int s0 = tid * MINE;
@@ -930,14 +989,16 @@ __global__ void __launch_bounds__(NT) k_draw(SmpArgs a, void* ws) {
 #pragma unroll
         for (int i = MINE - 1; i >= 0; --i)
             if (s0 + i < a.segs && w.seg_max[s0 + i] == head.top) at = s0 + i;
-        at = block_reduce(at, scratch, UMin());
+        at = block.reduce(at, UMin());
         const int id = (int)at * SEG + 4 * tid;
-        const v4f l = load_four<LD>(a, row, id);
         uint32_t first = ~0u;
+        if (tid < SEG / 4) {
+            const v4f l = load_four<LD>(a, row, id);
 #pragma unroll
-        for (int v = 3; v >= 0; --v)
-            if (l[v] == head.top) first = id + v;
-        first = block_reduce(first, scratch, UMin());
+            for (int v = 3; v >= 0; --v)
+                if (l[v] == head.top) first = id + v;
+        }
+        first = block.reduce(first, UMin());
         if (tid == 0) finish(a, row, (int)first, 1, 1);
         return;
     }
@@ -945,7 +1006,7 @@ __global__ void __launch_bounds__(NT) k_draw(SmpArgs a, void* ws) {
     if ((r.cut_k || r.cut_p) && head.cuts.any()) {
         const int n = (int)head.listed;
         if (n > LIST) {
-            select_row<LD>(a, r, row, hist, scratch, s_z, &s_key, &s_at);
+            select_row<LD, NT>(a, r, row, hist, scratch, s_z, &s_key, &s_at);
             return;
         }
 #pragma unroll
@@ -956,7 +1017,7 @@ __global__ void __launch_bounds__(NT) k_draw(SmpArgs a, void* ws) {
             list_mass[i] = r.mass(entry_value(e));
         }
         __syncthreads();
-        const u64 last = resolve(r, head.cuts, n, list, list_mass, hist, few, scratch, s_z, &s_at);
+        const u64 last = resolve<NT>(r, head.cuts, n, list, list_mass, hist, few, block, s_z, &s_at);
         bound = Bound(last);
         for (int i = tid; i < n; i += NT)
             if (list[i] >= last) atomicAdd(&seg_mass[entry_id(list[i]) / SEG], list_mass[i]);
@@ -967,7 +1028,7 @@ __global__ void __launch_bounds__(NT) k_draw(SmpArgs a, void* ws) {
     u64 sum = 0, z;
 #pragma unroll
     for (int i = 0; i < MINE; ++i) sum += mass[i];
-    u64 at = block_scan(sum, scratch, &z) - sum;
+    u64 at = block.scan(sum, z) - sum;
     const u64 target = r.target(z);
 #pragma unroll
     for (int i = 0; i < MINE; ++i) {
@@ -976,14 +1037,19 @@ __global__ void __launch_bounds__(NT) k_draw(SmpArgs a, void* ws) {
     }
     __syncthreads();
     // the segment's groups, a wave each
-    static_assert(GROUPS == NW, "a wave a group");
+    static_assert(GROUPS <= NT / 64, "a wave a group");
     const int id = s_at * SEG + 4 * tid;
     const u64 rest = s_target;
-    const v4f l = load_four<LD>(a, row, id);
-    u64 m[4];
-    const u64 all = moe::wave_all_sum(kept_masses(r, l, id, bound, m));
-    if (lane == 0) group_mass[wid] = all;
+    v4f l;
+    u64 all = 0;
+    if (wid < GROUPS) {
+        l = load_four<LD>(a, row, id);
+        u64 m[4];
+        all = moe::wave_all_sum(kept_masses(r, l, id, bound, m));
+        if (lane == 0) group_mass[wid] = all;
+    }
     __syncthreads();
+    if (wid >= GROUPS) return;
     u64 before = 0;
     for (int g = 0; g < wid; ++g) before += group_mass[g];
     if (before <= rest && before + all > rest) pick(a, r, row, l, id, bound, z, rest - before);
@@ -995,7 +1061,7 @@ template <int LD>
 int run(SmpArgs a, void* ws, hipStream_t st) {
     a.segs = segs_of(a.V);
     if (a.V <= ROW_MAX) {
-        hipLaunchKernelGGL(k_row<LD>, dim3(a.T), dim3(NT), 0, st, a);
+        hipLaunchKernelGGL(k_row<LD>, dim3(a.T), dim3(ROW_NT), 0, st, a);
         return moe_check_launch("moe_sample");
     }
     // one segment a wave where rows are few; from about four workgroups a CU
@@ -1003,7 +1069,8 @@ int run(SmpArgs a, void* ws, hipStream_t st) {
     const int64_t all = (int64_t)a.T * a.segs;
     const int64_t share = (all + 4096 - 1) / 4096;
     a.share = share < a.segs ? (int)share : a.segs;
-    const dim3 grid((a.segs + NW * a.share - 1) / (NW * a.share), a.T), block(NT);
+    constexpr int NW = CHUNK_NT / 64;
+    const dim3 grid((a.segs + NW * a.share - 1) / (NW * a.share), a.T), block(CHUNK_NT);
     hipLaunchKernelGGL(k_top<LD>, grid, block, 0, st, a, ws);
     if (int rc = moe_check_launch("moe_sample/top")) return rc;
     hipLaunchKernelGGL(k_bins<LD>, grid, block, 0, st, a, ws);
@@ -1012,7 +1079,7 @@ int run(SmpArgs a, void* ws, hipStream_t st) {
         hipLaunchKernelGGL(k_list<LD>, grid, block, 0, st, a, ws);
         if (int rc = moe_check_launch("moe_sample/list")) return rc;
     }
-    hipLaunchKernelGGL(k_draw<LD>, dim3(a.T), block, 0, st, a, ws);
+    hipLaunchKernelGGL(k_draw<LD>, dim3(a.T), dim3(DRAW_NT), 0, st, a, ws);
     return moe_check_launch("moe_sample/draw");
 }
 
