@@ -46,7 +46,6 @@ struct LinArgs {
     int64_t ldy;
     int T, N, K;
     int y_dtype;
-    int vec_scales;  // a chunk's scales of a row are one aligned load
     int wk;          // waves that share a row tile, each with every wk-th chunk
     int tp;          // token rows staged per tile: a power of two up to 16
     int kc;          // inputs staged at a time
@@ -154,72 +153,111 @@ struct Stage {
     }
 };
 
-// One chunk of codes and its scales, as loaded.
+// A wave's R row tiles: what its lanes add to a scalar base for their codes
+// and scales.  Rows from N on read the last row.
 template <int G, int R>
-struct Codes {
-    static constexpr int NS = CH / G;  // scales of a row
-    v4u w[R];
-    uint32_t s[R][(NS + 1) / 2];
-
-    // rows[r]: this lane's row; c: chunk
-    __device__ __forceinline__ void load(const LinArgs& a, const int64_t (&row)[R], int c, int q) {
-        const int nb = a.K >> 5, ng = a.K / G;
-        const int b = 4 * c + q < nb ? 4 * c + q : nb - 1;
+struct Rows {
+    static constexpr int NS = CH / G;  // scales of a row in a chunk
+    uint32_t code[R], code_end[R], scale[R];
+    __device__ __forceinline__ Rows(const LinArgs& a, int64_t n0, int lane) {
+        const int q = lane >> 4, nb = a.K >> 5, ng = a.K / G;
+        const int end = nb - 1 - (nb - 1) / 4 * 4;  // the last chunk's last block
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            w[r] = __builtin_nontemporal_load(&a.wq[row[r] * nb + b]);
-            const _Float16* sp = a.scales + row[r] * ng + c * NS;
-            if (a.vec_scales) {
-                if constexpr (NS == 4) {
-                    const v2u v = *reinterpret_cast<const v2u*>(sp);
-                    s[r][0] = v[0], s[r][1] = v[1];
-                } else if constexpr (NS == 2) {
-                    s[r][0] = *reinterpret_cast<const uint32_t*>(sp);
-                } else {
-                    s[r][0] = *reinterpret_cast<const uint16_t*>(sp);
-                }
-            } else {
-                const uint16_t* hp = reinterpret_cast<const uint16_t*>(sp);
-#pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    const uint32_t v = c * NS + i < ng ? hp[i] : 0;  // past the row: the scale 0
-                    s[r][i / 2] = i & 1 ? s[r][i / 2] | (v << 16) : v;
-                }
-            }
+            const int64_t left = a.N - 1 - n0;
+            const int i = 16 * r + (lane & 15) < left ? 16 * r + (lane & 15) : (int)left;
+            code[r] = (uint32_t)i * nb * 16 + 16 * q;
+            code_end[r] = (uint32_t)i * nb * 16 + 16 * (q < end ? q : end);
+            scale[r] = (uint32_t)i * ng * 2;
         }
-    }
-    __device__ __forceinline__ float scale(int r, int i) const {
-        return (float)__builtin_bit_cast(_Float16, (uint16_t)(s[r][i / 2] >> (16 * (i & 1))));
     }
 };
 
-template <int XD, int G, int NT, int R>
-__device__ __forceinline__ void multiply(const Codes<G, R>& cw, const Stage<XD, G, NT>& st, int block0, int lane,
+// One chunk of codes and its scales, as loaded.  EVEN: K is whole chunks and
+// the scales of a row's chunk are one aligned load.  Otherwise that load starts
+// on any scale, ends with the matrix at the latest, and what lies past the
+// row's end becomes the scale 0 (x is staged as 0 there).
+template <int G, int R, bool EVEN>
+struct Codes {
+    static constexpr int NS = CH / G;
+    using S = std::conditional_t<NS == 4, uint64_t, std::conditional_t<NS == 2, uint32_t, uint16_t>>;
+    typedef S Loose __attribute__((aligned(2)));
+    v4u w[R];
+    S s[R];
+
+    // c: chunk, at most the last one (the same in the wave)
+    __device__ __forceinline__ void load(const LinArgs& a, const char* codes, const char* scales, const Rows<G, R>& rows,
+                                         int c, int chunks) {
+        const char* cp = codes + (int64_t)c * 64;
+        const bool whole = EVEN || c + 1 < chunks || a.K % CH == 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) w[r] = *reinterpret_cast<const v4u*>(cp + (whole ? rows.code[r] : rows.code_end[r]));
+        const char* sp = scales + (int64_t)c * (2 * NS);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if constexpr (EVEN) {
+                s[r] = *reinterpret_cast<const S*>(sp + rows.scale[r]);
+            } else {
+                const int ng = a.K / G, left = ng - c * NS;
+                const char* end = reinterpret_cast<const char*>(a.scales) + (int64_t)a.N * ng * 2;
+                const char* at = sp + rows.scale[r];
+                if ((int64_t)a.N * ng >= NS) {
+                    const int64_t over = at + sizeof(S) - end;
+                    const int back = over > 0 ? (int)over : 0;
+                    s[r] = *reinterpret_cast<const Loose*>(at - back) >> (8 * back);
+                } else {  // fewer scales than a load in the whole matrix
+                    s[r] = 0;
+                    for (int i = 0; i < NS; ++i)
+                        if (i < left) s[r] |= (S)((S)reinterpret_cast<const uint16_t*>(at)[i] << (16 * i));
+                }
+                if (left < NS) s[r] &= (S)(((S)1 << (16 * left)) - 1);
+            }
+        }
+    }
+};
+
+// Takes a chunk out of its buffer (which is free for the next load from then
+// on) into the order the product wants.
+template <int G, int R, bool EVEN>
+struct Chunk {
+    v4u w[R];
+    typename Codes<G, R, EVEN>::S s[R];
+    __device__ __forceinline__ explicit Chunk(const Codes<G, R, EVEN>& c) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) w[r] = transpose4(c.w[r]), s[r] = c.s[r];
+    }
+    __device__ __forceinline__ float scale(int r, int i) const {
+        return (float)__builtin_bit_cast(_Float16, (uint16_t)(s[r] >> (16 * i)));
+    }
+};
+
+template <int XD, int G, int NT, int R, bool EVEN>
+__device__ __forceinline__ void multiply(const Chunk<G, R, EVEN>& cw, const Stage<XD, G, NT>& st, int block0, int lane,
                                          v4f (&acc)[R][NT]) {
     const int q = lane >> 4, tok = lane & (st.tp - 1);
-    v4u w[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) w[r] = transpose4(cw.w[r]);
+    const int step = NT * 64 * st.tp;
+    const char* at = st.piece(0, block0, 0, q, tok);
+    const float* sums = st.sums(block0 * 32 / G) + 4 * q;
     v4f d[R][NT];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         constexpr int BG = G / 32;  // blocks of a group
         bf16x8 b[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) b[r] = codes_bf16(w[r][i]);
+        for (int r = 0; r < R; ++r) b[r] = codes_bf16(cw.w[r][i]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if (i % BG == 0) {
-                const v4f c = *reinterpret_cast<const v4f*>(st.sums((block0 + i) / BG) + 16 * nt + 4 * q);
+                const v4f c = *reinterpret_cast<const v4f*>(sums + (i / BG * NT + nt) * 16);
 #pragma unroll
                 for (int r = 0; r < R; ++r) d[r][nt] = c;
             }
 #pragma unroll
             for (int p = 0; p < PLANES<XD>; ++p) {
-                const bf16x8 a = *reinterpret_cast<const bf16x8*>(st.piece(p, block0 + i, nt, q, tok));
+                const bf16x8 x = *reinterpret_cast<const bf16x8*>(at + p * st.plane_bytes() + nt * 64 * st.tp);
 #pragma unroll
                 for (int r = 0; r < R; ++r)
-                    d[r][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[r], d[r][nt], 0, 0, 0);
+                    d[r][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, b[r], d[r][nt], 0, 0, 0);
             }
             if (i % BG == BG - 1) {
 #pragma unroll
@@ -230,34 +268,32 @@ __device__ __forceinline__ void multiply(const Codes<G, R>& cw, const Stage<XD, 
                 }
             }
         }
+        at += step;
     }
 }
 
 // NW waves; wave = (row tiles of R * 16 rows) x (every wk-th chunk).  x is
-// staged kc inputs at a time in one buffer.
-template <int XD, int G, int NT, int R, int NW, int D>
+// staged kc inputs at a time in one buffer; D chunks a wave are on their way.
+template <int XD, int G, int NT, int R, int NW, int D, bool EVEN>
 __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
     extern __shared__ __align__(16) char smem[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
     const int wk = wave % a.wk, wn = wave / a.wk;
-    const int64_t n0 = ((int64_t)blockIdx.x * (NW / a.wk) + wn) * (16 * R);
+    int64_t n0 = ((int64_t)blockIdx.x * (NW / a.wk) + wn) * (16 * R);
+    const bool none = n0 >= a.N;  // this wave only helps to stage x
+    if (none) n0 = 0;
     const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
     const Stage<XD, G, NT> st{smem, a.tp, a.kc};
-    int64_t row[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        row[r] = n0 + 16 * r + (lane & 15);
-        if (row[r] >= a.N) row[r] = a.N - 1;
-    }
+    const char* codes = reinterpret_cast<const char*>(a.wq) + n0 * (a.K / 2);
+    const char* scales = reinterpret_cast<const char*>(a.scales) + n0 * (a.K / G) * 2;
+    const Rows<G, R> rows(a, n0, lane);
     v4f acc[R][NT] = {};
     const int chunks = (a.K + CH - 1) / CH;
     const int toks = NT == 1 ? a.tp : 16 * NT;
-    Codes<G, R> buf[D];
+    const auto clamp = [&](int c) { return c < chunks ? c : chunks - 1; };
+    Codes<G, R, EVEN> buf[D];
 #pragma unroll
-    for (int i = 0; i < D; ++i) {
-        const int c = i * a.wk + wk;
-        buf[i].load(a, row, c < chunks ? c : chunks - 1, q);
-    }
+    for (int i = 0; i < D; ++i) buf[i].load(a, codes, scales, rows, clamp(i * a.wk + wk), chunks);
     int c = wk;
     for (int k0 = 0; k0 < a.K; k0 += a.kc) {
         const int pieces = toks * (a.kc / 8), per = a.kc / 8;
@@ -270,22 +306,30 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
             st.put(v, tok, j, lane);
         }
         __syncthreads();
+        if (none) continue;
         const int end = (k0 + a.kc < a.K ? k0 + a.kc : a.K + CH - 1) / CH;
-        while (c < end) {
+        const int b0 = k0 / 32;
+        while (c + (D - 1) * a.wk < end) {
 #pragma unroll
             for (int i = 0; i < D; ++i) {
-                if (c < end) {
-                    const Codes<G, R> cur = buf[i];
-                    const int next = c + D * a.wk;
-                    buf[i].load(a, row, next < chunks ? next : chunks - 1, q);
-                    multiply<XD, G, NT, R>(cur, st, 4 * c - k0 / 32, lane, acc);
-                    c += a.wk;
-                }
+                const Chunk<G, R, EVEN> cur(buf[i]);
+                buf[i].load(a, codes, scales, rows, clamp(c + D * a.wk), chunks);
+                multiply<XD, G, NT, R, EVEN>(cur, st, 4 * c - b0, lane, acc);
+                c += a.wk;
+            }
+        }
+        if (c < end) {  // fewer than D are left, of all inputs
+#pragma unroll
+            for (int i = 0; i < D - 1; ++i) {
+                if (c < end) multiply<XD, G, NT, R, EVEN>(Chunk<G, R, EVEN>(buf[i]), st, 4 * c - b0, lane, acc);
+                c += a.wk;
             }
         }
     }
     // waves of one row tile: summed in wave order
-    if (a.wk > 1) {
+    if (a.wk == 1) {
+        if (none) return;
+    } else {
         __syncthreads();
         v4f* part = reinterpret_cast<v4f*>(smem);
         if (wk > 0) {
@@ -295,7 +339,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
                 for (int nt = 0; nt < NT; ++nt) part[(wave * R * NT + r * NT + nt) * 64 + lane] = acc[r][nt];
         }
         __syncthreads();
-        if (wk > 0) return;
+        if (wk > 0 || none) return;
         for (int w = 1; w < a.wk; ++w)
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -342,7 +386,9 @@ int launch(LinArgs a, hipStream_t st) {
     if (a.wk > 1 && lds < red) lds = red;
     const int rows = 16 * R * (NW / a.wk);
     const dim3 grid((unsigned)((a.N + rows - 1) / rows), (unsigned)((a.T + 16 * NT - 1) / (16 * NT)));
-    hipLaunchKernelGGL((k_linear_q4<XD, G, NT, R, NW, D>), grid, dim3(64 * NW), lds, st, a);
+    const bool even = a.K % CH == 0 && reinterpret_cast<uintptr_t>(a.scales) % (2 * CH / G) == 0;
+    const auto kern = even ? k_linear_q4<XD, G, NT, R, NW, D, true> : k_linear_q4<XD, G, NT, R, NW, D, false>;
+    hipLaunchKernelGGL(kern, grid, dim3(64 * NW), lds, st, a);
     return moe_check_launch("moe_linear_q4");
 }
 
@@ -390,7 +436,6 @@ extern "C" int moe_linear_q4(const void* x, int x_dtype, int64_t ldx, const void
     LinArgs a{};
     a.x = x, a.ldx = ldx, a.wq = reinterpret_cast<const v4u*>(wq), a.scales = reinterpret_cast<const _Float16*>(scales);
     a.bias = bias, a.y = y, a.ldy = ldy, a.T = T, a.N = N, a.K = K, a.y_dtype = y_dtype;
-    a.vec_scales = K % CH == 0 && (reinterpret_cast<uintptr_t>(scales) & 7u) == 0;
     const auto go = [&](auto xd) {
         constexpr int XD = decltype(xd)::value;
         return group == 32 ? pick<XD, 32>(a, stream) : group == 64 ? pick<XD, 64>(a, stream) : pick<XD, 128>(a, stream);

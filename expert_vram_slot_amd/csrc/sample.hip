@@ -45,8 +45,8 @@ using v4u = uint32_t __attribute__((ext_vector_type(4)));
 using v2u = uint32_t __attribute__((ext_vector_type(2)));
 
 constexpr int CHUNK_NT = 256;         // threads of a workgroup of k_top, k_bins and k_list
-constexpr int ROW_NT = 1024;          // of k_row: two groups a wave at most, and nothing of a row waits for much
-constexpr int DRAW_NT = 256;          // of k_draw
+constexpr int ROW_NT = 512;           // of k_row (17 x 5003: 256 threads 22 us, 512 15.2 us, 1024 19.9 us)
+constexpr int DRAW_NT = 256;          // of k_draw (512 threads: 1 to 2 us more)
 constexpr int BINS = 1024;
 constexpr int LIST = 2048;            // listed ids of a longer row
 constexpr int ROW_LIST = 1024;        // and of a short one
