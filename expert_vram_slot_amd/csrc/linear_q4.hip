@@ -12,16 +12,18 @@
 //    fp8 e4m3 is code * 2^-9 (the subnormals and the first binade are one
 //    line), so the fp8 -> bf16 conversion with scale 2^9 makes two codes at a
 //    time: 7 vector instructions for 8 codes, masks included.
-//  - The correction by 8 goes in as the product's C operand, -8 * sum of x
-//    over the group, and each group's result is scaled in fp32: no weight is
-//    rounded.  fp32 activations are split into three bf16 planes (8 + 8 + 8
-//    bits, exact) and take three products.
+//  - The correction by 8 is a product of its own, x against a constant -8,
+//    shared by the rows of a wave, and each group's result is scaled in fp32:
+//    no weight is rounded.  fp32 activations are split into three bf16 planes
+//    (8 + 8 + 8 bits, exact) and take three products.
 //  - A lane loads 16 bytes of codes: lane (row i, quarter q) the whole block q
 //    of a chunk of 128 inputs, so a load instruction takes 64 bytes of each of
 //    16 rows.  A product wants one block's codes over the four quarters: a
 //    4 x 4 transpose between quarters and registers, four lane swaps.
-//  - x is staged in LDS in the order the product takes it (block, quarter,
-//    token, the quarter's eight inputs), with the group sums beside it.
+//  - x lies in LDS, all of it where that fits (workgroups then stay and take
+//    one row tile after the other, the codes' loads running on across tiles),
+//    else a stretch of inputs at a time in two buffers.
+#include <atomic>
 #include <type_traits>
 
 #include "common.hpp"
@@ -46,9 +48,8 @@ struct LinArgs {
     int64_t ldy;
     int T, N, K;
     int y_dtype;
-    int wk;          // waves that share a row tile, each with every wk-th chunk
-    int tp;          // token rows staged per tile: a power of two up to 16
-    int kc;          // inputs staged at a time
+    int wk;  // waves that share a row tile, each with every wk-th chunk
+    int kc;  // inputs staged at a time
 };
 
 // Eight codes of a dword (low nibbles, then high) as bf16.
@@ -73,83 +74,51 @@ __device__ __forceinline__ v4u transpose4(v4u w) {
 template <int XD>
 constexpr int PLANES = XD == MOE_X_F32 ? 3 : 1;
 
-// Eight consecutive inputs of a token, as bf16 planes.
-template <int XD>
-struct Piece {
-    v4u raw[XD == MOE_X_F32 ? 2 : 1];
+// x in LDS: [plane][block of 32][token][64 bytes], the row's four 16-byte units
+// turned by (token / 4) % 4: a product's lanes read 8 bytes of 16 tokens, which
+// then lie in different banks.
+template <int XD, int NT, int TP>
+struct Stage {
+    static constexpr int TOKS = NT * TP;    // token rows (TP: of a tile)
+    static constexpr int BLOCK = TOKS * 64;  // bytes of a block of a plane
+    char* base;
+    int plane;  // bytes
 
-    __device__ __forceinline__ void zero() {
-        for (auto& r : raw) r = v4u{0, 0, 0, 0};
+    __device__ __forceinline__ static int turn(int tok) { return (tok >> 2) & 3; }
+    static __host__ __device__ size_t bytes(int kc) { return (size_t)PLANES<XD> * (kc / 32) * BLOCK; }
+    // Where unit u of the stage comes from.  Tokens and inputs past the end
+    // read the last ones: such tokens are not stored, such inputs meet the
+    // scale 0.
+    __device__ __forceinline__ static const char* source(const LinArgs& a, int64_t t0, int k0, int u) {
+        const int block = u / (TOKS * 4), tok = u / 4 % TOKS, k = k0 + 32 * block + 8 * ((u & 3) ^ turn(tok));
+        const int64_t t = t0 + tok < a.T ? t0 + tok : a.T - 1;
+        return reinterpret_cast<const char*>(a.x) + (t * a.ldx + (k < a.K ? k : a.K - 8)) * (XD == MOE_X_F32 ? 4 : 2);
     }
-    __device__ __forceinline__ void load(const LinArgs& a, int64_t t, int k) {
-        const char* p = reinterpret_cast<const char*>(a.x) + (t * a.ldx + k) * (XD == MOE_X_F32 ? 4 : 2);
+    // Unit u of eight fp32 inputs, cut (not rounded) into planes: three cuts of
+    // 8 bits take a whole significand.
+    __device__ __forceinline__ void put(int u, const v4u (&raw)[2]) const {
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < (XD == MOE_X_F32 ? 2 : 1); ++i) raw[i] = reinterpret_cast<const v4u*>(p)[i];
-    }
-    __device__ __forceinline__ float sum() const {
-        float s = 0.0f;
-        if constexpr (XD == MOE_X_F32) {
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(raw[i >> 2][i & 3]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += __uint_as_float(raw[i >> 2][i & 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s += moe::bf16_lo(raw[0][i]) + moe::bf16_hi(raw[0][i]);
-        }
-        return s;
-    }
-    // Plane p: the eight inputs less what the planes before it hold, cut to
-    // bf16 (cut, not rounded: three cuts of 8 bits take a whole significand).
-    __device__ __forceinline__ v4u plane(int p) const {
-        if constexpr (XD != MOE_X_F32) {
-            return raw[0];
-        } else {
+        for (int p = 0; p < 3; ++p) {
             v4u out;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t h[2];
+            for (int i = 0; i < 4; ++i)
+                out[i] = (__float_as_uint(v[2 * i]) >> 16) | (__float_as_uint(v[2 * i + 1]) & 0xFFFF0000u);
+            *reinterpret_cast<v4u*>(base + p * plane + u * 16) = out;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float v = __uint_as_float(raw[i >> 1][2 * (i & 1) + j]);
-                    for (int c = 0; c < p; ++c) v -= __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
-                    h[j] = __float_as_uint(v) >> 16;
-                }
-                out[i] = h[0] | (h[1] << 16);
-            }
-            return out;
+            for (int i = 0; i < 8; ++i) v[i] -= __uint_as_float(__float_as_uint(v[i]) & 0xFFFF0000u);
         }
     }
-};
-
-// LDS: planes of x [plane][block of 32][tile][quarter][tp tokens][8 bf16],
-// then the group sums [group][16 * NT] fp32.
-template <int XD, int G, int NT>
-struct Stage {
-    char* base;
-    int tp, kc;
-    __device__ __forceinline__ int plane_bytes() const { return kc / 32 * NT * 64 * tp; }
-    __device__ __forceinline__ char* piece(int p, int block, int nt, int q, int tok) const {
-        return base + p * plane_bytes() + (((block * NT + nt) * 4 + q) * tp + tok) * 16;
-    }
-    __device__ __forceinline__ float* sums(int group) const {
-        return reinterpret_cast<float*>(base + PLANES<XD> * plane_bytes()) + group * 16 * NT;
-    }
-    static __host__ __device__ size_t bytes(int tp, int kc) {
-        return (size_t)PLANES<XD> * (kc / 32) * NT * 64 * tp + (size_t)(kc / G) * 16 * NT * 4;
-    }
-    // inputs 8j .. 8j + 7 of token `tok` of the stage
-    __device__ __forceinline__ void put(const Piece<XD>& v, int tok, int j, int lane) const {
-        const int block = j >> 2, part = j & 3, nt = tok / 16, t = tok & 15;
-        const int half = part >> 1, q = (part & 1) * 2;
-#pragma unroll
-        for (int p = 0; p < PLANES<XD>; ++p) {
-            const v4u b = v.plane(p);
-            *reinterpret_cast<v2u*>(piece(p, block, nt, q, t) + 8 * half) = v2u{b[0], b[1]};
-            *reinterpret_cast<v2u*>(piece(p, block, nt, q + 1, t) + 8 * half) = v2u{b[2], b[3]};
-        }
-        float s = v.sum();
-#pragma unroll
-        for (int m = 1; m < G / 8; m <<= 1) s += __shfl_xor(s, m, moe::WAVE);
-        if (j % (G / 8) == 0) sums(j / (G / 8))[tok] = -8.0f * s;
+    // The wave's units first, first + 64, ... below end straight into LDS
+    // (bf16; whole waves of units).
+    __device__ __forceinline__ void fetch(const LinArgs& a, int64_t t0, int k0, int first, int step, int end) const {
+        typedef __attribute__((address_space(1))) const void* gptr;
+        typedef __attribute__((address_space(3))) void* lptr;
+        for (int u = first; u < end; u += step)
+            __builtin_amdgcn_global_load_lds((gptr)source(a, t0, k0, u + (int)(threadIdx.x & 63)),
+                                             (lptr)(base + u * 16), 16, 0, 0);
     }
 };
 
@@ -231,107 +200,60 @@ struct Chunk {
     }
 };
 
-template <int XD, int G, int NT, int R, bool EVEN>
-__device__ __forceinline__ void multiply(const Chunk<G, R, EVEN>& cw, const Stage<XD, G, NT>& st, int block0, int lane,
+// One chunk: R row tiles against the NT token tiles.  at0, at1: this lane's two
+// halves of its inputs of the chunk's first block, token tile 0.
+template <int XD, int G, int NT, int TP, int R, bool EVEN>
+__device__ __forceinline__ void multiply(const Chunk<G, R, EVEN>& cw, const char* at0, const char* at1, int plane,
                                          v4f (&acc)[R][NT]) {
-    const int q = lane >> 4, tok = lane & (st.tp - 1);
-    const int step = NT * 64 * st.tp;
-    const char* at = st.piece(0, block0, 0, q, tok);
-    const float* sums = st.sums(block0 * 32 / G) + 4 * q;
-    v4f d[R][NT];
+    using St = Stage<XD, NT, TP>;
+    constexpr uint32_t M8 = 0xC100C100u;  // bf16 -8 twice
+    const bf16x8 minus8 = __builtin_bit_cast(bf16x8, v4u{M8, M8, M8, M8});
+    constexpr int BG = G / 32;  // blocks of a group
+    v4f d[R][NT], eight[NT];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        constexpr int BG = G / 32;  // blocks of a group
         bf16x8 b[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) b[r] = codes_bf16(cw.w[r][i]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            if (i % BG == 0) {
-                const v4f c = *reinterpret_cast<const v4f*>(sums + (i / BG * NT + nt) * 16);
-#pragma unroll
-                for (int r = 0; r < R; ++r) d[r][nt] = c;
-            }
 #pragma unroll
             for (int p = 0; p < PLANES<XD>; ++p) {
-                const bf16x8 x = *reinterpret_cast<const bf16x8*>(at + p * st.plane_bytes() + nt * 64 * st.tp);
+                const int off = i * St::BLOCK + nt * 1024;
+                const v2u lo = *reinterpret_cast<const v2u*>(at0 + p * plane + off);
+                const v2u hi = *reinterpret_cast<const v2u*>(at1 + p * plane + off);
+                const bf16x8 x = __builtin_bit_cast(bf16x8, v4u{lo[0], lo[1], hi[0], hi[1]});
+                const bool first = i % BG == 0 && p == 0;
+                eight[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, minus8, first ? v4f{} : eight[nt], 0, 0, 0);
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    d[r][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, b[r], d[r][nt], 0, 0, 0);
+                for (int r = 0; r < R; ++r) {
+                    // groups of one block: the correction goes in as the product's C
+                    const v4f c = BG == 1 && PLANES<XD> == 1 ? eight[nt] : first ? v4f{} : d[r][nt];
+                    d[r][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, b[r], c, 0, 0, 0);
+                }
             }
             if (i % BG == BG - 1) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const float s = cw.scale(r, i / BG);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[r][nt][e] = fmaf(s, d[r][nt][e], acc[r][nt][e]);
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = BG == 1 && PLANES<XD> == 1 ? d[r][nt][e] : d[r][nt][e] + eight[nt][e];
+                        acc[r][nt][e] = fmaf(s, v, acc[r][nt][e]);
+                    }
                 }
             }
         }
-        at += step;
     }
 }
 
-// NW waves; wave = (row tiles of R * 16 rows) x (every wk-th chunk).  x is
-// staged kc inputs at a time in one buffer; D chunks a wave are on their way.
-template <int XD, int G, int NT, int R, int NW, int D, bool EVEN>
-__global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
-    extern __shared__ __align__(16) char smem[];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
-    const int wk = wave % a.wk, wn = wave / a.wk;
-    int64_t n0 = ((int64_t)blockIdx.x * (NW / a.wk) + wn) * (16 * R);
-    const bool none = n0 >= a.N;  // this wave only helps to stage x
-    if (none) n0 = 0;
-    const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
-    const Stage<XD, G, NT> st{smem, a.tp, a.kc};
-    const char* codes = reinterpret_cast<const char*>(a.wq) + n0 * (a.K / 2);
-    const char* scales = reinterpret_cast<const char*>(a.scales) + n0 * (a.K / G) * 2;
-    const Rows<G, R> rows(a, n0, lane);
-    v4f acc[R][NT] = {};
-    const int chunks = (a.K + CH - 1) / CH;
-    const int toks = NT == 1 ? a.tp : 16 * NT;
-    const auto clamp = [&](int c) { return c < chunks ? c : chunks - 1; };
-    Codes<G, R, EVEN> buf[D];
-#pragma unroll
-    for (int i = 0; i < D; ++i) buf[i].load(a, codes, scales, rows, clamp(i * a.wk + wk), chunks);
-    int c = wk;
-    for (int k0 = 0; k0 < a.K; k0 += a.kc) {
-        const int pieces = toks * (a.kc / 8), per = a.kc / 8;
-        if (k0) __syncthreads();
-        for (int p = threadIdx.x; p < pieces; p += 64 * NW) {
-            const int tok = p / per, j = p % per;
-            Piece<XD> v;
-            v.zero();
-            if (t0 + tok < a.T && k0 + 8 * j < a.K) v.load(a, t0 + tok, k0 + 8 * j);
-            st.put(v, tok, j, lane);
-        }
-        __syncthreads();
-        if (none) continue;
-        const int end = (k0 + a.kc < a.K ? k0 + a.kc : a.K + CH - 1) / CH;
-        const int b0 = k0 / 32;
-        while (c + (D - 1) * a.wk < end) {
-#pragma unroll
-            for (int i = 0; i < D; ++i) {
-                const Chunk<G, R, EVEN> cur(buf[i]);
-                buf[i].load(a, codes, scales, rows, clamp(c + D * a.wk), chunks);
-                multiply<XD, G, NT, R, EVEN>(cur, st, 4 * c - b0, lane, acc);
-                c += a.wk;
-            }
-        }
-        if (c < end) {  // fewer than D are left, of all inputs
-#pragma unroll
-            for (int i = 0; i < D - 1; ++i) {
-                if (c < end) multiply<XD, G, NT, R, EVEN>(Chunk<G, R, EVEN>(buf[i]), st, 4 * c - b0, lane, acc);
-                c += a.wk;
-            }
-        }
-    }
-    // waves of one row tile: summed in wave order
-    if (a.wk == 1) {
-        if (none) return;
-    } else {
-        __syncthreads();
-        v4f* part = reinterpret_cast<v4f*>(smem);
+// Adds up the waves of a row group (in wave order, through `part` in LDS) and
+// stores its rows of y.
+template <int NT, int R>
+__device__ __forceinline__ void store_tile(const LinArgs& a, char* part_, int64_t group, int64_t groups, int64_t t0,
+                                           int wk, int wave, int lane, v4f (&acc)[R][NT]) {
+    if (a.wk > 1) {
+        v4f* part = reinterpret_cast<v4f*>(part_);
         if (wk > 0) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -339,23 +261,26 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
                 for (int nt = 0; nt < NT; ++nt) part[(wave * R * NT + r * NT + nt) * 64 + lane] = acc[r][nt];
         }
         __syncthreads();
-        if (wk > 0 || none) return;
-        for (int w = 1; w < a.wk; ++w)
+        if (wk == 0) {
+            for (int w = 1; w < a.wk; ++w)
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) acc[r][nt] += part[((wave + w) * R * NT + r * NT + nt) * 64 + lane];
+                    for (int nt = 0; nt < NT; ++nt) acc[r][nt] += part[((wave + w) * R * NT + r * NT + nt) * 64 + lane];
+        }
+        __syncthreads();
     }
+    if (wk > 0 || group >= groups) return;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int64_t n = n0 + 16 * r + (lane & 15);
+        const int64_t n = group * (16 * R) + 16 * r + (lane & 15);
         if (n >= a.N) continue;
         const float b = a.bias ? a.bias[n] : 0.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int64_t t = t0 + 16 * nt + 4 * q + e;
+                const int64_t t = t0 + 16 * nt + 4 * (lane >> 4) + e;
                 if (t >= a.T) continue;
                 const float v = acc[r][nt][e] + b;
                 if (a.y_dtype == MOE_X_F32) reinterpret_cast<float*>(a.y)[t * a.ldy + n] = v;
@@ -364,45 +289,195 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
     }
 }
 
-constexpr size_t LIN_LDS = 64 << 10;
+constexpr int NW = 8;  // waves of a workgroup
 
-template <int XD, int G, int NT, int R, int D>
-int launch(LinArgs a, hipStream_t st) {
-    constexpr int NW = 8;
-    const int pad = (a.K + CH - 1) / CH * CH;
-    const int chunks = pad / CH;
-    // row tiles enough for the card's 256 CUs go to waves of their own; fewer
-    // share their inputs among several waves
-    const int64_t tiles = ((int64_t)a.N + 16 * R - 1) / (16 * R) * ((a.T + 16 * NT - 1) / (16 * NT));
-    a.wk = 1;
-    while (a.wk < NW && a.wk * 2 <= chunks && tiles * a.wk < 2048) a.wk *= 2;
-    a.kc = pad;
-    if (D < 4 || Stage<XD, G, NT>::bytes(a.tp, a.kc) > LIN_LDS) {
-        while (a.wk > 1 && Stage<XD, G, NT>::bytes(a.tp, CH * D * a.wk) > LIN_LDS) a.wk /= 2;
-        a.kc = CH * D * a.wk;
+// A wave takes R row tiles of 16 rows (WN = NW / wk such groups a workgroup)
+// and every wk-th chunk of them; the workgroup goes on to the groups gridDim.x
+// further.  A wave's chunks come D at a time: while D are multiplied the next D
+// are on their way, those of the next tile after a tile's last.
+// ALL: x is staged whole, once; else kc = D * wk chunks at a time.
+template <int XD, int G, int NT, int TP, int R, int D, bool ALL, bool EVEN>
+__global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
+    using St = Stage<XD, NT, TP>;
+    extern __shared__ __align__(16) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
+    const int wk = wave % a.wk, wn = wave / a.wk, per = NW / a.wk;
+    const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
+    const int64_t groups = ((int64_t)a.N + 16 * R - 1) / (16 * R);
+    const int stage_bytes = (int)St::bytes(a.kc);
+    const int chunks = (a.K + CH - 1) / CH;
+    const int rounds = ((chunks + a.wk - 1) / a.wk + D - 1) / D;  // of D chunks a wave, for one group
+    const int units = a.kc / 32 * St::TOKS * 4;                   // 16-byte units of a plane of a stage
+
+    // this lane's two 8-byte halves in a block
+    const int tok = lane & (TP - 1);
+    const int at0 = tok * 64 + (((q >> 1) ^ St::turn(tok)) * 16) + (q & 1) * 8, at1 = at0 ^ 32;
+
+    int64_t group = (int64_t)blockIdx.x * per + wn;
+    const auto group_at = [&](int64_t g) { return g < groups ? g : groups - 1; };
+    Rows<G, R> rows(a, group_at(group) * (16 * R), lane);
+    const char* codes = reinterpret_cast<const char*>(a.wq) + group_at(group) * (16 * R) * (a.K / 2);
+    const char* scales = reinterpret_cast<const char*>(a.scales) + group_at(group) * (16 * R) * (a.K / G) * 2;
+    const auto chunk_at = [&](int round, int i) {
+        const int c = (round * D + i) * a.wk + wk;
+        return c < chunks ? c : chunks - 1;
+    };
+    Codes<G, R, EVEN> buf[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) buf[i].load(a, codes, scales, rows, chunk_at(0, i), chunks);
+
+    // stage 0
+    if constexpr (XD == MOE_X_BF16 && TP == 16) {
+        St{smem, stage_bytes}.fetch(a, t0, 0, wave * 64, NW * 64, units);
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // all loads are there (the barrier waits for LDS writes alone)
+    } else {
+        const St st{smem, stage_bytes / PLANES<XD>};
+#pragma unroll 4
+        for (int u = tid; u < units; u += 64 * NW) {
+            const v4u* p = reinterpret_cast<const v4u*>(St::source(a, t0, 0, u));
+            if constexpr (XD == MOE_X_F32) {
+                const v4u raw[2] = {p[0], p[1]};
+                st.put(u, raw);
+            } else {
+                *reinterpret_cast<v4u*>(smem + u * 16) = p[0];
+            }
+        }
     }
-    size_t lds = Stage<XD, G, NT>::bytes(a.tp, a.kc);
-    const size_t red = (size_t)NW * R * NT * 1024;
-    if (a.wk > 1 && lds < red) lds = red;
-    const int rows = 16 * R * (NW / a.wk);
-    const dim3 grid((unsigned)((a.N + rows - 1) / rows), (unsigned)((a.T + 16 * NT - 1) / (16 * NT)));
-    const bool even = a.K % CH == 0 && reinterpret_cast<uintptr_t>(a.scales) % (2 * CH / G) == 0;
-    const auto kern = even ? k_linear_q4<XD, G, NT, R, NW, D, true> : k_linear_q4<XD, G, NT, R, NW, D, false>;
-    hipLaunchKernelGGL(kern, grid, dim3(64 * NW), lds, st, a);
+    __syncthreads();
+
+    v4f acc[R][NT] = {};
+    int now = 0;  // the stage's buffer
+    // every workgroup's waves take as many rounds, so that they meet at the barriers
+    const int64_t turns = (groups + per - 1) / per;
+    for (int64_t turn = blockIdx.x; turn < turns; turn += gridDim.x) {
+        const int64_t mine = group;
+        for (int round = 0; round < rounds; ++round) {
+            const bool last = round + 1 == rounds;
+            const bool more = !last || turn + gridDim.x < turns;
+            constexpr int PPT = ALL ? 1 : 256 * NT * D / (64 * NW);  // fp32 units a thread holds
+            v4u raw[XD == MOE_X_F32 && !ALL ? PPT : 1][2];
+            const int k_next = last ? 0 : (round + 1) * a.kc;
+            if constexpr (!ALL) {
+                // the next stage goes into the other buffer, which nobody reads since the last barrier
+                char* other = smem + (now ^ 1) * stage_bytes;
+                if (more) {
+                    if constexpr (XD == MOE_X_BF16) {
+                        St{other, stage_bytes}.fetch(a, t0, k_next, wave * 64, NW * 64, units);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < PPT; ++i) {
+                            const v4u* p = reinterpret_cast<const v4u*>(St::source(a, t0, k_next, tid + i * 64 * NW));
+                            raw[i][0] = p[0], raw[i][1] = p[1];
+                        }
+                        // what several waves a row group need besides (the registers hold one wave's share)
+                        const St st{other, stage_bytes / PLANES<XD>};
+                        for (int u = tid + PPT * 64 * NW; u < units; u += 64 * NW) {
+                            const v4u* p = reinterpret_cast<const v4u*>(St::source(a, t0, k_next, u));
+                            const v4u extra[2] = {p[0], p[1]};
+                            st.put(u, extra);
+                        }
+                    }
+                }
+            }
+            if (last) {  // the loads go on with the next group
+                group += (int64_t)gridDim.x * per;
+                const int64_t g = group_at(group);
+                rows = Rows<G, R>(a, g * (16 * R), lane);
+                codes = reinterpret_cast<const char*>(a.wq) + g * (16 * R) * (a.K / 2);
+                scales = reinterpret_cast<const char*>(a.scales) + g * (16 * R) * (a.K / G) * 2;
+            }
+            const int next = last ? 0 : round + 1;
+            const char* x = smem + (ALL ? 0 : now * stage_bytes);
+            const int c0 = round * D * a.wk + wk, k0 = ALL ? 0 : round * a.kc;
+            const auto at = [&](int i) { return x + (4 * (c0 + i * a.wk) - k0 / 32) * St::BLOCK; };
+            const int plane = stage_bytes / PLANES<XD>;
+            if (c0 + (D - 1) * a.wk < chunks) {
+#pragma unroll
+                for (int i = 0; i < D; ++i) {
+                    const Chunk<G, R, EVEN> cur(buf[i]);
+                    buf[i].load(a, codes, scales, rows, chunk_at(next, i), chunks);
+                    multiply<XD, G, NT, TP, R, EVEN>(cur, at(i) + at0, at(i) + at1, plane, acc);
+                }
+            } else {  // a tile's last chunks, fewer than D
+#pragma unroll
+                for (int i = 0; i < D; ++i) {
+                    const Chunk<G, R, EVEN> cur(buf[i]);
+                    buf[i].load(a, codes, scales, rows, chunk_at(next, i), chunks);
+                    if (c0 + i * a.wk < chunks)
+                        multiply<XD, G, NT, TP, R, EVEN>(cur, at(i) + at0, at(i) + at1, plane, acc);
+                }
+            }
+            if constexpr (!ALL) {
+                if constexpr (XD == MOE_X_F32) {
+                    if (more) {
+                        const St st{smem + (now ^ 1) * stage_bytes, plane};
+#pragma unroll
+                        for (int i = 0; i < PPT; ++i) st.put(tid + i * 64 * NW, raw[i]);
+                    }
+                } else {
+                    __builtin_amdgcn_s_waitcnt(0x0F70);
+                }
+                __syncthreads();
+                now ^= 1;
+            }
+        }
+        store_tile<NT, R>(a, smem + (ALL ? 1 : 2) * stage_bytes, mine, groups, t0, wk, wave, lane, acc);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) acc[r][nt] = v4f{};
+    }
+}
+
+constexpr size_t LDS_MAX = 160 << 10;
+
+template <int XD, int G, int NT, int TP, int R, int D, bool ALL, bool EVEN>
+int launch(LinArgs a, hipStream_t st) {
+    using St = Stage<XD, NT, TP>;
+    const auto kern = k_linear_q4<XD, G, NT, TP, R, D, ALL, EVEN>;
+    const int chunks = (a.K + CH - 1) / CH;
+    // row groups enough for the card go to waves of their own; fewer share
+    // their inputs among several waves
+    const int64_t groups = ((int64_t)a.N + 16 * R - 1) / (16 * R), tiles = ((int64_t)a.T + 16 * NT - 1) / (16 * NT);
+    a.wk = 1;
+    while (a.wk < NW && a.wk * 2 <= chunks && groups * tiles * a.wk < 2048 &&
+           (ALL || 2 * St::bytes(CH * D * a.wk * 2) <= 64 << 10))
+        a.wk *= 2;
+    a.kc = ALL ? chunks * CH : CH * D * a.wk;
+    const size_t lds = (ALL ? 1 : 2) * St::bytes(a.kc) + (a.wk > 1 ? (size_t)NW * R * NT * 1024 : 0);
+    if (lds > 64 << 10) {  // asked for once per kernel and device
+        static std::atomic<uint64_t> asked{0};
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e == hipSuccess && !(dev < 64 && (asked.load() >> dev & 1))) {
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)LDS_MAX);
+            if (e == hipSuccess && dev < 64) asked.fetch_or((uint64_t)1 << dev);
+        }
+        if (e != hipSuccess) return moe_fail(MOE_E_HIP, "moe_linear_q4: %zu bytes of LDS: %s", lds, hipGetErrorString(e));
+    }
+    // with x staged once, workgroups stay: as many as the card holds at a time
+    const int per = NW / a.wk;
+    int64_t blocks = (groups + per - 1) / per;
+    const int64_t most = 256 * (lds > 80 << 10 ? 1 : 2);
+    if (blocks * tiles > most) blocks = tiles >= most ? 1 : most / tiles;
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks, (unsigned)tiles), dim3(64 * NW), lds, st, a);
     return moe_check_launch("moe_linear_q4");
 }
 
-template <int XD, int G>
-int pick(LinArgs a, hipStream_t st) {
+template <int XD, int G, bool EVEN>
+int pick(const LinArgs& a, hipStream_t st) {
     const int pad = (a.K + CH - 1) / CH * CH;
-    a.tp = 1;
-    while (a.tp < 16 && a.tp < a.T) a.tp *= 2;
-    if (a.T <= 16) {
-        if (Stage<XD, G, 1>::bytes(a.tp, pad) <= LIN_LDS) return launch<XD, G, 1, 1, 4>(a, st);
-        return launch<XD, G, 1, 1, 2>(a, st);
-    }
-    if (a.T <= 32) return launch<XD, G, 2, 2, 2>(a, st);
-    return launch<XD, G, 4, 2, XD == MOE_X_F32 ? 1 : 2>(a, st);
+    // x whole in LDS: as long as two workgroups share a CU, or one of 16 tokens
+    const auto whole = [&](size_t bytes, size_t most) { return bytes <= most; };
+    if (a.T == 1 && whole(Stage<XD, 1, 1>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 1, 1, 4, true, EVEN>(a, st);
+    if (a.T <= 4 && whole(Stage<XD, 1, 4>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 4, 1, 4, true, EVEN>(a, st);
+    if (a.T <= 8 && whole(Stage<XD, 1, 8>::bytes(pad), 80 << 10)) return launch<XD, G, 1, 8, 1, 4, true, EVEN>(a, st);
+    if (a.T <= 16 && whole(Stage<XD, 1, 16>::bytes(pad), 128 << 10)) return launch<XD, G, 1, 16, 1, 4, true, EVEN>(a, st);
+    if (a.T <= 16) return launch<XD, G, 1, 16, 1, 2, false, EVEN>(a, st);
+    if (a.T <= 32) return launch<XD, G, 2, 16, 2, 2, false, EVEN>(a, st);
+    if constexpr (XD == MOE_X_F32) return launch<XD, G, 4, 16, 2, 1, false, EVEN>(a, st);
+    else return launch<XD, G, 4, 16, 2, 2, false, EVEN>(a, st);
 }
 
 }  // namespace
@@ -438,7 +513,14 @@ extern "C" int moe_linear_q4(const void* x, int x_dtype, int64_t ldx, const void
     a.bias = bias, a.y = y, a.ldy = ldy, a.T = T, a.N = N, a.K = K, a.y_dtype = y_dtype;
     const auto go = [&](auto xd) {
         constexpr int XD = decltype(xd)::value;
-        return group == 32 ? pick<XD, 32>(a, stream) : group == 64 ? pick<XD, 64>(a, stream) : pick<XD, 128>(a, stream);
+        const bool even = K % CH == 0 && reinterpret_cast<uintptr_t>(scales) % (2 * CH / group) == 0;
+        const auto by_group = [&](auto g) {
+            constexpr int G = decltype(g)::value;
+            return even ? pick<XD, G, true>(a, stream) : pick<XD, G, false>(a, stream);
+        };
+        return group == 32   ? by_group(std::integral_constant<int, 32>{})
+               : group == 64 ? by_group(std::integral_constant<int, 64>{})
+                             : by_group(std::integral_constant<int, 128>{});
     };
     return x_dtype == MOE_X_F32 ? go(std::integral_constant<int, MOE_X_F32>{})
                                 : go(std::integral_constant<int, MOE_X_BF16>{});
