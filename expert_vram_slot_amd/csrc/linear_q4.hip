@@ -289,14 +289,12 @@ __device__ __forceinline__ void store_tile(const LinArgs& a, char* part_, int64_
     }
 }
 
-constexpr int NW = 8;  // waves of a workgroup
-
-// A wave takes R row tiles of 16 rows (WN = NW / wk such groups a workgroup)
+// NW waves.  A wave takes R row tiles of 16 rows (NW / wk such groups a workgroup)
 // and every wk-th chunk of them; the workgroup goes on to the groups gridDim.x
 // further.  A wave's chunks come D at a time: while D are multiplied the next D
 // are on their way, those of the next tile after a tile's last.
 // ALL: x is staged whole, once; else kc = D * wk chunks at a time.
-template <int XD, int G, int NT, int TP, int R, int D, bool ALL, bool EVEN>
+template <int XD, int G, int NT, int TP, int R, int D, bool ALL, bool EVEN, int NW>
 __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
     using St = Stage<XD, NT, TP>;
     extern __shared__ __align__(16) char smem[];
@@ -391,21 +389,15 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
             const int c0 = round * D * a.wk + wk, k0 = ALL ? 0 : round * a.kc;
             const auto at = [&](int i) { return x + (4 * (c0 + i * a.wk) - k0 / 32) * St::BLOCK; };
             const int plane = stage_bytes / PLANES<XD>;
-            if (c0 + (D - 1) * a.wk < chunks) {
 #pragma unroll
-                for (int i = 0; i < D; ++i) {
-                    const Chunk<G, R, EVEN> cur(buf[i]);
-                    buf[i].load(a, codes, scales, rows, chunk_at(next, i), chunks);
+            for (int i = 0; i < D; ++i) {
+                // the load goes out before the product of the chunk it replaces; left to itself the compiler
+                // lets it wait for free registers
+                const Chunk<G, R, EVEN> cur(buf[i]);
+                buf[i].load(a, codes, scales, rows, chunk_at(next, i), chunks);
+                __builtin_amdgcn_sched_barrier(0);
+                if (c0 + i * a.wk < chunks)
                     multiply<XD, G, NT, TP, R, EVEN>(cur, at(i) + at0, at(i) + at1, plane, acc);
-                }
-            } else {  // a tile's last chunks, fewer than D
-#pragma unroll
-                for (int i = 0; i < D; ++i) {
-                    const Chunk<G, R, EVEN> cur(buf[i]);
-                    buf[i].load(a, codes, scales, rows, chunk_at(next, i), chunks);
-                    if (c0 + i * a.wk < chunks)
-                        multiply<XD, G, NT, TP, R, EVEN>(cur, at(i) + at0, at(i) + at1, plane, acc);
-                }
             }
             if constexpr (!ALL) {
                 if constexpr (XD == MOE_X_F32) {
@@ -431,10 +423,10 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
 
 constexpr size_t LDS_MAX = 160 << 10;
 
-template <int XD, int G, int NT, int TP, int R, int D, bool ALL, bool EVEN>
+template <int XD, int G, int NT, int TP, int R, int D, bool ALL, bool EVEN, int NW>
 int launch(LinArgs a, hipStream_t st) {
     using St = Stage<XD, NT, TP>;
-    const auto kern = k_linear_q4<XD, G, NT, TP, R, D, ALL, EVEN>;
+    const auto kern = k_linear_q4<XD, G, NT, TP, R, D, ALL, EVEN, NW>;
     const int chunks = (a.K + CH - 1) / CH;
     // row groups enough for the card go to waves of their own; fewer share
     // their inputs among several waves
@@ -470,14 +462,14 @@ int pick(const LinArgs& a, hipStream_t st) {
     const int pad = (a.K + CH - 1) / CH * CH;
     // x whole in LDS: as long as two workgroups share a CU, or one of 16 tokens
     const auto whole = [&](size_t bytes, size_t most) { return bytes <= most; };
-    if (a.T == 1 && whole(Stage<XD, 1, 1>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 1, 1, 4, true, EVEN>(a, st);
-    if (a.T <= 4 && whole(Stage<XD, 1, 4>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 4, 1, 4, true, EVEN>(a, st);
-    if (a.T <= 8 && whole(Stage<XD, 1, 8>::bytes(pad), 80 << 10)) return launch<XD, G, 1, 8, 1, 4, true, EVEN>(a, st);
-    if (a.T <= 16 && whole(Stage<XD, 1, 16>::bytes(pad), 128 << 10)) return launch<XD, G, 1, 16, 1, 4, true, EVEN>(a, st);
-    if (a.T <= 16) return launch<XD, G, 1, 16, 1, 2, false, EVEN>(a, st);
-    if (a.T <= 32) return launch<XD, G, 2, 16, 2, 2, false, EVEN>(a, st);
-    if constexpr (XD == MOE_X_F32) return launch<XD, G, 4, 16, 2, 1, false, EVEN>(a, st);
-    else return launch<XD, G, 4, 16, 2, 2, false, EVEN>(a, st);
+    if (a.T == 1 && whole(Stage<XD, 1, 1>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 1, 1, 4, true, EVEN, 8>(a, st);
+    if (a.T <= 4 && whole(Stage<XD, 1, 4>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 4, 1, 4, true, EVEN, 8>(a, st);
+    if (a.T <= 8 && whole(Stage<XD, 1, 8>::bytes(pad), 80 << 10)) return launch<XD, G, 1, 8, 1, 4, true, EVEN, 8>(a, st);
+    if (a.T <= 16 && whole(Stage<XD, 1, 16>::bytes(pad), 128 << 10)) return launch<XD, G, 1, 16, 1, 4, true, EVEN, 8>(a, st);
+    if (a.T <= 16) return launch<XD, G, 1, 16, 1, 2, false, EVEN, 8>(a, st);
+    if (a.T <= 32) return launch<XD, G, 2, 16, 2, 2, false, EVEN, 8>(a, st);
+    if constexpr (XD == MOE_X_F32) return launch<XD, G, 4, 16, 2, 1, false, EVEN, 8>(a, st);
+    else return launch<XD, G, 4, 16, 2, 2, false, EVEN, 8>(a, st);
 }
 
 }  // namespace
