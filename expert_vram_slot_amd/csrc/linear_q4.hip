@@ -16,10 +16,13 @@
 //    shared by the rows of a wave, and each group's result is scaled in fp32:
 //    no weight is rounded.  fp32 activations are split into three bf16 planes
 //    (8 + 8 + 8 bits, exact) and take three products.
-//  - A lane loads 16 bytes of codes: lane (row i, quarter q) the whole block q
-//    of a chunk of 128 inputs, so a load instruction takes 64 bytes of each of
-//    16 rows.  A product wants one block's codes over the four quarters: a
-//    4 x 4 transpose between quarters and registers, four lane swaps.
+//  - Two chunks of 128 inputs are loaded together, so that a load instruction
+//    takes whole 128-byte lines, one of each of 8 rows (64 bytes of 16 rows
+//    each: the more loads on their way, the more lines left the caches between
+//    their halves; one token, 131072 x 2048: 45 us).  An exchange between lanes
+//    8 apart gives each chunk 16 rows by four blocks, and a 4 x 4 transpose
+//    between quarters of the wave and registers (four lane swaps) gives each
+//    block's four dwords to the four quarters, as a product wants them.
 //  - x lies in LDS, all of it where that fits (workgroups then stay and take
 //    one row tile after the other, the codes' loads running on across tiles),
 //    else a stretch of inputs at a time in two buffers.
@@ -36,7 +39,8 @@ using v4f = float __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int CH = 128;  // inputs of a chunk: one 16-byte load of each lane
+constexpr int CH = 128;  // inputs of a chunk: one 16-byte piece of each lane
+constexpr int UNIT = 2 * CH;  // inputs loaded together
 
 struct LinArgs {
     const void* x;
@@ -69,6 +73,17 @@ __device__ __forceinline__ v4u transpose4(v4u w) {
     const auto c = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
     const auto d = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
     return v4u{c[0], d[0], c[1], d[1]};
+}
+
+// Registers a and b of lanes 8 apart: a keeps its lower eight lanes of each row
+// of 16 and takes b's lower for its upper; b the other way round.
+__device__ __forceinline__ void exchange8(v4u& a, v4u& b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = (int)a[i];
+        a[i] = (uint32_t)__builtin_amdgcn_update_dpp((int)a[i], (int)b[i], 0x128, 0xF, 0xC, false);  // row_ror:8
+        b[i] = (uint32_t)__builtin_amdgcn_update_dpp((int)b[i], t, 0x128, 0xF, 0x3, false);
+    }
 }
 
 template <int XD>
@@ -123,88 +138,118 @@ struct Stage {
 };
 
 // A wave's R row tiles: what its lanes add to a scalar base for their codes
-// and scales.  Rows from N on read the last row.
+// (pieces of rows l % 8 and 8 + l % 8 of a tile) and scales (of row l % 16).
+// Rows from N on read the last row.
 template <int G, int R>
 struct Rows {
-    static constexpr int NS = CH / G;  // scales of a row in a chunk
-    uint32_t code[R], code_end[R], scale[R];
+    uint32_t code[R][2], code_end[R][2], scale[R];
     __device__ __forceinline__ Rows(const LinArgs& a, int64_t n0, int lane) {
-        const int q = lane >> 4, nb = a.K >> 5, ng = a.K / G;
-        const int end = nb - 1 - (nb - 1) / 4 * 4;  // the last chunk's last block
+        const int piece = (lane >> 4) + 4 * ((lane >> 3) & 1), nb = a.K >> 5, ng = a.K / G;
+        const int end = (nb - 1) % 8;  // the last unit's last piece
+        const int64_t left = a.N - 1 - n0;
+        const auto row = [&](int i) { return (uint32_t)(i < left ? i : (int)left); };
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t left = a.N - 1 - n0;
-            const int i = 16 * r + (lane & 15) < left ? 16 * r + (lane & 15) : (int)left;
-            code[r] = (uint32_t)i * nb * 16 + 16 * q;
-            code_end[r] = (uint32_t)i * nb * 16 + 16 * (q < end ? q : end);
-            scale[r] = (uint32_t)i * ng * 2;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t at = row(16 * r + 8 * h + (lane & 7)) * nb * 16;
+                code[r][h] = at + 16 * piece;
+                code_end[r][h] = at + 16 * (piece < end ? piece : end);
+            }
+            scale[r] = row(16 * r + (lane & 15)) * ng * 2;
         }
     }
 };
 
-// One chunk of codes and its scales, as loaded.  EVEN: K is whole chunks and
-// the scales of a row's chunk are one aligned load.  Otherwise that load starts
-// on any scale, ends with the matrix at the latest, and what lies past the
-// row's end becomes the scale 0 (x is staged as 0 there).
+// One unit of codes and its scales, as loaded.  EVEN: K is whole units and the
+// scales of a row's unit are one aligned load.  Otherwise a chunk's scales are
+// a load that starts on any scale, ends with the matrix at the latest, and what
+// lies past the row's end becomes the scale 0.
 template <int G, int R, bool EVEN>
 struct Codes {
-    static constexpr int NS = CH / G;
+    static constexpr int NS = CH / G;  // scales of a row in a chunk
     using S = std::conditional_t<NS == 4, uint64_t, std::conditional_t<NS == 2, uint32_t, uint16_t>>;
     typedef S Loose __attribute__((aligned(2)));
-    v4u w[R];
-    S s[R];
+    v4u w[R][2];
+    S s[R][2];
 
-    // c: chunk, at most the last one (the same in the wave)
+    // u: unit, at most the last one (the same in the wave)
     __device__ __forceinline__ void load(const LinArgs& a, const char* codes, const char* scales, const Rows<G, R>& rows,
-                                         int c, int chunks) {
-        const char* cp = codes + (int64_t)c * 64;
-        const bool whole = EVEN || c + 1 < chunks || a.K % CH == 0;
+                                         int u, int units) {
+        const char* cp = codes + (int64_t)u * (UNIT / 2);
+        const bool whole = EVEN || u + 1 < units || a.K % UNIT == 0;
 #pragma unroll
-        for (int r = 0; r < R; ++r) w[r] = *reinterpret_cast<const v4u*>(cp + (whole ? rows.code[r] : rows.code_end[r]));
-        const char* sp = scales + (int64_t)c * (2 * NS);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w[r][h] = *reinterpret_cast<const v4u*>(cp + (whole ? rows.code[r][h] : rows.code_end[r][h]));
+        const char* sp = scales + (int64_t)u * (4 * NS);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if constexpr (EVEN) {
-                s[r] = *reinterpret_cast<const S*>(sp + rows.scale[r]);
+            if constexpr (EVEN && NS == 4) {
+                const v4u v = *reinterpret_cast<const v4u*>(sp + rows.scale[r]);
+                s[r][0] = v[0] | (uint64_t)v[1] << 32, s[r][1] = v[2] | (uint64_t)v[3] << 32;
+            } else if constexpr (EVEN && NS == 2) {
+                const v2u v = *reinterpret_cast<const v2u*>(sp + rows.scale[r]);
+                s[r][0] = v[0], s[r][1] = v[1];
+            } else if constexpr (EVEN) {
+                const uint32_t v = *reinterpret_cast<const uint32_t*>(sp + rows.scale[r]);
+                s[r][0] = (uint16_t)v, s[r][1] = (uint16_t)(v >> 16);
             } else {
-                const int ng = a.K / G, left = ng - c * NS;
+                const int ng = a.K / G;
                 const char* end = reinterpret_cast<const char*>(a.scales) + (int64_t)a.N * ng * 2;
-                const char* at = sp + rows.scale[r];
-                if ((int64_t)a.N * ng >= NS) {
-                    const int64_t over = at + sizeof(S) - end;
-                    const int back = over > 0 ? (int)over : 0;
-                    s[r] = *reinterpret_cast<const Loose*>(at - back) >> (8 * back);
-                } else {  // fewer scales than a load in the whole matrix
-                    s[r] = 0;
-                    for (int i = 0; i < NS; ++i)
-                        if (i < left) s[r] |= (S)((S)reinterpret_cast<const uint16_t*>(at)[i] << (16 * i));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int left = ng - (2 * u + h) * NS;
+                    const char* at = sp + rows.scale[r] + 2 * NS * h;
+                    s[r][h] = 0;
+                    if (left <= 0) continue;  // the unit's second chunk is past the row
+                    if ((int64_t)a.N * ng >= NS) {
+                        const int64_t over = at + sizeof(S) - end;
+                        const int back = over > 0 ? (int)over : 0;
+                        s[r][h] = *reinterpret_cast<const Loose*>(at - back) >> (8 * back);
+                    } else {  // fewer scales than a load in the whole matrix
+                        for (int i = 0; i < NS; ++i)
+                            if (i < left) s[r][h] |= (S)((S)reinterpret_cast<const uint16_t*>(at)[i] << (16 * i));
+                    }
+                    if (left < NS) s[r][h] &= (S)(((S)1 << (16 * left)) - 1);
                 }
-                if (left < NS) s[r] &= (S)(((S)1 << (16 * left)) - 1);
             }
         }
     }
 };
 
-// Takes a chunk out of its buffer (which is free for the next load from then
-// on) into the order the product wants.
+// Takes a unit's two chunks out of their buffer (which is free for the next
+// load from then on) into the order the product wants, the scales as fp32: kept
+// as they were loaded, they stay in the load's registers and the next load
+// waits.
 template <int G, int R, bool EVEN>
-struct Chunk {
-    v4u w[R];
-    typename Codes<G, R, EVEN>::S s[R];
-    __device__ __forceinline__ explicit Chunk(const Codes<G, R, EVEN>& c) {
+struct Chunks {
+    static constexpr int NS = CH / G;
+    v4u w[2][R];
+    float scale[2][R][NS];
+    __device__ __forceinline__ explicit Chunks(const Codes<G, R, EVEN>& c) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) w[r] = transpose4(c.w[r]), s[r] = c.s[r];
-    }
-    __device__ __forceinline__ float scale(int r, int i) const {
-        return (float)__builtin_bit_cast(_Float16, (uint16_t)(s[r] >> (16 * i)));
+        for (int r = 0; r < R; ++r) {
+            v4u lo = c.w[r][0], hi = c.w[r][1];
+            exchange8(lo, hi);
+            w[0][r] = transpose4(lo), w[1][r] = transpose4(hi);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    scale[h][r][i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(c.s[r][h] >> (16 * i)));
+                    asm volatile("" : "+v"(scale[h][r][i]));  // here and now, not folded into the product's last step
+                }
+        }
     }
 };
 
 // One chunk: R row tiles against the NT token tiles.  at0, at1: this lane's two
 // halves of its inputs of the chunk's first block, token tile 0.
-template <int XD, int G, int NT, int TP, int R, bool EVEN>
-__device__ __forceinline__ void multiply(const Chunk<G, R, EVEN>& cw, const char* at0, const char* at1, int plane,
-                                         v4f (&acc)[R][NT]) {
+template <int XD, int G, int NT, int TP, int R>
+__device__ __forceinline__ void multiply(const v4u (&w)[R], const float (&scale)[R][CH / G], const char* at0,
+                                         const char* at1, int plane, v4f (&acc)[R][NT]) {
     using St = Stage<XD, NT, TP>;
     constexpr uint32_t M8 = 0xC100C100u;  // bf16 -8 twice
     const bf16x8 minus8 = __builtin_bit_cast(bf16x8, v4u{M8, M8, M8, M8});
@@ -214,7 +259,7 @@ __device__ __forceinline__ void multiply(const Chunk<G, R, EVEN>& cw, const char
     for (int i = 0; i < 4; ++i) {
         bf16x8 b[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) b[r] = codes_bf16(cw.w[r][i]);
+        for (int r = 0; r < R; ++r) b[r] = codes_bf16(w[r][i]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -235,7 +280,7 @@ __device__ __forceinline__ void multiply(const Chunk<G, R, EVEN>& cw, const char
             if (i % BG == BG - 1) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float s = cw.scale(r, i / BG);
+                    const float s = scale[r][i / BG];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float v = BG == 1 && PLANES<XD> == 1 ? d[r][nt][e] : d[r][nt][e] + eight[nt][e];
@@ -251,7 +296,7 @@ __device__ __forceinline__ void multiply(const Chunk<G, R, EVEN>& cw, const char
 // stores its rows of y.
 template <int NT, int R>
 __device__ __forceinline__ void store_tile(const LinArgs& a, char* part_, int64_t group, int64_t groups, int64_t t0,
-                                           int wk, int wave, int lane, v4f (&acc)[R][NT]) {
+                                           int wk, int wave, int lane, const float (&bias)[R], v4f (&acc)[R][NT]) {
     if (a.wk > 1) {
         v4f* part = reinterpret_cast<v4f*>(part_);
         if (wk > 0) {
@@ -275,14 +320,13 @@ __device__ __forceinline__ void store_tile(const LinArgs& a, char* part_, int64_
     for (int r = 0; r < R; ++r) {
         const int64_t n = group * (16 * R) + 16 * r + (lane & 15);
         if (n >= a.N) continue;
-        const float b = a.bias ? a.bias[n] : 0.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int64_t t = t0 + 16 * nt + 4 * (lane >> 4) + e;
                 if (t >= a.T) continue;
-                const float v = acc[r][nt][e] + b;
+                const float v = acc[r][nt][e] + bias[r];
                 if (a.y_dtype == MOE_X_F32) reinterpret_cast<float*>(a.y)[t * a.ldy + n] = v;
                 else reinterpret_cast<__bf16*>(a.y)[t * a.ldy + n] = (__bf16)v;
             }
@@ -290,10 +334,10 @@ __device__ __forceinline__ void store_tile(const LinArgs& a, char* part_, int64_
 }
 
 // NW waves.  A wave takes R row tiles of 16 rows (NW / wk such groups a workgroup)
-// and every wk-th chunk of them; the workgroup goes on to the groups gridDim.x
-// further.  A wave's chunks come D at a time: while D are multiplied the next D
+// and every wk-th unit of them; the workgroup goes on to the groups gridDim.x
+// further.  A wave's units come D at a time: while D are multiplied the next D
 // are on their way, those of the next tile after a tile's last.
-// ALL: x is staged whole, once; else kc = D * wk chunks at a time.
+// ALL: x is staged whole, once; else kc = D * wk units at a time.
 template <int XD, int G, int NT, int TP, int R, int D, bool ALL, bool EVEN, int NW>
 __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
     using St = Stage<XD, NT, TP>;
@@ -303,9 +347,9 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
     const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
     const int64_t groups = ((int64_t)a.N + 16 * R - 1) / (16 * R);
     const int stage_bytes = (int)St::bytes(a.kc);
-    const int chunks = (a.K + CH - 1) / CH;
-    const int rounds = ((chunks + a.wk - 1) / a.wk + D - 1) / D;  // of D chunks a wave, for one group
-    const int units = a.kc / 32 * St::TOKS * 4;                   // 16-byte units of a plane of a stage
+    const int chunks = (a.K + CH - 1) / CH, units = (chunks + 1) / 2;
+    const int rounds = ((units + a.wk - 1) / a.wk + D - 1) / D;  // of D units a wave, for one group
+    const int pieces = a.kc / 32 * St::TOKS * 4;                 // of 16 bytes, of a plane of a stage
 
     // this lane's two 8-byte halves in a block
     const int tok = lane & (TP - 1);
@@ -316,22 +360,22 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
     Rows<G, R> rows(a, group_at(group) * (16 * R), lane);
     const char* codes = reinterpret_cast<const char*>(a.wq) + group_at(group) * (16 * R) * (a.K / 2);
     const char* scales = reinterpret_cast<const char*>(a.scales) + group_at(group) * (16 * R) * (a.K / G) * 2;
-    const auto chunk_at = [&](int round, int i) {
-        const int c = (round * D + i) * a.wk + wk;
-        return c < chunks ? c : chunks - 1;
+    const auto unit_at = [&](int round, int i) {
+        const int u = (round * D + i) * a.wk + wk;
+        return u < units ? u : units - 1;
     };
     Codes<G, R, EVEN> buf[D];
 #pragma unroll
-    for (int i = 0; i < D; ++i) buf[i].load(a, codes, scales, rows, chunk_at(0, i), chunks);
+    for (int i = 0; i < D; ++i) buf[i].load(a, codes, scales, rows, unit_at(0, i), units);
 
     // stage 0
     if constexpr (XD == MOE_X_BF16 && TP == 16) {
-        St{smem, stage_bytes}.fetch(a, t0, 0, wave * 64, NW * 64, units);
+        St{smem, stage_bytes}.fetch(a, t0, 0, wave * 64, NW * 64, pieces);
         __builtin_amdgcn_s_waitcnt(0x0F70);  // all loads are there (the barrier waits for LDS writes alone)
     } else {
         const St st{smem, stage_bytes / PLANES<XD>};
 #pragma unroll 4
-        for (int u = tid; u < units; u += 64 * NW) {
+        for (int u = tid; u < pieces; u += 64 * NW) {
             const v4u* p = reinterpret_cast<const v4u*>(St::source(a, t0, 0, u));
             if constexpr (XD == MOE_X_F32) {
                 const v4u raw[2] = {p[0], p[1]};
@@ -349,10 +393,20 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
     const int64_t turns = (groups + per - 1) / per;
     for (int64_t turn = blockIdx.x; turn < turns; turn += gridDim.x) {
         const int64_t mine = group;
+        // fetched before the chunks: loads come back in order, and at a tile's end this one would wait for all of
+        // the next tile's (and where the compiler sees it pending, so would every round)
+        float bias[R] = {};
+        if (a.bias) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t n = group_at(mine) * (16 * R) + 16 * r + (lane & 15);
+                bias[r] = a.bias[n < a.N ? n : a.N - 1];
+            }
+        }
         for (int round = 0; round < rounds; ++round) {
             const bool last = round + 1 == rounds;
             const bool more = !last || turn + gridDim.x < turns;
-            constexpr int PPT = ALL ? 1 : 256 * NT * D / (64 * NW);  // fp32 units a thread holds
+            constexpr int PPT = ALL ? 1 : 512 * NT * D / (64 * NW);  // fp32 pieces a thread holds
             v4u raw[XD == MOE_X_F32 && !ALL ? PPT : 1][2];
             const int k_next = last ? 0 : (round + 1) * a.kc;
             if constexpr (!ALL) {
@@ -360,7 +414,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
                 char* other = smem + (now ^ 1) * stage_bytes;
                 if (more) {
                     if constexpr (XD == MOE_X_BF16) {
-                        St{other, stage_bytes}.fetch(a, t0, k_next, wave * 64, NW * 64, units);
+                        St{other, stage_bytes}.fetch(a, t0, k_next, wave * 64, NW * 64, pieces);
                     } else {
 #pragma unroll
                         for (int i = 0; i < PPT; ++i) {
@@ -369,7 +423,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
                         }
                         // what several waves a row group need besides (the registers hold one wave's share)
                         const St st{other, stage_bytes / PLANES<XD>};
-                        for (int u = tid + PPT * 64 * NW; u < units; u += 64 * NW) {
+                        for (int u = tid + PPT * 64 * NW; u < pieces; u += 64 * NW) {
                             const v4u* p = reinterpret_cast<const v4u*>(St::source(a, t0, k_next, u));
                             const v4u extra[2] = {p[0], p[1]};
                             st.put(u, extra);
@@ -386,18 +440,20 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
             }
             const int next = last ? 0 : round + 1;
             const char* x = smem + (ALL ? 0 : now * stage_bytes);
-            const int c0 = round * D * a.wk + wk, k0 = ALL ? 0 : round * a.kc;
-            const auto at = [&](int i) { return x + (4 * (c0 + i * a.wk) - k0 / 32) * St::BLOCK; };
+            const int u0 = round * D * a.wk + wk, k0 = ALL ? 0 : round * a.kc;
             const int plane = stage_bytes / PLANES<XD>;
 #pragma unroll
             for (int i = 0; i < D; ++i) {
-                // the load goes out before the product of the chunk it replaces; left to itself the compiler
+                // the load goes out before the product of the unit it replaces; left to itself the compiler
                 // lets it wait for free registers
-                const Chunk<G, R, EVEN> cur(buf[i]);
-                buf[i].load(a, codes, scales, rows, chunk_at(next, i), chunks);
+                const Chunks<G, R, EVEN> cur(buf[i]);
+                buf[i].load(a, codes, scales, rows, unit_at(next, i), units);
                 __builtin_amdgcn_sched_barrier(0);
-                if (c0 + i * a.wk < chunks)
-                    multiply<XD, G, NT, TP, R, EVEN>(cur, at(i) + at0, at(i) + at1, plane, acc);
+                const int c = 2 * (u0 + i * a.wk);
+                const char* at = x + (4 * c - k0 / 32) * St::BLOCK;
+                if (c < chunks) multiply<XD, G, NT, TP, R>(cur.w[0], cur.scale[0], at + at0, at + at1, plane, acc);
+                at += 4 * St::BLOCK;
+                if (c + 1 < chunks) multiply<XD, G, NT, TP, R>(cur.w[1], cur.scale[1], at + at0, at + at1, plane, acc);
             }
             if constexpr (!ALL) {
                 if constexpr (XD == MOE_X_F32) {
@@ -413,7 +469,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
                 now ^= 1;
             }
         }
-        store_tile<NT, R>(a, smem + (ALL ? 1 : 2) * stage_bytes, mine, groups, t0, wk, wave, lane, acc);
+        store_tile<NT, R>(a, smem + (ALL ? 1 : 2) * stage_bytes, mine, groups, t0, wk, wave, lane, bias, acc);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -427,15 +483,15 @@ template <int XD, int G, int NT, int TP, int R, int D, bool ALL, bool EVEN, int 
 int launch(LinArgs a, hipStream_t st) {
     using St = Stage<XD, NT, TP>;
     const auto kern = k_linear_q4<XD, G, NT, TP, R, D, ALL, EVEN, NW>;
-    const int chunks = (a.K + CH - 1) / CH;
+    const int units = (a.K + UNIT - 1) / UNIT;
     // row groups enough for the card go to waves of their own; fewer share
     // their inputs among several waves
     const int64_t groups = ((int64_t)a.N + 16 * R - 1) / (16 * R), tiles = ((int64_t)a.T + 16 * NT - 1) / (16 * NT);
     a.wk = 1;
-    while (a.wk < NW && a.wk * 2 <= chunks && groups * tiles * a.wk < 2048 &&
-           (ALL || 2 * St::bytes(CH * D * a.wk * 2) <= 64 << 10))
+    while (a.wk < NW && a.wk * 2 <= units && groups * tiles * a.wk < 2048 &&
+           (ALL || 2 * St::bytes(UNIT * D * a.wk * 2) <= 64 << 10))
         a.wk *= 2;
-    a.kc = ALL ? chunks * CH : CH * D * a.wk;
+    a.kc = ALL ? (a.K + CH - 1) / CH * CH : UNIT * D * a.wk;
     const size_t lds = (ALL ? 1 : 2) * St::bytes(a.kc) + (a.wk > 1 ? (size_t)NW * R * NT * 1024 : 0);
     if (lds > 64 << 10) {  // asked for once per kernel and device
         static std::atomic<uint64_t> asked{0};
@@ -462,14 +518,15 @@ int pick(const LinArgs& a, hipStream_t st) {
     const int pad = (a.K + CH - 1) / CH * CH;
     // x whole in LDS: as long as two workgroups share a CU, or one of 16 tokens
     const auto whole = [&](size_t bytes, size_t most) { return bytes <= most; };
-    if (a.T == 1 && whole(Stage<XD, 1, 1>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 1, 1, 4, true, EVEN, 8>(a, st);
-    if (a.T <= 4 && whole(Stage<XD, 1, 4>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 4, 1, 4, true, EVEN, 8>(a, st);
-    if (a.T <= 8 && whole(Stage<XD, 1, 8>::bytes(pad), 80 << 10)) return launch<XD, G, 1, 8, 1, 4, true, EVEN, 8>(a, st);
-    if (a.T <= 16 && whole(Stage<XD, 1, 16>::bytes(pad), 128 << 10)) return launch<XD, G, 1, 16, 1, 4, true, EVEN, 8>(a, st);
-    if (a.T <= 16) return launch<XD, G, 1, 16, 1, 2, false, EVEN, 8>(a, st);
-    if (a.T <= 32) return launch<XD, G, 2, 16, 2, 2, false, EVEN, 8>(a, st);
-    if constexpr (XD == MOE_X_F32) return launch<XD, G, 4, 16, 2, 1, false, EVEN, 8>(a, st);
-    else return launch<XD, G, 4, 16, 2, 2, false, EVEN, 8>(a, st);
+    if (a.T == 1 && whole(Stage<XD, 1, 1>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 1, 1, 2, true, EVEN, 8>(a, st);
+    if (a.T <= 4 && whole(Stage<XD, 1, 4>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 4, 1, 2, true, EVEN, 8>(a, st);
+    if (a.T <= 8 && whole(Stage<XD, 1, 8>::bytes(pad), 80 << 10)) return launch<XD, G, 1, 8, 1, 2, true, EVEN, 8>(a, st);
+    if (a.T <= 16 && whole(Stage<XD, 1, 16>::bytes(pad), 128 << 10))
+        return launch<XD, G, 1, 16, 1, 2, true, EVEN, 8>(a, st);
+    if (a.T <= 16) return launch<XD, G, 1, 16, 1, 1, false, EVEN, 8>(a, st);
+    if (a.T <= 32 || XD == MOE_X_F32) return launch<XD, G, 2, 16, 2, 1, false, EVEN, 8>(a, st);
+    if constexpr (XD == MOE_X_BF16) return launch<XD, G, 4, 16, 2, 1, false, EVEN, 8>(a, st);
+    return MOE_OK;
 }
 
 }  // namespace
@@ -505,7 +562,7 @@ extern "C" int moe_linear_q4(const void* x, int x_dtype, int64_t ldx, const void
     a.bias = bias, a.y = y, a.ldy = ldy, a.T = T, a.N = N, a.K = K, a.y_dtype = y_dtype;
     const auto go = [&](auto xd) {
         constexpr int XD = decltype(xd)::value;
-        const bool even = K % CH == 0 && reinterpret_cast<uintptr_t>(scales) % (2 * CH / group) == 0;
+        const bool even = K % UNIT == 0 && reinterpret_cast<uintptr_t>(scales) % (2 * UNIT / group) == 0;
         const auto by_group = [&](auto g) {
             constexpr int G = decltype(g)::value;
             return even ? pick<XD, G, true>(a, stream) : pick<XD, G, false>(a, stream);
