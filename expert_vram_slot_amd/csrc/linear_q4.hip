@@ -56,15 +56,17 @@ struct LinArgs {
     int kc;  // inputs staged at a time
 };
 
-// Eight codes of a dword (low nibbles, then high) as bf16.
-__device__ __forceinline__ bf16x8 codes_bf16(uint32_t d) {
-    const uint32_t lo = d & 0x0F0F0F0Fu, hi = (d >> 4) & 0x0F0F0F0Fu;
+// Eight codes in bytes as bf16.
+__device__ __forceinline__ bf16x8 bytes_bf16(uint32_t lo, uint32_t hi) {
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
     const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
     const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
     const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
 }
+
+// Eight codes of a dword (low nibbles, then high) as bf16.
+__device__ __forceinline__ bf16x8 codes_bf16(uint32_t d) { return bytes_bf16(d & 0x0F0F0F0Fu, (d >> 4) & 0x0F0F0F0Fu); }
 
 // Register i of quarter q <-> register q of quarter i.
 __device__ __forceinline__ v4u transpose4(v4u w) {
@@ -161,28 +163,18 @@ struct Rows {
     }
 };
 
-// One unit of codes and its scales, as loaded.  EVEN: K is whole units and the
-// scales of a row's unit are one aligned load.  Otherwise a chunk's scales are
-// a load that starts on any scale, ends with the matrix at the latest, and what
-// lies past the row's end becomes the scale 0.
+// The scales of a wave's rows for one unit, as loaded.  EVEN: K is whole units
+// and the scales of a row's unit are one aligned load.  Otherwise a chunk's
+// scales are a load that starts on any scale, ends with the matrix at the
+// latest, and what lies past the row's end becomes the scale 0.
 template <int G, int R, bool EVEN>
-struct Codes {
+struct Scales {
     static constexpr int NS = CH / G;  // scales of a row in a chunk
     using S = std::conditional_t<NS == 4, uint64_t, std::conditional_t<NS == 2, uint32_t, uint16_t>>;
     typedef S Loose __attribute__((aligned(2)));
-    v4u w[R][2];
     S s[R][2];
 
-    // u: unit, at most the last one (the same in the wave)
-    __device__ __forceinline__ void load(const LinArgs& a, const char* codes, const char* scales, const Rows<G, R>& rows,
-                                         int u, int units) {
-        const char* cp = codes + (int64_t)u * (UNIT / 2);
-        const bool whole = EVEN || u + 1 < units || a.K % UNIT == 0;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[r][h] = *reinterpret_cast<const v4u*>(cp + (whole ? rows.code[r][h] : rows.code_end[r][h]));
+    __device__ __forceinline__ void load(const LinArgs& a, const char* scales, const Rows<G, R>& rows, int u) {
         const char* sp = scales + (int64_t)u * (4 * NS);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -217,36 +209,67 @@ struct Codes {
             }
         }
     }
+    // as fp32, here and now: kept as they were loaded, or folded into a later
+    // step, they stay in the load's registers and the next load waits
+    __device__ __forceinline__ void take(float (&out)[2][R][NS]) const {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    out[h][r][i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(s[r][h] >> (16 * i)));
+                    asm volatile("" : "+v"(out[h][r][i]));
+                }
+    }
+};
+
+// One unit of codes and its scales, as loaded.
+template <int G, int R, bool EVEN>
+struct Codes {
+    v4u w[R][2];
+    Scales<G, R, EVEN> s;
+
+    // u: unit, at most the last one (the same in the wave)
+    __device__ __forceinline__ void load(const LinArgs& a, const char* codes, const char* scales, const Rows<G, R>& rows,
+                                         int u, int units) {
+        const char* cp = codes + (int64_t)u * (UNIT / 2);
+        const bool whole = EVEN || u + 1 < units || a.K % UNIT == 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w[r][h] = *reinterpret_cast<const v4u*>(cp + (whole ? rows.code[r][h] : rows.code_end[r][h]));
+        s.load(a, scales, rows, u);
+    }
 };
 
 // Takes a unit's two chunks out of their buffer (which is free for the next
-// load from then on) into the order the product wants, the scales as fp32: kept
-// as they were loaded, they stay in the load's registers and the next load
-// waits.
+// load from then on) into the order the product wants.
 template <int G, int R, bool EVEN>
 struct Chunks {
-    static constexpr int NS = CH / G;
     v4u w[2][R];
-    float scale[2][R][NS];
+    float scale[2][R][CH / G];
     __device__ __forceinline__ explicit Chunks(const Codes<G, R, EVEN>& c) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             v4u lo = c.w[r][0], hi = c.w[r][1];
             exchange8(lo, hi);
             w[0][r] = transpose4(lo), w[1][r] = transpose4(hi);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    scale[h][r][i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(c.s[r][h] >> (16 * i)));
-                    asm volatile("" : "+v"(scale[h][r][i]));  // here and now, not folded into the product's last step
-                }
         }
+        c.s.take(scale);
     }
 };
 
-// One chunk: R row tiles against the NT token tiles.  at0, at1: this lane's two
-// halves of its inputs of the chunk's first block, token tile 0.
+// Values of a lane's column of a product that are tokens: all four, one of a
+// single token.
+template <int NT, int TP>
+constexpr int TOK4 = NT == 1 && TP == 1 ? 1 : 4;
+
+// One chunk: R row tiles against the NT token tiles, token tile by token tile,
+// so that R + 1 products at a time depend on nothing but their own sums.  at0,
+// at1: this lane's two halves of its inputs of the chunk's first block, token
+// tile 0.
 template <int XD, int G, int NT, int TP, int R>
 __device__ __forceinline__ void multiply(const v4u (&w)[R], const float (&scale)[R][CH / G], const char* at0,
                                          const char* at1, int plane, v4f (&acc)[R][NT]) {
@@ -254,14 +277,17 @@ __device__ __forceinline__ void multiply(const v4u (&w)[R], const float (&scale)
     constexpr uint32_t M8 = 0xC100C100u;  // bf16 -8 twice
     const bf16x8 minus8 = __builtin_bit_cast(bf16x8, v4u{M8, M8, M8, M8});
     constexpr int BG = G / 32;  // blocks of a group
-    v4f d[R][NT], eight[NT];
+    constexpr bool AS_C = BG == 1 && PLANES<XD> == 1;  // the correction goes in as the product's C
+    bf16x8 b[4][R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        bf16x8 b[R];
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int r = 0; r < R; ++r) b[r] = codes_bf16(w[r][i]);
+        for (int r = 0; r < R; ++r) b[i][r] = codes_bf16(w[r][i]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt) {
+        v4f d[R], eight;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int p = 0; p < PLANES<XD>; ++p) {
                 const int off = i * St::BLOCK + nt * 1024;
@@ -269,31 +295,45 @@ __device__ __forceinline__ void multiply(const v4u (&w)[R], const float (&scale)
                 const v2u hi = *reinterpret_cast<const v2u*>(at1 + p * plane + off);
                 const bf16x8 x = __builtin_bit_cast(bf16x8, v4u{lo[0], lo[1], hi[0], hi[1]});
                 const bool first = i % BG == 0 && p == 0;
-                eight[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, minus8, first ? v4f{} : eight[nt], 0, 0, 0);
+                eight = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, minus8, first ? v4f{} : eight, 0, 0, 0);
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    // groups of one block: the correction goes in as the product's C
-                    const v4f c = BG == 1 && PLANES<XD> == 1 ? eight[nt] : first ? v4f{} : d[r][nt];
-                    d[r][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, b[r], c, 0, 0, 0);
-                }
+                for (int r = 0; r < R; ++r)
+                    d[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, b[i][r], AS_C ? eight : first ? v4f{} : d[r], 0, 0, 0);
             }
             if (i % BG == BG - 1) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float s = scale[r][i / BG];
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float v = BG == 1 && PLANES<XD> == 1 ? d[r][nt][e] : d[r][nt][e] + eight[nt][e];
-                        acc[r][nt][e] = fmaf(s, v, acc[r][nt][e]);
-                    }
-                }
+                    for (int e = 0; e < TOK4<NT, TP>; ++e)
+                        acc[r][nt][e] = fmaf(scale[r][i / BG], AS_C ? d[r][e] : d[r][e] + eight[e], acc[r][nt][e]);
             }
         }
     }
 }
 
+// Stores the rows n0 .. n0 + 16 R - 1 of y, as far as they exist.
+template <int NT, int R>
+__device__ __forceinline__ void store_rows(const LinArgs& a, int64_t n0, int64_t t0, int lane, const float (&bias)[R],
+                                           const v4f (&acc)[R][NT]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t n = n0 + 16 * r + (lane & 15);
+        if (n >= a.N) continue;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t t = t0 + 16 * nt + 4 * (lane >> 4) + e;
+                if (t >= a.T) continue;
+                const float v = acc[r][nt][e] + bias[r];
+                if (a.y_dtype == MOE_X_F32) reinterpret_cast<float*>(a.y)[t * a.ldy + n] = v;
+                else reinterpret_cast<__bf16*>(a.y)[t * a.ldy + n] = (__bf16)v;
+            }
+    }
+}
+
 // Adds up the waves of a row group (in wave order, through `part` in LDS) and
-// stores its rows of y.
+// stores its rows.
 template <int NT, int R>
 __device__ __forceinline__ void store_tile(const LinArgs& a, char* part_, int64_t group, int64_t groups, int64_t t0,
                                            int wk, int wave, int lane, const float (&bias)[R], v4f (&acc)[R][NT]) {
@@ -316,21 +356,7 @@ __device__ __forceinline__ void store_tile(const LinArgs& a, char* part_, int64_
         __syncthreads();
     }
     if (wk > 0 || group >= groups) return;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t n = group * (16 * R) + 16 * r + (lane & 15);
-        if (n >= a.N) continue;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t t = t0 + 16 * nt + 4 * (lane >> 4) + e;
-                if (t >= a.T) continue;
-                const float v = acc[r][nt][e] + bias[r];
-                if (a.y_dtype == MOE_X_F32) reinterpret_cast<float*>(a.y)[t * a.ldy + n] = v;
-                else reinterpret_cast<__bf16*>(a.y)[t * a.ldy + n] = (__bf16)v;
-            }
-    }
+    store_rows<NT, R>(a, group * (16 * R), t0, lane, bias, acc);
 }
 
 // NW waves.  A wave takes R row tiles of 16 rows (NW / wk such groups a workgroup)
@@ -477,7 +503,223 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
     }
 }
 
+// Many tokens of bf16: a workgroup of NW waves takes NT token tiles against
+// NW * R row tiles, a unit of 256 inputs at a time in two buffers, codes and x
+// both brought into LDS by direct loads, which take no registers while they are
+// on their way.
+//  - Codes: each wave's own R * 16 rows of 128 bytes, the 16-byte pieces of row i
+//    turned (xor) by i / 2 % 8; x: rows of 512 bytes, the pieces of token t turned
+//    by t % 16.  A load instruction takes whole lines, and the lanes of a read lie
+//    in different banks.
+//  - A quarter q of the wave supplies inputs 8 q .. 8 q + 7 of a block: one
+//    16-byte read of x, and the low (q < 2) or high nibbles of the block's bytes
+//    8 (q % 2) ..
+//  - The corrections -8 * (sum of x over a group) are computed once per workgroup:
+//    each wave one (chunk, token tile) of the unit, and go into the products as
+//    their C.
+template <int G, int NT, int R, bool EVEN, int NW>
+struct Tile {
+    static constexpr int ROWS = NW * R * 16;
+    static constexpr int CODES = ROWS * (UNIT / 2), X = NT * 16 * UNIT * 2, STAGE = CODES + X;
+    static constexpr int NS = CH / G;
+    static constexpr int CORR = 2 * NS * NT * 16 * 4;
+    static constexpr size_t LDS = 2 * STAGE + CORR;
+    static_assert(2 * NT <= NW, "one (chunk, token tile) a wave");
+};
+
+template <int G, int NT, int R, bool EVEN, int NW>
+__global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
+    using Ti = Tile<G, NT, R, EVEN, NW>;
+    constexpr int NS = Ti::NS, BG = G / 32;
+    typedef __attribute__((address_space(1))) const void* gptr;
+    typedef __attribute__((address_space(3))) void* lptr;
+    extern __shared__ __align__(16) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
+    const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
+    const int64_t tiles = ((int64_t)a.N + Ti::ROWS - 1) / Ti::ROWS;
+    const int units = (a.K + UNIT - 1) / UNIT;
+    const int64_t wrow = (int64_t)wave * (R * 16);  // of the tile
+    // rows from N on read the last row, in whatever wave they are
+    const auto first_row = [&](int64_t tile) {
+        const int64_t n = tile * Ti::ROWS + wrow;
+        return n < a.N ? n : (int64_t)a.N - 1;
+    };
+    // What this lane brings: pieces of the wave's rows of codes (offsets from the first row's start, those of the
+    // row's last unit besides) and of tokens (addresses of their starts, pieces).
+    constexpr int XJ = NT * 8 / NW;
+    uint32_t code[2 * R], code_end[2 * R];
+    const auto code_rows = [&](int64_t n0) {
+        const int nb = a.K >> 5, end = (nb - 1) % 8;
+#pragma unroll
+        for (int j = 0; j < 2 * R; ++j) {
+            const int i = 8 * j + (lane >> 3), piece = (lane & 7) ^ ((i >> 1) & 7);
+            const uint32_t at = (uint32_t)(n0 + i < a.N ? i : (int)(a.N - 1 - n0)) * nb * 16;
+            code[j] = at + 16 * piece, code_end[j] = at + 16 * (piece < end ? piece : end);
+        }
+    };
+    const char* xrow[XJ];
+    int xk[XJ];
+#pragma unroll
+    for (int j = 0; j < XJ; ++j) {
+        const int tok = (wave * XJ + j) * 2 + (lane >> 5);
+        xrow[j] = reinterpret_cast<const char*>(a.x) + (t0 + tok < a.T ? t0 + tok : a.T - 1) * a.ldx * 2;
+        xk[j] = 16 * ((lane & 31) ^ (tok & 15));
+    }
+    // brings unit u of the rows from n0 on into buffer b
+    const auto fetch = [&](int64_t n0, int u, int b) {
+        const bool whole = EVEN || u + 1 < units || a.K % UNIT == 0;
+        const char* from = reinterpret_cast<const char*>(a.wq) + n0 * (a.K / 2) + (int64_t)u * (UNIT / 2);
+        char* to = smem + b * Ti::STAGE + wave * (R * 16 * 128);
+#pragma unroll
+        for (int j = 0; j < 2 * R; ++j)
+            __builtin_amdgcn_global_load_lds((gptr)(from + (whole ? code[j] : code_end[j])), (lptr)(to + j * 1024), 16, 0, 0);
+        char* xs = smem + b * Ti::STAGE + Ti::CODES + wave * (XJ * 1024);
+#pragma unroll
+        for (int j = 0; j < XJ; ++j) {
+            int k = xk[j] + u * (UNIT * 2);
+            if (!whole && k >= 2 * a.K) k = 2 * a.K - 16;
+            __builtin_amdgcn_global_load_lds((gptr)(xrow[j] + k), (lptr)(xs + j * 1024), 16, 0, 0);
+        }
+    };
+
+    // this lane's reads: code piece and x piece of a chunk's first block (the others are an xor away)
+    const int row16 = lane & 15;
+    const int code_at = wave * (R * 16 * 128) + row16 * 128 + (((row16 >> 1) & 7) * 16) + (q & 1) * 8;
+    const int x_at = Ti::CODES + row16 * 512 + ((q ^ row16) * 16);
+    const int shift = (q >> 1) * 4;
+    float* corr = reinterpret_cast<float*>(smem + 2 * Ti::STAGE);
+    constexpr uint32_t M8 = 0xC100C100u;  // bf16 -8 twice
+    const bf16x8 minus8 = __builtin_bit_cast(bf16x8, v4u{M8, M8, M8, M8});
+
+    int64_t tile = blockIdx.x;
+    Rows<G, R> rows(a, first_row(tile), lane);
+    const char* scales = reinterpret_cast<const char*>(a.scales) + first_row(tile) * (a.K / G) * 2;
+    Scales<G, R, EVEN> loaded;
+    loaded.load(a, scales, rows, 0);
+    code_rows(first_row(tile));
+    fetch(first_row(tile), 0, 0);
+    int now = 0;
+    for (; tile < tiles; tile += gridDim.x) {
+        float bias[R] = {};
+        const int64_t n0 = tile * Ti::ROWS + wrow;
+        if (a.bias) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t n = n0 + 16 * r + row16;
+                bias[r] = a.bias[n < a.N ? n : (int64_t)a.N - 1];
+            }
+        }
+        v4f acc[R][NT] = {};
+        int u = 0;
+        do {
+            __builtin_amdgcn_s_waitcnt(0x0F70);  // the unit is there
+            __syncthreads();                     // of every wave, and nobody reads the other buffer any more
+            float scale[2][R][NS];
+            loaded.take(scale);
+            const bool last = u + 1 == units;
+            if (!last || tile + gridDim.x < tiles) {
+                const int64_t next = first_row(last ? tile + gridDim.x : tile);
+                if (last) {
+                    rows = Rows<G, R>(a, next, lane);
+                    scales = reinterpret_cast<const char*>(a.scales) + next * (a.K / G) * 2;
+                    code_rows(next);
+                }
+                loaded.load(a, scales, rows, last ? 0 : u + 1);
+                fetch(next, last ? 0 : u + 1, now ^ 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const char* stage = smem + now * Ti::STAGE;
+            // A step is a chunk's token tile: its reads go out a step ahead.
+            const auto x_of = [&](int step, bf16x8(&x)[4]) {
+                const int h = step / NT, nt = step % NT;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = *reinterpret_cast<const bf16x8*>(stage + (x_at ^ (i * 64)) + nt * 8192 + h * 256);
+            };
+            const auto corr_of = [&](int step, v4f(&c)[NS]) {
+                const int h = step / NT, nt = step % NT;
+#pragma unroll
+                for (int g = 0; g < NS; ++g)
+                    c[g] = *reinterpret_cast<const v4f*>(corr + ((h * NS + g) * NT + nt) * 16 + 4 * q);
+            };
+            const auto codes_of = [&](int h, v2u(&w)[4][R]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        w[i][r] = *reinterpret_cast<const v2u*>(stage + (code_at ^ ((4 * h + i) * 16)) + r * 2048);
+            };
+            bf16x8 x[2][4];
+            v4f c[2][NS];
+            v2u w[4][R];
+            codes_of(0, w);
+            if (wave < 2 * NT) {
+                bf16x8 mine[4];
+                x_of(wave, mine);
+                v4f sum[NS];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum[i / BG] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mine[i], minus8, i % BG ? sum[i / BG] : v4f{}, 0, 0, 0);
+                if (row16 == 0) {
+#pragma unroll
+                    for (int g = 0; g < NS; ++g)
+                        *reinterpret_cast<v4f*>(corr + ((wave / NT * NS + g) * NT + wave % NT) * 16 + 4 * q) = sum[g];
+                }
+            }
+            x_of(0, x[0]);
+            bf16x8 b[4][R];
+            // the corrections are there (__syncthreads would wait for the next unit too)
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            corr_of(0, c[0]);
+#pragma unroll
+            for (int step = 0; step < 2 * NT; ++step) {
+                const int h = step / NT, nt = step % NT;
+                if (nt == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            b[i][r] = bytes_bf16((w[i][r][0] >> shift) & 0x0F0F0F0Fu, (w[i][r][1] >> shift) & 0x0F0F0F0Fu);
+                    if (h == 0) codes_of(1, w);
+                }
+                if (step + 1 < 2 * NT) x_of(step + 1, x[(step + 1) & 1]), corr_of(step + 1, c[(step + 1) & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                v4f d[R];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        d[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[step & 1][i], b[i][r],
+                                                                      i % BG == 0 ? c[step & 1][i / BG] : d[r], 0, 0, 0);
+                    if (i % BG == BG - 1) {
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[r][nt][e] = fmaf(scale[h][r][i / BG], d[r][e], acc[r][nt][e]);
+                    }
+                }
+            }
+            now ^= 1;
+        } while (++u < units);
+        store_rows<NT, R>(a, n0, t0, lane, bias, acc);
+    }
+}
+
 constexpr size_t LDS_MAX = 160 << 10;
+
+// More than 64 KB of LDS for `kern` is asked for once per kernel (`asked`: its
+// devices) and device.
+int ask_lds(const void* kern, size_t lds, std::atomic<uint64_t>& asked) {
+    if (lds <= 64 << 10) return moe_ok();
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess && !(dev < 64 && (asked.load() >> dev & 1))) {
+        e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)LDS_MAX);
+        if (e == hipSuccess && dev < 64) asked.fetch_or((uint64_t)1 << dev);
+    }
+    if (e != hipSuccess) return moe_fail(MOE_E_HIP, "moe_linear_q4: %zu bytes of LDS: %s", lds, hipGetErrorString(e));
+    return moe_ok();
+}
 
 template <int XD, int G, int NT, int TP, int R, int D, bool ALL, bool EVEN, int NW>
 int launch(LinArgs a, hipStream_t st) {
@@ -489,27 +731,34 @@ int launch(LinArgs a, hipStream_t st) {
     const int64_t groups = ((int64_t)a.N + 16 * R - 1) / (16 * R), tiles = ((int64_t)a.T + 16 * NT - 1) / (16 * NT);
     a.wk = 1;
     while (a.wk < NW && a.wk * 2 <= units && groups * tiles * a.wk < 2048 &&
-           (ALL || 2 * St::bytes(UNIT * D * a.wk * 2) <= 64 << 10))
+           (ALL || 2 * St::bytes(UNIT * D * a.wk * 2) + (size_t)NW * R * NT * 1024 <= LDS_MAX))
         a.wk *= 2;
     a.kc = ALL ? (a.K + CH - 1) / CH * CH : UNIT * D * a.wk;
     const size_t lds = (ALL ? 1 : 2) * St::bytes(a.kc) + (a.wk > 1 ? (size_t)NW * R * NT * 1024 : 0);
-    if (lds > 64 << 10) {  // asked for once per kernel and device
-        static std::atomic<uint64_t> asked{0};
-        int dev = 0;
-        hipError_t e = hipGetDevice(&dev);
-        if (e == hipSuccess && !(dev < 64 && (asked.load() >> dev & 1))) {
-            e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)LDS_MAX);
-            if (e == hipSuccess && dev < 64) asked.fetch_or((uint64_t)1 << dev);
-        }
-        if (e != hipSuccess) return moe_fail(MOE_E_HIP, "moe_linear_q4: %zu bytes of LDS: %s", lds, hipGetErrorString(e));
-    }
+    static std::atomic<uint64_t> asked{0};
+    const int rc = ask_lds(reinterpret_cast<const void*>(kern), lds, asked);
+    if (rc != MOE_OK) return rc;
     // with x staged once, workgroups stay: as many as the card holds at a time
     const int per = NW / a.wk;
     int64_t blocks = (groups + per - 1) / per;
     const int64_t most = 256 * (lds > 80 << 10 ? 1 : 2);
     if (blocks * tiles > most) blocks = tiles >= most ? 1 : most / tiles;
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks, (unsigned)tiles), dim3(64 * NW), lds, st, a);
+    return moe_check_launch("moe_linear_q4");
+}
+
+template <int G, int NT, bool EVEN>
+int launch_tile(const LinArgs& a, hipStream_t st) {
+    using Ti = Tile<G, NT, 2, EVEN, 8>;
+    static_assert(Ti::LDS <= LDS_MAX, "LDS");
+    const auto kern = k_linear_q4_tile<G, NT, 2, EVEN, 8>;
+    static std::atomic<uint64_t> asked{0};
+    const int rc = ask_lds(reinterpret_cast<const void*>(kern), Ti::LDS, asked);
+    if (rc != MOE_OK) return rc;
+    const int64_t tiles = ((int64_t)a.T + 16 * NT - 1) / (16 * NT);
+    int64_t blocks = ((int64_t)a.N + Ti::ROWS - 1) / Ti::ROWS;
+    if (blocks * tiles > 256) blocks = tiles >= 256 ? 1 : 256 / tiles;
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks, (unsigned)tiles), dim3(512), Ti::LDS, st, a);
     return moe_check_launch("moe_linear_q4");
 }
 
@@ -521,12 +770,16 @@ int pick(const LinArgs& a, hipStream_t st) {
     if (a.T == 1 && whole(Stage<XD, 1, 1>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 1, 1, 2, true, EVEN, 8>(a, st);
     if (a.T <= 4 && whole(Stage<XD, 1, 4>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 4, 1, 2, true, EVEN, 8>(a, st);
     if (a.T <= 8 && whole(Stage<XD, 1, 8>::bytes(pad), 80 << 10)) return launch<XD, G, 1, 8, 1, 2, true, EVEN, 8>(a, st);
-    if (a.T <= 16 && whole(Stage<XD, 1, 16>::bytes(pad), 128 << 10))
-        return launch<XD, G, 1, 16, 1, 2, true, EVEN, 8>(a, st);
-    if (a.T <= 16) return launch<XD, G, 1, 16, 1, 1, false, EVEN, 8>(a, st);
-    if (a.T <= 32 || XD == MOE_X_F32) return launch<XD, G, 2, 16, 2, 1, false, EVEN, 8>(a, st);
-    if constexpr (XD == MOE_X_BF16) return launch<XD, G, 4, 16, 2, 1, false, EVEN, 8>(a, st);
-    return MOE_OK;
+    // more tokens: tiles of 64 tokens by 256 rows a workgroup, or 32 by 256, where those give half the CUs work;
+    // else 16 by 16 a wave, the codes read again for each 16 tokens
+    if (a.T > 16) {
+        const int64_t big = ((int64_t)a.N + 255) / 256 * ((a.T + 63) / 64), mid = ((int64_t)a.N + 255) / 256 * ((a.T + 31) / 32);
+        if constexpr (XD == MOE_X_BF16)
+            if (a.T > 32 && big >= 128) return launch_tile<G, 4, EVEN>(a, st);
+        if (mid >= 128) return launch<XD, G, 2, 16, 2, 1, false, EVEN, 8>(a, st);
+    }
+    if (whole(Stage<XD, 1, 16>::bytes(pad), 128 << 10)) return launch<XD, G, 1, 16, 1, 2, true, EVEN, 8>(a, st);
+    return launch<XD, G, 1, 16, 1, 1, false, EVEN, 8>(a, st);
 }
 
 }  // namespace

@@ -72,7 +72,12 @@ def weights(N, K, group, seed, power_of_two=False):
 SHAPES = [(1, 1, 32, 32), (1, 3, 96, 32), (2, 16, 128, 128), (3, 17, 64, 64), (4, 63, 160, 32), (5, 257, 1056, 32),
           (8, 33, 192, 64), (15, 100, 256, 128), (16, 64, 512, 64), (17, 65, 1088, 64), (31, 130, 384, 128),
           (33, 48, 2048, 32), (64, 300, 640, 128), (65, 129, 128, 32), (130, 31, 1536, 64), (1, 2048, 2048, 32),
-          (300, 70, 256, 32), (7, 1, 8192, 128), (1, 5000, 4096, 128)]
+          (300, 70, 256, 32), (7, 1, 8192, 128), (1, 5000, 4096, 128),
+          # many rows by many tokens, in whole tiles and past them
+          (40, 32769, 128, 32), (64, 33000, 384, 128), (65, 16400, 160, 32), (130, 11000, 448, 64), (33, 32800, 1088, 64),
+          (20, 32777, 192, 64), (300, 7000, 96, 32), (64, 80000, 320, 32),
+          # rows of x too long to lie in LDS whole
+          (16, 64, 8192, 128), (13, 40, 8224, 32), (40, 100, 8256, 64)]
 
 
 @pytest.mark.parametrize("xt", ["bf16", "f32"])
@@ -122,6 +127,16 @@ def test_linear_random(m, T, N, K, group, xt, yt):
     # sqrt(34) * 2.6 * 2^-24 = 9e-7 relative, and the blocks' sums add sqrt(K / 32) * 2^-24 at most (K = 8192: 1e-6)
     if yt == "f32" and want.size >= 1000:
         assert np.linalg.norm(got - want) <= 2e-6 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("T,N,K,group", [(1, 37, 512, 128), (8, 100, 1024, 64), (16, 64, 512, 32), (64, 32800, 256, 128)])
+def test_linear_scales_aligned_to_their_elements_alone(m, T, N, K, group):
+    wq, scales, g = weights(N, K, group, T + N, True)
+    x = torch.randint(-2, 3, (T, K), device="cuda", generator=g).bfloat16()
+    moved = torch.empty(scales.numel() + 1, dtype=torch.float16, device="cuda")[1:].view_as(scales)
+    moved.copy_(scales)
+    assert moved.data_ptr() % 4 == 2
+    assert torch.equal(linear(m, x, wq, moved, group, None, "f32"), linear(m, x, wq, scales, group, None, "f32"))
 
 
 def test_linear_bits_do_not_depend_on_other_tokens(m):
