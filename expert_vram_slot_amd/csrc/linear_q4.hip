@@ -565,20 +565,23 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
         xrow[j] = reinterpret_cast<const char*>(a.x) + (t0 + tok < a.T ? t0 + tok : a.T - 1) * a.ldx * 2;
         xk[j] = 16 * ((lane & 31) ^ (tok & 15));
     }
-    // brings unit u of the rows from n0 on into buffer b
-    const auto fetch = [&](int64_t n0, int u, int b) {
-        const bool whole = EVEN || u + 1 < units || a.K % UNIT == 0;
+    // bring unit u of the rows from n0 on, of x into buffer b
+    const auto whole = [&](int u) { return EVEN || u + 1 < units || a.K % UNIT == 0; };
+    const auto fetch_codes = [&](int64_t n0, int u, int b, uint32_t mask) {
         const char* from = reinterpret_cast<const char*>(a.wq) + n0 * (a.K / 2) + (int64_t)u * (UNIT / 2);
         char* to = smem + b * Ti::STAGE + wave * (R * 16 * 128);
 #pragma unroll
         for (int j = 0; j < 2 * R; ++j)
-            __builtin_amdgcn_global_load_lds((gptr)(from + (whole ? code[j] : code_end[j])), (lptr)(to + j * 1024), 16, 0, 0);
-        char* xs = smem + b * Ti::STAGE + Ti::CODES + wave * (XJ * 1024);
+            __builtin_amdgcn_global_load_lds((gptr)(from + ((whole(u) ? code[j] : code_end[j]) & mask)),
+                                             (lptr)(to + j * 1024), 16, 0, 0);
+    };
+    const auto fetch_x = [&](int u, int b) {
+        char* to = smem + b * Ti::STAGE + Ti::CODES + wave * (XJ * 1024);
 #pragma unroll
         for (int j = 0; j < XJ; ++j) {
             int k = xk[j] + u * (UNIT * 2);
-            if (!whole && k >= 2 * a.K) k = 2 * a.K - 16;
-            __builtin_amdgcn_global_load_lds((gptr)(xrow[j] + k), (lptr)(xs + j * 1024), 16, 0, 0);
+            if (!whole(u) && k >= 2 * a.K) k = 2 * a.K - 16;
+            __builtin_amdgcn_global_load_lds((gptr)(xrow[j] + k), (lptr)(to + j * 1024), 16, 0, 0);
         }
     };
 
@@ -591,42 +594,61 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
     constexpr uint32_t M8 = 0xC100C100u;  // bf16 -8 twice
     const bf16x8 minus8 = __builtin_bit_cast(bf16x8, v4u{M8, M8, M8, M8});
 
-    int64_t tile = blockIdx.x;
+    // A unit's codes are asked for two units ahead, its scales and x one ahead: behind the last unit too (the codes
+    // then one piece for all lanes), so that the number of loads on their way is known.
+    int64_t tile = blockIdx.x, code_tile = tile;
+    int code_u = 0;
+    const auto ask_codes = [&](int b) {
+        const bool more = code_tile < tiles;
+        const int64_t n0 = first_row(more ? code_tile : 0);
+        if (code_u == 0) code_rows(n0);
+        fetch_codes(n0, code_u, b, more ? ~0u : 0u);
+        if (++code_u == units) code_u = 0, code_tile += gridDim.x;
+    };
     Rows<G, R> rows(a, first_row(tile), lane);
     const char* scales = reinterpret_cast<const char*>(a.scales) + first_row(tile) * (a.K / G) * 2;
     Scales<G, R, EVEN> loaded;
     loaded.load(a, scales, rows, 0);
-    code_rows(first_row(tile));
-    fetch(first_row(tile), 0, 0);
-    int now = 0;
-    for (; tile < tiles; tile += gridDim.x) {
-        float bias[R] = {};
-        const int64_t n0 = tile * Ti::ROWS + wrow;
+    // (asked for with the scales, before the tile: with loads of the next unit behind it alone, each store would wait
+    // for those)
+    float next_bias[R] = {};
+    const auto ask_bias = [&](int64_t t) {
         if (a.bias) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int64_t n = n0 + 16 * r + row16;
-                bias[r] = a.bias[n < a.N ? n : (int64_t)a.N - 1];
+                const int64_t n = t * Ti::ROWS + wrow + 16 * r + row16;
+                next_bias[r] = a.bias[n < a.N ? n : (int64_t)a.N - 1];
             }
         }
+    };
+    ask_bias(tile);
+    ask_codes(0);
+    fetch_x(0, 0);
+    ask_codes(1);
+    int now = 0;
+    for (; tile < tiles; tile += gridDim.x) {
+        const int64_t n0 = tile * Ti::ROWS + wrow;
+        float bias[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) bias[r] = next_bias[r];
         v4f acc[R][NT] = {};
         int u = 0;
         do {
-            __builtin_amdgcn_s_waitcnt(0x0F70);  // the unit is there
-            __syncthreads();                     // of every wave, and nobody reads the other buffer any more
+            // the unit is there: all but the 2 R loads of the next one's codes
+            __builtin_amdgcn_s_waitcnt(0x0F70 | 2 * R);
+            // of every wave, and nobody reads the other buffer of x any more (__syncthreads would wait for all loads)
+            asm volatile("s_barrier" ::: "memory");
             float scale[2][R][NS];
             loaded.take(scale);
             const bool last = u + 1 == units;
-            if (!last || tile + gridDim.x < tiles) {
-                const int64_t next = first_row(last ? tile + gridDim.x : tile);
-                if (last) {
-                    rows = Rows<G, R>(a, next, lane);
-                    scales = reinterpret_cast<const char*>(a.scales) + next * (a.K / G) * 2;
-                    code_rows(next);
-                }
-                loaded.load(a, scales, rows, last ? 0 : u + 1);
-                fetch(next, last ? 0 : u + 1, now ^ 1);
+            if (last) {
+                const int64_t to = tile + gridDim.x < tiles ? tile + gridDim.x : tile, next = first_row(to);
+                ask_bias(to);
+                rows = Rows<G, R>(a, next, lane);
+                scales = reinterpret_cast<const char*>(a.scales) + next * (a.K / G) * 2;
             }
+            loaded.load(a, scales, rows, last ? 0 : u + 1);
+            fetch_x(last ? 0 : u + 1, now ^ 1);
             __builtin_amdgcn_sched_barrier(0);
             const char* stage = smem + now * Ti::STAGE;
             // A step is a chunk's token tile: its reads go out a step ahead.
@@ -651,8 +673,9 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
             };
             bf16x8 x[2][4];
             v4f c[2][NS];
-            v2u w[4][R];
-            codes_of(0, w);
+            v2u w[2][4][R];
+            codes_of(0, w[0]);
+            codes_of(1, w[1]);
             if (wave < 2 * NT) {
                 bf16x8 mine[4];
                 x_of(wave, mine);
@@ -668,8 +691,10 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
             }
             x_of(0, x[0]);
             bf16x8 b[4][R];
-            // the corrections are there (__syncthreads would wait for the next unit too)
+            // the corrections are there, the codes out of their buffer
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            ask_codes(now);
+            __builtin_amdgcn_sched_barrier(0);
             corr_of(0, c[0]);
 #pragma unroll
             for (int step = 0; step < 2 * NT; ++step) {
@@ -679,8 +704,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int r = 0; r < R; ++r)
-                            b[i][r] = bytes_bf16((w[i][r][0] >> shift) & 0x0F0F0F0Fu, (w[i][r][1] >> shift) & 0x0F0F0F0Fu);
-                    if (h == 0) codes_of(1, w);
+                            b[i][r] = bytes_bf16((w[h][i][r][0] >> shift) & 0x0F0F0F0Fu, (w[h][i][r][1] >> shift) & 0x0F0F0F0Fu);
                 }
                 if (step + 1 < 2 * NT) x_of(step + 1, x[(step + 1) & 1]), corr_of(step + 1, c[(step + 1) & 1]);
                 __builtin_amdgcn_sched_barrier(0);
@@ -703,6 +727,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
         } while (++u < units);
         store_rows<NT, R>(a, n0, t0, lane, bias, acc);
     }
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // nothing may come into LDS after the workgroup's end
 }
 
 constexpr size_t LDS_MAX = 160 << 10;
