@@ -312,24 +312,27 @@ __device__ __forceinline__ void multiply(const v4u (&w)[R], const float (&scale)
 }
 
 // Stores the rows n0 .. n0 + 16 R - 1 of y, as far as they exist.
+template <typename Y, int NT, int R>
+__device__ __forceinline__ void store_as(const LinArgs& a, int64_t n0, int64_t t0, int lane, const float (&bias)[R],
+                                         const v4f (&acc)[R][NT]) {
+    Y* y = reinterpret_cast<Y*>(a.y) + (t0 + 4 * (lane >> 4)) * a.ldy + n0 + (lane & 15);
+    const bool all = t0 + 16 * NT <= a.T && n0 + 16 * R <= a.N;  // no lane has to be looked at
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            Y* row = y + (int64_t)(16 * nt + e) * a.ldy;
+            const bool in_t = t0 + 4 * (lane >> 4) + 16 * nt + e < a.T;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (all || (in_t && n0 + 16 * r + (lane & 15) < a.N)) row[16 * r] = (Y)(acc[r][nt][e] + bias[r]);
+        }
+}
 template <int NT, int R>
 __device__ __forceinline__ void store_rows(const LinArgs& a, int64_t n0, int64_t t0, int lane, const float (&bias)[R],
                                            const v4f (&acc)[R][NT]) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t n = n0 + 16 * r + (lane & 15);
-        if (n >= a.N) continue;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t t = t0 + 16 * nt + 4 * (lane >> 4) + e;
-                if (t >= a.T) continue;
-                const float v = acc[r][nt][e] + bias[r];
-                if (a.y_dtype == MOE_X_F32) reinterpret_cast<float*>(a.y)[t * a.ldy + n] = v;
-                else reinterpret_cast<__bf16*>(a.y)[t * a.ldy + n] = (__bf16)v;
-            }
-    }
+    if (a.y_dtype == MOE_X_F32) store_as<float>(a, n0, t0, lane, bias, acc);
+    else store_as<__bf16>(a, n0, t0, lane, bias, acc);
 }
 
 // Adds up the waves of a row group (in wave order, through `part` in LDS) and
@@ -511,9 +514,8 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
 //    turned (xor) by i / 2 % 8; x: rows of 512 bytes, the pieces of token t turned
 //    by t % 16.  A load instruction takes whole lines, and the lanes of a read lie
 //    in different banks.
-//  - A quarter q of the wave supplies inputs 8 q .. 8 q + 7 of a block: one
-//    16-byte read of x, and the low (q < 2) or high nibbles of the block's bytes
-//    8 (q % 2) ..
+//  - A quarter of the wave supplies eight inputs in a row, 16 bytes of x, against
+//    the low or the high nibbles of 8 bytes of codes.
 //  - The corrections -8 * (sum of x over a group) are computed once per workgroup:
 //    each wave one (chunk, token tile) of the unit, and go into the products as
 //    their C.
@@ -585,10 +587,14 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
         }
     };
 
-    // this lane's reads: code piece and x piece of a chunk's first block (the others are an xor away)
+    // This lane's reads: code piece and x piece of a chunk's first product (the others are an xor away).  Groups of
+    // two blocks and more: a pair of products takes 8 bytes of two blocks, the low and the high nibbles; else a product
+    // takes one block, its quarters the low (q < 2) or the high nibbles.
+    constexpr int CB = BG >= 2 ? 2 : 4;  // code reads of a chunk
     const int row16 = lane & 15;
-    const int code_at = wave * (R * 16 * 128) + row16 * 128 + (((row16 >> 1) & 7) * 16) + (q & 1) * 8;
-    const int x_at = Ti::CODES + row16 * 512 + ((q ^ row16) * 16);
+    const int code_at = wave * (R * 16 * 128) + row16 * 128 + (((CB == 2 ? q >> 1 : 0) ^ ((row16 >> 1) & 7)) * 16) + (q & 1) * 8;
+    const int x_at = Ti::CODES + row16 * 512 + (((CB == 2 ? 4 * (q >> 1) + (q & 1) : q) ^ row16) * 16);
+    const auto x_block = [](int i) { return CB == 2 ? (i >> 1) * 128 + (i & 1) * 32 : i * 64; };
     const int shift = (q >> 1) * 4;
     float* corr = reinterpret_cast<float*>(smem + 2 * Ti::STAGE);
     constexpr uint32_t M8 = 0xC100C100u;  // bf16 -8 twice
@@ -625,6 +631,14 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
     ask_codes(0);
     fetch_x(0, 0);
     ask_codes(1);
+    // Waits for the next unit, all but the 2 R loads of the one behind it: at a unit's end, so that the stores of a tile
+    // go out after the wait and have a unit's time.
+    float scale[2][R][NS];
+    const auto arrive = [&] {
+        __builtin_amdgcn_s_waitcnt(0x0F70 | 2 * R);
+        loaded.take(scale);
+    };
+    arrive();
     int now = 0;
     for (; tile < tiles; tile += gridDim.x) {
         const int64_t n0 = tile * Ti::ROWS + wrow;
@@ -634,12 +648,9 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
         v4f acc[R][NT] = {};
         int u = 0;
         do {
-            // the unit is there: all but the 2 R loads of the next one's codes
-            __builtin_amdgcn_s_waitcnt(0x0F70 | 2 * R);
-            // of every wave, and nobody reads the other buffer of x any more (__syncthreads would wait for all loads)
+            // the unit is there, of every wave, and nobody reads the other buffer of x any more (__syncthreads would
+            // wait for all loads)
             asm volatile("s_barrier" ::: "memory");
-            float scale[2][R][NS];
-            loaded.take(scale);
             const bool last = u + 1 == units;
             if (last) {
                 const int64_t to = tile + gridDim.x < tiles ? tile + gridDim.x : tile, next = first_row(to);
@@ -651,12 +662,13 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
             fetch_x(last ? 0 : u + 1, now ^ 1);
             __builtin_amdgcn_sched_barrier(0);
             const char* stage = smem + now * Ti::STAGE;
-            // A step is a chunk's token tile: its reads go out a step ahead.
+            // A step is a chunk's token tile.  Its reads go out a step ahead, and what it adds up, and the second
+            // chunk's codes as bf16, lie between the products.
             const auto x_of = [&](int step, bf16x8(&x)[4]) {
                 const int h = step / NT, nt = step % NT;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    x[i] = *reinterpret_cast<const bf16x8*>(stage + (x_at ^ (i * 64)) + nt * 8192 + h * 256);
+                    x[i] = *reinterpret_cast<const bf16x8*>(stage + (x_at ^ x_block(i)) + nt * 8192 + h * 256);
             };
             const auto corr_of = [&](int step, v4f(&c)[NS]) {
                 const int h = step / NT, nt = step % NT;
@@ -664,18 +676,23 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
                 for (int g = 0; g < NS; ++g)
                     c[g] = *reinterpret_cast<const v4f*>(corr + ((h * NS + g) * NT + nt) * 16 + 4 * q);
             };
-            const auto codes_of = [&](int h, v2u(&w)[4][R]) {
+            v2u w[2][CB][R];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < CB; ++i)
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        w[i][r] = *reinterpret_cast<const v2u*>(stage + (code_at ^ ((4 * h + i) * 16)) + r * 2048);
+                        w[h][i][r] = *reinterpret_cast<const v2u*>(stage + (code_at ^ ((4 * h + 4 / CB * i) * 16)) + r * 2048);
+            bf16x8 b[2][4][R];
+            const auto unpack = [&](int h, int i) {  // the codes of chunk h that product i takes
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const v2u v = w[h][CB == 4 ? i : i / 2][r];
+                    const int by = CB == 4 ? shift : 4 * (i % 2);
+                    b[h][i][r] = bytes_bf16((v[0] >> by) & 0x0F0F0F0Fu, (v[1] >> by) & 0x0F0F0F0Fu);
+                }
             };
-            bf16x8 x[2][4];
-            v4f c[2][NS];
-            v2u w[2][4][R];
-            codes_of(0, w[0]);
-            codes_of(1, w[1]);
             if (wave < 2 * NT) {
                 bf16x8 mine[4];
                 x_of(wave, mine);
@@ -689,40 +706,52 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
                         *reinterpret_cast<v4f*>(corr + ((wave / NT * NS + g) * NT + wave % NT) * 16 + 4 * q) = sum[g];
                 }
             }
+            bf16x8 x[2][4];
+            v4f c[2][NS], d[2][NS][R];
             x_of(0, x[0]);
-            bf16x8 b[4][R];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unpack(0, i);
+            __builtin_amdgcn_sched_barrier(0);
             // the corrections are there, the codes out of their buffer
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             ask_codes(now);
-            __builtin_amdgcn_sched_barrier(0);
             corr_of(0, c[0]);
-#pragma unroll
-            for (int step = 0; step < 2 * NT; ++step) {
+            __builtin_amdgcn_sched_barrier(0);
+            const auto add_up = [&](int step) {
                 const int h = step / NT, nt = step % NT;
-                if (nt == 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int r = 0; r < R; ++r)
-                            b[i][r] = bytes_bf16((w[h][i][r][0] >> shift) & 0x0F0F0F0Fu, (w[h][i][r][1] >> shift) & 0x0F0F0F0Fu);
-                }
-                if (step + 1 < 2 * NT) x_of(step + 1, x[(step + 1) & 1]), corr_of(step + 1, c[(step + 1) & 1]);
-                __builtin_amdgcn_sched_barrier(0);
-                v4f d[R];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int g = 0; g < NS; ++g)
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        d[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[step & 1][i], b[i][r],
-                                                                      i % BG == 0 ? c[step & 1][i / BG] : d[r], 0, 0, 0);
-                    if (i % BG == BG - 1) {
 #pragma unroll
-                        for (int r = 0; r < R; ++r)
+                        for (int e = 0; e < 4; ++e)
+                            acc[r][nt][e] = fmaf(scale[h][r][g], d[step & 1][g][r][e], acc[r][nt][e]);
+            };
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[r][nt][e] = fmaf(scale[h][r][i / BG], d[r][e], acc[r][nt][e]);
-                    }
+            for (int step = 0; step < 2 * NT; ++step) {
+                const int h = step / NT;
+                if (step + 1 < 2 * NT) x_of(step + 1, x[(step + 1) & 1]), corr_of(step + 1, c[(step + 1) & 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (h == 0 && i * NT / 4 == step) unpack(1, i);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        d[step & 1][i / BG][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            x[step & 1][i], b[h][i][r], i % BG == 0 ? c[step & 1][i / BG] : d[step & 1][i / BG][r], 0, 0, 0);
+                if (step) add_up(step - 1);
+                __builtin_amdgcn_sched_group_barrier(0x100, 4 + NS, 0);  // LDS reads
+#pragma unroll
+                for (int i = 0; i < 4 * R; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);  // a product
+                    __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);  // vector instructions
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
+            add_up(2 * NT - 1);
+            __builtin_amdgcn_sched_barrier(0);
+            arrive();
             now ^= 1;
         } while (++u < units);
         store_rows<NT, R>(a, n0, t0, lane, bias, acc);
