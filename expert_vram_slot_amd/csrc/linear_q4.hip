@@ -663,7 +663,8 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
             __builtin_amdgcn_sched_barrier(0);
             const char* stage = smem + now * Ti::STAGE;
             // A step is a chunk's token tile.  Its reads go out a step ahead, and what it adds up, and the second
-            // chunk's codes as bf16, lie between the products.
+            // chunk's codes as bf16, lie between the products (groups of one block have no registers for all of that:
+            // their corrections are read in the step, the second chunk's codes taken at its start).
             const auto x_of = [&](int step, bf16x8(&x)[4]) {
                 const int h = step / NT, nt = step % NT;
 #pragma unroll
@@ -715,7 +716,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
             // the corrections are there, the codes out of their buffer
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             ask_codes(now);
-            corr_of(0, c[0]);
+            if (CB == 2) corr_of(0, c[0]);
             __builtin_amdgcn_sched_barrier(0);
             const auto add_up = [&](int step) {
                 const int h = step / NT, nt = step % NT;
@@ -730,17 +731,20 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
 #pragma unroll
             for (int step = 0; step < 2 * NT; ++step) {
                 const int h = step / NT;
-                if (step + 1 < 2 * NT) x_of(step + 1, x[(step + 1) & 1]), corr_of(step + 1, c[(step + 1) & 1]);
+                if (step + 1 < 2 * NT) x_of(step + 1, x[(step + 1) & 1]);
+                if (CB == 4) corr_of(step, c[step & 1]);
+                else if (step + 1 < 2 * NT) corr_of(step + 1, c[(step + 1) & 1]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (h == 0 && i * NT / 4 == step) unpack(1, i);
+                    if (CB == 4 ? step == NT : h == 0 && i * NT / 4 == step) unpack(1, i);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int r = 0; r < R; ++r)
                         d[step & 1][i / BG][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                             x[step & 1][i], b[h][i][r], i % BG == 0 ? c[step & 1][i / BG] : d[step & 1][i / BG][r], 0, 0, 0);
-                if (step) add_up(step - 1);
+                if (CB == 4) add_up(step);
+                else if (step) add_up(step - 1);
                 __builtin_amdgcn_sched_group_barrier(0x100, 4 + NS, 0);  // LDS reads
 #pragma unroll
                 for (int i = 0; i < 4 * R; ++i) {
@@ -749,7 +753,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            add_up(2 * NT - 1);
+            if (CB == 2) add_up(2 * NT - 1);
             __builtin_amdgcn_sched_barrier(0);
             arrive();
             now ^= 1;
