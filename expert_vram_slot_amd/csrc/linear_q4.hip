@@ -26,6 +26,10 @@
 //  - x lies in LDS, all of it where that fits (workgroups then stay and take
 //    one row tile after the other, the codes' loads running on across tiles),
 //    else a stretch of inputs at a time in two buffers.
+// That is k_linear_q4, which memory bounds where it is large (one token, 131072 x
+// 2048 in groups of 32: 34 us, 4.5 TB/s; 16 x 8192 x 4096: 9.5 us) and its launch
+// and one tile's latencies where it is not (one token, 2048 x 2048: 5.5 us).
+// Many bf16 tokens by many rows go to k_linear_q4_tile, below.
 #include <atomic>
 #include <type_traits>
 
@@ -519,6 +523,12 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
 //  - The corrections -8 * (sum of x over a group) are computed once per workgroup:
 //    each wave one (chunk, token tile) of the unit, and go into the products as
 //    their C.
+// 64 x 131072 x 4096 in groups of 128: 100 us, 690 TFLOP/s; 61 us without the
+// products and the stores, 78 us with the same few lines loaded over and over.  A
+// unit takes 2.6 us of a CU whatever the others do: eight waves read x 8 times
+// from LDS (320 clocks a token tile, the products 256) and take the barriers
+// together.  Four waves of four row tiles read half of that and have nobody to
+// fill their waits: 113 us.
 template <int G, int NT, int R, bool EVEN, int NW>
 struct Tile {
     static constexpr int ROWS = NW * R * 16;
@@ -824,19 +834,26 @@ template <int XD, int G, bool EVEN>
 int pick(const LinArgs& a, hipStream_t st) {
     const int pad = (a.K + CH - 1) / CH * CH;
     // x whole in LDS: as long as two workgroups share a CU, or one of 16 tokens
-    const auto whole = [&](size_t bytes, size_t most) { return bytes <= most; };
-    if (a.T == 1 && whole(Stage<XD, 1, 1>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 1, 1, 2, true, EVEN, 8>(a, st);
-    if (a.T <= 4 && whole(Stage<XD, 1, 4>::bytes(pad), 64 << 10)) return launch<XD, G, 1, 4, 1, 2, true, EVEN, 8>(a, st);
-    if (a.T <= 8 && whole(Stage<XD, 1, 8>::bytes(pad), 80 << 10)) return launch<XD, G, 1, 8, 1, 2, true, EVEN, 8>(a, st);
-    // more tokens: tiles of 64 tokens by 256 rows a workgroup, or 32 by 256, where those give half the CUs work;
-    // else 16 by 16 a wave, the codes read again for each 16 tokens
+    if (a.T == 1 && Stage<XD, 1, 1>::bytes(pad) <= 64 << 10) return launch<XD, G, 1, 1, 1, 2, true, EVEN, 8>(a, st);
+    if (a.T <= 4 && Stage<XD, 1, 4>::bytes(pad) <= 64 << 10) return launch<XD, G, 1, 4, 1, 2, true, EVEN, 8>(a, st);
+    if (a.T <= 8 && Stage<XD, 1, 8>::bytes(pad) <= 80 << 10) return launch<XD, G, 1, 8, 1, 2, true, EVEN, 8>(a, st);
+    // More tokens.  bf16: tiles of 64 tokens by 256 rows or of 32 by 256, one a CU at a time, of which the first take
+    // half as long again (2.6 and 1.75 us a unit): whichever ends sooner (131072 x 4096: 64 tokens 102 and 124 us, 32
+    // tokens 96 and 75 us), as long as half the CUs get one (64 x 24576 x 4096: 32 us, by 16 tokens a wave 48; 64 x
+    // 8192 x 4096: 28 and 18).  fp32: tiles of 32 by 256 where every CU gets one (32 x 65536 x 2048: 51 us, by 16 tokens
+    // 63; 64 x 16384 x 2048: 41 and 33).  Else 16 tokens by 16 rows a wave, the codes read again for each 16 tokens.
     if (a.T > 16) {
-        const int64_t big = ((int64_t)a.N + 255) / 256 * ((a.T + 63) / 64), mid = ((int64_t)a.N + 255) / 256 * ((a.T + 31) / 32);
-        if constexpr (XD == MOE_X_BF16)
-            if (a.T > 32 && big >= 128) return launch_tile<G, 4, EVEN>(a, st);
-        if (mid >= 128) return launch<XD, G, 2, 16, 2, 1, false, EVEN, 8>(a, st);
+        const int64_t by64 = ((int64_t)a.N + 255) / 256 * ((a.T + 63) / 64), by32 = ((int64_t)a.N + 255) / 256 * ((a.T + 31) / 32);
+        if constexpr (XD == MOE_X_BF16) {
+            if (by32 >= 128) {
+                if (3 * ((by64 + 255) / 256) <= 2 * ((by32 + 255) / 256)) return launch_tile<G, 4, EVEN>(a, st);
+                return launch_tile<G, 2, EVEN>(a, st);
+            }
+        } else if (by32 >= 256) {
+            return launch<XD, G, 2, 16, 2, 1, false, EVEN, 8>(a, st);
+        }
     }
-    if (whole(Stage<XD, 1, 16>::bytes(pad), 128 << 10)) return launch<XD, G, 1, 16, 1, 2, true, EVEN, 8>(a, st);
+    if (Stage<XD, 1, 16>::bytes(pad) <= 128 << 10) return launch<XD, G, 1, 16, 1, 2, true, EVEN, 8>(a, st);
     return launch<XD, G, 1, 16, 1, 1, false, EVEN, 8>(a, st);
 }
 
