@@ -57,7 +57,7 @@ __device__ __forceinline__ void load_row(const void* z, int64_t t, int E, int la
 
 // Workspace: per block of the row kernel the sums of p per expert, the sum of
 // lse^2, the picks per expert and the counted tokens; per block of the second
-// pass its part of sum_e c_e P_e and of sum_e c_e.
+// pass its part of sum_e c_e P_e and of sum_e c_e, and how many are done.
 struct BalWs {
     double* share;   // [blocks][E]
     double* lse2;    // [blocks]
@@ -65,6 +65,7 @@ struct BalWs {
     int32_t* picks;  // [blocks][E]
     int32_t* toks;   // [blocks]
     int32_t* sum;    // [parts]
+    int32_t* done;
 };
 
 inline int bal_blocks(int T, int waves) {
@@ -75,7 +76,7 @@ inline int bal_blocks(int T, int waves) {
 inline int bal_parts(int E) { return (E + SUM_E - 1) / SUM_E; }
 
 inline size_t bal_bytes(int blocks, int E) {
-    return (size_t)blocks * (12 * (size_t)E + 12) + (size_t)bal_parts(E) * 12;
+    return (size_t)blocks * (12 * (size_t)E + 12) + (size_t)bal_parts(E) * 12 + 4;
 }
 
 inline BalWs bal_ws(void* ws, int blocks, int E) {
@@ -86,6 +87,7 @@ inline BalWs bal_ws(void* ws, int blocks, int E) {
     w.picks = reinterpret_cast<int32_t*>(w.dot + bal_parts(E));
     w.toks = w.picks + (size_t)blocks * E;
     w.sum = w.toks + blocks;
+    w.done = w.sum + bal_parts(E);
     return w;
 }
 
@@ -221,6 +223,7 @@ __global__ void __launch_bounds__(64 * bal_waves(NE, ONE)) k_balance(const void*
             ws.picks[(int64_t)blockIdx.x * E + e] = s_picks[e];
         }
         if (threadIdx.x == 0) ws.lse2[blockIdx.x] = l2, ws.toks[blockIdx.x] = n;
+        if (blockIdx.x == 0 && threadIdx.x == 0) *ws.done = 0;
     } else {
         double dot = 0.0;
         int picks = 0;
@@ -246,7 +249,8 @@ __global__ void __launch_bounds__(64 * bal_waves(NE, ONE)) k_balance(const void*
 }
 
 // Second pass: SUM_E experts a workgroup, 64 groups of threads each adding up
-// every 64th block, then the groups in order.
+// every 64th block, then the groups in order.  The last workgroup to end (its
+// count says so) writes the losses, from every part in the parts' order.
 __global__ void __launch_bounds__(SUM_THREADS) k_balance_sum(BalWs ws, int blocks, int E, BalOut o) {
     __shared__ double s_share[SUM_THREADS];
     __shared__ int s_picks[SUM_THREADS], s_n[SUM_THREADS / 64];
@@ -258,6 +262,7 @@ __global__ void __launch_bounds__(SUM_THREADS) k_balance_sum(BalWs ws, int block
     double s = 0.0;
     int c = 0;
     if (e < E)
+#pragma unroll 8
         for (int b = tid / SUM_E; b < blocks; b += SUM_THREADS / SUM_E)
             s += ws.share[(int64_t)b * E + e], c += ws.picks[(int64_t)b * E + e];
     s_share[tid] = s;
@@ -279,27 +284,22 @@ __global__ void __launch_bounds__(SUM_THREADS) k_balance_sum(BalWs ws, int block
     if (mine) o.share[e] = s, o.counts[e] = c;
     const double dot = moe::wave_sum(mine ? s * c : 0.0);
     const int picks = moe::wave_sum(mine ? c : 0);
-    if (tid == 0) ws.dot[blockIdx.x] = dot, ws.sum[blockIdx.x] = picks;
-}
-
-__global__ void __launch_bounds__(256) k_balance_loss(BalWs ws, int blocks, int parts, int E, BalOut o) {
-    __shared__ double s_dot[4], s_l2[4];
-    __shared__ int s_picks[4], s_n[4];
-    const int tid = threadIdx.x;
-    double dot = 0.0, l2 = 0.0;
-    int picks = 0, n = 0;
-    for (int p = tid; p < parts; p += 256) dot += ws.dot[p], picks += ws.sum[p];
-    for (int b = tid; b < blocks; b += 256) l2 += ws.lse2[b], n += ws.toks[b];
-    dot = moe::wave_sum(dot);
-    l2 = moe::wave_sum(l2);
-    picks = moe::wave_sum(picks);
-    n = moe::wave_sum(n);
-    if ((tid & 63) == 0) s_dot[tid >> 6] = dot, s_l2[tid >> 6] = l2, s_picks[tid >> 6] = picks, s_n[tid >> 6] = n;
-    __syncthreads();
+    int last = 0;
     if (tid == 0) {
-        for (int w = 1; w < 4; ++w) dot += s_dot[w], l2 += s_l2[w], picks += s_picks[w], n += s_n[w];
-        write_totals(o, E, n, picks, dot, l2);
+        ws.dot[blockIdx.x] = dot, ws.sum[blockIdx.x] = picks;
+        last = __hip_atomic_fetch_add(ws.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
     }
+    if (!__shfl(last, 0, moe::WAVE)) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    double all = 0.0, l2 = 0.0;
+    int of = 0;
+    for (int p = tid; p < (int)gridDim.x; p += 64) all += ws.dot[p], of += ws.sum[p];
+#pragma unroll 8
+    for (int b = tid; b < blocks; b += 64) l2 += ws.lse2[b];
+    all = moe::wave_sum(all);
+    l2 = moe::wave_sum(l2);
+    of = moe::wave_sum(of);
+    if (tid == 0) write_totals(o, E, n, of, all, l2);
 }
 
 // f is taken less its mean 1/E, as whole numbers over whole numbers: the
@@ -426,11 +426,8 @@ int moe_balance_loss(const void* z, int z_dtype, const int32_t* ids, const uint8
     });
     if (int rc = moe_check_launch("moe_balance_loss")) return rc;
     if (T <= BAL_ONE) return moe_ok();
-    const int parts = bal_parts(E);
-    hipLaunchKernelGGL(k_balance_sum, dim3(parts), dim3(SUM_THREADS), 0, stream, w, blocks, E, o);
-    if (int rc = moe_check_launch("moe_balance_loss/sum")) return rc;
-    hipLaunchKernelGGL(k_balance_loss, dim3(1), dim3(256), 0, stream, w, blocks, parts, E, o);
-    return moe_check_launch("moe_balance_loss/loss");
+    hipLaunchKernelGGL(k_balance_sum, dim3(bal_parts(E)), dim3(SUM_THREADS), 0, stream, w, blocks, E, o);
+    return moe_check_launch("moe_balance_loss/sum");
 }
 
 int moe_balance_loss_bwd(const void* z, int z_dtype, const float* lse, const uint8_t* mask, const int32_t* counts,
