@@ -640,6 +640,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
     ask_bias(tile);
     ask_codes(0);
     fetch_x(0, 0);
+    __builtin_amdgcn_sched_barrier(0);  // the codes waited for last go out last
     ask_codes(1);
     // Waits for the next unit, all but the 2 R loads of the one behind it: at a unit's end, so that the stores of a tile
     // go out after the wait and have a unit's time.

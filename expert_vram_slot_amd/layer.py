@@ -184,6 +184,7 @@ class SlotLayer:
         """Gradient of the last balance()'s losses (weights dloss: device
         float [2]; same T and mask) to the last step's logits, [T][E] fp32."""
         o = self.stats_out
+        assert o is not None and T <= self.T_max
         dz = torch.empty(T, self.E, dtype=torch.float32, device=self.ids.device)
         moe_balance_loss_bwd(self.logits, MOE_X_F32, o["lse"], mask, o["counts"], o["totals"], dloss, T, self.E, dz,
                              torch.cuda.current_stream())
@@ -351,6 +352,9 @@ class DecodeHead:
 
     def __init__(self, *, H, V, wq, scales, group, T_max, x_dtype=MOE_X_BF16, bias=None, device="cuda"):
         dev = torch.device(device)
+        assert H % group == 0 and tuple(wq.shape) == (V, H // 2) and tuple(scales.shape) == (V, H // group)
+        assert wq.dtype == torch.uint8 and scales.dtype == torch.float16 and wq.is_contiguous() and scales.is_contiguous()
+        assert bias is None or (tuple(bias.shape) == (V,) and bias.dtype == torch.float32)
         self.H, self.V, self.T_max, self.x_dtype = H, V, T_max, x_dtype
         self.wq, self.scales, self.group, self.bias = wq, scales, group, bias
         self.logits_buf = torch.empty(T_max, V, dtype=torch.float32, device=dev)

@@ -427,9 +427,10 @@ int moe_residual(const void* x, int x_dtype, const float* y, void* x_out, int T,
  *           (code[n][k] - 8)), summed in fp32 (bf16: rounded once, RNE).
  *           Columns from N to ldy are left as they are; y must not overlap
  *           the inputs.
- * fp32 activations keep their 24 bits.  A token whose x or bias holds an
- * infinity or a NaN gets non-finite outputs; other tokens are not touched by
- * it.  A token's bits do not depend on the other tokens' values.
+ * fp32 activations keep their 24 bits (below 2^-100 in magnitude the last of
+ * them are lost).  Outputs that an infinity or a NaN enters, or whose sums
+ * leave fp32's range on the way, are not finite; other tokens are not touched
+ * by it.  A token's bits do not depend on the other tokens' values.
  * T = 0 does nothing (x and y may be NULL).
  * Errors: ARG (null, sizes, ldx < K, ldy < N), DTYPE, SHAPE (group, K not a
  * multiple of it, the limits below), ALIGN (x, its rows and wq on 16 bytes;

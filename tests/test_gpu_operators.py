@@ -139,8 +139,22 @@ def test_linear_scales_aligned_to_their_elements_alone(m, T, N, K, group):
     assert torch.equal(linear(m, x, wq, moved, group, None, "f32"), linear(m, x, wq, scales, group, None, "f32"))
 
 
-def test_linear_bits_do_not_depend_on_other_tokens(m):
-    wq, scales, g = weights(200, 1024, 32, 5)
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,K,group", [(1, 300, 512, 64), (7, 300, 512, 64), (24, 300, 1024, 32), (20, 66000, 256, 128),
+                                         (40, 33000, 256, 32)])
+def test_linear_scales_with_its_input(m, T, N, K, group, xt):
+    """Powers of two go through every rounding, 90 up and down, in all 24 bits of an fp32 x."""
+    wq, scales, g = weights(N, K, group, N + K)
+    x = torch.randn(T, K, device="cuda", generator=g).to(DT[xt])
+    x = torch.where(x.abs() < 2.0 ** -10, torch.ones_like(x), x)  # the smallest bit of x times 2^-90: 2^-123
+    want = linear(m, x, wq, scales, group, None, "f32")
+    for s in (2.0 ** 90, 2.0 ** -90):
+        assert torch.equal(linear(m, x * s, wq, scales, group, None, "f32"), want * s)
+
+
+@pytest.mark.parametrize("N", [200, 66000])
+def test_linear_bits_do_not_depend_on_other_tokens(m, N):
+    wq, scales, g = weights(N, 1024, 32, 5)
     x = torch.randn(24, 1024, device="cuda", generator=g).bfloat16()
     a = linear(m, x, wq, scales, 32, None, "f32")
     x2 = x.clone()
@@ -563,7 +577,7 @@ def _whole_path(m, T, V, K, group, seed):
     return call, (x, u, z), (y, ids, prob, counts, totals, share, lse, loss, dz)
 
 
-@pytest.mark.parametrize("T,V", [(1, 5001), (12, 40000)])
+@pytest.mark.parametrize("T,V", [(1, 5001), (12, 40000), (40, 33000)])
 def test_captured_and_replayed_with_eager_calls_between(m, T, V):
     call, inputs, outputs = _whole_path(m, T, V, 512, 32, 1)
     other, _, _ = _whole_path(m, T + 3, V + 77, 256, 64, 2)
@@ -594,7 +608,7 @@ def test_captured_and_replayed_with_eager_calls_between(m, T, V):
 
 
 def test_two_streams_with_workspaces_of_their_own(m):
-    paths = [_whole_path(m, 6, 30000, 512, 32, n) for n in range(2)]
+    paths = [_whole_path(m, T, 33000, 512, 32, T) for T in (6, 40)]
     want = []
     for call, _, outputs in paths:
         call()

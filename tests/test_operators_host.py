@@ -130,6 +130,25 @@ def test_binding_raises_with_the_reason(mlib):
 # ------------------------------------------------------------ references
 
 
+@pytest.mark.parametrize("change", [dict(V=9), dict(H=128), dict(group=128), dict(bias="short"), dict(scales="f32"),
+                                    dict(wq="strided")])
+def test_decode_head_refuses(mlib, change):
+    torch = pytest.importorskip("torch")
+    from expert_vram_slot_amd.layer import DecodeHead
+    a = dict(H=64, V=8, wq=torch.zeros(8, 32, dtype=torch.uint8), scales=torch.zeros(8, 2, dtype=torch.float16), group=32,
+             T_max=2, device="cpu")
+    DecodeHead(**a)
+    change = dict(change)
+    if "bias" in change:
+        change["bias"] = torch.zeros(7)
+    if "scales" in change:
+        change["scales"] = torch.zeros(8, 2)
+    if "wq" in change:
+        change["wq"] = torch.zeros(8, 64, dtype=torch.uint8)[:, ::2]
+    with pytest.raises(AssertionError):
+        DecodeHead(**{**a, **change})
+
+
 def test_reference_codes_are_the_slab_planes():
     """The nibble order is a Q4B32 slab's: decoding the generator's gate plane gives the oracle's weights."""
     import oracle
