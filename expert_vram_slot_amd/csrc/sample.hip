@@ -1064,10 +1064,12 @@ int run(SmpArgs a, void* ws, hipStream_t st) {
         hipLaunchKernelGGL(k_row<LD>, dim3(a.T), dim3(ROW_NT), 0, st, a);
         return moe_check_launch("moe_sample");
     }
-    // one segment a wave where rows are few; from about four workgroups a CU
+    // one segment a wave, so that the CUs end together; from 16 workgroups a CU
     // on a wave takes several, so that a row's bins are gathered fewer times
+    // (128 x 100003: several from 4, 8 and 16 a CU on 78, 69 and 68 us; 64 x
+    // 131072: 47 to 48 us)
     const int64_t all = (int64_t)a.T * a.segs;
-    const int64_t share = (all + 4096 - 1) / 4096;
+    const int64_t share = (all + 16384 - 1) / 16384;
     a.share = share < a.segs ? (int)share : a.segs;
     constexpr int NW = CHUNK_NT / 64;
     const dim3 grid((a.segs + NW * a.share - 1) / (NW * a.share), a.T), block(CHUNK_NT);
