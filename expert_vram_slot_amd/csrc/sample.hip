@@ -30,6 +30,11 @@
 // A row whose cut bins hold more than LIST ids (many equal logits, or one far
 // outlier under a high temperature) takes a radix selection instead, eight
 // bits of the logit's key a pass over the whole row: slower, the same result.
+//
+// 64 x 131072 fp32: k_top 8 us (4 TB/s), k_bins 17, k_list 13.5, k_draw 11.6 us;
+// k_bins and k_list are bound by the vector unit (a mass costs about 24 double
+// instructions), k_draw and a single row (3 + 5.5 + 7 + 6.6 us) by the steps that
+// wait for one another.  17 x 5003 bf16 in k_row: 15.5 us, about 25 barriers.
 #include <math.h>
 
 #include <type_traits>
