@@ -167,7 +167,8 @@ def test_linear_bits_do_not_depend_on_other_tokens(m, N):
     assert not torch.any(torch.isfinite(b[3])) and not torch.any(torch.isfinite(b[17]))
 
 
-def test_linear_offsets_past_32_bits(m):
+@pytest.mark.parametrize("T", [2, 40])
+def test_linear_offsets_past_32_bits(m, T):
     """Codes past 4 GiB: the last rows of a tall matrix."""
     N, K, group = (1 << 20) + 70000, 8192, 128  # 4.58 GB of codes
     if torch.cuda.mem_get_info()[0] < 8 << 30:
@@ -177,13 +178,30 @@ def test_linear_offsets_past_32_bits(m):
     g = torch.Generator(device="cuda").manual_seed(3)
     rows = torch.tensor([0, 1, (1 << 20) - 1, 1 << 20, (1 << 20) + 5, N - 2, N - 1], device="cuda")
     wq[rows] = torch.randint(0, 256, (7, K // 2), dtype=torch.uint8, device="cuda", generator=g)
-    x = torch.randint(-1, 2, (2, K), device="cuda", generator=g).bfloat16()
-    y = torch.empty(2, N, device="cuda")
-    m.moe_linear_q4(x, m.MOE_X_BF16, K, wq, scales, group, None, 2, N, K, y, m.MOE_X_F32, N)
+    x = torch.randint(-1, 2, (T, K), device="cuda", generator=g).bfloat16()
+    y = torch.empty(T, N, device="cuda")
+    m.moe_linear_q4(x, m.MOE_X_BF16, K, wq, scales, group, None, T, N, K, y, m.MOE_X_F32, N)
     want, _ = ref.linear_q4(host64(x), wq[rows].cpu().numpy(), scales[rows].cpu().numpy(), group)
     np.testing.assert_array_equal(host64(y[:, rows]), want)
     zero = -8.0 * x.float().sum(dim=1, keepdim=True)
     assert torch.all(y[:, 2:(1 << 20) - 1] == zero)
+
+
+@pytest.mark.parametrize("T,N", [(8, 100), (16, 100), (34, 100), (40, 33000)])
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+def test_linear_rows_past_32_bits(m, T, N, xt):
+    """Tokens and outputs 2^26 values apart and more: the last start past 2^31 bytes, or values."""
+    K, group = 256, 64
+    ld = (1 << 31) // (T - 1) // 8 * 8 + 8
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GiB of device memory")
+    wq, scales, g = weights(N, K, group, T)
+    x = torch.randn(T, K, device="cuda", generator=g).to(DT[xt])
+    far = torch.empty((T - 1) * ld + K, dtype=DT[xt], device="cuda")
+    y = torch.empty((T - 1) * ld + N, device="cuda")
+    torch.as_strided(far, (T, K), (ld, 1)).copy_(x)
+    m.moe_linear_q4(far, code(m, xt), ld, wq, scales, group, None, T, N, K, y, m.MOE_X_F32, ld)
+    assert torch.equal(torch.as_strided(y, (T, N), (ld, 1)), linear(m, x, wq, scales, group, None, "f32"))
 
 
 # ------------------------------------------------------------------ sample
@@ -496,6 +514,41 @@ def test_balance_gradient_in_place(m):
     zz = z.clone()
     m.moe_balance_loss_bwd(zz, m.MOE_X_F32, o["lse"].contiguous(), None, o["counts"].contiguous(), o["totals"], d, 100, 48, zz)
     assert torch.equal(zz, o["dz"])
+
+
+def test_balance_offsets_past_32_bits(m):
+    """More than 2^32 logits, all 0 but the last token's."""
+    E, T = 512, (1 << 23) + 5
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GiB of device memory")
+    z = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    z[T - 1, 3] = 20.0
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    ids[T - 1] = 3
+    dev = dict(device="cuda")
+    counts, totals = torch.empty(E, dtype=torch.int32, **dev), torch.empty(2, dtype=torch.int32, **dev)
+    share, lse, loss = torch.empty(E, dtype=torch.float64, **dev), torch.empty(T, **dev), torch.empty(2, **dev)
+    n = m.moe_balance_workspace_bytes(T, E)
+    ws = torch.empty(n, dtype=torch.uint8, **dev)
+    m.moe_balance_loss(z, m.MOE_X_BF16, ids, None, T, E, 1, counts, totals, share, lse, loss, ws, n)
+    d, dz = torch.tensor([0.0, 1.0], **dev), torch.full_like(z, 7.0)
+    m.moe_balance_loss_bwd(z, m.MOE_X_BF16, lse, None, counts, totals, d, T, E, dz)
+    torch.cuda.synchronize()
+    assert counts[0] == T - 1 and counts[3] == 1 and totals.tolist() == [T, T]
+    big = np.exp(20.0)
+    p3, p = big / (big + E - 1), 1.0 / (big + E - 1)
+    want = np.full(E, ((T - 1) / E + p) / T)
+    want[3] = ((T - 1) / E + p3) / T
+    np.testing.assert_allclose(host64(share), want, rtol=(T + E + 64) * 2.0 ** -52)
+    for t, l in ((0, np.log(E)), (T // 2, np.log(E)), (T - 2, np.log(E)), (T - 1, np.log(big + E - 1))):
+        assert abs(float(lse[t]) - l) <= 2.0 ** -24 * l * 1.01
+        # dz = 2 lse p / n: p of fp32 numbers (an exponent of up to 20 in size, rounded, and lse's rounding: 2^-18
+        # relative in all), three products, one rounding to bf16
+        q = np.full(E, p if t == T - 1 else 1.0 / E)
+        if t == T - 1:
+            q[3] = p3
+        w = 2 * l * q / T
+        assert np.all(np.abs(host64(dz[t]) - w) <= (2.0 ** -8 + 2.0 ** -17) * w)
 
 
 # ------------------------------------------- together, streams and graphs
