@@ -176,8 +176,9 @@ class SlotLayer:
                                       lse=torch.empty(self.T_max, dtype=torch.float32, device=dev),
                                       loss=torch.empty(2, dtype=torch.float32, device=dev),
                                       ws=torch.empty(n, dtype=torch.uint8, device=dev), ws_bytes=n)
-        moe_balance_loss(self.logits, MOE_X_F32, self.ids, mask, T, self.E, self.k, o["counts"], o["totals"],
-                         o["share"], o["lse"], o["loss"], o["ws"], o["ws_bytes"], torch.cuda.current_stream())
+        with torch.cuda.device(self.ids.device):
+            moe_balance_loss(self.logits, MOE_X_F32, self.ids, mask, T, self.E, self.k, o["counts"], o["totals"],
+                             o["share"], o["lse"], o["loss"], o["ws"], o["ws_bytes"], torch.cuda.current_stream())
         return dict(counts=o["counts"], totals=o["totals"], share=o["share"], lse=o["lse"][:T], loss=o["loss"])
 
     def balance_grad(self, T, dloss, mask=None):
@@ -186,8 +187,9 @@ class SlotLayer:
         o = self.stats_out
         assert o is not None and T <= self.T_max
         dz = torch.empty(T, self.E, dtype=torch.float32, device=self.ids.device)
-        moe_balance_loss_bwd(self.logits, MOE_X_F32, o["lse"], mask, o["counts"], o["totals"], dloss, T, self.E, dz,
-                             torch.cuda.current_stream())
+        with torch.cuda.device(self.ids.device):
+            moe_balance_loss_bwd(self.logits, MOE_X_F32, o["lse"], mask, o["counts"], o["totals"], dloss, T, self.E, dz,
+                                 torch.cuda.current_stream())
         return dz
 
 
@@ -366,14 +368,16 @@ class DecodeHead:
     def logits(self, x, T):
         """Logits [T][V] fp32 of x (device [T][H] in x_dtype): a view of this object's buffer."""
         assert T <= self.T_max
-        moe_linear_q4(x, self.x_dtype, self.H, self.wq, self.scales, self.group, self.bias, T, self.V, self.H,
-                      self.logits_buf, MOE_X_F32, self.V, torch.cuda.current_stream())
+        with torch.cuda.device(self.ids.device):
+            moe_linear_q4(x, self.x_dtype, self.H, self.wq, self.scales, self.group, self.bias, T, self.V, self.H,
+                          self.logits_buf, MOE_X_F32, self.V, torch.cuda.current_stream())
         return self.logits_buf[:T]
 
     def step(self, x, T, u, temperature=None, min_p=None, top_k=None, top_p=None):
         """The next token of each of T rows of x: (ids [T], prob [T]), views of
         this object's buffers.  u and the settings as moe_sample takes them."""
         self.logits(x, T)
-        moe_sample(self.logits_buf, MOE_X_F32, self.V, T, self.V, temperature, min_p, top_k, top_p, u, self.ids,
-                   self.prob, self.ws, self.ws_bytes, torch.cuda.current_stream())
+        with torch.cuda.device(self.ids.device):
+            moe_sample(self.logits_buf, MOE_X_F32, self.V, T, self.V, temperature, min_p, top_k, top_p, u, self.ids,
+                       self.prob, self.ws, self.ws_bytes, torch.cuda.current_stream())
         return self.ids[:T], self.prob[:T]

@@ -412,7 +412,9 @@ int moe_residual(const void* x, int x_dtype, const float* y, void* x_out, int T,
 
 /* ------------------------------------------------------------------------
  * Around the stack: dense 4-bit products, the draw of a token, and the
- * router's statistics.
+ * router's statistics.  The stream is one of the current device, where the
+ * buffers are (DecodeHead and SlotLayer.balance make theirs current).  All of
+ * these calls may be captured into a graph.
  */
 
 /* Dense product with 4-bit weights and group scales: the projections and the
