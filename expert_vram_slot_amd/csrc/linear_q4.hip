@@ -523,12 +523,12 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
 //  - The corrections -8 * (sum of x over a group) are computed once per workgroup:
 //    each wave one (chunk, token tile) of the unit, and go into the products as
 //    their C.
-// 64 x 131072 x 4096 in groups of 128: 100 us, 690 TFLOP/s; 61 us without the
+// 64 x 131072 x 4096 in groups of 128: 102 us, 670 TFLOP/s; 61 us without the
 // products and the stores, 78 us with the same few lines loaded over and over.  A
-// unit takes 2.6 us of a CU whatever the others do: eight waves read x 8 times
-// from LDS (320 clocks a token tile, the products 256) and take the barriers
-// together.  Four waves of four row tiles read half of that and have nobody to
-// fill their waits: 113 us.
+// unit takes 5400 clocks of its CU: x from LDS eight times over 2560, products
+// 2176, vector instructions 1870, two barriers; they overlap in part.  Four row
+// tiles a wave would read half of that LDS: in eight waves 45 registers are
+// spilled (121 us), in four nobody fills the waits (113 us).
 template <int G, int NT, int R, bool EVEN, int NW>
 struct Tile {
     static constexpr int ROWS = NW * R * 16;
