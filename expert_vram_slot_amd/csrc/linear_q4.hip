@@ -92,6 +92,8 @@ __device__ __forceinline__ void exchange8(v4u& a, v4u& b) {
     }
 }
 
+constexpr int PIECES = 2;  // fp32 pieces of a stage that a thread holds on their way
+
 template <int XD>
 constexpr int PLANES = XD == MOE_X_F32 ? 3 : 1;
 
@@ -315,35 +317,35 @@ __device__ __forceinline__ void multiply(const v4u (&w)[R], const float (&scale)
     }
 }
 
-// Stores the rows n0 .. n0 + 16 R - 1 of y, as far as they exist.
+// Stores the rows n0 .. n0 + 16 R - 1 of the tokens t0 .. t_end - 1, as far as they exist.
 template <typename Y, int NT, int R>
-__device__ __forceinline__ void store_as(const LinArgs& a, int64_t n0, int64_t t0, int lane, const float (&bias)[R],
-                                         const v4f (&acc)[R][NT]) {
+__device__ __forceinline__ void store_as(const LinArgs& a, int64_t n0, int64_t t0, int64_t t_end, int lane,
+                                         const float (&bias)[R], const v4f (&acc)[R][NT]) {
     Y* y = reinterpret_cast<Y*>(a.y) + (t0 + 4 * (lane >> 4)) * a.ldy + n0 + (lane & 15);
-    const bool all = t0 + 16 * NT <= a.T && n0 + 16 * R <= a.N;  // no lane has to be looked at
+    const bool all = t0 + 16 * NT <= t_end && n0 + 16 * R <= a.N;  // no lane has to be looked at
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             Y* row = y + (int64_t)(16 * nt + e) * a.ldy;
-            const bool in_t = t0 + 4 * (lane >> 4) + 16 * nt + e < a.T;
+            const bool in_t = t0 + 4 * (lane >> 4) + 16 * nt + e < t_end;
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 if (all || (in_t && n0 + 16 * r + (lane & 15) < a.N)) row[16 * r] = (Y)(acc[r][nt][e] + bias[r]);
         }
 }
 template <int NT, int R>
-__device__ __forceinline__ void store_rows(const LinArgs& a, int64_t n0, int64_t t0, int lane, const float (&bias)[R],
-                                           const v4f (&acc)[R][NT]) {
-    if (a.y_dtype == MOE_X_F32) store_as<float>(a, n0, t0, lane, bias, acc);
-    else store_as<__bf16>(a, n0, t0, lane, bias, acc);
+__device__ __forceinline__ void store_rows(const LinArgs& a, int64_t n0, int64_t t0, int64_t t_end, int lane,
+                                           const float (&bias)[R], const v4f (&acc)[R][NT]) {
+    if (a.y_dtype == MOE_X_F32) store_as<float>(a, n0, t0, t_end, lane, bias, acc);
+    else store_as<__bf16>(a, n0, t0, t_end, lane, bias, acc);
 }
 
 // Adds up the waves of a row group (in wave order, through `part` in LDS) and
 // stores its rows.
 template <int NT, int R>
 __device__ __forceinline__ void store_tile(const LinArgs& a, char* part_, int64_t group, int64_t groups, int64_t t0,
-                                           int wk, int wave, int lane, const float (&bias)[R], v4f (&acc)[R][NT]) {
+                                           int64_t t_end, int wk, int wave, int lane, const float (&bias)[R], v4f (&acc)[R][NT]) {
     if (a.wk > 1) {
         v4f* part = reinterpret_cast<v4f*>(part_);
         if (wk > 0) {
@@ -363,7 +365,7 @@ __device__ __forceinline__ void store_tile(const LinArgs& a, char* part_, int64_
         __syncthreads();
     }
     if (wk > 0 || group >= groups) return;
-    store_rows<NT, R>(a, group * (16 * R), t0, lane, bias, acc);
+    store_rows<NT, R>(a, group * (16 * R), t0, t_end, lane, bias, acc);
 }
 
 // NW waves.  A wave takes R row tiles of 16 rows (NW / wk such groups a workgroup)
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
     extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
     const int wk = wave % a.wk, wn = wave / a.wk, per = NW / a.wk;
-    const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
+    const int64_t t0 = (int64_t)blockIdx.y * St::TOKS, t_end = t0 + St::TOKS < a.T ? t0 + St::TOKS : a.T;
     const int64_t groups = ((int64_t)a.N + 16 * R - 1) / (16 * R);
     const int stage_bytes = (int)St::bytes(a.kc);
     const int chunks = (a.K + CH - 1) / CH, units = (chunks + 1) / 2;
@@ -439,8 +441,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
         for (int round = 0; round < rounds; ++round) {
             const bool last = round + 1 == rounds;
             const bool more = !last || turn + gridDim.x < turns;
-            constexpr int PPT = ALL ? 1 : 512 * NT * D / (64 * NW);  // fp32 pieces a thread holds
-            v4u raw[XD == MOE_X_F32 && !ALL ? PPT : 1][2];
+            v4u raw[XD == MOE_X_F32 && !ALL ? PIECES : 1][2];
             const int k_next = last ? 0 : (round + 1) * a.kc;
             if constexpr (!ALL) {
                 // the next stage goes into the other buffer, which nobody reads since the last barrier
@@ -450,16 +451,10 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
                         St{other, stage_bytes}.fetch(a, t0, k_next, wave * 64, NW * 64, pieces);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < PPT; ++i) {
+                        for (int i = 0; i < PIECES; ++i) {
+                            if (tid + i * 64 * NW >= pieces) break;
                             const v4u* p = reinterpret_cast<const v4u*>(St::source(a, t0, k_next, tid + i * 64 * NW));
                             raw[i][0] = p[0], raw[i][1] = p[1];
-                        }
-                        // what several waves a row group need besides (the registers hold one wave's share)
-                        const St st{other, stage_bytes / PLANES<XD>};
-                        for (int u = tid + PPT * 64 * NW; u < pieces; u += 64 * NW) {
-                            const v4u* p = reinterpret_cast<const v4u*>(St::source(a, t0, k_next, u));
-                            const v4u extra[2] = {p[0], p[1]};
-                            st.put(u, extra);
                         }
                     }
                 }
@@ -493,7 +488,8 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
                     if (more) {
                         const St st{smem + (now ^ 1) * stage_bytes, plane};
 #pragma unroll
-                        for (int i = 0; i < PPT; ++i) st.put(tid + i * 64 * NW, raw[i]);
+                        for (int i = 0; i < PIECES; ++i)
+                            if (tid + i * 64 * NW < pieces) st.put(tid + i * 64 * NW, raw[i]);
                     }
                 } else {
                     __builtin_amdgcn_s_waitcnt(0x0F70);
@@ -502,7 +498,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4(LinArgs a) {
                 now ^= 1;
             }
         }
-        store_tile<NT, R>(a, smem + (ALL ? 1 : 2) * stage_bytes, mine, groups, t0, wk, wave, lane, bias, acc);
+        store_tile<NT, R>(a, smem + (ALL ? 1 : 2) * stage_bytes, mine, groups, t0, t_end, wk, wave, lane, bias, acc);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -769,7 +765,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_q4_tile(LinArgs a) {
             arrive();
             now ^= 1;
         } while (++u < units);
-        store_rows<NT, R>(a, n0, t0, lane, bias, acc);
+        store_rows<NT, R>(a, n0, t0, a.T, lane, bias, acc);
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);  // nothing may come into LDS after the workgroup's end
 }
@@ -797,10 +793,11 @@ int launch(LinArgs a, hipStream_t st) {
     const int units = (a.K + UNIT - 1) / UNIT;
     // row groups enough for the card go to waves of their own; fewer share
     // their inputs among several waves
-    const int64_t groups = ((int64_t)a.N + 16 * R - 1) / (16 * R), tiles = ((int64_t)a.T + 16 * NT - 1) / (16 * NT);
+    const int64_t groups = ((int64_t)a.N + 16 * R - 1) / (16 * R), tiles = ((int64_t)a.T + St::TOKS - 1) / St::TOKS;
     a.wk = 1;
     while (a.wk < NW && a.wk * 2 <= units && groups * tiles * a.wk < 2048 &&
-           (ALL || 2 * St::bytes(UNIT * D * a.wk * 2) + (size_t)NW * R * NT * 1024 <= LDS_MAX))
+           (ALL || 2 * St::bytes(UNIT * D * a.wk * 2) + (size_t)NW * R * NT * 1024 <= LDS_MAX) &&
+           (ALL || XD == MOE_X_BF16 || UNIT * D * a.wk * 2 / 32 * St::TOKS * 4 <= PIECES * 64 * NW))
         a.wk *= 2;
     a.kc = ALL ? (a.K + CH - 1) / CH * CH : UNIT * D * a.wk;
     const size_t lds = (ALL ? 1 : 2) * St::bytes(a.kc) + (a.wk > 1 ? (size_t)NW * R * NT * 1024 : 0);
@@ -855,6 +852,14 @@ int pick(const LinArgs& a, hipStream_t st) {
         }
     }
     if (Stage<XD, 1, 16>::bytes(pad) <= 128 << 10) return launch<XD, G, 1, 16, 1, 2, true, EVEN, 8>(a, st);
+    if constexpr (XD == MOE_X_F32) {
+        // Long rows of fp32: the fewer tokens a stage holds, the more inputs, and the more waves share a row tile; each
+        // tile of tokens reads the codes again.  By 4, 8 and 16 tokens: 16 x 300 x 8192 13, 21 and 39 us; 16 x 2000 x
+        // 8192 24, 23 and 40 us; 64 x 2000 x 8192 53, 43 and 43 us; 64 x 8192 x 4096 97, 54 and 39 us.
+        const int64_t groups = ((int64_t)a.N + 15) / 16;
+        if (a.T <= 4 || groups * ((a.T + 3) / 4) <= 256) return launch<XD, G, 1, 4, 1, 1, false, EVEN, 8>(a, st);
+        if (a.T <= 8 || groups * ((a.T + 7) / 8) <= 1024) return launch<XD, G, 1, 8, 1, 1, false, EVEN, 8>(a, st);
+    }
     return launch<XD, G, 1, 16, 1, 1, false, EVEN, 8>(a, st);
 }
 

@@ -77,7 +77,8 @@ SHAPES = [(1, 1, 32, 32), (1, 3, 96, 32), (2, 16, 128, 128), (3, 17, 64, 64), (4
           (40, 32769, 128, 32), (64, 33000, 384, 128), (65, 16400, 160, 32), (130, 11000, 448, 64), (33, 32800, 1088, 64),
           (20, 32777, 192, 64), (300, 7000, 96, 32), (64, 80000, 320, 32),
           # rows of x too long to lie in LDS whole
-          (16, 64, 8192, 128), (13, 40, 8224, 32), (40, 100, 8256, 64)]
+          (16, 64, 8192, 128), (13, 40, 8224, 32), (40, 100, 8256, 64), (3, 50, 8224, 32), (8, 5000, 4128, 32),
+          (23, 2000, 4160, 64), (64, 4099, 2048, 32), (33, 70, 2080, 32)]
 
 
 @pytest.mark.parametrize("xt", ["bf16", "f32"])
