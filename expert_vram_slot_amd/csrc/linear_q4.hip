@@ -831,10 +831,12 @@ int launch_tile(const LinArgs& a, hipStream_t st) {
 template <int XD, int G, bool EVEN>
 int pick(const LinArgs& a, hipStream_t st) {
     const int pad = (a.K + CH - 1) / CH * CH;
-    // x whole in LDS: as long as two workgroups share a CU, or one of 16 tokens
-    if (a.T == 1 && Stage<XD, 1, 1>::bytes(pad) <= 64 << 10) return launch<XD, G, 1, 1, 1, 2, true, EVEN, 8>(a, st);
-    if (a.T <= 4 && Stage<XD, 1, 4>::bytes(pad) <= 64 << 10) return launch<XD, G, 1, 4, 1, 2, true, EVEN, 8>(a, st);
-    if (a.T <= 8 && Stage<XD, 1, 8>::bytes(pad) <= 80 << 10) return launch<XD, G, 1, 8, 1, 2, true, EVEN, 8>(a, st);
+    // x whole in LDS: as long as two workgroups share a CU, and bf16 as long as one has room (8 x 4000 x 6144: 8.5 us,
+    // in stages 10 us; 5 x 20000 x 8192 33 and 40 us; but fp32, 8 x 40000 x 2688: 59 and 49 us)
+    const size_t most = XD == MOE_X_BF16 ? 128 << 10 : 80 << 10;
+    if (a.T == 1 && Stage<XD, 1, 1>::bytes(pad) <= most) return launch<XD, G, 1, 1, 1, 2, true, EVEN, 8>(a, st);
+    if (a.T <= 4 && Stage<XD, 1, 4>::bytes(pad) <= most) return launch<XD, G, 1, 4, 1, 2, true, EVEN, 8>(a, st);
+    if (a.T <= 8 && Stage<XD, 1, 8>::bytes(pad) <= most) return launch<XD, G, 1, 8, 1, 2, true, EVEN, 8>(a, st);
     // More tokens.  bf16: tiles of 64 tokens by 256 rows or of 32 by 256, one a CU at a time, of which the first take
     // half as long again (2.6 and 1.75 us a unit): whichever ends sooner (131072 x 4096: 64 tokens 102 and 124 us, 32
     // tokens 96 and 75 us), as long as half the CUs get one (64 x 24576 x 4096: 32 us, by 16 tokens a wave 48; 64 x

@@ -78,13 +78,14 @@ SHAPES = [(1, 1, 32, 32), (1, 3, 96, 32), (2, 16, 128, 128), (3, 17, 64, 64), (4
           (20, 32777, 192, 64), (300, 7000, 96, 32), (64, 80000, 320, 32),
           # rows of x too long to lie in LDS whole
           (16, 64, 8192, 128), (13, 40, 8224, 32), (40, 100, 8256, 64), (3, 50, 8224, 32), (8, 5000, 4128, 32),
-          (23, 2000, 4160, 64), (64, 4099, 2048, 32), (33, 70, 2080, 32)]
+          (23, 2000, 4160, 64), (64, 4099, 2048, 32), (33, 70, 2080, 32), (4, 300, 12320, 32), (7, 333, 8064, 64),
+          (1, 37, 40000, 64)]
 
 
 @pytest.mark.parametrize("xt", ["bf16", "f32"])
 @pytest.mark.parametrize("T,N,K,group", SHAPES)
 def test_linear_exact(m, T, N, K, group, xt):
-    # |x| <= 2, K * 23 * 2 < 2^19, scales 1, 1/2, 1/4 (units of 1/4): below 2^24 units
+    # |x| <= 2, K * 23 * 2 < 2^21, scales 1, 1/2, 1/4 (units of 1/4): below 2^24 units
     wq, scales, g = weights(N, K, group, T * 1000 + N, True)
     x = torch.randint(-2, 3, (T, K), device="cuda", generator=g).to(DT[xt])
     bias = torch.randint(-8, 9, (N,), device="cuda", generator=g).float() if N % 2 else None
