@@ -308,11 +308,16 @@ __global__ void __launch_bounds__(SUM_THREADS) k_balance_sum(BalWs ws, int block
     if (tid == 0) write_totals(o, E, n, of, all, l2);
 }
 
-// f is taken less its mean 1/E, as whole numbers over whole numbers: the
-// subtraction f_e - sum f p of nearly equal numbers (a balanced router) then
-// costs no digits, since sum p = 1.  p, lse and dz are fp32 numbers: fp32 is
-// enough for exp and the products.  Bound by memory: 65537 x 512 bf16 in 31 us,
-// 4.3 TB/s of z and dz.
+// p is exp(z - lse) over its own sum: lse is rounded to fp32, and without the
+// division that rounding, 2^-24 |lse|, would be in every p (at logits around 10^4
+// the fourth digit), and p would not add up to 1.  Where the sum shows that lse is
+// further off than a factor of 2, the row's largest logit takes its place.  f is
+// taken less its mean 1/E, as whole numbers over whole numbers: the subtraction
+// f_e - sum f p of nearly equal numbers (a balanced router) then costs no digits,
+// since sum p = 1.  The differences are rounded once, the exponentials, sums of
+// positive terms and products are good to fp32's last bits, and dz is an fp32
+// number or shorter: fp32 is enough.
+// 65537 x 512 bf16 in 32.5 us, 4.1 TB/s of z and dz (31.5 us without the sum).
 template <int ZD, int VEC, int NE>
 __global__ void __launch_bounds__(256) k_balance_bwd(const void* z, const float* __restrict__ lse,
                                                      const uint8_t* __restrict__ mask,
@@ -332,33 +337,54 @@ __global__ void __launch_bounds__(256) k_balance_bwd(const void* z, const float*
         f[j] = e < E ? (float)((double)((int64_t)counts[e] * E - picks) * gb) : 0.0f;
     }
     for (int64_t t = (int64_t)blockIdx.x * NW + wid; t < T; t += (int64_t)gridDim.x * NW) {
-        const bool live = !mask || mask[t];
-        float p[NE], dot = 0.0f, l = 0.0f;
-        if (live) {
-            l = lse[t];
-            load_row<ZD, VEC, NE>(z, t, E, lane, p);
+        const auto put = [&](const auto& d) {
+#pragma unroll
+            for (int j = 0; j < NE / VEC; ++j) {
+                const int e = (lane + 64 * j) * VEC;
+                if (e >= E) continue;
+                if constexpr (ZD == MOE_X_F32) {
+                    reinterpret_cast<float*>(dz)[t * E + e] = d(j);
+                } else if constexpr (VEC == 1) {
+                    reinterpret_cast<__bf16*>(dz)[t * E + e] = (__bf16)d(j);
+                } else {
+                    reinterpret_cast<bf16x2*>(dz)[(t * E + e) / 2] = bf16x2{(__bf16)d(2 * j), (__bf16)d(2 * j + 1)};
+                }
+            }
+        };
+        if (mask && !mask[t]) {
+            put([](int) { return 0.0f; });
+            continue;
+        }
+        float p[NE], sum, dot;  // p: before the division
+        const auto softmax = [&](float at) {
+            sum = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int j = 0; j < NE; ++j) {
-                p[j] = expf(p[j] - l);
+                p[j] = expf(p[j] - at);
+                sum += p[j];
                 dot = fmaf(p[j], f[j], dot);
             }
-        }
-        dot = moe::wave_all_sum(dot);
-        const float c = gz * l - dot;
+            sum = moe::wave_all_sum(sum);
+            dot = moe::wave_all_sum(dot);
+        };
+        const float l = lse[t];
+        load_row<ZD, VEC, NE>(z, t, E, lane, p);
+        softmax(l);
+        if (!(sum > 0.5f && sum < 2.0f)) {
+            load_row<ZD, VEC, NE>(z, t, E, lane, p);
+            float m = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NE / VEC; ++j) {
-            const int e = (lane + 64 * j) * VEC;
-            if (e >= E) continue;
-            const float d = live ? p[VEC * j] * (f[VEC * j] + c) : 0.0f;
-            if constexpr (ZD == MOE_X_F32) {
-                reinterpret_cast<float*>(dz)[t * E + e] = d;
-            } else if constexpr (VEC == 1) {
-                reinterpret_cast<__bf16*>(dz)[t * E + e] = (__bf16)d;
-            } else {
-                const float d1 = live ? p[VEC * j + 1] * (f[VEC * j + 1] + c) : 0.0f;
-                reinterpret_cast<bf16x2*>(dz)[(t * E + e) / 2] = bf16x2{(__bf16)d, (__bf16)d1};
+            for (int j = 0; j < NE; ++j) m = fmaxf(m, p[j]);
+            m = moe::wave_all_max(m);
+            softmax(m == -INFINITY ? 0.0f : m);  // nothing above -inf: all 0 (a NaN stays one)
+            if (sum == 0.0f) {
+                put([](int) { return 0.0f; });
+                continue;
             }
         }
+        const float r = __builtin_amdgcn_rcpf(sum);  // to the last bit
+        const float c = (gz * l - dot * r) * r;
+        put([&](int i) { return p[i] * fmaf(f[i], r, c); });
     }
 }
 

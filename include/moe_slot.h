@@ -511,7 +511,9 @@ int moe_balance_loss(const void* z, int z_dtype, const int32_t* ids, const uint8
  * with g_b, g_z = dloss[0..1] (device float[2], the losses' own gradients or
  * weights).  z, mask: as given to moe_balance_loss; lse, counts, totals: its
  * outputs.  dz: device [T][E] in z_dtype out (overwritten; may alias z), 0 for
- * tokens left out.  Errors: as moe_balance_loss. */
+ * tokens left out, whatever the weights.  In fp32; p is divided by its own sum,
+ * so its digits do not depend on where the logits lie, nor on lse's rounding.
+ * Errors: as moe_balance_loss. */
 int moe_balance_loss_bwd(const void* z, int z_dtype, const float* lse, const uint8_t* mask, const int32_t* counts,
                          const int32_t* totals, const float* dloss, int T, int E, void* dz, hipStream_t stream);
 

@@ -508,6 +508,60 @@ def test_balance_gradient_against_differences(m):
             assert abs(float(o["dz"][t, e]) - want) <= tol
 
 
+def check_balance_grad(z, o, dloss, mask=None):
+    """dz of fp32 softmaxes against the formula in double, from the logits themselves.
+
+    In units of u = 2^-24: an exponential is off by |z - max| (the difference is rounded) and 2 (its own last bit); a sum
+    of a row by that of its terms and D = E / 64 + 8 roundings; the division by it by 5, a product by 1.  f less its mean
+    is rounded once, lse, its factor and their product once each, the two sums inside the bracket once each."""
+    zh = host64(z)
+    E = zh.shape[1]
+    w = ref.balance(zh, np.zeros((len(zh), 1), np.int32), None if mask is None else mask.cpu().numpy())
+    counts, (n, picks) = o["counts"].cpu().numpy().astype(np.float64), o["totals"].cpu().numpy().astype(np.float64)
+    p, live = w["p"], w["live"]
+    f = (counts * E - picks) * dloss[0] / (n * picks)
+    zt = 2 * dloss[1] * w["lse"][:, None] / n
+    want = p * (f[None] - (p @ f)[:, None] + zt)
+    u, D = 2.0 ** -24, E / 64 + 8
+    with np.errstate(invalid="ignore"):
+        e = np.where(p > 0, zh.max(axis=1, keepdims=True) - zh, 0) + 2
+    total = (p * e).sum(axis=1, keepdims=True) + D
+    dot, size = (p * np.abs(f)).sum(axis=1, keepdims=True), np.abs(f)[None] + np.abs(zt)
+    inner = (p * np.abs(f) * e).sum(axis=1, keepdims=True) + dot * (1 + D + total + 6)
+    tol = p * (np.abs(f)[None] + inner + 3 * np.abs(zt) + (size + dot) * (2 + e + total + 7)) * u * (1 + 2.0 ** -10)
+    tol = tol + 2.0 ** -126 * (size + dot + 1)
+    if z.dtype == torch.bfloat16:
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want)
+    got = host64(o["dz"])
+    assert np.all(np.abs(got - want)[live] <= tol[live])
+    assert np.all(got[~live] == 0)
+
+
+@pytest.mark.parametrize("zt,shift", [("f32", 0.0), ("f32", 1e4), ("f32", -1e6), ("f32", 1e6), ("bf16", 1e6),
+                                      ("f32", 1e9), ("f32", -2e38), ("bf16", -1e30)])
+@pytest.mark.parametrize("T,E,k", [(33, 64, 4), (257, 288, 8), (40, 1025, 6), (5, 4096, 2)])
+def test_balance_gradient_of_far_logits(m, T, E, k, zt, shift):
+    """The softmax does not depend on where the logits lie, nor does its gradient."""
+    z, g = logits(T, E, T * E, "f32")
+    z = (z * max(1.0, abs(shift) * 2.0 ** -24) + shift).to(DT[zt])  # at least about one step of fp32 apart
+    ids = torch.randint(0, E, (T, k), device="cuda", generator=g).to(torch.int32)
+    mask = (torch.rand(T, device="cuda", generator=g) < 0.8).to(torch.uint8)
+    for dloss in ((0.7, 0.0), (0.0, 0.2), (-0.4, 0.1)):
+        check_balance_grad(z, run_balance(m, z, ids, mask, dloss), dloss, mask)
+
+
+def test_balance_gradient_of_tokens_left_out_is_0_whatever_the_weights(m):
+    z, g = logits(9, 70, 5)
+    ids = torch.randint(0, 70, (9, 3), device="cuda", generator=g).to(torch.int32)
+    mask = torch.ones(9, dtype=torch.uint8, device="cuda")
+    mask[1] = 0
+    z[4] = -float("inf")
+    for dloss in ((float("inf"), 0.0), (0.0, float("nan"))):
+        dz = run_balance(m, z, ids, mask, dloss)["dz"]
+        assert torch.all(dz[1] == 0) and torch.all(dz[4] == 0)
+        assert torch.isnan(dz[0]).any()
+
+
 def test_balance_gradient_in_place(m):
     z, g = logits(100, 48, 3)
     ids = z.topk(4, dim=1).indices.to(torch.int32)
