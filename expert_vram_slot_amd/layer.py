@@ -37,6 +37,19 @@ def host_threads() -> int:
     return max(1, min(16, os.cpu_count() or 1))
 
 
+# Element types that the kernels read as an activation format (bf16 also as the bits of it).
+X_TYPES = {MOE_X_F32: (torch.float32,), MOE_X_BF16: (torch.bfloat16, torch.int16, torch.uint16)}
+
+
+def _check_given(what, t, n, dtypes, device):
+    """A tensor that a call brings: n elements at least, one after the other,
+    of a type that the kernels read as what it is, on the object's device."""
+    assert isinstance(t, torch.Tensor), f"{what} is no tensor"
+    assert t.dtype in dtypes, f"{what} is {t.dtype}, not {dtypes[0]}"
+    assert t.device == device, f"{what} is on {t.device}, not {device}"
+    assert t.is_contiguous() and t.numel() >= n, f"{what} is {tuple(t.shape)}, strides {t.stride()}: {n} values needed in a row"
+
+
 class SlotLayer:
     def __init__(self, *, E, k, H, I, S, w_type, T_max, policy, host_store, slot_store, G, bias=None,
                  n_threads=None, device="cuda"):
@@ -349,14 +362,15 @@ class DecodeHead:
 
     wq: device uint8 [V][H/2], scales: device fp16 [V][H/group] (the layout of
     moe_linear_q4); bias: device float [V] or None.  x_dtype is the stack's
-    activation format.
+    activation format.  What a call brings has to be of the types given here
+    and on the head's device (AssertionError otherwise, before any launch).
     """
 
     def __init__(self, *, H, V, wq, scales, group, T_max, x_dtype=MOE_X_BF16, bias=None, device="cuda"):
         dev = torch.device(device)
         assert H % group == 0 and tuple(wq.shape) == (V, H // 2) and tuple(scales.shape) == (V, H // group)
         assert wq.dtype == torch.uint8 and scales.dtype == torch.float16 and wq.is_contiguous() and scales.is_contiguous()
-        assert bias is None or (tuple(bias.shape) == (V,) and bias.dtype == torch.float32)
+        assert bias is None or (tuple(bias.shape) == (V,) and bias.dtype == torch.float32 and bias.is_contiguous())
         self.H, self.V, self.T_max, self.x_dtype = H, V, T_max, x_dtype
         self.wq, self.scales, self.group, self.bias = wq, scales, group, bias
         self.logits_buf = torch.empty(T_max, V, dtype=torch.float32, device=dev)
@@ -364,18 +378,37 @@ class DecodeHead:
         self.prob = torch.empty(T_max, dtype=torch.float32, device=dev)
         self.ws_bytes = moe_sample_workspace_bytes(T_max, V)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
+        assert all(w is None or w.device == self.ids.device for w in (wq, scales, bias))
+
+    def _row_stride(self, x, T):
+        """Elements from one row of x to the next, of T rows of H: rows of a
+        wider matrix, or H where x is contiguous in whatever shape."""
+        if isinstance(x, torch.Tensor) and x.dim() == 2 and x.shape[0] >= T and x.shape[1] == self.H and x.stride(1) == 1:
+            _check_given("x", x[:1].reshape(-1), min(T, 1) * self.H, X_TYPES[self.x_dtype], self.ids.device)
+            return x.stride(0) if T > 1 else self.H
+        _check_given("x", x, T * self.H, X_TYPES[self.x_dtype], self.ids.device)
+        return self.H
 
     def logits(self, x, T):
-        """Logits [T][V] fp32 of x (device [T][H] in x_dtype): a view of this object's buffer."""
+        """Logits [T][V] fp32 of x (device [T][H] in x_dtype, rows any
+        16-byte multiple apart): a view of this object's buffer."""
         assert T <= self.T_max
+        ldx = self._row_stride(x, T)
         with torch.cuda.device(self.ids.device):
-            moe_linear_q4(x, self.x_dtype, self.H, self.wq, self.scales, self.group, self.bias, T, self.V, self.H,
+            moe_linear_q4(x, self.x_dtype, ldx, self.wq, self.scales, self.group, self.bias, T, self.V, self.H,
                           self.logits_buf, MOE_X_F32, self.V, torch.cuda.current_stream())
         return self.logits_buf[:T]
 
     def step(self, x, T, u, temperature=None, min_p=None, top_k=None, top_p=None):
         """The next token of each of T rows of x: (ids [T], prob [T]), views of
-        this object's buffers.  u and the settings as moe_sample takes them."""
+        this object's buffers.  u and the settings as moe_sample takes them:
+        device float32 [T], top_k int32 [T]."""
+        _check_given("u", u, T, (torch.float32,), self.ids.device)
+        for what, t in (("temperature", temperature), ("min_p", min_p), ("top_p", top_p)):
+            if t is not None:
+                _check_given(what, t, T, (torch.float32,), self.ids.device)
+        if top_k is not None:
+            _check_given("top_k", top_k, T, (torch.int32,), self.ids.device)
         self.logits(x, T)
         with torch.cuda.device(self.ids.device):
             moe_sample(self.logits_buf, MOE_X_F32, self.V, T, self.V, temperature, min_p, top_k, top_p, u, self.ids,

@@ -657,6 +657,28 @@ def test_decode_head_behind_a_stack(m):
         assert np.all(np.abs(bias.cpu().numpy() - want_bias) <= np.spacing(np.abs(want_bias)))
 
 
+def test_decode_head_takes_x_as_it_lies(m):
+    """Rows of a wider matrix, a flat x, one with dimensions between and the bits of bf16 give what a copy gives."""
+    from expert_vram_slot_amd.layer import DecodeHead
+    H, V, T, group = 256, 1003, 5, 32
+    wq, scales, g = weights(V, H, group, 12)
+    head = DecodeHead(H=H, V=V, wq=wq, scales=scales, group=group, T_max=8)
+    wide = torch.randn(T + 1, 3 * H, device="cuda", generator=g).bfloat16()
+    u = torch.rand(T, device="cuda", generator=g)
+    k = torch.full((T,), 20, dtype=torch.int32, device="cuda")
+    x = wide[:T, H:2 * H].contiguous()
+    want = [o.clone() for o in (head.logits(x, T), *head.step(x, T, u, top_k=k))]
+    for given in (wide[:, H:2 * H], x.reshape(-1), x.view(T, 1, H), x.view(torch.int16)):
+        got = (head.logits(given, T), *head.step(given, T, u, top_k=k))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    got = head.step(wide[2:3, H:2 * H], 1, u[2:], top_k=k[2:])
+    assert all(torch.equal(a, b[2:3]) for a, b in zip(got, want[1:]))
+    with pytest.raises(m.MoeError):
+        head.logits(torch.zeros(T, H + 4, dtype=torch.bfloat16, device="cuda")[:, :H], T)  # rows 8 bytes off 16
+    with pytest.raises(m.MoeError):
+        head.logits(x[:1].expand(T, H), T)  # one row for all
+
+
 def _whole_path(m, T, V, K, group, seed):
     """Buffers and a call of every operator; returns (call, inputs to refill, outputs)."""
     wq, scales, g = weights(V, K, group, seed)

@@ -149,6 +149,45 @@ def test_decode_head_refuses(mlib, change):
         DecodeHead(**{**a, **change})
 
 
+@pytest.mark.parametrize("change", [
+    dict(x="f32"), dict(x="f16"), dict(x="short"), dict(x="few rows"), dict(x="every other column"), dict(x="numpy"),
+    dict(x="elsewhere"), dict(T=3), dict(u="f64"), dict(u="short"), dict(u="strided"), dict(u="elsewhere"),
+    dict(temperature="f64"), dict(min_p="f16"), dict(top_p="short"), dict(top_k="i64"), dict(top_k="f32"),
+    dict(top_k="short"), dict(u=None)])
+def test_decode_head_step_refuses(change):
+    """What the kernels would read as something else, or past its end (nothing is launched: the head is on the CPU)."""
+    torch = pytest.importorskip("torch")
+    from expert_vram_slot_amd.layer import DecodeHead
+    head = DecodeHead(H=64, V=8, wq=torch.zeros(8, 32, dtype=torch.uint8), scales=torch.zeros(8, 2, dtype=torch.float16),
+                      group=32, T_max=2, device="cpu")
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    bad = {"f32": torch.zeros(2), "f64": torch.zeros(2, dtype=torch.float64), "f16": torch.zeros(2, dtype=torch.float16),
+           "i64": torch.zeros(2, dtype=torch.int64), "short": torch.zeros(1), "strided": torch.zeros(4)[::2],
+           "elsewhere": torch.zeros(2, device="meta"), None: None}
+    bad_x = {"f32": x.float(), "f16": x.half(), "short": x.reshape(-1)[:127], "few rows": x[:1],
+             "every other column": torch.zeros(2, 128, dtype=torch.bfloat16)[:, ::2], "numpy": x.float().numpy(),
+             "elsewhere": torch.zeros(2, 64, dtype=torch.bfloat16, device="meta")}
+    a = dict(x=x, T=2, u=torch.zeros(2))
+    for name, value in change.items():
+        a[name] = value if name == "T" else bad_x[value] if name == "x" else bad[value]
+        if (name, value) == ("top_k", "short"):
+            a[name] = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(AssertionError):
+        head.step(**a)
+
+
+@pytest.mark.parametrize("what", ["wq", "scales", "bias", "strided bias"])
+def test_decode_head_refuses_weights_elsewhere(what):
+    torch = pytest.importorskip("torch")
+    from expert_vram_slot_amd.layer import DecodeHead
+    a = dict(H=64, V=8, wq=torch.zeros(8, 32, dtype=torch.uint8), scales=torch.zeros(8, 2, dtype=torch.float16), group=32,
+             T_max=2, device="cpu", bias=torch.zeros(8))
+    DecodeHead(**a)
+    a.update({"bias": torch.zeros(16)[::2]} if what == "strided bias" else {what: a[what].to("meta")})
+    with pytest.raises(AssertionError):
+        DecodeHead(**a)
+
+
 def test_reference_codes_are_the_slab_planes():
     """The nibble order is a Q4B32 slab's: decoding the generator's gate plane gives the oracle's weights."""
     import oracle
