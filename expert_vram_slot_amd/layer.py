@@ -37,7 +37,8 @@ def host_threads() -> int:
     return max(1, min(16, os.cpu_count() or 1))
 
 
-# Element types that the kernels read as an activation format (bf16 also as the bits of it).
+# Element types that the kernels read as an activation format (bf16 also as the bits of it), and as a mask.
+MASK_TYPES = (torch.uint8, torch.bool, torch.int8)
 X_TYPES = {MOE_X_F32: (torch.float32,), MOE_X_BF16: (torch.bfloat16, torch.int16, torch.uint16)}
 
 
@@ -105,6 +106,9 @@ class SlotLayer:
         self.gather_events = None  # (start, end) torch events recorded around cache_gather when set
         self.route_flags = 0       # moe_route_ex flags (MOE_ROUTE_DAMPED)
         self.stats_out = None      # moe_balance_loss's outputs and workspace, made by the first balance()
+        # steps so far, tokens of the last one, and (steps, T) at the last balance(); a replayed graph moves on without
+        # them, so from the first capture on they are not held against a call
+        self.steps, self.step_T, self.balanced, self.captured = 0, 0, None, False
 
     def init_cache(self, resident=None):
         cache_init(self.st, resident)
@@ -131,6 +135,8 @@ class SlotLayer:
         # 1. router (picks, or weights of given picks)
         moe_route_ex(x, self.x_dtype, self.G, self.bias, None if ids_in is None else self.ids, T, self.H, self.E,
                      self.k, self.route_flags, self.ids, self.w, self.logits, cur)
+        self.steps, self.step_T = self.steps + 1, T
+        self.captured |= torch.cuda.is_current_stream_capturing()
         ids = self.ids
         # 2. cache step: victims, miss list, remap
         cache_manage(self.st, self.policy, ids, P, self.slot_ids, self.miss, self.n_miss, self.host_miss,
@@ -173,12 +179,17 @@ class SlotLayer:
 
 
     def balance(self, T, mask=None):
-        """Router statistics of the last step's T tokens (moe_balance_loss on
-        its logits and picks; mask: device uint8 [T], 0 = padding).  Returns
-        a dict of counts [E], totals [2], share [E] (double: the brightness
-        moe_bias_table takes), lse [T] and loss [2], views of buffers the next
-        call overwrites."""
+        """Router statistics of the last step's first T tokens (moe_balance_loss
+        on its logits and picks; mask: device uint8 or bool [T], 0 = padding).
+        Returns a dict of counts [E], totals [2], share [E] (double: the
+        brightness moe_bias_table takes), lse [T] and loss [2], views of buffers
+        the next call overwrites.  Layers of a SlotStack share one SlotLayer:
+        after a stack's step it holds the last layer's, each layer's are there
+        in on_layer."""
         assert T <= self.T_max
+        assert T <= self.step_T or self.captured, f"the last step had {self.step_T} tokens"
+        if mask is not None:
+            _check_given("mask", mask, T, MASK_TYPES, self.ids.device)
         o = self.stats_out
         if o is None:
             dev = self.ids.device
@@ -192,13 +203,20 @@ class SlotLayer:
         with torch.cuda.device(self.ids.device):
             moe_balance_loss(self.logits, MOE_X_F32, self.ids, mask, T, self.E, self.k, o["counts"], o["totals"],
                              o["share"], o["lse"], o["loss"], o["ws"], o["ws_bytes"], torch.cuda.current_stream())
+            self.captured |= torch.cuda.is_current_stream_capturing()
+        self.balanced = (self.steps, T)
         return dict(counts=o["counts"], totals=o["totals"], share=o["share"], lse=o["lse"][:T], loss=o["loss"])
 
     def balance_grad(self, T, dloss, mask=None):
         """Gradient of the last balance()'s losses (weights dloss: device
-        float [2]; same T and mask) to the last step's logits, [T][E] fp32."""
+        float32 [2]; same T and mask, no step between) to the last step's
+        logits, [T][E] fp32."""
         o = self.stats_out
         assert o is not None and T <= self.T_max
+        assert self.balanced == (self.steps, T) or self.captured, "balance() of the last step, with the same T, comes first"
+        _check_given("dloss", dloss, 2, (torch.float32,), self.ids.device)
+        if mask is not None:
+            _check_given("mask", mask, T, MASK_TYPES, self.ids.device)
         dz = torch.empty(T, self.E, dtype=torch.float32, device=self.ids.device)
         with torch.cuda.device(self.ids.device):
             moe_balance_loss_bwd(self.logits, MOE_X_F32, o["lse"], mask, o["counts"], o["totals"], dloss, T, self.E, dz,

@@ -679,6 +679,63 @@ def test_decode_head_takes_x_as_it_lies(m):
         head.logits(x[:1].expand(T, H), T)  # one row for all
 
 
+def test_layer_balance_of_steps_of_different_sizes(m):
+    """The statistics are the last step's, its first tokens' alone too; a graph's step and balance may be of another size."""
+    import synth
+    from expert_vram_slot_amd.layer import SlotLayer
+    E, k, H, I, S = 16, 4, 256, 128, 16
+    base = synth.config_seed("c4")
+    store = synth.slabs(synth.W_Q4B32, base, 0, 0, E, H, I, 0.05)
+    pinned = torch.empty(store.shape, dtype=torch.uint8, pin_memory=True)
+    pinned.copy_(torch.from_numpy(store))
+    G = synth.normal(synth.key(base, synth.TAG_G, 0, 0), (E, H), 0.5, synth.X_BF16)
+    L = SlotLayer(E=E, k=k, H=H, I=I, S=S, w_type=synth.W_Q4B32, T_max=8, policy="static", host_store=pinned,
+                  slot_store=torch.from_numpy(store).cuda(), G=torch.from_numpy(G.view(np.int16)).cuda(), n_threads=1)
+    L.init_cache(torch.arange(S, dtype=torch.int32, device="cuda"))
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(8, H, device="cuda", generator=g).bfloat16()
+    d = torch.tensor([1.0, 0.1], device="cuda")
+
+    def check(T, mask=None):
+        b, dz = L.balance(T, mask), L.balance_grad(T, d, mask)
+        z, picks = host64(L.logits[:T * E].view(T, E)), L.ids[:T * k].view(T, k).cpu().numpy()
+        mh = None if mask is None else mask[:T].cpu().numpy()
+        w = ref.balance(z, picks, mh)
+        np.testing.assert_array_equal(b["counts"].cpu().numpy(), w["counts"])
+        np.testing.assert_allclose(host64(b["share"]), w["share"], rtol=(T + E + 64) * 2.0 ** -52)
+        np.testing.assert_allclose(host64(dz), ref.balance_grad(z, picks, np.array([1.0, 0.1]), mh), rtol=1e-4, atol=1e-7)
+
+    for T in (8, 3):
+        L.step(x[:T], T, host_pass=False)
+        check(T)
+        check(T - 1, torch.arange(8, device="cuda") > 0)  # a mask of bool, longer than the batch
+    with pytest.raises(AssertionError):
+        L.balance(4)
+    L.balance(3)
+    L.step(x[:5], 5, host_pass=False)
+    with pytest.raises(AssertionError):
+        L.balance_grad(3, d)
+    check(5)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        L.step(x, 8, host_pass=False)
+        L.balance(8)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.step(x, 8, host_pass=False)
+        L.balance(8)
+    for rep in range(3):
+        L.step(x[:2], 2, host_pass=False)
+        check(2)
+        x.copy_(torch.randn(8, H, device="cuda", generator=g))
+        graph.replay()
+        dz = L.balance_grad(8, d).clone()
+        check(8)
+        assert torch.equal(dz, L.balance_grad(8, d))
+
+
 def _whole_path(m, T, V, K, group, seed):
     """Buffers and a call of every operator; returns (call, inputs to refill, outputs)."""
     wq, scales, g = weights(V, K, group, seed)

@@ -188,6 +188,55 @@ def test_decode_head_refuses_weights_elsewhere(what):
         DecodeHead(**a)
 
 
+def _layer_after_a_step(T):
+    """The part of a SlotLayer that balance() looks at, on the CPU, as a step of T tokens leaves it."""
+    import torch
+
+    from expert_vram_slot_amd.layer import SlotLayer
+    L = SlotLayer.__new__(SlotLayer)
+    L.E, L.k, L.T_max, L.stats_out = 8, 2, 4, None
+    L.logits, L.ids = torch.zeros(32), torch.zeros(8, dtype=torch.int32)
+    L.steps, L.step_T, L.captured, L.balanced = 1, T, False, None
+    return L
+
+
+@pytest.mark.parametrize("change", [dict(T=3), dict(T=5), dict(mask="i64"), dict(mask="f32"), dict(mask="short"),
+                                    dict(mask="strided"), dict(mask="elsewhere"), dict(mask="numpy")])
+def test_layer_balance_refuses(change):
+    torch = pytest.importorskip("torch")
+    L = _layer_after_a_step(2)
+    bad = {"i64": torch.ones(2, dtype=torch.int64), "f32": torch.ones(2), "short": torch.ones(1, dtype=torch.uint8),
+           "strided": torch.ones(4, dtype=torch.uint8)[::2], "elsewhere": torch.ones(2, dtype=torch.uint8, device="meta"),
+           "numpy": np.ones(2, np.uint8)}
+    a = dict(T=2)
+    a.update((n, bad.get(v, v)) for n, v in change.items())
+    with pytest.raises(AssertionError):
+        L.balance(**a)
+
+
+@pytest.mark.parametrize("change", [dict(T=1), dict(mask="i64"), dict(mask="short"), dict(dloss="f64"), dict(dloss="short"),
+                                    dict(dloss="strided"), dict(dloss="elsewhere"), dict(dloss=(1.0, 0.1)),
+                                    dict(before="no balance"), dict(before="another step")])
+def test_layer_balance_grad_refuses(change):
+    torch = pytest.importorskip("torch")
+    L = _layer_after_a_step(2)
+    L.stats_out, L.balanced = dict(lse=torch.zeros(4), counts=torch.zeros(8), totals=torch.zeros(2)), (1, 2)
+    bad = {"i64": torch.ones(2, dtype=torch.int64), "short": torch.ones(1), "f64": torch.ones(2, dtype=torch.float64),
+           "strided": torch.ones(4)[::2], "elsewhere": torch.ones(2, device="meta")}
+    a = dict(T=2, dloss=torch.ones(2))
+    for n, v in change.items():
+        if v == "no balance":
+            L.stats_out = L.balanced = None
+        elif v == "another step":
+            L.steps += 1
+        elif (n, v) == ("mask", "short"):
+            a[n] = torch.ones(1, dtype=torch.uint8)
+        else:
+            a[n] = bad.get(v, v) if isinstance(v, str) else v
+    with pytest.raises(AssertionError):
+        L.balance_grad(**a)
+
+
 def test_reference_codes_are_the_slab_planes():
     """The nibble order is a Q4B32 slab's: decoding the generator's gate plane gives the oracle's weights."""
     import oracle
