@@ -206,6 +206,16 @@ def test_linear_rows_past_32_bits(m, T, N, xt):
     assert torch.equal(torch.as_strided(y, (T, N), (ld, 1)), linear(m, x, wq, scales, group, None, "f32"))
 
 
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,K,group", [(513, 700, 256, 64), (4097, 300, 288, 32), (8193, 520, 256, 128), (1 << 20, 3, 32, 32)])
+def test_linear_prompts(m, T, N, K, group, xt):
+    """Whole numbers, as in test_linear_exact, by as many tokens as a prompt has, and by as many as a call takes."""
+    wq, scales, g = weights(N, K, group, T + N, True)
+    x = torch.randint(-2, 3, (T, K), device="cuda", generator=g).to(DT[xt])
+    want, _ = ref.linear_q4(host64(x), wq.cpu().numpy(), scales.cpu().numpy(), group)
+    np.testing.assert_array_equal(host64(linear(m, x, wq, scales, group, None, "f32")), want)
+
+
 # ------------------------------------------------------------------ sample
 
 
@@ -370,6 +380,50 @@ def test_sample_largest_vocabulary(m):
     check_draw(m, l, u)
     check_draw(m, l, u, one, None, (300 * one).to(torch.int32), 0.9 * one)
     check_draw(m, l, u, 3 * one, 1e-4 * one, None, 0.7 * one)
+
+
+@pytest.mark.parametrize("kind", ["none", "min", "k", "p", "wide", "mixed"])
+@pytest.mark.parametrize("T,V,lt", [(600, 33001, "bf16"), (600, 33001, "f32"), (2000, 33001, "f32"), (2001, 20479, "bf16"),
+                                    (65535, 8193, "bf16")])
+def test_sample_many_long_rows(m, T, V, lt, kind):
+    """More than 16384 segments of 1024 ids: a wave takes several of a row, the row's last wave fewer.  The first row of
+    each setting, the last and some between are looked at, and that no row lacks its id."""
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    l = torch.randn(T, V, device="cuda", generator=g, dtype=DT[lt]) * 2.5
+    u = torch.rand(T, device="cuda", generator=g)
+    opt = settings(T, g, kind, V)
+    ids, prob = draw(m, l, u, *opt, ldl=V + 1)
+    assert ids.min() >= 0 and ids.max() < V and prob.min() > 0
+    rows = list(range(12)) + [T // 2 + 60 * i + i for i in range(4)] + [T - 1]
+    one = lambda a, t: None if a is None else a[t:t + 1]  # noqa: E731
+    for t in rows:
+        o = [None if a is None else float(a[t]) for a in opt]
+        a = [d if v is None else v for v, d in zip(o, (1.0, 0.0, 0, 1.0))]
+        want, p, _ = ref.sample_row(host64(l[t]), float(u[t]), a[0], a[1], int(a[2]), a[3])
+        assert ids[t] == want, f"row {t}: {ids[t]}, not {want} ({a})"
+        assert abs(prob[t] - p) <= 2.0 ** -24 * p + V * 2.0 ** -min(51, 62 - (V - 1).bit_length()) + 1e-38
+        # the row alone, a segment a wave
+        alone = draw(m, l[t:t + 1], u[t:t + 1], *[one(x, t) for x in opt])
+        assert alone[0][0] == ids[t] and alone[1][0] == prob[t]
+
+
+@pytest.mark.parametrize("V", [40, 3000, 40000])
+def test_sample_signalling_nan(m, V):
+    """NaN of either kind and sign is never drawn."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    l = torch.randn(6, V, device="cuda", generator=g)
+    u = torch.rand(6, device="cuda", generator=g)
+    for lt, bits in (("f32", (0x7F800001, 0x7FC00000, -0x7FFFFF, -1)), ("bf16", (0x7F81, 0x7FC0, -0x7F, -1))):
+        x = l.to(DT[lt])
+        raw = x.view(torch.int32 if lt == "f32" else torch.int16)
+        for r, b in enumerate(bits):
+            raw[r, ::2] = b
+        raw[4] = bits[0]
+        raw[4, V // 2] = x[5].view(raw.dtype)[0]
+        check_draw(m, x, u)
+        check_draw(m, x, u, torch.full((6,), 0.9, device="cuda"), None, torch.full((6,), 7, dtype=torch.int32, device="cuda"),
+                   torch.full((6,), 0.8, device="cuda"))
+        check_draw(m, x, u, torch.zeros(6, device="cuda"))
 
 
 # ------------------------------------------------------------------ balance
