@@ -8,8 +8,9 @@
 // (the picks are whole numbers and carry no gradient).
 //
 // P_e is the brightness that "Nudge, don't cut" (oois.ee/pgo-sgb), "The method
-// in five lines", grades its bias by, so it is made in double: the softmax and
-// its sums run in double, in a fixed order.  One wave takes one token at a
+// in five lines", grades its bias by.  The bias table ranks the experts by it, and
+// experts nearly as bright would change places with fp32's rounding, so the softmax
+// and its sums run in double, in a fixed order.  One wave takes one token at a
 // time and keeps its experts' running sums in registers (lane l holds experts
 // l, l + 64, ...).
 #include <math.h>
@@ -24,9 +25,16 @@ namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int BAL_MAX_BLOCKS = 512;   // of the row kernel: two a CU
-constexpr int BAL_ONE = 128;          // batches of up to this many tokens: one workgroup does it all
-constexpr int SUM_E = 16;             // experts of a workgroup of the second pass
+constexpr int BAL_MAX_BLOCKS = 512;  // of the row kernel: two a CU
+// Batches of up to this many tokens: one workgroup does it all, in one launch.  One
+// and many workgroups, us, 4 picks, fp32: 64 experts 16 tokens 6.0 and 8.9, 64 tokens
+// 8.0 and 9.0, 128 tokens 10.7 and 9.7; 256 experts 16 tokens 7.4 and 10.8, 128 tokens
+// 16.2 and 10.9; 1024 experts 16 tokens 12.6 and 14.5, 128 tokens 49 and 15; 4096
+// experts 4 tokens 25 and 34, 128 tokens 202 and 35.  The two cross near 100 tokens of
+// 64 experts, 55 of 256, 35 of 512, 22 of 1024 and 10 of 4096: this rule, of tokens
+// alone, does not follow that.
+constexpr int BAL_ONE = 128;
+constexpr int SUM_E = 16;            // experts of a workgroup of the second pass
 constexpr int SUM_THREADS = 1024;
 
 // Waves of a row-kernel workgroup: sixteen where it is the only one, eight, or
@@ -113,8 +121,8 @@ __device__ __forceinline__ void write_totals(const BalOut& o, int E, int n, int 
 // side by side (a lane a token) for the logarithm, lse and the picks.  ONE: a
 // single workgroup, which also writes the outputs (64 x 128: 8.8 us).
 // Bound by the vector unit: about 40 instructions an exponential in double with
-// its share of the token's reductions (65537 x 512 bf16: 53 us, the unit busy
-// for three quarters of it; 16384 x 288 fp32: 15 us).
+// its share of the token's reductions (65537 x 512 bf16: 52 us, the unit busy
+// for four fifths of it; 16384 x 288 fp32: 15 us).
 template <int ZD, int VEC, int NE, bool ONE>
 __global__ void __launch_bounds__(64 * bal_waves(NE, ONE)) k_balance(const void* __restrict__ z,
                                                                      const int32_t* __restrict__ ids,
@@ -317,7 +325,8 @@ __global__ void __launch_bounds__(SUM_THREADS) k_balance_sum(BalWs ws, int block
 // since sum p = 1.  The differences are rounded once, the exponentials, sums of
 // positive terms and products are good to fp32's last bits, and dz is an fp32
 // number or shorter: fp32 is enough.
-// 65537 x 512 bf16 in 32.5 us, 4.1 TB/s of z and dz (31.5 us without the sum).
+// Bound by the vector unit: 65537 x 512 bf16 in 33 us, 4.1 TB/s of z and dz, 235
+// instructions a token, the unit busy throughout (31.5 us without the sum).
 template <int ZD, int VEC, int NE>
 __global__ void __launch_bounds__(256) k_balance_bwd(const void* z, const float* __restrict__ lse,
                                                      const uint8_t* __restrict__ mask,

@@ -26,9 +26,11 @@
 //  - x lies in LDS, all of it where that fits (workgroups then stay and take
 //    one row tile after the other, the codes' loads running on across tiles),
 //    else a stretch of inputs at a time in two buffers.
-// That is k_linear_q4, which memory bounds where it is large (one token, 131072 x
-// 2048 in groups of 32: 34 us, 4.5 TB/s; 16 x 8192 x 4096: 9.5 us) and its launch
-// and one tile's latencies where it is not (one token, 2048 x 2048: 5.5 us).
+// That is k_linear_q4.  One token, 131072 x 2048 in groups of 32: 34 us, 4.5 TB/s, 65
+// vector instructions for a chunk of 16 rows (8 of them products), the vector unit
+// busy half of the time: the waits for loads bound it.  Its launch and one tile's
+// latencies bound it where it is small (one token, 2048 x 2048: 5.5 us), the staging
+// of x before the first product in between (16 x 8192 x 4096: 9.4 us).
 // Many bf16 tokens by many rows go to k_linear_q4_tile, below.
 #include <atomic>
 #include <type_traits>
@@ -804,7 +806,9 @@ int launch(LinArgs a, hipStream_t st) {
     static std::atomic<uint64_t> asked{0};
     const int rc = ask_lds(reinterpret_cast<const void*>(kern), lds, asked);
     if (rc != MOE_OK) return rc;
-    // with x staged once, workgroups stay: as many as the card holds at a time
+    // with x staged once, workgroups stay: as many as the card holds at a time, the same number for each tile of
+    // tokens.  That number is cut down, so that with many tiles CUs may idle: fp32, 4096 rows, 4096 tokens 618 us (128
+    // tiles, 2 each), 4097 tokens 1213 us (129 tiles, 1 each).
     const int per = NW / a.wk;
     int64_t blocks = (groups + per - 1) / per;
     const int64_t most = 256 * (lds > 80 << 10 ? 1 : 2);
@@ -823,6 +827,8 @@ int launch_tile(const LinArgs& a, hipStream_t st) {
     if (rc != MOE_OK) return rc;
     const int64_t tiles = ((int64_t)a.T + 16 * NT - 1) / (16 * NT);
     int64_t blocks = ((int64_t)a.N + Ti::ROWS - 1) / Ti::ROWS;
+    // one workgroup a CU, the same number for each tile of tokens, cut down: 8192 tokens by 4096 x 4096 378 us (128
+    // tiles, 2 each, 727 TFLOP/s), 8193 tokens 625 us (129 tiles, 1 each: half of the CUs idle)
     if (blocks * tiles > 256) blocks = tiles >= 256 ? 1 : 256 / tiles;
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks, (unsigned)tiles), dim3(512), Ti::LDS, st, a);
     return moe_check_launch("moe_linear_q4");
@@ -841,7 +847,8 @@ int pick(const LinArgs& a, hipStream_t st) {
     // half as long again (2.6 and 1.75 us a unit): whichever ends sooner (131072 x 4096: 64 tokens 102 and 124 us, 32
     // tokens 96 and 75 us), as long as half the CUs get one (64 x 24576 x 4096: 32 us, by 16 tokens a wave 48; 64 x
     // 8192 x 4096: 28 and 18).  fp32: tiles of 32 by 256 where every CU gets one (32 x 65536 x 2048: 51 us, by 16 tokens
-    // 63; 64 x 16384 x 2048: 41 and 33).  Else 16 tokens by 16 rows a wave, the codes read again for each 16 tokens.
+    // 63; 64 x 16384 x 2048: 41 and 33), although all forms of that kernel spill 4 to 19 vector registers.  Else 16 tokens
+    // by 16 rows a wave, the codes read again for each 16 tokens.
     if (a.T > 16) {
         const int64_t by64 = ((int64_t)a.N + 255) / 256 * ((a.T + 63) / 64), by32 = ((int64_t)a.N + 255) / 256 * ((a.T + 31) / 32);
         if constexpr (XD == MOE_X_BF16) {

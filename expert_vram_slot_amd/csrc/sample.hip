@@ -27,14 +27,20 @@
 //                               mass of each segment above them) -> k_draw (one
 //                               workgroup a row: the cuts, the draw's segment,
 //                               the draw)
-// A row whose cut bins hold more than LIST ids (many equal logits, or one far
-// outlier under a high temperature) takes a radix selection instead, eight
-// bits of the logit's key a pass over the whole row: slower, the same result.
+// A row whose cut bins hold more than LIST ids takes a radix selection instead,
+// eight bits of the logit's key a pass over the whole row by one workgroup: the
+// same result, but 1.8 ms for a row of 131072 and 2.2 ms for 64 of them, against 26
+// and 58 us.  Many equal logits lead there, or one far outlier under a high
+// temperature; so may bf16 logits far from 0, where a step is wide (131072 of
+// spread 2 around 24 lie on steps of 1/8, some 3000 on each: any top-p whose cut
+// falls among the many).
 //
-// 64 x 131072 fp32: k_top 8 us (4 TB/s), k_bins 17, k_list 13.5, k_draw 11.6 us;
+// 64 x 131072 fp32: k_top 7.5 us (4.5 TB/s), k_bins 17, k_list 13.5, k_draw 11.7 us;
 // k_bins and k_list are bound by the vector unit (a mass costs about 24 double
-// instructions), k_draw and a single row (3 + 5.5 + 7 + 6.6 us) by the steps that
-// wait for one another.  17 x 5003 bf16 in k_row: 15.5 us, about 25 barriers.
+// instructions; 200 and 140 for 256 ids, 225 in both with bf16 and top-p, the unit
+// busy for 64 to 88 hundredths of the time), k_draw and a single row (3 + 5.5 + 7 +
+// 6.7 us) by the steps that wait for one another.  17 x 5003 bf16 in k_row: 15.5 us,
+// about 25 barriers.
 #include <math.h>
 
 #include <type_traits>
