@@ -25,6 +25,8 @@ MOE_W_F32, MOE_W_BF16, MOE_W_W8A8, MOE_W_Q4B32 = 0, 1, 2, 3
 MOE_STATIC, MOE_LRU, MOE_LFU = 0, 1, 2
 MOE_MAX_E, MOE_MAX_S, MOE_MAX_K = 4096, 1024, 32
 MOE_ROUTE_DAMPED = 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 POLICIES = {"static": MOE_STATIC, "lru": MOE_LRU, "lfu": MOE_LFU}
 
 
@@ -41,6 +43,12 @@ class CacheState(ctypes.Structure):
 
 class SlabLayout(ctypes.Structure):
     _fields_ = [("w", ctypes.c_int64 * 3), ("s", ctypes.c_int64 * 3), ("total", ctypes.c_int64)]
+
+
+class SelectRule(ctypes.Structure):
+    """moe_select_rule: how moe_route_select chooses and weighs."""
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("groups_kept", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class LayerDesc(ctypes.Structure):
@@ -99,6 +107,13 @@ def lib():
             "moe_balance_workspace_bytes": (sz, [i32, i32]),
             "moe_balance_loss": (i32, [vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
             "moe_balance_loss_bwd": (i32, [vp, i32, vp, vp, vp, vp, vp, i32, i32, vp, vp]),
+            "moe_route_logits": (i32, [vp, i32, vp, i32, i32, i32, vp, vp]),
+            "moe_route_select": (i32, [vp, i32, vp, vp, vp, i32, i32, i32, ctypes.POINTER(SelectRule), vp, vp, vp]),
+            "moe_route_select_bwd": (i32, [vp, i32, vp, vp, i32, i32, i32, ctypes.POINTER(SelectRule), vp, vp, vp]),
+            "moe_bias_balance": (i32, [vp, vp, i32, i32, f32, vp, vp]),
+            "moe_lora_workspace_bytes": (sz, [i32, i32, i32]),
+            "moe_lora_add": (i32, [vp, i32, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, i64, vp, i32, i64, vp,
+                                   sz, vp]),
             "moe_host_alloc": (vp, [sz]),
             "moe_host_free": (i32, [vp]),
         }
@@ -280,6 +295,44 @@ def moe_balance_loss_bwd(z, z_dtype, lse, mask, counts, totals, dloss, T, E, dz,
     return _check("moe_balance_loss_bwd", lib().moe_balance_loss_bwd(_p(z), z_dtype, _p(lse), _p(mask), _p(counts),
                                                                      _p(totals), _p(dloss), T, E, _p(dz),
                                                                      _stream(stream)))
+
+
+def select_rule(score="softmax", groups=1, groups_kept=None, group_top=1, renorm=True, scale=1.0) -> SelectRule:
+    """A moe_select_rule (groups_kept None: all of them)."""
+    return SelectRule(SCORES.get(score, score), groups, groups if groups_kept is None else groups_kept, group_top,
+                      int(renorm), scale)
+
+
+def moe_route_logits(x, x_dtype, G, T, H, E, logits, stream=None):
+    return _check("moe_route_logits", lib().moe_route_logits(_p(x), x_dtype, _p(G), T, H, E, _p(logits),
+                                                             _stream(stream)))
+
+
+def moe_route_select(z, z_dtype, bias, mask, ids_in, T, E, k, rule, ids, w, stream=None):
+    return _check("moe_route_select", lib().moe_route_select(_p(z), z_dtype, _p(bias), _p(mask), _p(ids_in), T, E, k,
+                                                             ctypes.byref(rule), _p(ids), _p(w), _stream(stream)))
+
+
+def moe_route_select_bwd(z, z_dtype, ids, dw, T, E, k, rule, dz_add, dz, stream=None):
+    return _check("moe_route_select_bwd", lib().moe_route_select_bwd(_p(z), z_dtype, _p(ids), _p(dw), T, E, k,
+                                                                     ctypes.byref(rule), _p(dz_add), _p(dz),
+                                                                     _stream(stream)))
+
+
+def moe_bias_balance(counts, bias, L, E, rate, bias_out, stream=None):
+    return _check("moe_bias_balance", lib().moe_bias_balance(_p(counts), _p(bias), L, E, rate, _p(bias_out),
+                                                             _stream(stream)))
+
+
+def moe_lora_workspace_bytes(T, K, r) -> int:
+    return int(lib().moe_lora_workspace_bytes(T, K, r))
+
+
+def moe_lora_add(x, x_dtype, ldx, a, b, ranks, scale, ids, n, r, T, N, K, base, ldb, y, y_dtype, ldy, ws, ws_bytes,
+                 stream=None):
+    return _check("moe_lora_add", lib().moe_lora_add(_p(x), x_dtype, ldx, _p(a), _p(b), _p(ranks), _p(scale), _p(ids), n,
+                                                     r, T, N, K, _p(base), ldb, _p(y), y_dtype, ldy, _p(ws), ws_bytes,
+                                                     _stream(stream)))
 
 
 def moe_step_create(T_max, E, k, H, I, S, w_type):

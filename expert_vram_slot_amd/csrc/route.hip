@@ -482,28 +482,34 @@ int launch_logits(const void* x, const void* G, int T, int H, int E, float* z, h
     return moe_check_launch("moe_route/logits");
 }
 
+// Logits of a batch by the kernel for its size.
 template <int XD>
-int route_split(const void* x, const void* G, const float* bias, const int32_t* ids_in, int T, int H, int E, int k,
-                int32_t* ids, float* w, float* logits, int damped, hipStream_t s) {
+int logits_split(const void* x, const void* G, int T, int H, int E, float* logits, hipStream_t s) {
     // tokens per workgroup: more for larger batches (fewer reads of G), within 64 KiB of LDS
     const size_t xrow = (size_t)H * (XD == MOE_X_F32 ? 4 : 2);
     int tb = T >= 512 ? 8 : T >= 128 ? 4 : T >= 32 ? 2 : 1;
     while (tb > 1 && tb * xrow > 64 * 1024) tb >>= 1;
     if (xrow > 64 * 1024) return moe_fail(MOE_E_SHAPE, "moe_route: H=%d is too long for one token in LDS", H);
-    int rc;
     // the fp64 matrix cores for large batches (the 288-expert layer's 2048
     // tokens: 215 -> 121 us for logits and top-k)
     if (XD == MOE_X_BF16 && T >= 512 && H % 32 == 0) {
         const dim3 grid((T + LM_WT - 1) / LM_WT, (E + 2 * LM_WT - 1) / (2 * LM_WT));
         hipLaunchKernelGGL(k_logits_mfma, grid, dim3(ROUTE_THREADS), 0, s, reinterpret_cast<const uint16_t*>(x),
                            reinterpret_cast<const uint16_t*>(G), T, H, E, logits);
-        rc = moe_check_launch("moe_route/logits_mfma");
-    } else switch (tb) {
-        case 8: rc = launch_logits<XD, 8>(x, G, T, H, E, logits, s); break;
-        case 4: rc = launch_logits<XD, 4>(x, G, T, H, E, logits, s); break;
-        case 2: rc = launch_logits<XD, 2>(x, G, T, H, E, logits, s); break;
-        default: rc = launch_logits<XD, 1>(x, G, T, H, E, logits, s); break;
+        return moe_check_launch("moe_route/logits_mfma");
     }
+    switch (tb) {
+        case 8: return launch_logits<XD, 8>(x, G, T, H, E, logits, s);
+        case 4: return launch_logits<XD, 4>(x, G, T, H, E, logits, s);
+        case 2: return launch_logits<XD, 2>(x, G, T, H, E, logits, s);
+        default: return launch_logits<XD, 1>(x, G, T, H, E, logits, s);
+    }
+}
+
+template <int XD>
+int route_split(const void* x, const void* G, const float* bias, const int32_t* ids_in, int T, int H, int E, int k,
+                int32_t* ids, float* w, float* logits, int damped, hipStream_t s) {
+    const int rc = logits_split<XD>(x, G, T, H, E, logits, s);
     if (rc) return rc;
     const dim3 grid((T + ROUTE_KSPLIT - 1) / ROUTE_KSPLIT);
     const int nj = (E + 63) / 64;
@@ -608,6 +614,23 @@ int moe_route_ex(const void* x, int x_dtype, const void* G, const float* bias, c
 int moe_route(const void* x, int x_dtype, const void* G, const float* bias, const int32_t* ids_in, int T, int H,
               int E, int k, int32_t* ids, float* w, float* logits, hipStream_t stream) {
     return moe_route_ex(x, x_dtype, G, bias, ids_in, T, H, E, k, 0, ids, w, logits, stream);
+}
+
+int moe_route_logits(const void* x, int x_dtype, const void* G, int T, int H, int E, float* logits,
+                     hipStream_t stream) {
+    MOE_REQUIRE(T >= 0 && H >= 1 && E >= 1, MOE_E_ARG, "moe_route_logits: T=%d H=%d E=%d out of range", T, H, E);
+    MOE_REQUIRE(T == 0 || (x && G && logits), MOE_E_ARG, "moe_route_logits: x, G and logits must be non-NULL");
+    MOE_REQUIRE(x_dtype == MOE_X_F32 || x_dtype == MOE_X_BF16, MOE_E_DTYPE, "moe_route_logits: activation format %d",
+                x_dtype);
+    MOE_REQUIRE(E <= MOE_MAX_E, MOE_E_SHAPE, "moe_route_logits: E=%d exceeds %d", E, MOE_MAX_E);
+    MOE_REQUIRE(H <= 64 * 1024 / (x_dtype == MOE_X_F32 ? 4 : 2), MOE_E_SHAPE,
+                "moe_route_logits: H=%d is too long for one token in LDS", H);
+    MOE_REQUIRE(moe_aligned16(x) && moe_aligned16(G), MOE_E_ALIGN, "moe_route_logits: x and G must be 16-byte aligned");
+    MOE_REQUIRE(H % (x_dtype == MOE_X_F32 ? 4 : 8) == 0, MOE_E_ALIGN,
+                "moe_route_logits: H=%d must fill whole 16-byte granules", H);
+    if (T == 0) return moe_ok();
+    return x_dtype == MOE_X_F32 ? logits_split<MOE_X_F32>(x, G, T, H, E, logits, stream)
+                                : logits_split<MOE_X_BF16>(x, G, T, H, E, logits, stream);
 }
 
 }  // extern "C"

@@ -26,9 +26,10 @@ import os
 import torch
 
 from . import (MOE_W_F32, MOE_X_BF16, MOE_X_F32, POLICIES, LayerDesc, cache_gather, cache_init, cache_manage,
-               cache_state, moe_balance_loss, moe_balance_loss_bwd, moe_balance_workspace_bytes, moe_combine,
-               moe_ffn_host_misses, moe_ffn_slots, moe_ffn_workspace_bytes, moe_layer_step, moe_linear_q4,
-               moe_residual, moe_route_ex, moe_sample, moe_sample_workspace_bytes, moe_slab_layout, moe_stack_step,
+               cache_state, moe_balance_loss, moe_balance_loss_bwd, moe_balance_workspace_bytes, moe_bias_balance,
+               moe_combine, moe_ffn_host_misses, moe_ffn_slots, moe_ffn_workspace_bytes, moe_layer_step, moe_linear_q4,
+               moe_lora_add, moe_lora_workspace_bytes, moe_residual, moe_route_ex, moe_route_logits, moe_route_select,
+               moe_route_select_bwd, moe_sample, moe_sample_workspace_bytes, moe_slab_layout, moe_stack_step,
                moe_step_create, moe_step_destroy, moe_step_last_host_mode, moe_step_set_stream_threshold,
                moe_step_stats)
 
@@ -51,9 +52,23 @@ def _check_given(what, t, n, dtypes, device):
     assert t.is_contiguous() and t.numel() >= n, f"{what} is {tuple(t.shape)}, strides {t.stride()}: {n} values needed in a row"
 
 
+def _row_stride(what, x, T, n, dtypes, device):
+    """Elements from one row of x to the next, of T rows of n: rows of a wider
+    matrix, or n where x is contiguous in whatever shape."""
+    if isinstance(x, torch.Tensor) and x.dim() == 2 and x.shape[0] >= T and x.shape[1] == n and x.stride(1) == 1:
+        _check_given(what, x[:1].reshape(-1), min(T, 1) * n, dtypes, device)
+        return x.stride(0) if T > 1 else n
+    _check_given(what, x, T * n, dtypes, device)
+    return n
+
+
 class SlotLayer:
+    """One layer's buffers and the order of its step.  select: a select_rule, by
+    which moe_route_select then takes the picks and weights (bias goes on the
+    scores); None: moe_route's rule."""
+
     def __init__(self, *, E, k, H, I, S, w_type, T_max, policy, host_store, slot_store, G, bias=None,
-                 n_threads=None, device="cuda"):
+                 n_threads=None, device="cuda", select=None):
         dev = torch.device(device)
         self.E, self.k, self.H, self.I, self.S = E, k, H, I, S
         self.w_type = w_type
@@ -105,6 +120,7 @@ class SlotLayer:
         self.ffn_events = None     # (start, end) torch events recorded around moe_ffn_slots when set
         self.gather_events = None  # (start, end) torch events recorded around cache_gather when set
         self.route_flags = 0       # moe_route_ex flags (MOE_ROUTE_DAMPED)
+        self.select = select       # moe_select_rule or None
         self.stats_out = None      # moe_balance_loss's outputs and workspace, made by the first balance()
         # steps so far, tokens of the last one, and (steps, T) at the last balance(); a replayed graph moves on without
         # them, so from the first capture on they are not held against a call
@@ -118,9 +134,15 @@ class SlotLayer:
         moe_ffn_host_misses(self.h_x, self.x_dtype, self.h_ids, self.h_slot, self.h_w, T, self.k, self.host_store,
                             self.slab, self.E, self.w_type, self.H, self.I, self.h_y, self.n_threads)
 
-    def step(self, x, T, ids_in=None, host_pass=True):
-        """One layer step for T tokens of x (device, [T][H]); returns y [T][H] fp32 (device)."""
+    def step(self, x, T, ids_in=None, host_pass=True, mask=None):
+        """One layer step for T tokens of x (device, [T][H]); returns y [T][H] fp32 (device).
+        mask (with a select rule, without ids_in): device uint8 or bool [T]; tokens with 0 (padding) pick no
+        expert and get a y of 0."""
         assert T <= self.T_max
+        assert self.select is None or not self.route_flags, "a select rule takes the place of moe_route_ex's flags"
+        if mask is not None:
+            assert self.select is not None and ids_in is None, "a mask goes with a select rule, and without given picks"
+            _check_given("mask", mask, T, MASK_TYPES, self.ids.device)
         cur = torch.cuda.current_stream()
         P = T * self.k
         if host_pass:
@@ -133,8 +155,14 @@ class SlotLayer:
             # given picks are copied into the packed block (the host pass reads them from there)
             self.ids[:P].copy_(ids_in.reshape(-1)[:P], non_blocking=True)
         # 1. router (picks, or weights of given picks)
-        moe_route_ex(x, self.x_dtype, self.G, self.bias, None if ids_in is None else self.ids, T, self.H, self.E,
-                     self.k, self.route_flags, self.ids, self.w, self.logits, cur)
+        given = None if ids_in is None else self.ids
+        if self.select is None:
+            moe_route_ex(x, self.x_dtype, self.G, self.bias, given, T, self.H, self.E, self.k, self.route_flags,
+                         self.ids, self.w, self.logits, cur)
+        else:
+            moe_route_logits(x, self.x_dtype, self.G, T, self.H, self.E, self.logits, cur)
+            moe_route_select(self.logits, MOE_X_F32, self.bias, mask, given, T, self.E, self.k, self.select, self.ids,
+                             self.w, cur)
         self.steps, self.step_T = self.steps + 1, T
         self.captured |= torch.cuda.is_current_stream_capturing()
         ids = self.ids
@@ -224,6 +252,34 @@ class SlotLayer:
         return dz
 
 
+    def select_grad(self, T, dw, dz_add=None):
+        """Gradient of the last step's weights to its logits, [T][E] fp32
+        (moe_route_select_bwd; the layer has a select rule).  dw: device
+        float32 [T][k], the weights' gradient; dz_add: device float32 [T][E] or
+        None, added (balance_grad's)."""
+        assert self.select is not None, "the layer has no select rule"
+        assert T <= self.T_max
+        assert T <= self.step_T or self.captured, f"the last step had {self.step_T} tokens"
+        _check_given("dw", dw, T * self.k, (torch.float32,), self.ids.device)
+        if dz_add is not None:
+            _check_given("dz_add", dz_add, T * self.E, (torch.float32,), self.ids.device)
+        dz = torch.empty(T, self.E, dtype=torch.float32, device=self.ids.device)
+        with torch.cuda.device(self.ids.device):
+            moe_route_select_bwd(self.logits, MOE_X_F32, self.ids, dw, T, self.E, self.k, self.select, dz_add, dz,
+                                 torch.cuda.current_stream())
+            self.captured |= torch.cuda.is_current_stream_capturing()
+        return dz
+
+    def balance_bias(self, rate):
+        """One step of the layer's bias, in place, by the last balance()'s counts
+        (moe_bias_balance): experts picked less than the mean move up by rate."""
+        o = self.stats_out
+        assert self.bias is not None and o is not None, "a bias and a balance() come first"
+        _check_given("bias", self.bias, self.E, (torch.float32,), self.ids.device)
+        with torch.cuda.device(self.ids.device):
+            moe_bias_balance(o["counts"], self.bias, 1, self.E, rate, self.bias, torch.cuda.current_stream())
+
+
 class SlotStack:
     """Stacked expert-slot MoE layers joined by a residual stream kept in the
     activation format: x_{l+1} = x_l + y_l ("Nudge, don't cut", "Experts that
@@ -235,12 +291,12 @@ class SlotStack:
     other).
     """
 
-    def __init__(self, *, E, k, H, I, S, w_type, T_max, layers, n_threads=None, device="cuda"):
+    def __init__(self, *, E, k, H, I, S, w_type, T_max, layers, n_threads=None, device="cuda", select=None):
         self.layers = layers
         first = layers[0]
         self.layer = SlotLayer(E=E, k=k, H=H, I=I, S=S, w_type=w_type, T_max=T_max, policy="static",
                                host_store=first["host_store"], slot_store=first["slot_store"], G=first["G"],
-                               bias=first.get("bias"), n_threads=n_threads, device=device)
+                               bias=first.get("bias"), n_threads=n_threads, device=device, select=select)
         dev = torch.device(device)
         self.states = []
         for spec in layers:
@@ -374,17 +430,54 @@ class NativeStack:
             pass
 
 
+class Adapters:
+    """A pool of low-rank adapters beside one product (moe_lora_add), a
+    request's each: a: device bf16 [n][r][K], b: device bf16 [n][N][r], ranks:
+    device int32 [n] or None, scale: device float32 [n] or None.  x_dtype and
+    y_dtype are the product's.
+    """
+
+    def __init__(self, *, a, b, T_max, ranks=None, scale=None, x_dtype=MOE_X_BF16, y_dtype=MOE_X_F32):
+        self.n, self.r, self.K = a.shape
+        self.N = b.shape[1]
+        assert tuple(b.shape) == (self.n, self.N, self.r)
+        for what, t, n, dtype in (("a", a, a.numel(), torch.bfloat16), ("b", b, b.numel(), torch.bfloat16),
+                                  ("ranks", ranks, self.n, torch.int32), ("scale", scale, self.n, torch.float32)):
+            if t is not None:
+                _check_given(what, t, n, (dtype,), a.device)
+        self.a, self.b, self.ranks, self.scale, self.T_max = a, b, ranks, scale, T_max
+        self.x_dtype, self.y_dtype = x_dtype, y_dtype
+        self.ws_bytes = moe_lora_workspace_bytes(T_max, self.K, self.r)
+        assert self.ws_bytes, f"T_max={T_max}, K={self.K}, r={self.r} beyond moe_lora_add's limits"
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=a.device)
+
+    def add(self, x, T, ids, y):
+        """y += each token's adapter of x, in place: x device [T][K] in x_dtype,
+        y device [T][N] in y_dtype (rows of both possibly of wider matrices), ids
+        device int32 [T], a token's adapter (outside [0, n): none)."""
+        assert T <= self.T_max
+        dev = self.a.device
+        ldx = _row_stride("x", x, T, self.K, X_TYPES[self.x_dtype], dev)
+        ldy = _row_stride("y", y, T, self.N, X_TYPES[self.y_dtype], dev)
+        _check_given("ids", ids, T, (torch.int32,), dev)
+        with torch.cuda.device(dev):
+            moe_lora_add(x, self.x_dtype, ldx, self.a, self.b, self.ranks, self.scale, ids, self.n, self.r, T, self.N,
+                         self.K, y, ldy, y, self.y_dtype, ldy, self.ws, self.ws_bytes, torch.cuda.current_stream())
+        return y
+
+
 class DecodeHead:
     """The end of a decode step behind a stack: the 4-bit output head's
     logits and the token drawn from them.
 
     wq: device uint8 [V][H/2], scales: device fp16 [V][H/group] (the layout of
     moe_linear_q4); bias: device float [V] or None.  x_dtype is the stack's
-    activation format.  What a call brings has to be of the types given here
+    activation format.  adapters: an Adapters of [V] outputs or None.  What a call brings has to be of the types given here
     and on the head's device (AssertionError otherwise, before any launch).
     """
 
-    def __init__(self, *, H, V, wq, scales, group, T_max, x_dtype=MOE_X_BF16, bias=None, device="cuda"):
+    def __init__(self, *, H, V, wq, scales, group, T_max, x_dtype=MOE_X_BF16, bias=None, device="cuda",
+                 adapters=None):
         dev = torch.device(device)
         assert H % group == 0 and tuple(wq.shape) == (V, H // 2) and tuple(scales.shape) == (V, H // group)
         assert wq.dtype == torch.uint8 and scales.dtype == torch.float16 and wq.is_contiguous() and scales.is_contiguous()
@@ -397,37 +490,37 @@ class DecodeHead:
         self.ws_bytes = moe_sample_workspace_bytes(T_max, V)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
         assert all(w is None or w.device == self.ids.device for w in (wq, scales, bias))
+        assert adapters is None or (adapters.K, adapters.N, adapters.x_dtype, adapters.y_dtype) == (H, V, x_dtype, MOE_X_F32)
+        assert adapters is None or (adapters.T_max >= T_max and adapters.a.device == self.ids.device)
+        self.adapters = adapters
 
-    def _row_stride(self, x, T):
-        """Elements from one row of x to the next, of T rows of H: rows of a
-        wider matrix, or H where x is contiguous in whatever shape."""
-        if isinstance(x, torch.Tensor) and x.dim() == 2 and x.shape[0] >= T and x.shape[1] == self.H and x.stride(1) == 1:
-            _check_given("x", x[:1].reshape(-1), min(T, 1) * self.H, X_TYPES[self.x_dtype], self.ids.device)
-            return x.stride(0) if T > 1 else self.H
-        _check_given("x", x, T * self.H, X_TYPES[self.x_dtype], self.ids.device)
-        return self.H
-
-    def logits(self, x, T):
+    def logits(self, x, T, adapter_ids=None):
         """Logits [T][V] fp32 of x (device [T][H] in x_dtype, rows any
-        16-byte multiple apart): a view of this object's buffer."""
+        16-byte multiple apart): a view of this object's buffer.  adapter_ids:
+        device int32 [T], each token's adapter, or None (none has one)."""
         assert T <= self.T_max
-        ldx = self._row_stride(x, T)
+        ldx = _row_stride("x", x, T, self.H, X_TYPES[self.x_dtype], self.ids.device)
+        if adapter_ids is not None:
+            assert self.adapters is not None, "the head has no adapters"
+            _check_given("adapter_ids", adapter_ids, T, (torch.int32,), self.ids.device)
         with torch.cuda.device(self.ids.device):
             moe_linear_q4(x, self.x_dtype, ldx, self.wq, self.scales, self.group, self.bias, T, self.V, self.H,
                           self.logits_buf, MOE_X_F32, self.V, torch.cuda.current_stream())
+        if adapter_ids is not None:
+            self.adapters.add(x, T, adapter_ids, self.logits_buf)
         return self.logits_buf[:T]
 
-    def step(self, x, T, u, temperature=None, min_p=None, top_k=None, top_p=None):
+    def step(self, x, T, u, temperature=None, min_p=None, top_k=None, top_p=None, adapter_ids=None):
         """The next token of each of T rows of x: (ids [T], prob [T]), views of
         this object's buffers.  u and the settings as moe_sample takes them:
-        device float32 [T], top_k int32 [T]."""
+        device float32 [T], top_k int32 [T]; adapter_ids as logits() takes it."""
         _check_given("u", u, T, (torch.float32,), self.ids.device)
         for what, t in (("temperature", temperature), ("min_p", min_p), ("top_p", top_p)):
             if t is not None:
                 _check_given(what, t, T, (torch.float32,), self.ids.device)
         if top_k is not None:
             _check_given("top_k", top_k, T, (torch.int32,), self.ids.device)
-        self.logits(x, T)
+        self.logits(x, T, adapter_ids)
         with torch.cuda.device(self.ids.device):
             moe_sample(self.logits_buf, MOE_X_F32, self.V, T, self.V, temperature, min_p, top_k, top_p, u, self.ids,
                        self.prob, self.ws, self.ws_bytes, torch.cuda.current_stream())

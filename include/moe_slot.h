@@ -20,6 +20,11 @@
  *   moe_sample           a token id from each row of the head's logits
  *   moe_balance_loss     picks and router mass per expert, balance and z loss
  *                        (moe_balance_loss_bwd: their gradient)
+ *   moe_route_select     experts and weights by another rule than moe_route's:
+ *                        sigmoid or softmax scores, a bias on the scores,
+ *                        groups (moe_route_select_bwd: the weights' gradient)
+ *   moe_bias_balance     a step of the bias that balances the picks
+ *   moe_lora_add         low-rank adapters of many requests beside a product
  *
  * Sources (web pages, by title and section):
  *   [BEL] the Betelgeuse engine post: an in-stream kernel resolves expert hits
@@ -518,6 +523,128 @@ int moe_balance_loss(const void* z, int z_dtype, const int32_t* ids, const uint8
  * Errors: as moe_balance_loss. */
 int moe_balance_loss_bwd(const void* z, int z_dtype, const float* lse, const uint8_t* mask, const int32_t* counts,
                          const int32_t* totals, const float* dloss, int T, int E, void* dz, hipStream_t stream);
+
+/* The logits of moe_route alone: x G, device float[T][E], in double and
+ * rounded once.  x, G as moe_route takes them; T = 0 does nothing.
+ * Errors: ARG, DTYPE, SHAPE (E > MOE_MAX_E, a row of x over 64 KiB), ALIGN
+ * (x and G on 16 bytes, rows of whole 16-byte units), HIP. */
+int moe_route_logits(const void* x, int x_dtype, const void* G, int T, int H, int E, float* logits,
+                     hipStream_t stream);
+
+/* A router's rule of selection.
+ *   score        MOE_SCORE_SOFTMAX: s = exp(z) / sum exp(z) over the experts;
+ *                MOE_SCORE_SIGMOID: s = 1 / (1 + exp(-z))
+ *   groups       the E experts lie in that many groups of E / groups
+ *                neighbours (1: no groups)
+ *   groups_kept  how many groups a token may pick from (<= groups)
+ *   group_top    1 or 2: a group counts what its best, or its two best,
+ *                experts' choice scores add up to
+ *   renorm       nonzero: weights are divided by their sum over the picks
+ *   scale        factor of every weight, finite */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_SELECT_MAX_GROUPS 64
+#define MOE_SELECT_MAX_T (1 << 24)
+typedef struct {
+    int32_t score;
+    int32_t groups;
+    int32_t groups_kept;
+    int32_t group_top;
+    int32_t renorm;
+    float scale;
+} moe_select_rule;
+
+/* Experts and weights of each token from the router's logits.
+ *   z       device [T][E] in z_dtype.  An expert is open where its logit and
+ *           its bias are above -inf (NaN is not); others are never picked and
+ *           have the score 0.  +inf outweighs every finite logit (several share)
+ *   bias    device float[E] or NULL: added to the scores for the choice alone
+ *   mask    device uint8[T] or NULL: tokens with 0 (padding) pick nothing
+ *   ids_in  device int32[T][k] or NULL.  If given, these are the picks and only
+ *           w is produced (bias and groups play no part); a pick outside
+ *           [0, E), or of an expert whose logit is not above -inf, has weight 0
+ *   rule    read by the call itself (host memory)
+ *   ids     device int32[T][k] out: of the open experts in the groups_kept
+ *           best groups (ties: the lower group; a group with nothing open is
+ *           never kept, one with less than group_top counts what it has) the k
+ *           first by falling choice score c = s + bias, then by falling logit,
+ *           then by rising id; -1 where there are no more.  Not written if
+ *           ids_in is given
+ *   w       device float[T][k] out: scale * s of each pick, or scale * s / sum
+ *           of s over the token's picks; 0 for a pick of -1 and a masked token
+ * Choice scores are taken in double.  Their ids do not depend on the other
+ * tokens.  T = 0 does nothing.
+ * Errors: ARG (null, sizes, score, group_top or scale out of range), DTYPE,
+ * SHAPE (E > MOE_MAX_E, k > MOE_MAX_K, groups that do not divide E or are over
+ * MOE_SELECT_MAX_GROUPS, k more than the kept groups hold, T beyond the limit),
+ * ALIGN (z on 16 bytes, ids and w on their elements), HIP. */
+int moe_route_select(const void* z, int z_dtype, const float* bias, const uint8_t* mask, const int32_t* ids_in, int T,
+                     int E, int k, const moe_select_rule* rule, int32_t* ids, float* w, hipStream_t stream);
+
+/* Gradient of moe_route_select's weights to the logits (the picks and the bias
+ * carry none).
+ *   z, rule  as given to moe_route_select
+ *   ids      device int32[T][k]: the picks (moe_route_select's ids, or the
+ *            ids_in given to it).  Those outside [0, E), or of an expert whose
+ *            logit is not above -inf, carry nothing and their dw is not used; an
+ *            expert picked twice gets both parts.  A masked token given picks
+ *            has to have them at -1 here
+ *   dw       device float[T][k]: gradient of w
+ *   dz_add   device [T][E] in z_dtype or NULL (0): added, as another loss's
+ *            gradient (moe_balance_loss_bwd's)
+ *   dz       device [T][E] in z_dtype out: dz_add + sum over i of dw_i dw_i/dz;
+ *            may be z or dz_add
+ * In fp32, rounded once at the end.  T = 0 does nothing.
+ * Errors: as moe_route_select; ALIGN (z, dz_add and dz on 16 bytes). */
+int moe_route_select_bwd(const void* z, int z_dtype, const int32_t* ids, const float* dw, int T, int E, int k,
+                         const moe_select_rule* rule, const void* dz_add, void* dz, hipStream_t stream);
+
+/* One step of the bias that balances the picks without a loss, for L layers
+ * at once.  Over the n open experts of a layer (those whose bias is above
+ * -inf) and the sum C of their counts:
+ *   bias_out[l][e] = fl32(bias[l][e] + rate * sign(C - n counts[l][e]))
+ * so an expert with fewer picks than the mean moves up by rate, one with more
+ * moves down.  The others keep their bias.
+ *   counts    device int32[L][E]: moe_balance_loss's counts
+ *   bias      device float[L][E]
+ *   rate      finite, >= 0
+ *   bias_out  device float[L][E]; may be bias
+ * Errors: ARG, SHAPE (E > MOE_MAX_E, L > 65535), HIP. */
+int moe_bias_balance(const int32_t* counts, const float* bias, int L, int E, float rate, float* bias_out,
+                     hipStream_t stream);
+
+/* Low-rank adapters of many requests beside a shared product (moe_linear_q4's
+ * y is the base): y[t] = base[t] + scale[i] * B_i (A_i x[t]) with i = ids[t].
+ *   x      device [T][ldx] in x_dtype, K inputs a row
+ *   a      device bf16 [n][r][K]
+ *   b      device bf16 [n][N][r]
+ *   ranks  device int32[n] or NULL (r each): adapter i uses its first
+ *          ranks[i] rows of A and columns of B (values outside [0, r] are taken
+ *          as the nearest end); what lies behind them does not matter
+ *   scale  device float[n] or NULL (1)
+ *   ids    device int32[T]: tokens with an id outside [0, n) have no adapter,
+ *          their y is base
+ *   base   device [T][ldb] in y_dtype or NULL (0)
+ *   y      device [T][ldy] in y_dtype out; may be base (ldb = ldy then), must
+ *          not overlap the inputs otherwise.  Columns from N to ldy are left as
+ *          they are
+ *   ws     device workspace of >= moe_lora_workspace_bytes(T, K, r) bytes;
+ *          need not be cleared; calls that may overlap need one each
+ * Both products are summed in fp32; A x keeps its 24 bits (below 2^-100 in
+ * magnitude the last of them are lost, as those of fp32 x), y is rounded once.
+ * An infinity or a NaN of a token or an adapter makes outputs of that token or
+ * that adapter's tokens not finite, and no others.  A token's bits do not
+ * depend on the other tokens' values.  T = 0 does nothing.
+ * Errors: ARG (null, sizes, ldx < K, ldb or ldy < N, base = y with other
+ * strides, workspace too small), DTYPE, SHAPE (K or r not a multiple of 8, the
+ * limits below and moe_linear_q4's), ALIGN (x, its rows, a, b and ws on 16
+ * bytes; base and y on their elements), HIP. */
+#define MOE_LORA_MAX_N (1 << 16)
+#define MOE_LORA_MAX_R 256
+size_t moe_lora_workspace_bytes(int T, int K, int r);
+int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const void* b, const int32_t* ranks,
+                 const float* scale, const int32_t* ids, int n, int r, int T, int N, int K, const void* base,
+                 int64_t ldb, void* y, int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Pinned, device-mapped host memory for the host expert store. */
 void* moe_host_alloc(size_t bytes);
