@@ -1,10 +1,38 @@
 // Low-rank adapters of many requests beside a shared product:
 //   y_t = base_t + scale_i B_i (A_i x_t), i = ids_t
-// in two passes: h = scale A x (each token with its own adapter's rows), then
-// y = base + B h.
+// in two passes: h = A x (each token with its own adapter's rows), then y = base
+// + B (scale h).
+//
+// Both run on the matrix cores, v_mfma_f32_16x16x32_bf16, 16 rows of A or B
+// against 16 tokens.  Tokens that share an adapter share its rows: the tokens are
+// taken in order of their adapters (of 16 at most as they come, of 64 sorted inside
+// each wave, else by k_lora_order, in windows of 1024), in tiles of 16, or of 64
+// where there are more than 1024.  A tile that holds several adapters takes them one
+// after the other, and of each product every token keeps the columns of its own
+// adapter alone: nothing of one adapter, an infinity or a NaN, reaches another's
+// tokens.  fp32 x and h are cut into three bf16 planes (8 + 8 + 8 bits, exact) and
+// take three products: A x keeps its 24 bits, and the products are no bound.
+//
+// The inputs of A x are split over waves and workgroups; the partial sums (one of
+// each split in the workspace) are added in a fixed order.
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace {
+
+using v4u = uint32_t __attribute__((ext_vector_type(4)));
+using v4f = float __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef v4f v4f_loose __attribute__((aligned(4)));
+typedef v4u v4u_loose __attribute__((aligned(2)));
+
+constexpr int WINDOW = 1024;     // tokens sorted together
+constexpr int WAVE_TOKENS = 64;  // up to so many are sorted in a wave
+constexpr int MANY = 1024;       // tokens from which tiles are of 64
+constexpr int DOWN_WAVES = 4;    // of a workgroup of the first pass
+constexpr int MAX_SPLITS = 8;
+constexpr int RANKS = 64;        // rows of A that a workgroup of the first pass takes
 
 struct LoraArgs {
     const void* x;
@@ -19,56 +47,357 @@ struct LoraArgs {
     int64_t ldb;
     void* y;
     int64_t ldy;
-    float* h;  // [T][r]
+    float* h;        // [splits][T][r]
+    int32_t* order;  // [T], or NULL: up to WAVE_TOKENS tokens
+    int splits;
+    int steps;       // of 32 rows of B that a wave of the second pass takes
 };
 
-// The adapter of token t and its rank; 0: none.
-__device__ __forceinline__ int adapter(const LoraArgs& a, int64_t t, int& rank) {
+__device__ __forceinline__ int adapter_of(const LoraArgs& a, int t) {
+    if (t < 0) return -1;
     const int i = a.ids[t];
-    rank = i < 0 || i >= a.n ? 0 : a.ranks ? min(max(a.ranks[i], 0), a.r) : a.r;
-    return i;
+    return i >= 0 && i < a.n ? i : -1;
 }
 
-template <int D>
-__device__ __forceinline__ float load(const void* p, int64_t i) {
-    if constexpr (D == MOE_X_F32) return reinterpret_cast<const float*>(p)[i];
-    else return moe::bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]);
+__device__ __forceinline__ int rank_of(const LoraArgs& a, int i) {
+    return i < 0 ? 0 : a.ranks ? min(max(a.ranks[i], 0), a.r) : a.r;
 }
 
-// One workgroup a token, one wave a row of A at a time.
-template <int XD>
-__global__ void __launch_bounds__(256) k_lora_down(LoraArgs a) {
-    const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-    int rank;
-    const int i = adapter(a, t, rank);
-    for (int j = wid; j < rank; j += 4) {
-        const uint16_t* row = a.a + ((int64_t)i * a.r + j) * a.K;
-        float s = 0.0f;
-        for (int k = lane; k < a.K; k += 64) s = fmaf(load<XD>(a.x, t * a.ldx + k), moe::bf16_to_f32(row[k]), s);
-        s = moe::wave_sum(s);
-        if (lane == 0) a.h[t * a.r + j] = a.scale ? a.scale[i] * s : s;
+// The token (-1: none) and adapter (-1: none) of this lane in a tile of TM
+// places: lane l holds place l % TM.
+template <int TM>
+__device__ __forceinline__ void member(const LoraArgs& a, int tile, int lane, int& tok, int& ad) {
+    const int place = tile * TM + (lane & (TM - 1));
+    if (a.order) {
+        tok = place < a.T ? a.order[place] : -1;
+        ad = adapter_of(a, tok);
+        return;
+    }
+    tok = lane < a.T ? lane : -1;
+    ad = adapter_of(a, tok);
+    if (a.T <= 16) {
+        tok = __shfl(tok, lane & 15, moe::WAVE);
+        ad = __shfl(ad, lane & 15, moe::WAVE);
+        return;
+    }
+    const uint32_t key = tok < 0 ? ~0u : ((uint32_t)(ad + 1) << 6) | (uint32_t)lane;
+    int rank = 0;
+    for (int j = 0; j < a.T; ++j) rank += (uint32_t)__builtin_amdgcn_readlane((int)key, j) < key;
+    if (tok < 0) rank = lane;  // behind the others
+    const int from = __builtin_amdgcn_ds_permute(4 * rank, lane);  // the lane whose rank this one's number is
+    const int src = __shfl(from, place & 63, moe::WAVE);
+    tok = __shfl(tok, src, moe::WAVE);
+    ad = __shfl(ad, src, moe::WAVE);
+}
+
+// Places of the tokens of a window in order of their adapters, then of their
+// numbers: each counts the window's smaller keys.  One workgroup for 64 tokens,
+// four threads a token.
+__global__ void __launch_bounds__(256) k_lora_order(LoraArgs a) {
+    __shared__ __align__(16) uint32_t key[WINDOW];
+    __shared__ int part[4][64];
+    const int tid = threadIdx.x, q = tid >> 6;
+    const int first = blockIdx.x * 64, w0 = first / WINDOW * WINDOW, n = min(WINDOW, a.T - w0);
+    for (int i = tid; i < WINDOW; i += 256)
+        key[i] = i < n ? ((uint32_t)(adapter_of(a, w0 + i) + 1) << 10) | (uint32_t)i : ~0u;
+    __syncthreads();
+    const int at = first - w0 + (tid & 63);
+    const uint32_t mine = key[at];
+    const int len = (n + 15) / 16 * 4;  // a quarter, in fours
+    const v4u* k4 = reinterpret_cast<const v4u*>(key) + q * (len / 4);
+    int smaller = 0;
+    for (int i = 0; i < len / 4; ++i) {
+        const v4u v = k4[i];
+        smaller += (v[0] < mine) + (v[1] < mine) + (v[2] < mine) + (v[3] < mine);
+    }
+    part[q][tid & 63] = smaller;
+    __syncthreads();
+    if (q == 0 && at < n) a.order[w0 + part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid]] = w0 + at;
+}
+
+// Eight floats as three planes of bf16, cut, not rounded.
+__device__ __forceinline__ void cut8(float (&v)[8], bf16x8 (&out)[3]) {
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+        v4u w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (__float_as_uint(v[2 * i]) >> 16) | (__float_as_uint(v[2 * i + 1]) & 0xFFFF0000u);
+        out[p] = __builtin_bit_cast(bf16x8, w);
+        if (p < 2) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] -= __uint_as_float(__float_as_uint(v[i]) & 0xFFFF0000u);
+        }
     }
 }
 
-// One thread an output.
-template <int YD>
+// Eight inputs of x, in planes.
+template <int XD>
+struct Piece {
+    v4u raw[XD == MOE_X_F32 ? 2 : 1];
+    static constexpr int PLANES = XD == MOE_X_F32 ? 3 : 1;
+    __device__ __forceinline__ void get(const char* p) {
+        raw[0] = *reinterpret_cast<const v4u*>(p);
+        if constexpr (XD == MOE_X_F32) raw[1] = *reinterpret_cast<const v4u*>(p + 16);
+    }
+    __device__ __forceinline__ void planes(bf16x8 (&out)[PLANES]) const {
+        if constexpr (XD == MOE_X_F32) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(raw[i >> 2][i & 3]);
+            cut8(v, out);
+        } else {
+            out[0] = __builtin_bit_cast(bf16x8, raw[0]);
+        }
+    }
+};
+
+// h of a tile of 16 NT tokens, RB blocks of 16 rows of A, a share of the inputs.
+// A product takes 32 inputs: lane (m, q) brings inputs 8q.. of row m of A and of
+// token m, and holds h of rows 4q.. of token m.  Rows of A past the rank are read
+// where there are any and change nothing but h of those rows, which the second
+// pass does not use.
+template <int XD, int NT, int RB>
+__global__ void __launch_bounds__(64 * DOWN_WAVES) k_lora_down(LoraArgs a) {
+    constexpr int U = NT == 1 ? 4 : XD == MOE_X_BF16 ? 2 : 1;  // products of 32 inputs loaded together
+    constexpr int XB = XD == MOE_X_F32 ? 4 : 2;
+    __shared__ __align__(16) v4f red[DOWN_WAVES][NT * RB][64];
+    __shared__ int s_tok[16 * NT], s_ad[16 * NT];
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, m = lane & 15, q = lane >> 4;
+    const int split = blockIdx.z % a.splits, row0 = blockIdx.z / a.splits * RANKS;
+    int tok, ad;
+    member<16 * NT>(a, blockIdx.x, lane, tok, ad);
+    if (wid == 0 && lane < 16 * NT) s_tok[lane] = tok, s_ad[lane] = ad;
+    const int units = (a.K + 31) / 32, waves = a.splits * DOWN_WAVES, wi = split * DOWN_WAVES + wid;
+    const int u0 = (int)((int64_t)units * wi / waves), u1 = (int)((int64_t)units * (wi + 1) / waves);
+    const char* xp[NT];
+#pragma unroll
+    for (int s = 0; s < NT; ++s) {
+        const int t = __shfl(tok, NT == 1 ? lane : 16 * s + m, moe::WAVE);
+        xp[s] = reinterpret_cast<const char*>(a.x) + (int64_t)max(t, 0) * a.ldx * XB;
+    }
+    unsigned long long rest = __ballot(ad >= 0);
+    for (int pass = 0; rest; ++pass) {
+        const int d = __builtin_amdgcn_readlane(ad, __builtin_ctzll(rest));
+        rest &= ~__ballot(ad == d);
+        if (pass % gridDim.y != blockIdx.y || row0 >= rank_of(a, d)) continue;
+        const uint16_t* ap[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) ap[b] = a.a + ((int64_t)d * a.r + min(row0 + 16 * b + m, a.r - 1)) * a.K;
+        v4f acc[NT][RB] = {};
+        v4u af[2][U][RB];
+        Piece<XD> xf[2][U][NT];
+        const auto fetch = [&](int buf, int u) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int un = min(u + i, u1 - 1), k = min(32 * un + 8 * q, a.K - 8);
+#pragma unroll
+                for (int b = 0; b < RB; ++b) af[buf][i][b] = *reinterpret_cast<const v4u*>(ap[b] + k);
+#pragma unroll
+                for (int s = 0; s < NT; ++s) xf[buf][i][s].get(xp[s] + (int64_t)k * XB);
+            }
+        };
+        const auto multiply = [&](int buf, int u) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (u + i >= u1) break;
+                bf16x8 av[RB];
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+                    // past the last inputs: a product with 0
+                    if (32 * (u + i) + 32 > a.K && 32 * (u + i) + 8 * q >= a.K) af[buf][i][b] = v4u{};
+                    av[b] = __builtin_bit_cast(bf16x8, af[buf][i][b]);
+                }
+#pragma unroll
+                for (int s = 0; s < NT; ++s) {
+                    bf16x8 xv[Piece<XD>::PLANES];
+                    xf[buf][i][s].planes(xv);
+#pragma unroll
+                    for (int b = 0; b < RB; ++b)
+#pragma unroll
+                        for (int p = 0; p < Piece<XD>::PLANES; ++p)
+                            acc[s][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[b], xv[p], acc[s][b], 0, 0, 0);
+                }
+            }
+        };
+        if (u0 < u1) {
+            fetch(0, u0);
+            for (int u = u0; u < u1; u += 2 * U) {
+                if (u + U < u1) fetch(1, u + U);
+                multiply(0, u);
+                if (u + U < u1) {
+                    if (u + 2 * U < u1) fetch(0, u + 2 * U);
+                    multiply(1, u + U);
+                }
+            }
+        }
+        __syncthreads();  // the tokens are there, and the last adapter's sums are read
+#pragma unroll
+        for (int s = 0; s < NT; ++s)
+#pragma unroll
+            for (int b = 0; b < RB; ++b) red[wid][s * RB + b][lane] = acc[s][b];
+        __syncthreads();
+        for (int i = threadIdx.x; i < NT * RB * 64; i += 64 * DOWN_WAVES) {
+            const int sb = i >> 6, l = i & 63, at = 16 * (sb / RB) + (l & 15), j = row0 + 16 * (sb % RB) + 4 * (l >> 4);
+            if (s_ad[at] != d || s_tok[at] < 0 || j >= a.r) continue;
+            v4f sum = red[0][sb][l];
+#pragma unroll
+            for (int w = 1; w < DOWN_WAVES; ++w) sum += red[w][sb][l];
+            *reinterpret_cast<v4f*>(a.h + ((int64_t)split * a.T + s_tok[at]) * a.r + j) = sum;
+        }
+    }
+}
+
+// y of a tile of tokens, 32 rows of B a step: lane (m, q) brings columns 8q.. of a
+// row and of a token's h, and holds outputs of token m: of fp32 y rows 4q.. and 16 +
+// 4q.. (a token's 128 bytes together), of bf16 y rows 8q.. (the rows are taken in
+// that order, so that a lane stores 16 bytes).
+template <int YD, int TM, int NT, int RC>
 __global__ void __launch_bounds__(256) k_lora_up(LoraArgs a) {
-    const int64_t t = blockIdx.y;
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= a.N) return;
-    int rank;
-    const int i = adapter(a, t, rank);
-    float s = 0.0f;
-    for (int j = 0; j < rank; ++j)
-        s = fmaf(a.h[t * a.r + j], moe::bf16_to_f32(a.b[((int64_t)i * a.N + n) * a.r + j]), s);
-    const float v = (a.base ? load<YD>(a.base, t * a.ldb + n) : 0.0f) + s;
-    if constexpr (YD == MOE_X_F32) reinterpret_cast<float*>(a.y)[t * a.ldy + n] = v;
-    else reinterpret_cast<__bf16*>(a.y)[t * a.ldy + n] = (__bf16)v;
+    const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
+    const int wave = blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+    const int first = wave * a.steps, last = min(first + a.steps, (a.N + 31) / 32);
+    int tok, ad;
+    member<TM>(a, blockIdx.y, lane, tok, ad);
+#pragma unroll 1
+    for (int grp = 0; grp < TM / 16 / NT; ++grp) {
+        int t[NT], d_of[NT];
+        bf16x8 hp[NT][RC][3];
+#pragma unroll
+        for (int s = 0; s < NT; ++s) {
+            const int src = TM == 16 ? lane : 16 * (grp * NT + s) + m;
+            t[s] = __shfl(tok, src, moe::WAVE);
+            d_of[s] = __shfl(ad, src, moe::WAVE);
+            const int rank = rank_of(a, d_of[s]);
+            const float f = a.scale && d_of[s] >= 0 ? a.scale[d_of[s]] : 1.0f;
+#pragma unroll
+            for (int c = 0; c < RC; ++c) {
+                const int j = 32 * c + 8 * q;
+                float v[8] = {};
+                if (j < rank) {
+                    for (int sp = 0; sp < a.splits; ++sp) {
+                        const v4f* p = reinterpret_cast<const v4f*>(a.h + ((int64_t)sp * a.T + t[s]) * a.r + j);
+                        const v4f lo = p[0], hi = p[1];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] += lo[i], v[4 + i] += hi[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = j + i < rank ? f * v[i] : 0.0f;
+                }
+                cut8(v, hp[s][c]);
+            }
+        }
+        for (int step = first; step < last; ++step) {
+            const int n0 = 32 * step;
+            v4f acc[NT][2] = {};
+            // every adapter of these tokens in turn
+            unsigned long long rest = __ballot(ad >= 0 && (TM == 16 || (lane >> 4) / NT == grp));
+            while (rest) {
+                const int d = __builtin_amdgcn_readlane(ad, __builtin_ctzll(rest));
+                rest &= ~__ballot(ad == d);
+                const int rank = rank_of(a, d);
+                v4f one[NT][2] = {};
+#pragma unroll
+                for (int c = 0; c < RC; ++c) {
+                    const int j = 32 * c + 8 * q;
+                    if (32 * c >= rank) break;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = YD == MOE_X_F32 ? n0 + 16 * h + m : n0 + 8 * (m >> 2) + 4 * h + (m & 3);
+                        v4u w = {};
+                        if (j < rank) {
+                            w = *reinterpret_cast<const v4u*>(a.b + ((int64_t)d * a.N + min(row, a.N - 1)) * a.r + j);
+                            if (j + 8 > rank) {  // columns past the rank may hold anything
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    w[i] &= (j + 2 * i < rank ? 0xFFFFu : 0u) | (j + 2 * i + 1 < rank ? 0xFFFF0000u : 0u);
+                            }
+                        }
+#pragma unroll
+                        for (int s = 0; s < NT; ++s)
+#pragma unroll
+                            for (int p = 0; p < 3; ++p)
+                                one[s][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), hp[s][c][p],
+                                                                                    one[s][h], 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int s = 0; s < NT; ++s)
+                    if (d_of[s] == d) acc[s][0] = one[s][0], acc[s][1] = one[s][1];
+            }
+#pragma unroll
+            for (int s = 0; s < NT; ++s) {
+                if (t[s] < 0) continue;
+                if constexpr (YD == MOE_X_F32) {
+                    const float* bp = reinterpret_cast<const float*>(a.base) + (int64_t)t[s] * a.ldb;
+                    float* yp = reinterpret_cast<float*>(a.y) + (int64_t)t[s] * a.ldy;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int n = n0 + 16 * h + 4 * q;
+                        if (n + 4 <= a.N) {
+                            v4f v = acc[s][h];
+                            if (a.base) v += *reinterpret_cast<const v4f_loose*>(bp + n);
+                            *reinterpret_cast<v4f_loose*>(yp + n) = v;
+                        } else {
+                            for (int i = 0; n + i < a.N; ++i) yp[n + i] = (a.base ? bp[n + i] : 0.0f) + acc[s][h][i];
+                        }
+                    }
+                } else {
+                    const uint16_t* bp = reinterpret_cast<const uint16_t*>(a.base) + (int64_t)t[s] * a.ldb;
+                    __bf16* yp = reinterpret_cast<__bf16*>(a.y) + (int64_t)t[s] * a.ldy;
+                    const int n = n0 + 8 * q;
+                    if (n + 8 <= a.N) {
+                        v4u w = {};
+                        if (a.base) w = *reinterpret_cast<const v4u_loose*>(bp + n);
+                        bf16x8 o;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            o[i] = (__bf16)((i & 1 ? moe::bf16_hi(w[i >> 1]) : moe::bf16_lo(w[i >> 1])) + acc[s][i >> 2][i & 3]);
+                        *reinterpret_cast<v4u_loose*>(yp + n) = __builtin_bit_cast(v4u, o);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (n + i < a.N) yp[n + i] = (__bf16)((a.base ? moe::bf16_to_f32(bp[n + i]) : 0.0f) + acc[s][i >> 2][i & 3]);
+                    }
+                }
+            }
+        }
+    }
 }
 
 bool on_elements(const void* p, int dtype) {
     return (reinterpret_cast<uintptr_t>(p) & (dtype == MOE_X_F32 ? 3u : 1u)) == 0;
+}
+
+int tile_tokens(int T) { return T > MANY ? 64 : 16; }
+
+// Parts that the inputs are split in between workgroups: enough for one a CU where
+// every token has the same adapter, none shorter than 256 inputs.
+int down_splits(int T, int K) {
+    const int tm = tile_tokens(T), tiles = (T + tm - 1) / tm;
+    int s = 256 / (tiles > 0 ? tiles : 1);
+    if (s > K / 256) s = K / 256;
+    if (s > MAX_SPLITS) s = MAX_SPLITS;
+    return s < 1 ? 1 : s;
+}
+
+size_t h_bytes(int T, int K, int r) { return (size_t)down_splits(T, K) * (T > 0 ? T : 1) * r * 4; }
+
+template <int XD, int NT>
+void launch_down(const LoraArgs& g, int tiles, int spread, hipStream_t stream) {
+    const dim3 grid(tiles, spread, g.splits * ((g.r + RANKS - 1) / RANKS)), block(64 * DOWN_WAVES);
+    if (g.r <= 16) hipLaunchKernelGGL((k_lora_down<XD, NT, 1>), grid, block, 0, stream, g);
+    else if (g.r <= 32) hipLaunchKernelGGL((k_lora_down<XD, NT, 2>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_lora_down<XD, NT, 4>), grid, block, 0, stream, g);
+}
+
+template <int YD, int TM>
+void launch_up(const LoraArgs& g, const dim3& grid, const dim3& block, hipStream_t stream) {
+    constexpr int S = TM / 16;
+    if (g.r <= 32) hipLaunchKernelGGL((k_lora_up<YD, TM, S, 1>), grid, block, 0, stream, g);
+    else if (g.r <= 64) hipLaunchKernelGGL((k_lora_up<YD, TM, S, 2>), grid, block, 0, stream, g);
+    else if (g.r <= 128) hipLaunchKernelGGL((k_lora_up<YD, TM, (S > 2 ? 2 : S), 4>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_lora_up<YD, TM, 1, 8>), grid, block, 0, stream, g);
 }
 
 }  // namespace
@@ -77,7 +406,7 @@ extern "C" {
 
 size_t moe_lora_workspace_bytes(int T, int K, int r) {
     if (T < 0 || T > MOE_LINEAR_MAX_T || K < 8 || K > MOE_LINEAR_MAX_NK || r < 8 || r > MOE_LORA_MAX_R) return 0;
-    return (size_t)(T > 0 ? T : 1) * r * 4;
+    return h_bytes(T, K, r) + (T > WAVE_TOKENS ? (size_t)T * 4 : 0);
 }
 
 int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const void* b, const int32_t* ranks,
@@ -102,24 +431,38 @@ int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const v
     MOE_REQUIRE(ws_bytes >= moe_lora_workspace_bytes(T, K, r), MOE_E_ARG, "moe_lora_add: workspace of %zu bytes, %zu needed",
                 ws_bytes, moe_lora_workspace_bytes(T, K, r));
     if (T == 0) return moe_ok();
-    const LoraArgs g{x, ldx, reinterpret_cast<const uint16_t*>(a), reinterpret_cast<const uint16_t*>(b), ranks, scale,
-                     ids, n, r, T, N, K, base, ldb, y, ldy, reinterpret_cast<float*>(ws)};
-    if (x_dtype == MOE_X_F32) hipLaunchKernelGGL(k_lora_down<MOE_X_F32>, dim3(T), dim3(256), 0, stream, g);
-    else hipLaunchKernelGGL(k_lora_down<MOE_X_BF16>, dim3(T), dim3(256), 0, stream, g);
-    if (int rc = moe_check_launch("moe_lora_add/down")) return rc;
-    for (int t0 = 0; t0 < T; t0 += 65535) {
-        LoraArgs c = g;
-        const int rows = T - t0 < 65535 ? T - t0 : 65535;
-        const size_t yb = y_dtype == MOE_X_F32 ? 4 : 2;
-        c.ids += t0, c.h += (size_t)t0 * r;
-        c.y = reinterpret_cast<char*>(y) + (size_t)t0 * ldy * yb;
-        if (base) c.base = reinterpret_cast<const char*>(base) + (size_t)t0 * ldb * yb;
-        const dim3 grid((N + 255) / 256, rows);
-        if (y_dtype == MOE_X_F32) hipLaunchKernelGGL(k_lora_up<MOE_X_F32>, grid, dim3(256), 0, stream, c);
-        else hipLaunchKernelGGL(k_lora_up<MOE_X_BF16>, grid, dim3(256), 0, stream, c);
-        if (int rc = moe_check_launch("moe_lora_add/up")) return rc;
+    LoraArgs g{x, ldx, reinterpret_cast<const uint16_t*>(a), reinterpret_cast<const uint16_t*>(b), ranks, scale, ids, n, r,
+               T, N, K, base, ldb, y, ldy, reinterpret_cast<float*>(ws), nullptr, down_splits(T, K), 1};
+    if (T > WAVE_TOKENS) {
+        g.order = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(ws) + h_bytes(T, K, r));
+        hipLaunchKernelGGL(k_lora_order, dim3((T + 63) / 64), dim3(256), 0, stream, g);
+        if (int rc = moe_check_launch("moe_lora_add/order")) return rc;
     }
-    return moe_ok();
+    const int tm = tile_tokens(T), tiles = (T + tm - 1) / tm;
+    const int most = n < tm ? n : tm;  // adapters of a tile
+    const int spread = tm == 16 ? most : most < 4 ? most : 4;
+    if (x_dtype == MOE_X_F32) {
+        if (tm == 16) launch_down<MOE_X_F32, 1>(g, tiles, spread, stream);
+        else launch_down<MOE_X_F32, 4>(g, tiles, spread, stream);
+    } else {
+        if (tm == 16) launch_down<MOE_X_BF16, 1>(g, tiles, spread, stream);
+        else launch_down<MOE_X_BF16, 4>(g, tiles, spread, stream);
+    }
+    if (int rc = moe_check_launch("moe_lora_add/down")) return rc;
+    // steps a wave: as many as leave 16 waves a CU, up to 8
+    const int steps = (N + 31) / 32;
+    while (g.steps < 8 && (int64_t)tiles * steps / (2 * g.steps) >= 256 * 16) g.steps *= 2;
+    const int need = (steps + g.steps - 1) / g.steps;  // waves a tile
+    const int per = (int64_t)need * tiles <= 1024 ? 1 : 4;
+    const dim3 grid((need + per - 1) / per, tiles), block(64 * per);
+    if (y_dtype == MOE_X_F32) {
+        if (tm == 16) launch_up<MOE_X_F32, 16>(g, grid, block, stream);
+        else launch_up<MOE_X_F32, 64>(g, grid, block, stream);
+    } else {
+        if (tm == 16) launch_up<MOE_X_BF16, 16>(g, grid, block, stream);
+        else launch_up<MOE_X_BF16, 64>(g, grid, block, stream);
+    }
+    return moe_check_launch("moe_lora_add/up");
 }
 
 }  // extern "C"
