@@ -35,7 +35,7 @@ struct SelArgs {
     int32_t* ids;
     float* w;
     int batch;  // tokens that a wave takes, one after the other
-    int seg;    // lanes of a token's weights: 8, 16 or 32
+    int seg;    // lanes of a token's candidates and picks, 16, 32 or 64 (of the gradient's 8, 16 or 32)
 };
 
 template <int ZD>
@@ -75,7 +75,7 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// Reduction over segments of 8, 16 or 32 lanes.
+// Reduction over segments of 8, 16, 32 or 64 lanes.
 template <typename T, typename Op>
 __device__ __forceinline__ T seg_all(T v, int seg, Op op) {
     v = op(v, moe::dpp_of<moe::DPP_XOR1>(v));
@@ -85,6 +85,11 @@ __device__ __forceinline__ T seg_all(T v, int seg, Op op) {
     if (seg > 16) {
         T x, y;
         moe::row_pair<false>(v, x, y);
+        v = op(x, y);
+    }
+    if (seg > 32) {
+        T x, y;
+        moe::row_pair<true>(v, x, y);
         v = op(x, y);
     }
     return v;
@@ -115,30 +120,31 @@ __device__ __forceinline__ double lane_of(double v, int lane) {
 
 // LDS of a wave.
 struct SelLds {
-    double* row;   // [E], 64-bit choices (or, fp32, those of the group stage)
-    float2* cand;  // [CAND] logit, id
-    double* ord;   // [CAND + 1] choices in order
-    float* ordz;   // [CAND + 1] and their logits
-    float2* pick;  // [64] logit, id: `batch` tokens by `seg`
+    double* ord;   // [CAND + 2] choices in order
+    float* ordz;   // [CAND + 2] and their logits
+    float* candz;  // [CAND] candidates: logits
+    int* candi;    // [CAND] and ids
+    float* pickz;  // [CAND] picks
+    int* picki;    // [CAND]
+    uint32_t* kept;  // [2 * 4] lanes of the kept groups of a token
 };
 
-constexpr size_t SEL_FIXED = CAND * 8 + (CAND + 2) * 8 + (CAND + 2) * 4 + 64 * 8;
-__host__ __device__ constexpr size_t sel_lds(int E) { return (((size_t)8 * E + SEL_FIXED) + 15) & ~(size_t)15; }
+constexpr size_t SEL_LDS = (CAND + 2) * 12 + CAND * 16 + 40;
 
-__device__ __forceinline__ SelLds sel_parts(unsigned char* p, int E) {
+__device__ __forceinline__ SelLds sel_parts(unsigned char* p) {
     SelLds l;
-    l.row = reinterpret_cast<double*>(p);
-    l.cand = reinterpret_cast<float2*>(l.row + E);
-    l.ord = reinterpret_cast<double*>(l.cand + CAND);
-    l.pick = reinterpret_cast<float2*>(l.ord + CAND + 2);
-    l.ordz = reinterpret_cast<float*>(l.pick + 64);
+    l.ord = reinterpret_cast<double*>(p);
+    l.ordz = reinterpret_cast<float*>(l.ord + CAND + 2);
+    l.candz = l.ordz + CAND + 2;
+    l.candi = reinterpret_cast<int*>(l.candz + CAND);
+    l.pickz = reinterpret_cast<float*>(l.candi + CAND);
+    l.picki = reinterpret_cast<int*>(l.pickz + CAND);
+    l.kept = reinterpret_cast<uint32_t*>(l.picki + CAND);
     return l;
 }
 
-__device__ __forceinline__ float2 packed(float z, int id) { return float2{z, __int_as_float(id)}; }
-
-// Which groups are kept, as bits: every one of the `per` lanes of a group holds
-// that group's value.  unsure: values are off by up to err, and that may matter.
+// Which lanes hold experts of a kept group: every one of the `per` lanes of a group
+// has that group's value.  unsure: values are off by up to err, and that may matter.
 template <typename T>
 __device__ __forceinline__ unsigned long long keep_groups(T value, T err, int G, int kept, int per, T* sorted, bool& unsure) {
     const int lane = threadIdx.x & 63, g = lane / per;
@@ -147,99 +153,121 @@ __device__ __forceinline__ unsigned long long keep_groups(T value, T err, int G,
         const T v = lane_of(value, o * per);
         rank += v > value || (v == value && o < g);
     }
-    const bool leads = lane % per == 0 && g < G && value > (T)-INFINITY;
-    unsigned long long b = __ballot(leads && rank < kept);
+    const bool open = g < G && value > (T)-INFINITY;
     unsure = false;
     if (err > 0 && kept < G) {
-        if (lane % per == 0 && g < G) sorted[rank] = value;
+        if (g < G) sorted[rank] = value;
         wave_sync();
         const T last = sorted[kept - 1], next = sorted[kept];
         const T mid = next > (T)-INFINITY ? next + (T)0.5 * (last - next) : (T)-INFINITY;
-        unsure = __any(leads && !(rank < kept ? value - err > mid : value + err < mid));
+        unsure = __any(open && !(rank < kept ? value - err > mid : value + err < mid));
+        wave_sync();
     }
-    if (per == 1) return b;
-    unsigned long long out = 0;  // a bit a group
-    for (; b; b &= b - 1) out |= 1ull << (__builtin_ctzll(b) / per);
-    return out;
+    return __ballot(open && rank < kept);
 }
 
-// The two largest of a group's choices that a lane sees, joined with another's.
+// The two largest of what was seen, and one more.
 template <typename T>
 __device__ __forceinline__ void top2(T v, T& best, T& second) {
     second = v > best ? best : v > second ? v : second;
     best = v > best ? v : best;
 }
 
-// A group's value: its lanes (per: a power of two, neighbours) go through its row.
-// size: the magnitudes of what was added.
+// A group's value from the two largest choices of each of its lanes (per: a power
+// of two, neighbours).  size: the magnitudes of what was added.
 template <typename T>
-__device__ __forceinline__ T group_value(const T* row, int G, int gs, int per, int top, T& size) {
-    const int lane = threadIdx.x & 63, g = lane / per;
-    T best = -INFINITY, second = -INFINITY;
-    if (g < G)
-        for (int i = lane % per; i < gs; i += per) top2(row[g * gs + i], best, second);
-    for (int s = 1; s < per; s <<= 1) {
-        const T b = __shfl_xor(best, s, moe::WAVE), c = __shfl_xor(second, s, moe::WAVE);
+__device__ __forceinline__ T group_value(T best, T second, int per, int top, T& size) {
+    const auto join = [&](T b, T c) {
         top2(b, best, second);
         top2(c, best, second);
-    }
+    };
+    if (per > 1) join(moe::dpp_of<moe::DPP_XOR1>(best), moe::dpp_of<moe::DPP_XOR1>(second));
+    if (per > 2) join(moe::dpp_of<moe::DPP_XOR2>(best), moe::dpp_of<moe::DPP_XOR2>(second));
+    if (per > 4) join(moe::dpp_of<moe::DPP_HALF_MIRROR>(best), moe::dpp_of<moe::DPP_HALF_MIRROR>(second));
+    if (per > 8) join(moe::dpp_of<moe::DPP_MIRROR>(best), moe::dpp_of<moe::DPP_MIRROR>(second));
+    if (per > 16) join(__shfl_xor(best, 16, moe::WAVE), __shfl_xor(second, 16, moe::WAVE));
     const bool two = top > 1 && second > (T)-INFINITY;
     size = two ? fabs(best) + fabs(second) : fabs(best);
     return two ? best + second : best;
 }
 
-__device__ __forceinline__ int lanes_per_group(int G) {
+__host__ __device__ __forceinline__ int lanes_per_group(int G) {
     int per = 64;
     while (per * G > 64) per >>= 1;
     return per;
 }
 
-// A token's picks with every choice in double, by k rounds: where fp32 does not
-// tell the groups apart, or leaves more candidates than lanes (many logits equal,
-// or nearly so).  plain: choices are the logits themselves.
+// 1 / the sum of a softmax, in double (0: nothing open), and the largest logit.
 template <int ZD>
-__device__ __forceinline__ void choose64(const SelArgs& a, int64_t t, bool plain, SelLds l, float2* out) {
-    const int lane = threadIdx.x & 63, E = a.E, G = a.rule.groups, gs = E / G;
-    const bool sigmoid = a.rule.score == MOE_SCORE_SIGMOID;
-    float m = -INFINITY;
+__device__ __forceinline__ double softmax64(const SelArgs& a, int64_t t, float& m) {
+    const int lane = threadIdx.x & 63;
+    m = -INFINITY;
+    for (int e = lane; e < a.E; e += 64) m = fmaxf(m, load_z<ZD>(a.z, t * a.E + e));
+    m = moe::wave_all_max(m);
+    double sum = 0.0;
+    for (int e = lane; e < a.E; e += 64) {
+        const float z = load_z<ZD>(a.z, t * a.E + e);
+        sum += z > -INFINITY ? soft64(z, m) : 0.0;
+    }
+    return rcp64(moe::wave_all_sum(sum));
+}
+
+// A token's choices in double, an expert at a time.
+template <int ZD>
+struct Choice64 {
+    const SelArgs& a;
+    int64_t row;
+    float m = 0.0f;
     double r = 1.0;
-    if (!sigmoid && !plain) {
-        for (int e = lane; e < E; e += 64) m = fmaxf(m, load_z<ZD>(a.z, t * E + e));
-        m = moe::wave_all_max(m);
-        double sum = 0.0;
-        for (int e = lane; e < E; e += 64) {
-            const float z = load_z<ZD>(a.z, t * E + e);
-            sum += z > -INFINITY ? soft64(z, m) : 0.0;
-        }
-        r = rcp64(moe::wave_all_sum(sum));
+    __device__ __forceinline__ Choice64(const SelArgs& args, int64_t t) : a(args), row(t * args.E) {
+        if (a.rule.score == MOE_SCORE_SOFTMAX) r = softmax64<ZD>(a, t, m);
     }
-    for (int e = lane; e < E; e += 64) {
-        const float z = load_z<ZD>(a.z, t * E + e), b = a.bias ? a.bias[e] : 0.0f;
-        double c = -INFINITY, rest;
-        if (z > -INFINITY && b > -INFINITY) c = plain ? (double)z : (sigmoid ? sigmoid64(z, rest) : soft64(z, m) * r) + (double)b;
-        l.row[e] = c;
+    __device__ __forceinline__ double operator()(int e, float& z) const {
+        z = load_z<ZD>(a.z, row + e);
+        const float b = a.bias ? a.bias[e] : 0.0f;
+        double rest;
+        if (!(z > -INFINITY && b > -INFINITY)) return -INFINITY;
+        return (a.rule.score == MOE_SCORE_SIGMOID ? sigmoid64(z, rest) : soft64(z, m) * r) + (double)b;
     }
-    wave_sync();
-    if (G > 1) {
-        const int per = lanes_per_group(G);
-        double size;
-        bool unsure;
-        const double value = group_value<double>(l.row, G, gs, per, a.rule.group_top, size);
-        const unsigned long long kept = keep_groups<double>(value, 0.0, G, a.rule.groups_kept, per, l.ord, unsure);
-        for (int e = lane; e < E; e += 64)
-            if (!((kept >> (e / gs)) & 1)) l.row[e] = -INFINITY;
-        wave_sync();
-    }
+};
+
+// The lanes of the kept groups, in double: where fp32 does not tell the groups apart.
+template <int ZD>
+__device__ __forceinline__ unsigned long long groups64(const SelArgs& a, const Choice64<ZD>& choice, double* sorted) {
+    const int lane = threadIdx.x & 63, G = a.rule.groups, gs = a.E / G, per = lanes_per_group(G), g = lane / per;
+    double best = -INFINITY, second = -INFINITY, size;
+    bool unsure;
+    float z;
+    if (g < G)
+#pragma unroll 1
+        for (int i = lane % per; i < gs; i += per) top2(choice(g * gs + i, z), best, second);
+    const double value = group_value<double>(best, second, per, a.rule.group_top, size);
+    return keep_groups<double>(value, 0.0, G, a.rule.groups_kept, per, sorted, unsure);
+}
+
+// A token's picks, round by round, each the best behind the one before: where more
+// candidates than lanes are nearly equal, or a group is larger than the registers.
+// Picks go to places `to` and up.
+template <int ZD>
+__device__ __forceinline__ void choose64(const SelArgs& a, int64_t t, const SelLds& l, int to) {
+    const int lane = threadIdx.x & 63, E = a.E, G = a.rule.groups, gs = E / G, per = lanes_per_group(G);
+    const int first = lane / per * gs + lane % per, end = lane / per < G ? (lane / per + 1) * gs : 0;
+    const Choice64<ZD> choice(a, t);
+    const bool kept = G == 1 || (groups64<ZD>(a, choice, l.ord) >> lane) & 1;
+    double pc = INFINITY;
+    float pz = INFINITY;
+    int pe = -1;
     for (int i = 0; i < a.k; ++i) {
         double bc = -INFINITY;
         float bz = -INFINITY;
         int be = E;
-        for (int e = lane; e < E; e += 64) {
-            const double c = l.row[e];
-            if (c < bc || !(c > -INFINITY)) continue;
-            const float z = load_z<ZD>(a.z, t * E + e);
-            if (c > bc || z > bz) bc = c, bz = z, be = e;
-        }
+        if (kept)
+            for (int e = first; e < end; e += per) {
+                float z;
+                const double c = choice(e, z);
+                if (c > pc || (c == pc && (z > pz || (z == pz && e <= pe)))) continue;  // taken
+                if (c > bc || (c == bc && z > bz)) bc = c, bz = z, be = e;
+            }
 #pragma unroll
         for (int s = 32; s >= 1; s >>= 1) {
             const double oc = __shfl_xor(bc, s, moe::WAVE);
@@ -248,248 +276,409 @@ __device__ __forceinline__ void choose64(const SelArgs& a, int64_t t, bool plain
             if (oc > bc || (oc == bc && (oz > bz || (oz == bz && oe < be)))) bc = oc, bz = oz, be = oe;
         }
         if (!(bc > -INFINITY)) break;
-        if (lane == 0) out[i] = packed(bz, be), l.row[be] = -INFINITY;
-        wave_sync();
+        if (lane == 0) l.pickz[to + i] = bz, l.picki[to + i] = be;
+        pc = bc, pz = bz, pe = be;
     }
+    wave_sync();
 }
 
-// One wave a token at a time.  Lane l holds experts (l + 64 j) VEC + v.
+// How a token's experts are compared: by logits (PLAIN), or by choice scores, in a
+// row of experts or in a group of lanes for each group of experts.
+enum { PLAIN, SCORED, GROUPED };
+
+// Largest of three; the instruction by itself, without the compiler's step that makes
+// a signalling NaN quiet first.
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float d;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(x), "v"(y), "v"(z));
+    return d;
+}
+
+// Largest of a lane's numbers, -inf without any.  A signalling NaN may hide some.
+template <int NE>
+__device__ __forceinline__ float lane_max(const float (&v)[NE]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j + 1 < NE; j += 2) m = max3(m, v[j], v[j + 1]);
+    if (NE & 1) m = max3(m, v[NE - 1], m);
+    return max3(m, -INFINITY, -INFINITY);
+}
+
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    return moe::wave_all(v, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+}
+
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+template <int N = 1, typename F>
+__device__ __forceinline__ void rotations(const F& f) {  // f(1) .. f(15)
+    if constexpr (N < 16) {
+        f(Int<N>{});
+        rotations<N + 1>(f);
+    }
+}
+template <int N, typename T>
+__device__ __forceinline__ T turned(T v) { return moe::dpp_of<0x120 + N>(v); }  // of the lane N below in the row of 16
+
+// How far a share of k_select's fp32 softmax may be off, relative to it.  A term: 0.63
+// |z| 2^-23 for the rounding of its argument, |z| up to 11 where no maximum is taken
+// off and weighed to ln E at most otherwise, and its last bit; E / 64 + 6 additions, a
+// quotient, a product.
+__device__ __forceinline__ float share_error(int E) { return (2.0f * __logf((float)E) + (float)E * 0x1p-6f + 32.0f) * 0x1p-23f; }
+
+// One wave takes `batch` tokens.
 //
-// The k best of E without k rounds: the lanes' largest keys bound the k-th best
-// from below (there are k at least as good), by bisection between the smallest
-// maximum of 8, 16 or 32 sets of lanes and the largest of all; whatever reaches
-// that bound, some k + 4 experts, moves to a lane of its own and is ranked against
-// the others.  The keys are the logits, or, where a bias or groups
-// makes the scores themselves count (SCORED), fp32 choices with a bound on how far
-// they are from the 64-bit ones: candidates are taken twice that below the bound,
-// and ranked by 64-bit choices of which there is one a lane.
-// The weights of up to eight tokens are then taken side by side.
-template <int ZD, int VEC, int NE, bool SCORED>
+// One after the other: the k best of E without k rounds.  The lanes' largest keys
+// bound the k-th best from below (there are k at least as good), by bisection
+// between the smallest maximum of 8, 16 or 32 sets of lanes and the largest of all;
+// whatever reaches that bound, some k + 3 experts, are the candidates.  Keys are the
+// logits, or fp32 choices with a bound on how far they are from the 64-bit ones:
+// candidates are then taken from twice that below the bound.  A logit or bias that
+// closes an expert makes its key NaN or -inf, by 0 * -inf.  With groups each group
+// has lanes of its own (as many as there are for all, a power of two), which hold its
+// experts; what a token drops is dropped with the lane.
+//
+// Side by side, a segment of lanes a token: candidates are ranked, by 64-bit choices,
+// and the picks weighed.
+template <int ZD, int VEC, int NE, int HOW>
 __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
-    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ __align__(16) unsigned char smem[SEL_WAVES * SEL_LDS];
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-    const int64_t t0 = ((int64_t)blockIdx.x * (blockDim.x >> 6) + wid) * a.batch;
+    const int64_t t0 = ((int64_t)blockIdx.x * SEL_WAVES + wid) * a.batch;
     if (t0 >= a.T) return;
     const int E = a.E, k = a.k, G = a.rule.groups, gs = E / G, seg = a.seg;
     const int n = a.T - t0 < a.batch ? (int)(a.T - t0) : a.batch;
-    const SelLds l = sel_parts(smem + (size_t)wid * sel_lds(E), E);
+    const SelLds l = sel_parts(smem + wid * SEL_LDS);
     const bool sigmoid = a.rule.score == MOE_SCORE_SIGMOID;
-    const bool sums = !sigmoid && (SCORED || !a.rule.renorm);  // the softmax over all experts is needed
-    const auto at = [&](int j) { return (lane + 64 * (j / VEC)) * VEC + j % VEC; };
-    const int mine = lane / seg;  // the token whose weights this lane takes
+    const bool sums = !sigmoid && (HOW != PLAIN || !a.rule.renorm);  // the softmax over all experts is needed
+    // this lane's experts: first, first + stride, ... `own` of them (of pairs: of bf16 pairs)
+    const int per = HOW == GROUPED ? lanes_per_group(G) : 64;
+    const int first = HOW == GROUPED ? lane / per * gs + lane % per : lane * VEC, stride = HOW == GROUPED ? per : 64 * VEC;
+    const int own = HOW == GROUPED ? (lane / per < G ? (gs - lane % per + per - 1) / per : 0) : (E - first + stride - 1) / stride;
+    const auto at = [&](int j) { return first + j / VEC * stride + j % VEC; };
+    l.pickz[lane] = -INFINITY;
+    l.picki[lane] = -1;
+    const int mine = lane / seg;  // the token whose candidates and picks this lane takes
+    int my_c = 0;
     float my_m = 0.0f, my_sum = 1.0f;
-    l.pick[lane] = packed(-INFINITY, -1);
-    wave_sync();
+    uint32_t slow = 0;  // tokens to be taken in double from the start
     unsigned long long todo = __ballot(lane < n && (!a.mask || a.mask[t0 + lane]));
 
-    float bias[SCORED ? NE : 1];
-    if constexpr (SCORED) {
+    constexpr bool KEEP = NE <= 16;  // the biases stay in registers; the next token's logits are read while this one's are looked at
+    float bias[HOW != PLAIN && KEEP ? NE : 1];
+    const auto bias_at = [&](int j) { return j / VEC < own ? (a.bias ? a.bias[at(j)] : 0.0f) : -INFINITY; };
+    if constexpr (HOW != PLAIN && KEEP) {
 #pragma unroll
-        for (int j = 0; j < NE; ++j) bias[j] = a.bias ? (at(j) < E ? a.bias[at(j)] : -INFINITY) : 0.0f;
+        for (int j = 0; j < NE; ++j) bias[j] = bias_at(j);
     }
-    constexpr bool AHEAD = NE <= 16;  // the next token's logits while this one's are looked at
     float zn[NE];
     const auto load = [&](int64_t t) {
 #pragma unroll
         for (int j = 0; j < NE / VEC; ++j) {
-            const int e = (lane + 64 * j) * VEC;
-            const int64_t i = t * E + e;
+            const int64_t i = t * E + first + j * stride;
             if constexpr (VEC == 1) {
-                zn[j] = e < E ? load_z<ZD>(a.z, i) : -INFINITY;
+                zn[j] = j < own ? load_z<ZD>(a.z, i) : -INFINITY;
             } else {
-                const uint32_t p = e < E ? *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(a.z) + i) : 0xFF80FF80u;
+                const uint32_t p = j < own ? *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(a.z) + i) : 0xFF80FF80u;
                 zn[2 * j] = moe::bf16_lo(p);
                 zn[2 * j + 1] = moe::bf16_hi(p);
             }
         }
     };
     const bool rows = !a.ids_in || sums;
-    if (AHEAD && rows && (todo & 1)) load(t0);
-    for (int i = 0; i < n && rows; ++i) {
-        const int64_t t = t0 + i;
-        float z[NE];
-        if (!AHEAD && (todo & 1)) load(t);
+    uint32_t close = 0;  // tokens whose groups fp32 does not tell apart
+    for (bool exact = false; rows && todo; exact = true) {
+        if (KEEP) load(t0 + __builtin_ctzll(todo));
+        while (todo) {
+            const int i = __builtin_ctzll(todo);
+            todo &= todo - 1;
+            const int64_t t = t0 + i;
+            float z[NE];
+            if (!KEEP) load(t);
 #pragma unroll
-        for (int j = 0; j < NE; ++j) z[j] = zn[j] > -INFINITY ? zn[j] : -INFINITY;
-        if (AHEAD && (todo >> 1) & 1) load(t + 1);
-        const bool on = todo & 1;
-        todo >>= 1;
-        if (!on) continue;
-
-        float m = 0.0f, sum = 1.0f;
-        if (sums) {
-            m = z[0];
-#pragma unroll
-            for (int j = 1; j < NE; ++j) m = fmaxf(m, z[j]);
-            m = moe::wave_all_max(m);
-            if (m == -INFINITY) continue;  // nothing open
-        }
-        float key[NE];
-        if (sums) {
-            sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < NE; ++j) {
-                key[j] = z[j] > -INFINITY ? soft32(z[j], m) : 0.0f;
-                sum += key[j];
+            for (int j = 0; j < NE; ++j) z[j] = zn[j];
+            if (KEEP && todo) load(t0 + __builtin_ctzll(todo));
+            if (HOW == GROUPED && NE == 64 && gs > NE * per) {  // more than registers
+                slow |= 1u << i;
+                continue;
             }
-            sum = moe::wave_all_sum(sum);
-            if (mine == i) my_m = m, my_sum = sum;
-        }
-        if (a.ids_in) continue;
-        float slack = 0.0f;  // how far a key may be from its 64-bit choice, but for the rounding of a sum with the bias
-        if constexpr (SCORED) {
-            if (sigmoid) {
-                // |z| s (1 - s) 2^-23 < 2^-25 for the argument, 2^-25 for the exponential, 2^-24 + 2^-23 for sum and quotient
-                slack = 0x1p-22f;
+            float key[NE], m = 0.0f, sum = 1.0f;
+            bool careful = false;
+            if (sums) {
+                // the softmax needs no maximum taken off where its sum is neither large nor small
 #pragma unroll
-                for (int j = 0; j < NE; ++j) key[j] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[j] * -1.44269504f));
+                for (int j = 0; j < NE; ++j) key[j] = __builtin_amdgcn_exp2f(z[j] * 1.44269504f);
+                sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NE; ++j) sum += key[j];
+                sum = moe::wave_all_sum(sum);
+                careful = __any(!(sum > 0x1p-8f && sum < 0x1p16f));  // or NaN, or nothing open; the same on every lane
+                if (careful) {
+#pragma unroll
+                    for (int j = 0; j < NE; ++j) z[j] = z[j] > -INFINITY ? z[j] : -INFINITY;
+                    m = of_code(wave_max_u32(code_of(lane_max(z))));
+                    if (m == -INFINITY) continue;
+                    sum = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < NE; ++j) {
+                        key[j] = z[j] > -INFINITY ? soft32(z[j], m) : 0.0f;
+                        sum += key[j];
+                    }
+                    sum = moe::wave_all_sum(sum);
+                }
+                if (mine == i) my_m = m, my_sum = sum;
+            }
+            if (a.ids_in) continue;
+            float slack = 0.0f;  // how far a key may be from its 64-bit choice, but for the rounding of a sum with the bias
+            unsigned long long in_kept = ~0ull;
+            if constexpr (HOW == PLAIN) {
+#pragma unroll
+                for (int j = 0; j < NE; ++j) key[j] = z[j];
             } else {
-                // (1.5 ln E + 2 + E / 64 + 6) 2^-23 of a share for the sum, 3 of them for the term; shares are 1 / sum at most
-                const float r = __builtin_amdgcn_rcpf(sum);
-                slack = (2.0f * __logf((float)E) + (float)E * 0x1p-6f + 16.0f) * 0x1p-23f * r;
+                if (sigmoid) {
+                    // |z| s (1 - s) 2^-23 < 2^-25 for the argument, 2^-25 for the exponential, 2^-24 + 2^-23 for sum and quotient
+                    slack = 0x1p-22f;
 #pragma unroll
-                for (int j = 0; j < NE; ++j) key[j] *= r;
-            }
+                    for (int j = 0; j < NE; ++j) {
+                        const float b = KEEP ? bias[KEEP ? j : 0] : bias_at(j);
+                        key[j] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[j] * -1.44269504f)) + fmaf(fminf(z[j], 0.0f), 0.0f, b);
+                    }
+                } else {
+                    const float r = __builtin_amdgcn_rcpf(sum);
+                    slack = share_error(E);
+                    const auto b = [&](int j) { return KEEP ? bias[KEEP ? j : 0] : bias_at(j); };
+                    if (careful) {
 #pragma unroll
-            for (int j = 0; j < NE; ++j) key[j] = z[j] > -INFINITY && bias[j] > -INFINITY ? key[j] + bias[j] : -INFINITY;
-        } else {
+                        for (int j = 0; j < NE; ++j) key[j] = z[j] > -INFINITY ? fmaf(key[j], r, b(j)) : -INFINITY;
+                    } else {
 #pragma unroll
-            for (int j = 0; j < NE; ++j) key[j] = z[j];
-        }
-        float2* out = l.pick + i * seg;
-        bool again = false;  // in double from the start
-        if (SCORED && G > 1) {
-            float* row = reinterpret_cast<float*>(l.row);
-#pragma unroll
-            for (int j = 0; j < NE; ++j)
-                if (at(j) < E) row[at(j)] = key[j];
-            wave_sync();
-            const int per = lanes_per_group(G);
-            float size;
-            const float value = group_value<float>(row, G, gs, per, a.rule.group_top, size);
-            // a choice is off by the slack and a rounding, a sum of two by a rounding more
-            const float err = 2.0f * slack + size * 0x1p-22f;
-            const unsigned long long kept = keep_groups<float>(value, err, G, a.rule.groups_kept, per, reinterpret_cast<float*>(l.ord), again);
-#pragma unroll
-            for (int j = 0; j < NE; ++j)
-                if (at(j) < E && !((kept >> (at(j) / gs)) & 1)) key[j] = -INFINITY;
-            wave_sync();
-        }
-        // a bound that k keys reach
-        float v = key[0];
-#pragma unroll
-        for (int j = 1; j < NE; ++j) v = fmaxf(v, key[j]);
-        const uint32_t code = code_of(v);
-        uint32_t lo, hi;
-        {
-            const auto up = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
-            const auto down = [](uint32_t x, uint32_t y) { return x < y ? x : y; };
-            uint32_t c = up(code, moe::dpp_of<moe::DPP_XOR1>(code));
-            uint32_t d = c, x, y;
-            c = up(c, moe::dpp_of<moe::DPP_XOR2>(c));
-            d = k > 16 ? down(d, moe::dpp_of<moe::DPP_XOR2>(d)) : c;
-            const uint32_t c8 = up(c, moe::dpp_of<moe::DPP_HALF_MIRROR>(c));
-            d = k > 8 ? down(d, moe::dpp_of<moe::DPP_HALF_MIRROR>(d)) : c8;
-            c = up(c8, moe::dpp_of<moe::DPP_MIRROR>(c8));
-            d = down(d, moe::dpp_of<moe::DPP_MIRROR>(d));
-            moe::row_pair<false>(c, x, y);
-            c = up(x, y);
-            moe::row_pair<false>(d, x, y);
-            d = down(x, y);
-            moe::row_pair<true>(c, x, y);
-            hi = __builtin_amdgcn_readfirstlane((int)up(x, y));
-            moe::row_pair<true>(d, x, y);
-            lo = __builtin_amdgcn_readfirstlane((int)down(x, y));
-        }
-        int have = __builtin_popcountll(__ballot(code >= lo));
-        for (int it = 0; it < 24 && have > k + 2 && hi - lo > 1; ++it) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            const int c = __builtin_popcountll(__ballot(code >= mid));
-            if (c >= k) lo = mid, have = c;
-            else hi = mid;
-        }
-        float bound = of_code(lo);
-        if constexpr (SCORED) bound = bound < INFINITY ? bound - (2.0f * slack + fabsf(bound) * 0x1p-22f) : bound;
-        bound = fmaxf(bound, -3.402823466e38f);  // whatever is open
-        int C = 0;
-#pragma unroll
-        for (int j = 0; j < NE / VEC; ++j) {
-            if constexpr (VEC == 1) {
-                const bool in = key[j] >= bound;
-                const unsigned long long b = __ballot(in);
-                if (!b) continue;
-                const int p = __builtin_amdgcn_mbcnt_hi((uint32_t)(b >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)b, C));
-                if (in && p < CAND) l.cand[p] = packed(z[j], at(j));
-                C += __builtin_popcountll(b);
-            } else {
-                const bool in0 = key[2 * j] >= bound, in1 = key[2 * j + 1] >= bound;
-                const unsigned long long b0 = __ballot(in0), b1 = __ballot(in1);
-                if (!(b0 | b1)) continue;
-                int p = __builtin_amdgcn_mbcnt_hi((uint32_t)(b0 >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)b0, C));
-                p = __builtin_amdgcn_mbcnt_hi((uint32_t)(b1 >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)b1, p));
-                if (in0 && p < CAND) l.cand[p] = packed(z[2 * j], at(2 * j));
-                p += in0;
-                if (in1 && p < CAND) l.cand[p] = packed(z[2 * j + 1], at(2 * j + 1));
-                C += __builtin_popcountll(b0) + __builtin_popcountll(b1);
-            }
-        }
-        again |= C > CAND;
-        wave_sync();
-        // candidates in order of their ids, one a lane
-        C = C < CAND ? C : CAND;
-        const float2 cd = lane < C ? l.cand[lane] : packed(-INFINITY, 0);
-        const float zc = cd.x;
-        const int id = __float_as_int(cd.y);
-        int rank = 0;
-        if (!SCORED || !a.bias) {
-            for (int j = 0; j < C; ++j) {
-                const float o = lane_of(zc, j);
-                rank += o > zc || (o == zc && j < lane);
-            }
-        } else {
-            double c = -INFINITY, rest;
-            if (lane < C) c = (sigmoid ? sigmoid64(zc, rest) : soft64(zc, m) * rcp64((double)sum)) + (double)a.bias[id];
-            for (int j = 0; j < C; ++j) rank += lane_of(c, j) > c;
-            if (lane >= C) rank = lane;
-            // equal choices share a rank: the logits, then the ids decide
-            l.ordz[rank] = __int_as_float(lane);
-            wave_sync();
-            if (__any(__float_as_int(l.ordz[rank]) != lane)) {
-                for (int j = 0; j < C; ++j) {
-                    const float o = lane_of(zc, j);
-                    if (lane < C) rank += lane_of(c, j) == c && (o > zc || (o == zc && j < lane));
+                        for (int j = 0; j < NE; ++j) key[j] = fmaf(key[j], r, fmaf(z[j], 0.0f, b(j)));
+                    }
                 }
             }
-            if (!sigmoid) {
-                // the sum of the softmax is an fp32 one: neighbours that a sum as far off as that may order otherwise
-                wave_sync();
-                l.ord[rank] = c;
-                l.ordz[rank] = zc;
-                wave_sync();
-                const bool near = lane < k && lane + 1 < C && l.ordz[lane] != l.ordz[lane + 1] &&
-                                  l.ord[lane] - l.ord[lane + 1] <= (double)slack;
-                again |= __any(near);
+            float v = lane_max(key);
+            if constexpr (HOW == GROUPED) {
+                float best = -INFINITY, second = -INFINITY, size;
+#pragma unroll
+                for (int j = 0; j < NE; ++j) top2(key[j], best, second);
+                const float value = group_value<float>(best, second, per, a.rule.group_top, size);
+                // a choice is off by the slack and a rounding, a sum of two by a rounding more
+                bool unsure;
+                in_kept = keep_groups<float>(value, 2.0f * slack + size * 0x1p-22f, G, a.rule.groups_kept, per, l.ordz, unsure);
+                if (exact) {
+                    in_kept = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)l.kept[2 * i]) |
+                              ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)l.kept[2 * i + 1]) << 32);
+                } else if (unsure) {
+                    close |= 1u << i;
+                    continue;
+                }
+                if (!((in_kept >> lane) & 1)) v = -INFINITY;
+            }
+            // a bound that k keys reach
+            const uint32_t code = code_of(v);
+            uint32_t lo, hi;
+            {
+                const auto up = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+                const auto down = [](uint32_t x, uint32_t y) { return x < y ? x : y; };
+                // the sets' lanes lie in every row, and so in other groups
+                uint32_t x, y, c, d;
+                moe::row_pair<true>(code, x, y);
+                c = up(x, y), d = c;  // 32 sets of two
+                moe::row_pair<false>(c, x, y);
+                c = up(x, y);
+                d = k > 16 ? (moe::row_pair<false>(d, x, y), down(x, y)) : c;  // 16 of four
+                c = up(c, moe::dpp_of<moe::DPP_MIRROR>(c));
+                d = k > 8 ? down(d, moe::dpp_of<moe::DPP_MIRROR>(d)) : c;  // 8 of eight
+                c = up(c, moe::dpp_of<moe::DPP_HALF_MIRROR>(c));
+                d = down(d, moe::dpp_of<moe::DPP_HALF_MIRROR>(d));
+                c = up(c, moe::dpp_of<moe::DPP_XOR2>(c));
+                d = down(d, moe::dpp_of<moe::DPP_XOR2>(d));
+                hi = __builtin_amdgcn_readfirstlane((int)up(c, moe::dpp_of<moe::DPP_XOR1>(c)));
+                lo = __builtin_amdgcn_readfirstlane((int)down(d, moe::dpp_of<moe::DPP_XOR1>(d)));
+            }
+            int have = __builtin_popcountll(__ballot(code >= lo));
+            const int enough = k + (seg - k) / 4;
+            for (uint32_t step = hi > lo ? 0x80000000u >> __builtin_clz(hi - lo) : 0u; step && have > enough; step >>= 1) {
+                const int c = step <= hi - lo ? __builtin_popcountll(__ballot(code >= lo + step)) : 0;
+                if (c >= k) lo += step, have = c;
+            }
+            // the least key of an expert that may be better than one with this key; above -inf: whatever is open
+            const auto least_of = [&](float kth) {
+                if constexpr (HOW != PLAIN) kth = kth < INFINITY ? kth - (2.0f * slack + fabsf(kth) * 0x1p-22f) : kth;
+                return fmaxf(kth, -3.402823466e38f);
+            };
+            float bound = least_of(of_code(lo));
+            int C = 0;
+            unsigned long long in[NE];
+            const auto reach = [&](float least) {
+                C = 0;
+#pragma unroll
+                for (int j = 0; j < NE; ++j) {
+                    in[j] = __ballot(key[j] >= least) & in_kept;
+                    C += __builtin_popcountll(in[j]);
+                }
+            };
+            reach(bound);
+            if (C > seg) {
+                // lanes with several, or equals: the same search over every key
+                for (++hi; hi - lo > 1 && C > seg;) {
+                    const uint32_t mid = lo + (hi - lo) / 2;
+                    const float kth = fmaxf(of_code(mid), -3.402823466e38f);
+                    reach(kth);
+                    if (C < k) {
+                        hi = mid;
+                        C = seg + 1;
+                        continue;
+                    }
+                    lo = mid;
+                    bound = least_of(kth);
+                    reach(bound);
+                }
+                if (C > seg) {
+                    // what lies above the k-th key for certain, and of the rest, if it is all alike, the lowest ids
+                    const float kth = fmaxf(of_code(lo), -3.402823466e38f), over = kth + (kth - least_of(kth));
+                    reach(least_of(kth));
+                    unsigned long long sure[NE];
+                    int n_sure = 0;
+                    float z0 = 0.0f, b0 = 0.0f;
+                    bool any = false, alike = true;
+#pragma unroll
+                    for (int j = 0; j < NE; ++j) {
+                        sure[j] = in[j] & __ballot(key[j] > over);
+                        n_sure += __builtin_popcountll(sure[j]);
+                        const unsigned long long band = in[j] & ~sure[j];
+                        if (!band) continue;
+                        const float b = HOW == PLAIN ? 0.0f : KEEP ? bias[HOW != PLAIN && KEEP ? j : 0] : bias_at(j);
+                        if (!any) z0 = lane_of(z[j], __builtin_ctzll(band)), b0 = lane_of(b, __builtin_ctzll(band));
+                        any = true;
+                        if (band & __ballot(!(z[j] == z0 && b == b0))) alike = false;
+                    }
+                    if (!alike) {
+                        slow |= 1u << i;
+                        continue;
+                    }
+                    int most = -1;  // the ids up to it number seg or fewer
+                    for (int bit = 1 << 12; bit; bit >>= 1) {
+                        int c = n_sure;
+#pragma unroll
+                        for (int j = 0; j < NE; ++j) c += __builtin_popcountll(in[j] & ~sure[j] & __ballot(at(j) <= most + bit));
+                        if (c <= seg) most += bit;
+                    }
+                    C = 0;
+#pragma unroll
+                    for (int j = 0; j < NE; ++j) {
+                        in[j] &= sure[j] | __ballot(at(j) <= most);
+                        C += __builtin_popcountll(in[j]);
+                    }
+                }
+            }
+            if (mine == i) my_c = C;
+            int base = i * seg;
+#pragma unroll
+            for (int j = 0; j < NE; ++j) {
+                if (!in[j]) continue;
+                if (__builtin_amdgcn_inverse_ballot_w64(in[j])) {
+                    const int p = __builtin_amdgcn_mbcnt_hi((uint32_t)(in[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in[j], base));
+                    l.candz[p] = z[j];
+                    l.candi[p] = at(j);
+                }
+                base += __builtin_popcountll(in[j]);
             }
         }
-        if (again) choose64<ZD>(a, t, !SCORED, l, out);
-        else if (lane < C && rank < k) out[rank] = cd;
+        if constexpr (HOW == GROUPED) {  // their groups in double, then once more
+            for (uint32_t c = close; c; c &= c - 1) {
+                const int i = __builtin_ctz(c);
+                const Choice64<ZD> choice(a, t0 + i);
+                const unsigned long long kept = groups64<ZD>(a, choice, l.ord);
+                if (lane < 2) l.kept[2 * i + lane] = (uint32_t)(kept >> (32 * lane));
+                wave_sync();
+            }
+        }
+        todo = close;
+        close = 0;
     }
     wave_sync();
-    // the weights, a segment of lanes a token
-    const int i = mine, r = lane & (seg - 1);
-    const bool here = i < n && r < k;
-    const float2 p = l.pick[lane];
-    float zp = p.x;
-    int pick = __float_as_int(p.y);
-    if (a.ids_in) {
-        pick = -1;
-        zp = -INFINITY;
-        if (here && (!a.mask || a.mask[t0 + i])) {
-            const int e = a.ids_in[(t0 + i) * k + r];
-            if (e >= 0 && e < E) {
-                zp = load_z<ZD>(a.z, (t0 + i) * E + e);
-                if (zp > -INFINITY) pick = e;
+    const int r = lane & (seg - 1);
+    if (!a.ids_in) {
+        const bool live = r < my_c;
+        const float zc = live ? l.candz[lane] : -INFINITY;
+        const int id = live ? l.candi[lane] : 0x7FFFFFFF;
+        int rank = 0;
+        if (HOW == PLAIN || !a.bias) {
+            // by logits, then ids
+            for (int x = 0; x < seg; x += 16) {
+                const float oz = x ? __shfl_xor(zc, x, moe::WAVE) : zc;
+                const int oi = x ? __shfl_xor(id, x, moe::WAVE) : id;
+                if (x) rank += oz > zc || (oz == zc && oi < id);
+                rotations([&](auto by) {
+                    constexpr int N = decltype(by)::value;
+                    const float tz = turned<N>(oz);
+                    const int ti = turned<N>(oi);  // by every lane, whatever tz is
+                    rank += (tz > zc) | ((tz == zc) & (ti < id));
+                });
             }
+        } else {
+            double c, rest, share = rcp64((double)my_sum);
+            for (bool exact = sigmoid;; exact = true) {
+                const double p = !live ? 0.0 : sigmoid ? sigmoid64(zc, rest) : soft64(zc, my_m) * share;
+                c = live ? p + (double)a.bias[id] : -INFINITY;
+                rank = 0;
+                for (int x = 0; x < seg; x += 16) {
+                    const double o = x ? __shfl_xor(c, x, moe::WAVE) : c;
+                    if (x) rank += o > c;
+                    rotations([&](auto by) { rank += turned<decltype(by)::value>(o) > c; });
+                }
+                // equal choices share a rank: the logits, then the ids decide
+                int* who = reinterpret_cast<int*>(l.ordz) + mine * seg;
+                if (live) who[rank] = lane;
+                wave_sync();
+                if (__any(live && who[rank] != lane)) {
+                    for (int x = 0; x < seg; ++x) {
+                        const int src = mine * seg + x;
+                        const double o = __shfl(c, src, moe::WAVE);
+                        const float oz = __shfl(zc, src, moe::WAVE);
+                        const int oi = __shfl(id, src, moe::WAVE);
+                        if (live) rank += o == c && (oz > zc || (oz == zc && oi < id));
+                    }
+                }
+                if (exact) break;
+                // the sum of the softmax is an fp32 one: where neighbours are so close that it may have put them the wrong
+                // way round, one in double
+                wave_sync();
+                if (live) l.ord[mine * seg + rank] = c, l.ordz[mine * seg + rank] = zc, l.candz[mine * seg + rank] = (float)p * share_error(E);
+                wave_sync();
+                unsigned long long near = __ballot(r < k && r + 1 < my_c && l.ordz[lane] != l.ordz[lane + 1] &&
+                                                   l.ord[lane] - l.ord[lane + 1] <= (double)(l.candz[lane] + l.candz[(lane + 1) & 63]));
+                if (!near) break;
+                while (near) {
+                    const int i = __builtin_ctzll(near) / seg;
+                    float m;
+                    const double s = softmax64<ZD>(a, t0 + i, m);
+                    if (mine == i) share = s;
+                    near &= ~__ballot(mine == i);
+                }
+                wave_sync();
+            }
+        }
+        if (live && rank < k && !((slow >> mine) & 1)) l.pickz[mine * seg + rank] = zc, l.picki[mine * seg + rank] = id;
+        wave_sync();
+        for (; slow && HOW != PLAIN; slow &= slow - 1) {
+            const int i = __builtin_ctz(slow);
+            choose64<ZD>(a, t0 + i, l, i * seg);
+        }
+    }
+    // the weights
+    const bool here = mine < n && r < k;
+    const int64_t o = (t0 + mine) * k + r;
+    float zp = l.pickz[lane];
+    int pick = l.picki[lane];
+    if (a.ids_in && here && (!a.mask || a.mask[t0 + mine])) {
+        const int e = a.ids_in[o];
+        if (e >= 0 && e < E) {
+            zp = load_z<ZD>(a.z, (t0 + mine) * E + e);
+            if (zp > -INFINITY) pick = e;
         }
     }
     const bool live = pick >= 0;
@@ -497,8 +686,8 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
     if (a.rule.renorm) s = share64(a.rule.score, zp, live, seg);
     else if (live) s = sigmoid ? sigmoid64(zp, rest) : soft64(zp, my_m) * rcp64((double)my_sum);
     if (here) {
-        if (!a.ids_in) a.ids[(t0 + i) * k + r] = pick;
-        a.w[(t0 + i) * k + r] = (float)((double)a.rule.scale * s);
+        if (!a.ids_in) a.ids[o] = pick;
+        a.w[o] = (float)((double)a.rule.scale * s);
     }
 }
 
@@ -592,7 +781,7 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select_bwd(SelBwdArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
-            if constexpr (DENSE) z[j] = zn[j] > -INFINITY ? zn[j] : -INFINITY;
+            if constexpr (DENSE) z[j] = zn[j];
             ad[j] = an[j];
         }
         if (AHEAD && i + 1 < n) {
@@ -614,22 +803,32 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select_bwd(SelBwdArgs a) {
         wave_sync();
         if (live && mine == i) row[e] = 0.0f;
         if constexpr (DENSE) {
-            float m = z[0], s = 0.0f, dot = 0.0f;
-#pragma unroll
-            for (int j = 1; j < NE; ++j) m = fmaxf(m, z[j]);
-            m = moe::wave_all_max(m);
+            float s = 0.0f, dot = 0.0f, ex[NE];  // the softmax as in k_select
 #pragma unroll
             for (int j = 0; j < NE; ++j) {
-                z[j] = z[j] > -INFINITY ? soft32(z[j], m) : 0.0f;
-                s += z[j];
-                dot = fmaf(z[j], d[j], dot);
+                ex[j] = __builtin_amdgcn_exp2f(z[j] * 1.44269504f);
+                s += ex[j];
+                dot = fmaf(ex[j], d[j], dot);
             }
             s = moe::wave_all_sum(s);
+            if (__any(!(s > 0x1p-8f && s < 0x1p16f))) {
+#pragma unroll
+                for (int j = 0; j < NE; ++j) z[j] = z[j] > -INFINITY ? z[j] : -INFINITY;
+                const float m = of_code(wave_max_u32(code_of(lane_max(z))));
+                s = dot = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NE; ++j) {
+                    ex[j] = z[j] > -INFINITY ? soft32(z[j], m) : 0.0f;
+                    s += ex[j];
+                    dot = fmaf(ex[j], d[j], dot);
+                }
+                s = moe::wave_all_sum(s);
+            }
             dot = moe::wave_all_sum(dot);
             const float f = s > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f;
             dot *= f;
 #pragma unroll
-            for (int j = 0; j < NE; ++j) d[j] = z[j] * f * (d[j] - dot);
+            for (int j = 0; j < NE; ++j) d[j] = ex[j] * f * (d[j] - dot);
         }
         if (a.add) {
 #pragma unroll
@@ -667,28 +866,33 @@ __global__ void __launch_bounds__(256) k_bias_balance(const int32_t* __restrict_
     }
 }
 
-// Calls go with the number of experts a lane holds; bf16 rows of an even length are
-// read in pairs.
-template <int ZD, int VEC, typename Go>
-void by_experts(int E, const Go& go) {
+// Calls go with the number of experts a lane holds (64: what is more is taken in
+// double from the start); bf16 rows of an even length are read in pairs.
+template <typename Go>
+void by_count(int ne, const Go& go) {
     using std::integral_constant;
-    const auto with = [&](auto ne) { go(integral_constant<int, ZD>{}, integral_constant<int, VEC>{}, ne); };
-    const int ne = (E + 64 * VEC - 1) / (64 * VEC) * VEC;
-    if (ne <= 2) with(integral_constant<int, 2>{});
-    else if (ne <= 4) with(integral_constant<int, 4>{});
-    else if (ne <= 5 && VEC == 1) with(integral_constant<int, VEC == 1 ? 5 : 6>{});
-    else if (ne <= 6) with(integral_constant<int, 6>{});
-    else if (ne <= 8) with(integral_constant<int, 8>{});
-    else if (ne <= 16) with(integral_constant<int, 16>{});
-    else if (ne <= 32) with(integral_constant<int, 32>{});
-    else with(integral_constant<int, 64>{});
+    if (ne <= 2) go(integral_constant<int, 2>{});
+    else if (ne <= 4) go(integral_constant<int, 4>{});
+    else if (ne <= 5) go(integral_constant<int, 5>{});
+    else if (ne <= 6) go(integral_constant<int, 6>{});
+    else if (ne <= 8) go(integral_constant<int, 8>{});
+    else if (ne <= 16) go(integral_constant<int, 16>{});
+    else if (ne <= 32) go(integral_constant<int, 32>{});
+    else go(integral_constant<int, 64>{});
 }
 
 template <typename Go>
 void by_format(int z_dtype, int E, const Go& go) {
-    if (z_dtype == MOE_X_F32) by_experts<MOE_X_F32, 1>(E, go);
-    else if (E % 2 == 0) by_experts<MOE_X_BF16, 2>(E, go);
-    else by_experts<MOE_X_BF16, 1>(E, go);
+    using std::integral_constant;
+    const integral_constant<int, 1> one;
+    const int ne = (E + 63) / 64;
+    if (z_dtype == MOE_X_F32) by_count(ne, [&](auto c) { go(integral_constant<int, MOE_X_F32>{}, one, c); });
+    else if (E % 2) by_count(ne, [&](auto c) { go(integral_constant<int, MOE_X_BF16>{}, one, c); });
+    else
+        by_count((E + 127) / 128 * 2, [&](auto c) {
+            constexpr int NE = decltype(c)::value == 5 ? 6 : decltype(c)::value;
+            go(integral_constant<int, MOE_X_BF16>{}, integral_constant<int, 2>{}, integral_constant<int, NE>{});
+        });
 }
 
 int check_rule(const char* who, int z_dtype, int T, int E, int k, const moe_select_rule* rule) {
@@ -714,6 +918,8 @@ int check_rule(const char* who, int z_dtype, int T, int E, int k, const moe_sele
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int seg_of(int k) { return k <= 8 ? 8 : k <= 16 ? 16 : 32; }
+// Lanes of a token's candidates: k, some equal ones and a few for the bound's sake.
+int cand_of(int k) { return k <= 10 ? 16 : k <= 22 ? 32 : 64; }
 
 // Tokens a wave: as many as leave 16 waves a CU, and as have their picks side by side.
 int batch_of(int T, int seg) {
@@ -734,17 +940,27 @@ int moe_route_select(const void* z, int z_dtype, const float* bias, const uint8_
     MOE_REQUIRE(moe_aligned16(z) && aligned4(ids) && aligned4(ids_in) && aligned4(w) && aligned4(bias), MOE_E_ALIGN,
                 "moe_route_select: z must start on 16 bytes; ids, ids_in, w and bias on 4");
     if (T == 0) return moe_ok();
-    SelArgs a{z, bias, mask, ids_in, T, E, k, *rule, ids, w, 1, seg_of(k)};
+    SelArgs a{z, bias, mask, ids_in, T, E, k, *rule, ids, w, 1, cand_of(k)};
     a.batch = batch_of(T, a.seg);
-    const int waves = E <= 1024 ? SEL_WAVES : 1;
-    const int per = waves * a.batch;
-    const bool scored = bias || rule->groups > 1;
-    by_format(z_dtype, E, [&](auto zd, auto vec, auto ne) {
-        constexpr int ZD = decltype(zd)::value, VEC = decltype(vec)::value, NE = decltype(ne)::value;
-        const dim3 grid((T + per - 1) / per), block(64 * waves);
-        if (scored) hipLaunchKernelGGL((k_select<ZD, VEC, NE, true>), grid, block, waves * sel_lds(E), stream, a);
-        else hipLaunchKernelGGL((k_select<ZD, VEC, NE, false>), grid, block, waves * sel_lds(E), stream, a);
-    });
+    const int per = SEL_WAVES * a.batch, G = rule->groups;
+    const dim3 grid((T + per - 1) / per), block(64 * SEL_WAVES);
+    using std::integral_constant;
+    const auto go = [&](auto zd, auto vec, auto ne, auto how) {
+        hipLaunchKernelGGL((k_select<decltype(zd)::value, decltype(vec)::value, decltype(ne)::value, decltype(how)::value>), grid,
+                           block, 0, stream, a);
+    };
+    if (G > 1 && !ids_in) {
+        const int per_group = lanes_per_group(G), ne = (E / G + per_group - 1) / per_group;
+        const integral_constant<int, GROUPED> how;
+        const integral_constant<int, 1> one;
+        if (z_dtype == MOE_X_F32) by_count(ne, [&](auto c) { go(integral_constant<int, MOE_X_F32>{}, one, c, how); });
+        else by_count(ne, [&](auto c) { go(integral_constant<int, MOE_X_BF16>{}, one, c, how); });
+    } else {
+        by_format(z_dtype, E, [&](auto zd, auto vec, auto ne) {
+            if (bias && !ids_in) go(zd, vec, ne, integral_constant<int, SCORED>{});
+            else go(zd, vec, ne, integral_constant<int, PLAIN>{});
+        });
+    }
     return moe_check_launch("moe_route_select");
 }
 
