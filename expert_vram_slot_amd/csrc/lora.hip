@@ -251,114 +251,160 @@ __global__ void __launch_bounds__(64 * DOWN_WAVES) k_lora_down(LoraArgs a) {
 // y of a tile of tokens, 32 rows of B a step: lane (m, q) brings columns 8q.. of a
 // row and of a token's h, and holds outputs of token m: of fp32 y rows 4q.. and 16 +
 // 4q.. (a token's 128 bytes together), of bf16 y rows 8q.. (the rows are taken in
-// that order, so that a lane stores 16 bytes).
-template <int YD, int TM, int NT, int RC>
+// that order, so that a lane stores 16 bytes).  h, added up, scaled and cut, lies in
+// LDS for all of the workgroup's waves, as the products want it.  The tile's adapters
+// are found once; of a step the base and up to AT adapters' rows are loaded together.
+template <int YD, int TM, int RC>
 __global__ void __launch_bounds__(256) k_lora_up(LoraArgs a) {
+    constexpr int NT = TM / 16;
+    constexpr int AT = TM == 16 ? (RC == 1 ? 4 : RC == 2 ? 2 : 1) : 1;  // adapters at a time
+    __shared__ __align__(16) v4u hs[NT][RC][3][64];
+    __shared__ int s_tok[TM], s_ad[TM], s_of[TM], s_rank[TM];
     const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
     const int wave = blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
     const int first = wave * a.steps, last = min(first + a.steps, (a.N + 31) / 32);
     int tok, ad;
     member<TM>(a, blockIdx.y, lane, tok, ad);
-#pragma unroll 1
-    for (int grp = 0; grp < TM / 16 / NT; ++grp) {
-        int t[NT], d_of[NT];
-        bf16x8 hp[NT][RC][3];
-#pragma unroll
-        for (int s = 0; s < NT; ++s) {
-            const int src = TM == 16 ? lane : 16 * (grp * NT + s) + m;
-            t[s] = __shfl(tok, src, moe::WAVE);
-            d_of[s] = __shfl(ad, src, moe::WAVE);
-            const int rank = rank_of(a, d_of[s]);
-            const float f = a.scale && d_of[s] >= 0 ? a.scale[d_of[s]] : 1.0f;
-#pragma unroll
-            for (int c = 0; c < RC; ++c) {
-                const int j = 32 * c + 8 * q;
-                float v[8] = {};
-                if (j < rank) {
-                    for (int sp = 0; sp < a.splits; ++sp) {
-                        const v4f* p = reinterpret_cast<const v4f*>(a.h + ((int64_t)sp * a.T + t[s]) * a.r + j);
-                        const v4f lo = p[0], hi = p[1];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] += lo[i], v[4 + i] += hi[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = j + i < rank ? f * v[i] : 0.0f;
-                }
-                cut8(v, hp[s][c]);
+    int n_ad = 0;
+    {
+        unsigned long long rest = __ballot(ad >= 0 && lane < TM);
+        while (rest) {
+            const int d = __builtin_amdgcn_readlane(ad, __builtin_ctzll(rest));
+            rest &= ~__ballot(ad == d);
+            const int rank = rank_of(a, d);
+            if (rank > 0) {
+                if (threadIdx.x == 0) s_of[n_ad] = d, s_rank[n_ad] = rank;
+                ++n_ad;
             }
         }
-        for (int step = first; step < last; ++step) {
-            const int n0 = 32 * step;
-            v4f acc[NT][2] = {};
-            // every adapter of these tokens in turn
-            unsigned long long rest = __ballot(ad >= 0 && (TM == 16 || (lane >> 4) / NT == grp));
-            while (rest) {
-                const int d = __builtin_amdgcn_readlane(ad, __builtin_ctzll(rest));
-                rest &= ~__ballot(ad == d);
-                const int rank = rank_of(a, d);
-                v4f one[NT][2] = {};
+    }
+    if (threadIdx.x < TM) s_tok[lane] = tok, s_ad[lane] = ad;
+    __syncthreads();
+    for (int i = threadIdx.x; i < TM * RC * 4; i += blockDim.x) {
+        const int at = i / (RC * 4), j = i % (RC * 4) * 8, t = s_tok[at], d = s_ad[at], rank = rank_of(a, d);
+        float v[8] = {};
+        if (j < rank) {
+            for (int sp = 0; sp < a.splits; ++sp) {
+                const v4f* p = reinterpret_cast<const v4f*>(a.h + ((int64_t)sp * a.T + t) * a.r + j);
+                const v4f lo = p[0], hi = p[1];
 #pragma unroll
-                for (int c = 0; c < RC; ++c) {
-                    const int j = 32 * c + 8 * q;
-                    if (32 * c >= rank) break;
+                for (int k = 0; k < 4; ++k) v[k] += lo[k], v[4 + k] += hi[k];
+            }
+            const float f = a.scale ? a.scale[d] : 1.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = j + k < rank ? f * v[k] : 0.0f;
+        }
+        bf16x8 w[3];
+        cut8(v, w);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) hs[at >> 4][j >> 5][p][(at & 15) + 16 * (j >> 3 & 3)] = __builtin_bit_cast(v4u, w[p]);
+    }
+    __syncthreads();
+    int t[NT], mine[NT];
+#pragma unroll
+    for (int s = 0; s < NT; ++s) t[s] = s_tok[16 * s + m], mine[s] = s_ad[16 * s + m];
+    using Piece = std::conditional_t<YD == MOE_X_F32, v4f, v4u>;  // 16 bytes of base
+    constexpr int PIECES = YD == MOE_X_F32 ? 2 : 1;
+    const auto place = [&](int step, int h) { return 32 * step + (YD == MOE_X_F32 ? 16 * h + 4 * q : 8 * q); };
+    constexpr int WIDE = YD == MOE_X_F32 ? 4 : 8;  // outputs of a piece
+    for (int step = first; step < last; ++step) {
+        if constexpr (NT * RC > 4) asm volatile("" ::: "memory");  // h is read from LDS where it is used: it does not fit registers
+        const int n0 = 32 * step;
+        Piece base[NT][PIECES] = {};
+        if (a.base) {
+#pragma unroll
+            for (int s = 0; s < NT; ++s)
+#pragma unroll
+                for (int h = 0; h < PIECES; ++h) {
+                    const int n = place(step, h);
+                    if (t[s] >= 0 && n + WIDE <= a.N) {
+                        if constexpr (YD == MOE_X_F32)
+                            base[s][h] = *reinterpret_cast<const v4f_loose*>(reinterpret_cast<const float*>(a.base) + (int64_t)t[s] * a.ldb + n);
+                        else
+                            base[s][h] = *reinterpret_cast<const v4u_loose*>(reinterpret_cast<const uint16_t*>(a.base) + (int64_t)t[s] * a.ldb + n);
+                    }
+                }
+        }
+        v4f acc[NT][2] = {};
+        for (int i0 = 0; i0 < n_ad; i0 += AT) {
+            v4u w[AT][RC][2];
+            int d[AT];
+#pragma unroll
+            for (int i = 0; i < AT; ++i) {
+                const int at = min(i0 + i, n_ad - 1);
+                d[i] = __builtin_amdgcn_readfirstlane(s_of[at]);
+                const int rank = __builtin_amdgcn_readfirstlane(s_rank[at]);
+#pragma unroll
+                for (int c = 0; c < RC; ++c)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        const int j = 32 * c + 8 * q;
                         const int row = YD == MOE_X_F32 ? n0 + 16 * h + m : n0 + 8 * (m >> 2) + 4 * h + (m & 3);
-                        v4u w = {};
-                        if (j < rank) {
-                            w = *reinterpret_cast<const v4u*>(a.b + ((int64_t)d * a.N + min(row, a.N - 1)) * a.r + j);
-                            if (j + 8 > rank) {  // columns past the rank may hold anything
+                        w[i][c][h] = v4u{};
+                        if (j < rank)
+                            w[i][c][h] = *reinterpret_cast<const v4u*>(a.b + ((int64_t)d[i] * a.N + min(row, a.N - 1)) * a.r + j);
+                    }
+            }
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    w[i] &= (j + 2 * i < rank ? 0xFFFFu : 0u) | (j + 2 * i + 1 < rank ? 0xFFFF0000u : 0u);
-                            }
+            for (int i = 0; i < AT; ++i) {
+                if (i0 + i >= n_ad) break;
+                const int rank = __builtin_amdgcn_readfirstlane(s_rank[i0 + i]);
+                if (rank & 7) {  // columns past the rank may hold anything
+#pragma unroll
+                    for (int c = 0; c < RC; ++c) {
+                        const int j = 32 * c + 8 * q;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t keep = (j + 2 * k < rank ? 0xFFFFu : 0u) | (j + 2 * k + 1 < rank ? 0xFFFF0000u : 0u);
+                            w[i][c][0][k] &= keep, w[i][c][1][k] &= keep;
                         }
-#pragma unroll
-                        for (int s = 0; s < NT; ++s)
-#pragma unroll
-                            for (int p = 0; p < 3; ++p)
-                                one[s][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), hp[s][c][p],
-                                                                                    one[s][h], 0, 0, 0);
                     }
                 }
 #pragma unroll
-                for (int s = 0; s < NT; ++s)
-                    if (d_of[s] == d) acc[s][0] = one[s][0], acc[s][1] = one[s][1];
-            }
+                for (int s = 0; s < NT; ++s) {
+                    v4f one[2] = {};
 #pragma unroll
-            for (int s = 0; s < NT; ++s) {
-                if (t[s] < 0) continue;
-                if constexpr (YD == MOE_X_F32) {
-                    const float* bp = reinterpret_cast<const float*>(a.base) + (int64_t)t[s] * a.ldb;
-                    float* yp = reinterpret_cast<float*>(a.y) + (int64_t)t[s] * a.ldy;
+                    for (int c = 0; c < RC; ++c)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int n = n0 + 16 * h + 4 * q;
-                        if (n + 4 <= a.N) {
-                            v4f v = acc[s][h];
-                            if (a.base) v += *reinterpret_cast<const v4f_loose*>(bp + n);
-                            *reinterpret_cast<v4f_loose*>(yp + n) = v;
-                        } else {
-                            for (int i = 0; n + i < a.N; ++i) yp[n + i] = (a.base ? bp[n + i] : 0.0f) + acc[s][h][i];
+                        for (int p = 0; p < 3; ++p) {
+                            const bf16x8 hv = __builtin_bit_cast(bf16x8, hs[s][c][p][lane]);
+                            one[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i][c][0]), hv, one[0], 0, 0, 0);
+                            one[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i][c][1]), hv, one[1], 0, 0, 0);
                         }
-                    }
-                } else {
-                    const uint16_t* bp = reinterpret_cast<const uint16_t*>(a.base) + (int64_t)t[s] * a.ldb;
-                    __bf16* yp = reinterpret_cast<__bf16*>(a.y) + (int64_t)t[s] * a.ldy;
-                    const int n = n0 + 8 * q;
-                    if (n + 8 <= a.N) {
-                        v4u w = {};
-                        if (a.base) w = *reinterpret_cast<const v4u_loose*>(bp + n);
-                        bf16x8 o;
+                    if (mine[s] == d[i]) acc[s][0] = one[0], acc[s][1] = one[1];
+                }
+            }
+        }
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            o[i] = (__bf16)((i & 1 ? moe::bf16_hi(w[i >> 1]) : moe::bf16_lo(w[i >> 1])) + acc[s][i >> 2][i & 3]);
-                        *reinterpret_cast<v4u_loose*>(yp + n) = __builtin_bit_cast(v4u, o);
+        for (int s = 0; s < NT; ++s) {
+            if (t[s] < 0) continue;
+            if constexpr (YD == MOE_X_F32) {
+                const float* bp = reinterpret_cast<const float*>(a.base) + (int64_t)t[s] * a.ldb;
+                float* yp = reinterpret_cast<float*>(a.y) + (int64_t)t[s] * a.ldy;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int n = place(step, h);
+                    if (n + 4 <= a.N) {
+                        *reinterpret_cast<v4f_loose*>(yp + n) = acc[s][h] + base[s][h];
                     } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (n + i < a.N) yp[n + i] = (__bf16)((a.base ? moe::bf16_to_f32(bp[n + i]) : 0.0f) + acc[s][i >> 2][i & 3]);
+                        for (int i = 0; n + i < a.N; ++i) yp[n + i] = (a.base ? bp[n + i] : 0.0f) + acc[s][h][i];
                     }
+                }
+            } else {
+                const uint16_t* bp = reinterpret_cast<const uint16_t*>(a.base) + (int64_t)t[s] * a.ldb;
+                __bf16* yp = reinterpret_cast<__bf16*>(a.y) + (int64_t)t[s] * a.ldy;
+                const int n = place(step, 0);
+                if (n + 8 <= a.N) {
+                    const v4u w = base[s][0];
+                    bf16x8 o;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o[i] = (__bf16)((i & 1 ? moe::bf16_hi(w[i >> 1]) : moe::bf16_lo(w[i >> 1])) + acc[s][i >> 2][i & 3]);
+                    *reinterpret_cast<v4u_loose*>(yp + n) = __builtin_bit_cast(v4u, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (n + i < a.N) yp[n + i] = (__bf16)((a.base ? moe::bf16_to_f32(bp[n + i]) : 0.0f) + acc[s][i >> 2][i & 3]);
                 }
             }
         }
@@ -393,11 +439,10 @@ void launch_down(const LoraArgs& g, int tiles, int spread, hipStream_t stream) {
 
 template <int YD, int TM>
 void launch_up(const LoraArgs& g, const dim3& grid, const dim3& block, hipStream_t stream) {
-    constexpr int S = TM / 16;
-    if (g.r <= 32) hipLaunchKernelGGL((k_lora_up<YD, TM, S, 1>), grid, block, 0, stream, g);
-    else if (g.r <= 64) hipLaunchKernelGGL((k_lora_up<YD, TM, S, 2>), grid, block, 0, stream, g);
-    else if (g.r <= 128) hipLaunchKernelGGL((k_lora_up<YD, TM, (S > 2 ? 2 : S), 4>), grid, block, 0, stream, g);
-    else hipLaunchKernelGGL((k_lora_up<YD, TM, 1, 8>), grid, block, 0, stream, g);
+    if (g.r <= 32) hipLaunchKernelGGL((k_lora_up<YD, TM, 1>), grid, block, 0, stream, g);
+    else if (g.r <= 64) hipLaunchKernelGGL((k_lora_up<YD, TM, 2>), grid, block, 0, stream, g);
+    else if (g.r <= 128) hipLaunchKernelGGL((k_lora_up<YD, TM, 4>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_lora_up<YD, TM, 8>), grid, block, 0, stream, g);
 }
 
 }  // namespace
