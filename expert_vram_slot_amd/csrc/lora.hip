@@ -252,17 +252,26 @@ __global__ void __launch_bounds__(64 * DOWN_WAVES) k_lora_down(LoraArgs a) {
 // row and of a token's h, and holds outputs of token m: of fp32 y rows 4q.. and 16 +
 // 4q.. (a token's 128 bytes together), of bf16 y rows 8q.. (the rows are taken in
 // that order, so that a lane stores 16 bytes).  h, added up, scaled and cut, lies in
-// LDS for all of the workgroup's waves, as the products want it.  The tile's adapters
-// are found once; of a step the base and up to AT adapters' rows are loaded together.
-template <int YD, int TM, int RC>
+// LDS for all of the workgroup's waves, as the products want it; the tile's adapters
+// are found once.  The next step's base and rows (those of the first AT adapters) are
+// on their way before this one's y is stored: loads and stores count as one, and a
+// wait for loads behind stores would wait for those too.  For the same reason no lane
+// is without a token: the places behind the last are those of the wave's first.
+template <int YD, int TM, int RC, int AT, bool BASE>
 __global__ void __launch_bounds__(256) k_lora_up(LoraArgs a) {
-    constexpr int NT = TM / 16;
-    constexpr int AT = TM == 16 ? (RC == 1 ? 4 : RC == 2 ? 2 : 1) : 1;  // adapters at a time
-    __shared__ __align__(16) v4u hs[NT][RC][3][64];
+    constexpr int HALVES = TM == 64 ? 2 : 1;  // waves that share the rows, each with its part of the tokens
+    constexpr int NT = TM / 16 / HALVES;
+    constexpr int PIECES = YD == MOE_X_F32 ? 2 : 1;  // of 16 bytes, a token and step
+    constexpr int WIDE = YD == MOE_X_F32 ? 4 : 8;    // outputs of a piece
+    using Out = std::conditional_t<YD == MOE_X_F32, float, __bf16>;
+    using Piece = std::conditional_t<YD == MOE_X_F32, v4f, v4u>;
+    using Loose = std::conditional_t<YD == MOE_X_F32, v4f_loose, v4u_loose>;
+    __shared__ __align__(16) v4u hs[TM / 16][RC][3][64];
     __shared__ int s_tok[TM], s_ad[TM], s_of[TM], s_rank[TM];
     const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
-    const int wave = blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
-    const int first = wave * a.steps, last = min(first + a.steps, (a.N + 31) / 32);
+    const int wid = threadIdx.x >> 6, sub = NT * (wid % HALVES);
+    const int wave = blockIdx.x * ((blockDim.x >> 6) / HALVES) + wid / HALVES;
+    const int first = wave * a.steps, last = min(first + a.steps, (a.N + 31) / 32), whole = min(last, a.N / 32);
     int tok, ad;
     member<TM>(a, blockIdx.y, lane, tok, ad);
     int n_ad = 0;
@@ -300,114 +309,132 @@ __global__ void __launch_bounds__(256) k_lora_up(LoraArgs a) {
         for (int p = 0; p < 3; ++p) hs[at >> 4][j >> 5][p][(at & 15) + 16 * (j >> 3 & 3)] = __builtin_bit_cast(v4u, w[p]);
     }
     __syncthreads();
-    int t[NT], mine[NT];
+    if (first >= last || s_tok[16 * sub] < 0) return;
+    // where this lane's outputs of a step start, less 32 for each step
+    const auto place = [&](int h) { return YD == MOE_X_F32 ? 16 * h + 4 * q : 8 * q; };
+    int mine[NT], from[NT];
+    const Out* bp[NT];
+    Out* yp[NT];
 #pragma unroll
-    for (int s = 0; s < NT; ++s) t[s] = s_tok[16 * s + m], mine[s] = s_ad[16 * s + m];
-    using Piece = std::conditional_t<YD == MOE_X_F32, v4f, v4u>;  // 16 bytes of base
-    constexpr int PIECES = YD == MOE_X_F32 ? 2 : 1;
-    const auto place = [&](int step, int h) { return 32 * step + (YD == MOE_X_F32 ? 16 * h + 4 * q : 8 * q); };
-    constexpr int WIDE = YD == MOE_X_F32 ? 4 : 8;  // outputs of a piece
-    for (int step = first; step < last; ++step) {
-        if constexpr (NT * RC > 4) asm volatile("" ::: "memory");  // h is read from LDS where it is used: it does not fit registers
-        const int n0 = 32 * step;
-        Piece base[NT][PIECES] = {};
-        if (a.base) {
+    for (int s = 0; s < NT; ++s) {
+        from[s] = s_tok[16 * (sub + s) + m] < 0 ? 16 * sub : 16 * (sub + s) + m;
+        const int64_t t = s_tok[from[s]];
+        mine[s] = s_ad[from[s]];
+        bp[s] = reinterpret_cast<const Out*>(a.base) + t * a.ldb;
+        yp[s] = reinterpret_cast<Out*>(a.y) + t * a.ldy;
+    }
+    const auto h_of = [&](int s, int c, int p) { return __builtin_bit_cast(bf16x8, hs[from[s] >> 4][c][p][(from[s] & 15) + 16 * q]); };
+    struct Rows {
+        v4u w[AT][RC][2];
+    };
+    const auto fetch_rows = [&](Rows& r, int i0, int step) {
 #pragma unroll
-            for (int s = 0; s < NT; ++s)
+        for (int i = 0; i < AT; ++i) {
+            const int64_t d = __builtin_amdgcn_readfirstlane(s_of[min(i0 + i, n_ad - 1)]);
 #pragma unroll
-                for (int h = 0; h < PIECES; ++h) {
-                    const int n = place(step, h);
-                    if (t[s] >= 0 && n + WIDE <= a.N) {
-                        if constexpr (YD == MOE_X_F32)
-                            base[s][h] = *reinterpret_cast<const v4f_loose*>(reinterpret_cast<const float*>(a.base) + (int64_t)t[s] * a.ldb + n);
-                        else
-                            base[s][h] = *reinterpret_cast<const v4u_loose*>(reinterpret_cast<const uint16_t*>(a.base) + (int64_t)t[s] * a.ldb + n);
-                    }
+            for (int c = 0; c < RC; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = 32 * step + (YD == MOE_X_F32 ? 16 * h + m : 8 * (m >> 2) + 4 * h + (m & 3));
+                    r.w[i][c][h] = *reinterpret_cast<const v4u*>(a.b + (d * a.N + min(row, a.N - 1)) * a.r + min(32 * c + 8 * q, a.r - 8));
                 }
         }
-        v4f acc[NT][2] = {};
-        for (int i0 = 0; i0 < n_ad; i0 += AT) {
-            v4u w[AT][RC][2];
-            int d[AT];
+    };
+    const auto multiply = [&](Rows& r, int i0, v4f (&acc)[NT][2]) {
 #pragma unroll
-            for (int i = 0; i < AT; ++i) {
-                const int at = min(i0 + i, n_ad - 1);
-                d[i] = __builtin_amdgcn_readfirstlane(s_of[at]);
-                const int rank = __builtin_amdgcn_readfirstlane(s_rank[at]);
+        for (int i = 0; i < AT; ++i) {
+            if (i0 + i >= n_ad) break;
+            const int d = __builtin_amdgcn_readfirstlane(s_of[i0 + i]), rank = __builtin_amdgcn_readfirstlane(s_rank[i0 + i]);
+#pragma unroll
+            for (int c = 0; c < RC; ++c) {
+                if (32 * c + 32 <= rank) continue;
+                const int j = 32 * c + 8 * q;  // columns past the rank may hold anything
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t keep = (j + 2 * k < rank ? 0xFFFFu : 0u) | (j + 2 * k + 1 < rank ? 0xFFFF0000u : 0u);
+                    r.w[i][c][0][k] &= keep, r.w[i][c][1][k] &= keep;
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < NT; ++s) {
+                v4f one[2] = {};
 #pragma unroll
                 for (int c = 0; c < RC; ++c)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int j = 32 * c + 8 * q;
-                        const int row = YD == MOE_X_F32 ? n0 + 16 * h + m : n0 + 8 * (m >> 2) + 4 * h + (m & 3);
-                        w[i][c][h] = v4u{};
-                        if (j < rank)
-                            w[i][c][h] = *reinterpret_cast<const v4u*>(a.b + ((int64_t)d[i] * a.N + min(row, a.N - 1)) * a.r + j);
+                    for (int p = 0; p < 3; ++p) {
+                        const bf16x8 hv = h_of(s, c, p);
+                        one[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r.w[i][c][0]), hv, one[0], 0, 0, 0);
+                        one[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r.w[i][c][1]), hv, one[1], 0, 0, 0);
                     }
-            }
-#pragma unroll
-            for (int i = 0; i < AT; ++i) {
-                if (i0 + i >= n_ad) break;
-                const int rank = __builtin_amdgcn_readfirstlane(s_rank[i0 + i]);
-                if (rank & 7) {  // columns past the rank may hold anything
-#pragma unroll
-                    for (int c = 0; c < RC; ++c) {
-                        const int j = 32 * c + 8 * q;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t keep = (j + 2 * k < rank ? 0xFFFFu : 0u) | (j + 2 * k + 1 < rank ? 0xFFFF0000u : 0u);
-                            w[i][c][0][k] &= keep, w[i][c][1][k] &= keep;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int s = 0; s < NT; ++s) {
-                    v4f one[2] = {};
-#pragma unroll
-                    for (int c = 0; c < RC; ++c)
-#pragma unroll
-                        for (int p = 0; p < 3; ++p) {
-                            const bf16x8 hv = __builtin_bit_cast(bf16x8, hs[s][c][p][lane]);
-                            one[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i][c][0]), hv, one[0], 0, 0, 0);
-                            one[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i][c][1]), hv, one[1], 0, 0, 0);
-                        }
-                    if (mine[s] == d[i]) acc[s][0] = one[0], acc[s][1] = one[1];
-                }
+                if (mine[s] == d) acc[s][0] = one[0], acc[s][1] = one[1];
             }
         }
+    };
+    struct Base {
+        Piece p[NT][PIECES];
+    };
+    const auto fetch_base = [&](Base& b, int step) {
+#pragma unroll
+        for (int s = 0; s < NT; ++s)
+#pragma unroll
+            for (int h = 0; h < PIECES; ++h) {
+                b.p[s][h] = Piece{};
+                if constexpr (BASE) b.p[s][h] = *reinterpret_cast<const Loose*>(bp[s] + 32 * step + place(h));
+            }
+    };
+    Rows rows;
+    Base base;
+    if (n_ad) fetch_rows(rows, 0, first);
+    if (first < whole) fetch_base(base, first);
+    for (int step = first; step < whole; ++step) {
+        if constexpr (NT * RC > 4) asm volatile("" ::: "memory");  // h is read from LDS where it is used: it does not fit registers
+        v4f acc[NT][2] = {};
+        if (n_ad) multiply(rows, 0, acc);
+        for (int i0 = AT; i0 < n_ad; i0 += AT) {
+            Rows more;
+            fetch_rows(more, i0, step);
+            multiply(more, i0, acc);
+        }
+        const Base b = base;
+        if (n_ad) fetch_rows(rows, 0, min(step + 1, last - 1));
+        fetch_base(base, min(step + 1, whole - 1));
 #pragma unroll
         for (int s = 0; s < NT; ++s) {
-            if (t[s] < 0) continue;
             if constexpr (YD == MOE_X_F32) {
-                const float* bp = reinterpret_cast<const float*>(a.base) + (int64_t)t[s] * a.ldb;
-                float* yp = reinterpret_cast<float*>(a.y) + (int64_t)t[s] * a.ldy;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int n = place(step, h);
-                    if (n + 4 <= a.N) {
-                        *reinterpret_cast<v4f_loose*>(yp + n) = acc[s][h] + base[s][h];
-                    } else {
-                        for (int i = 0; n + i < a.N; ++i) yp[n + i] = (a.base ? bp[n + i] : 0.0f) + acc[s][h][i];
-                    }
-                }
+                for (int h = 0; h < 2; ++h) *reinterpret_cast<Loose*>(yp[s] + 32 * step + place(h)) = acc[s][h] + b.p[s][h];
             } else {
-                const uint16_t* bp = reinterpret_cast<const uint16_t*>(a.base) + (int64_t)t[s] * a.ldb;
-                __bf16* yp = reinterpret_cast<__bf16*>(a.y) + (int64_t)t[s] * a.ldy;
-                const int n = place(step, 0);
-                if (n + 8 <= a.N) {
-                    const v4u w = base[s][0];
-                    bf16x8 o;
+                bf16x8 o;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        o[i] = (__bf16)((i & 1 ? moe::bf16_hi(w[i >> 1]) : moe::bf16_lo(w[i >> 1])) + acc[s][i >> 2][i & 3]);
-                    *reinterpret_cast<v4u_loose*>(yp + n) = __builtin_bit_cast(v4u, o);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (n + i < a.N) yp[n + i] = (__bf16)((a.base ? moe::bf16_to_f32(bp[n + i]) : 0.0f) + acc[s][i >> 2][i & 3]);
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t w = b.p[s][0][i >> 1];
+                    o[i] = (__bf16)((i & 1 ? moe::bf16_hi(w) : moe::bf16_lo(w)) + acc[s][i >> 2][i & 3]);
                 }
+                *reinterpret_cast<Loose*>(yp[s] + 32 * step + place(0)) = __builtin_bit_cast(v4u, o);
             }
         }
+    }
+    if (whole >= last) return;
+    // the last rows, fewer than 32
+    v4f acc[NT][2] = {};
+    if (n_ad) multiply(rows, 0, acc);
+    for (int i0 = AT; i0 < n_ad; i0 += AT) {
+        Rows more;
+        fetch_rows(more, i0, whole);
+        multiply(more, i0, acc);
+    }
+#pragma unroll
+    for (int s = 0; s < NT; ++s) {
+        if (from[s] != 16 * (sub + s) + m) continue;
+#pragma unroll
+        for (int h = 0; h < PIECES; ++h)
+#pragma unroll
+            for (int i = 0; i < WIDE; ++i) {
+                const int n = 32 * whole + place(h) + i;
+                if (n >= a.N) continue;
+                const float v = acc[s][YD == MOE_X_F32 ? h : i >> 2][i & 3];
+                yp[s][n] = (Out)(BASE ? (float)bp[s][n] + v : v);
+            }
     }
 }
 
@@ -437,12 +464,23 @@ void launch_down(const LoraArgs& g, int tiles, int spread, hipStream_t stream) {
     else hipLaunchKernelGGL((k_lora_down<XD, NT, 4>), grid, block, 0, stream, g);
 }
 
+template <int YD, int TM, int RC>
+void launch_up(const LoraArgs& g, const dim3& grid, const dim3& block, hipStream_t stream) {
+    // four adapters at a time where a tile has several: where tokens that share one are few
+    constexpr int AT = TM == 16 && RC <= 2 ? 4 : 1;
+    const bool several = AT > 1 && g.n > 1 && (int64_t)g.T < 16 * (int64_t)g.n;
+    if (several && g.base) hipLaunchKernelGGL((k_lora_up<YD, TM, RC, AT, true>), grid, block, 0, stream, g);
+    else if (several) hipLaunchKernelGGL((k_lora_up<YD, TM, RC, AT, false>), grid, block, 0, stream, g);
+    else if (g.base) hipLaunchKernelGGL((k_lora_up<YD, TM, RC, 1, true>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_lora_up<YD, TM, RC, 1, false>), grid, block, 0, stream, g);
+}
+
 template <int YD, int TM>
 void launch_up(const LoraArgs& g, const dim3& grid, const dim3& block, hipStream_t stream) {
-    if (g.r <= 32) hipLaunchKernelGGL((k_lora_up<YD, TM, 1>), grid, block, 0, stream, g);
-    else if (g.r <= 64) hipLaunchKernelGGL((k_lora_up<YD, TM, 2>), grid, block, 0, stream, g);
-    else if (g.r <= 128) hipLaunchKernelGGL((k_lora_up<YD, TM, 4>), grid, block, 0, stream, g);
-    else hipLaunchKernelGGL((k_lora_up<YD, TM, 8>), grid, block, 0, stream, g);
+    if (g.r <= 32) launch_up<YD, TM, 1>(g, grid, block, stream);
+    else if (g.r <= 64) launch_up<YD, TM, 2>(g, grid, block, stream);
+    else if (g.r <= 128) launch_up<YD, TM, 4>(g, grid, block, stream);
+    else launch_up<YD, TM, 8>(g, grid, block, stream);
 }
 
 }  // namespace
@@ -498,8 +536,8 @@ int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const v
     const int steps = (N + 31) / 32;
     while (g.steps < 8 && (int64_t)tiles * steps / (2 * g.steps) >= 256 * 16) g.steps *= 2;
     const int need = (steps + g.steps - 1) / g.steps;  // waves a tile
-    const int per = (int64_t)need * tiles <= 1024 ? 1 : 4;
-    const dim3 grid((need + per - 1) / per, tiles), block(64 * per);
+    const int per = tm == 64 ? 2 : (int64_t)need * tiles <= 1024 ? 1 : 4;  // waves a workgroup (of 64 tokens: pairs)
+    const dim3 grid((need + per - 1) / per, tiles), block(tm == 64 ? 256 : 64 * per);
     if (y_dtype == MOE_X_F32) {
         if (tm == 16) launch_up<MOE_X_F32, 16>(g, grid, block, stream);
         else launch_up<MOE_X_F32, 64>(g, grid, block, stream);
