@@ -22,16 +22,19 @@
 namespace {
 
 using v4u = uint32_t __attribute__((ext_vector_type(4)));
+using v2u = uint32_t __attribute__((ext_vector_type(2)));
 using v4f = float __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef v4f v4f_loose __attribute__((aligned(4)));
-typedef v4u v4u_loose __attribute__((aligned(2)));
+typedef v2u v2u_loose __attribute__((aligned(2)));
 
 constexpr int WINDOW = 1024;     // tokens sorted together
 constexpr int WAVE_TOKENS = 64;  // up to so many are sorted in a wave
 constexpr int MANY = 1024;       // tokens from which tiles are of 64
 constexpr int DOWN_WAVES = 4;    // of a workgroup of the first pass
-constexpr int MAX_SPLITS = 8;
+constexpr int MAX_SPLITS = 4;
+constexpr int STEP = 64;         // rows of B of a step of the second pass
 constexpr int RANKS = 64;        // rows of A that a workgroup of the first pass takes
 
 struct LoraArgs {
@@ -50,7 +53,8 @@ struct LoraArgs {
     float* h;        // [splits][T][r]
     int32_t* order;  // [T], or NULL: up to WAVE_TOKENS tokens
     int splits;
-    int steps;       // of 32 rows of B that a wave of the second pass takes
+    int parts;       // workgroups a tile in the second pass
+    int steps;       // of STEP rows of B that a wave of the second pass takes
 };
 
 __device__ __forceinline__ int adapter_of(const LoraArgs& a, int t) {
@@ -75,11 +79,6 @@ __device__ __forceinline__ void member(const LoraArgs& a, int tile, int lane, in
     }
     tok = lane < a.T ? lane : -1;
     ad = adapter_of(a, tok);
-    if (a.T <= 16) {
-        tok = __shfl(tok, lane & 15, moe::WAVE);
-        ad = __shfl(ad, lane & 15, moe::WAVE);
-        return;
-    }
     const uint32_t key = tok < 0 ? ~0u : ((uint32_t)(ad + 1) << 6) | (uint32_t)lane;
     int rank = 0;
     for (int j = 0; j < a.T; ++j) rank += (uint32_t)__builtin_amdgcn_readlane((int)key, j) < key;
@@ -248,193 +247,212 @@ __global__ void __launch_bounds__(64 * DOWN_WAVES) k_lora_down(LoraArgs a) {
     }
 }
 
-// y of a tile of tokens, 32 rows of B a step: lane (m, q) brings columns 8q.. of a
-// row and of a token's h, and holds outputs of token m: of fp32 y rows 4q.. and 16 +
-// 4q.. (a token's 128 bytes together), of bf16 y rows 8q.. (the rows are taken in
-// that order, so that a lane stores 16 bytes).  h, added up, scaled and cut, lies in
-// LDS for all of the workgroup's waves, as the products want it; the tile's adapters
-// are found once.  The next step's base and rows (those of the first AT adapters) are
-// on their way before this one's y is stored: loads and stores count as one, and a
-// wait for loads behind stores would wait for those too.  For the same reason no lane
-// is without a token: the places behind the last are those of the wave's first.
-template <int YD, int TM, int RC, int AT, bool BASE>
-__global__ void __launch_bounds__(256) k_lora_up(LoraArgs a) {
-    constexpr int HALVES = TM == 64 ? 2 : 1;  // waves that share the rows, each with its part of the tokens
-    constexpr int NT = TM / 16 / HALVES;
-    constexpr int PIECES = YD == MOE_X_F32 ? 2 : 1;  // of 16 bytes, a token and step
-    constexpr int WIDE = YD == MOE_X_F32 ? 4 : 8;    // outputs of a piece
+// The second pass takes a tile of tokens by 64 rows of B a step, in four products:
+// lane (m, q) brings columns 8q.. of rows 4m.., a row a product, and of token m's h,
+// and holds outputs 4m.. of tokens 4q.., so that a load of the base or a store takes
+// 256 bytes of fp32 or 128 of bf16 in a row.
+template <int YD>
+struct Outputs {
     using Out = std::conditional_t<YD == MOE_X_F32, float, __bf16>;
-    using Piece = std::conditional_t<YD == MOE_X_F32, v4f, v4u>;
-    using Loose = std::conditional_t<YD == MOE_X_F32, v4f_loose, v4u_loose>;
-    __shared__ __align__(16) v4u hs[TM / 16][RC][3][64];
-    __shared__ int s_tok[TM], s_ad[TM], s_of[TM], s_rank[TM];
-    const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
-    const int wid = threadIdx.x >> 6, sub = NT * (wid % HALVES);
-    const int wave = blockIdx.x * ((blockDim.x >> 6) / HALVES) + wid / HALVES;
-    const int first = wave * a.steps, last = min(first + a.steps, (a.N + 31) / 32), whole = min(last, a.N / 32);
-    int tok, ad;
-    member<TM>(a, blockIdx.y, lane, tok, ad);
-    int n_ad = 0;
-    {
-        unsigned long long rest = __ballot(ad >= 0 && lane < TM);
-        while (rest) {
-            const int d = __builtin_amdgcn_readlane(ad, __builtin_ctzll(rest));
-            rest &= ~__ballot(ad == d);
-            const int rank = rank_of(a, d);
-            if (rank > 0) {
-                if (threadIdx.x == 0) s_of[n_ad] = d, s_rank[n_ad] = rank;
-                ++n_ad;
+    using Piece = std::conditional_t<YD == MOE_X_F32, v4f, v2u>;  // four outputs
+    using Loose = std::conditional_t<YD == MOE_X_F32, v4f_loose, v2u_loose>;
+
+    static __device__ __forceinline__ Piece get(const void* base, int64_t at) {
+        return *reinterpret_cast<const Loose*>(reinterpret_cast<const Out*>(base) + at);
+    }
+    static __device__ __forceinline__ void put(void* y, int64_t at, const Piece& b, const v4f& v) {
+        Loose* to = reinterpret_cast<Loose*>(reinterpret_cast<Out*>(y) + at);
+        if constexpr (YD == MOE_X_F32) {
+            *to = v + b;
+        } else {
+            const bf16x4 o = {(__bf16)(moe::bf16_lo(b[0]) + v[0]), (__bf16)(moe::bf16_hi(b[0]) + v[1]),
+                              (__bf16)(moe::bf16_lo(b[1]) + v[2]), (__bf16)(moe::bf16_hi(b[1]) + v[3])};
+            *to = __builtin_bit_cast(v2u, o);
+        }
+    }
+    static __device__ __forceinline__ void put_one(void* y, int64_t at, const void* base, int64_t at_base, float v) {
+        reinterpret_cast<Out*>(y)[at] = (Out)(base ? (float)reinterpret_cast<const Out*>(base)[at_base] + v : v);
+    }
+};
+
+// Rows 4m + h of step `step` of adapter d, columns 32c + 8q..
+template <int RC>
+struct Rows {
+    v4u w[RC][4];
+    __device__ __forceinline__ void fetch(const LoraArgs& a, int d, int step) {
+        const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
+#pragma unroll
+        for (int c = 0; c < RC; ++c)
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                w[c][h] = *reinterpret_cast<const v4u*>(a.b + ((int64_t)d * a.N + min(STEP * step + 4 * m + h, a.N - 1)) * a.r +
+                                                        min(32 * c + 8 * q, a.r - 8));
+    }
+    // columns past the rank may hold anything
+    __device__ __forceinline__ void cut(int rank) {
+        const int q = (threadIdx.x & 63) >> 4;
+#pragma unroll
+        for (int c = 0; c < RC; ++c) {
+            if (32 * c + 32 <= rank) continue;
+            const int j = 32 * c + 8 * q;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t keep = (j + 2 * k < rank ? 0xFFFFu : 0u) | (j + 2 * k + 1 < rank ? 0xFFFF0000u : 0u);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) w[c][h][k] &= keep;
             }
         }
     }
-    if (threadIdx.x < TM) s_tok[lane] = tok, s_ad[lane] = ad;
-    __syncthreads();
-    for (int i = threadIdx.x; i < TM * RC * 4; i += blockDim.x) {
-        const int at = i / (RC * 4), j = i % (RC * 4) * 8, t = s_tok[at], d = s_ad[at], rank = rank_of(a, d);
-        float v[8] = {};
-        if (j < rank) {
-            for (int sp = 0; sp < a.splits; ++sp) {
-                const v4f* p = reinterpret_cast<const v4f*>(a.h + ((int64_t)sp * a.T + t) * a.r + j);
-                const v4f lo = p[0], hi = p[1];
+    // sum += rows times h, as it lies in LDS
+    __device__ __forceinline__ void multiply(const v4u (&hs)[RC][3][64], int at, v4f (&sum)[4]) const {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] += lo[k], v[4 + k] += hi[k];
+        for (int c = 0; c < RC; ++c)
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                const bf16x8 hv = __builtin_bit_cast(bf16x8, hs[c][p][at]);
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    sum[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv, __builtin_bit_cast(bf16x8, w[c][h]), sum[h], 0, 0, 0);
             }
-            const float f = a.scale ? a.scale[d] : 1.0f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = j + k < rank ? f * v[k] : 0.0f;
-        }
-        bf16x8 w[3];
-        cut8(v, w);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) hs[at >> 4][j >> 5][p][(at & 15) + 16 * (j >> 3 & 3)] = __builtin_bit_cast(v4u, w[p]);
     }
-    __syncthreads();
-    if (first >= last || s_tok[16 * sub] < 0) return;
-    // where this lane's outputs of a step start, less 32 for each step
-    const auto place = [&](int h) { return YD == MOE_X_F32 ? 16 * h + 4 * q : 8 * q; };
-    int mine[NT], from[NT];
-    const Out* bp[NT];
-    Out* yp[NT];
+};
+
+// Up to 16 NT tokens of one adapter, list[0 .. cnt), and their y; rank 0: y = base.
+// Token j of a product's 16 stands in row 4 (j % 4) + j / 4 of h, so that outputs i of
+// the lanes are tokens 4i..4i + 3: with few tokens most loads and stores are left out
+// whole.  The next step's rows and base are on their way before this one's y is stored:
+// loads and stores count as one, and a wait for loads behind stores would wait for those
+// too.  For the same reason no lane is without a token: the places behind the last are
+// the first's.  FULL: no place is.
+template <int YD, int RC, int NT, bool BASE, bool FULL>
+__device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[NT][RC][3][64], const int* list, int cnt, int d,
+                                         int rank, int first, int last) {
+    using O = Outputs<YD>;
+    const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4, whole = min(last, a.N / STEP);
+    int own[NT], tok[NT][4];
 #pragma unroll
     for (int s = 0; s < NT; ++s) {
-        from[s] = s_tok[16 * (sub + s) + m] < 0 ? 16 * sub : 16 * (sub + s) + m;
-        const int64_t t = s_tok[from[s]];
-        mine[s] = s_ad[from[s]];
-        bp[s] = reinterpret_cast<const Out*>(a.base) + t * a.ldb;
-        yp[s] = reinterpret_cast<Out*>(a.y) + t * a.ldy;
+        own[s] = 16 * s + 4 * (m & 3) + (m >> 2) < cnt ? 64 * s + m : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = 16 * s + 4 * i + q;
+            tok[s][i] = list[j < cnt ? j : 0];
+        }
     }
-    const auto h_of = [&](int s, int c, int p) { return __builtin_bit_cast(bf16x8, hs[from[s] >> 4][c][p][(from[s] & 15) + 16 * q]); };
-    struct Rows {
-        v4u w[AT][RC][2];
+    const auto used = [&](int s, int i) { return FULL || 16 * s + 4 * i < cnt; };
+    Rows<RC> rows;
+    typename O::Piece base[NT][4] = {};
+    const auto fetch_base = [&](int step) {
+        if constexpr (BASE)
+#pragma unroll
+            for (int s = 0; s < NT; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (used(s, i)) base[s][i] = O::get(a.base, tok[s][i] * a.ldb + (STEP * step + 4 * m));
     };
-    const auto fetch_rows = [&](Rows& r, int i0, int step) {
+    const auto multiply = [&](v4f (&acc)[NT][4]) {
+        rows.cut(rank);
 #pragma unroll
-        for (int i = 0; i < AT; ++i) {
-            const int64_t d = __builtin_amdgcn_readfirstlane(s_of[min(i0 + i, n_ad - 1)]);
-#pragma unroll
-            for (int c = 0; c < RC; ++c)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = 32 * step + (YD == MOE_X_F32 ? 16 * h + m : 8 * (m >> 2) + 4 * h + (m & 3));
-                    r.w[i][c][h] = *reinterpret_cast<const v4u*>(a.b + (d * a.N + min(row, a.N - 1)) * a.r + min(32 * c + 8 * q, a.r - 8));
-                }
-        }
+        for (int s = 0; s < NT; ++s)
+            if (s == 0 || used(s, 0)) rows.multiply(hs[own[s] >> 6], (own[s] & 63) + 16 * q, acc[s]);
     };
-    const auto multiply = [&](Rows& r, int i0, v4f (&acc)[NT][2]) {
-#pragma unroll
-        for (int i = 0; i < AT; ++i) {
-            if (i0 + i >= n_ad) break;
-            const int d = __builtin_amdgcn_readfirstlane(s_of[i0 + i]), rank = __builtin_amdgcn_readfirstlane(s_rank[i0 + i]);
-#pragma unroll
-            for (int c = 0; c < RC; ++c) {
-                if (32 * c + 32 <= rank) continue;
-                const int j = 32 * c + 8 * q;  // columns past the rank may hold anything
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t keep = (j + 2 * k < rank ? 0xFFFFu : 0u) | (j + 2 * k + 1 < rank ? 0xFFFF0000u : 0u);
-                    r.w[i][c][0][k] &= keep, r.w[i][c][1][k] &= keep;
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < NT; ++s) {
-                v4f one[2] = {};
-#pragma unroll
-                for (int c = 0; c < RC; ++c)
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        const bf16x8 hv = h_of(s, c, p);
-                        one[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r.w[i][c][0]), hv, one[0], 0, 0, 0);
-                        one[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r.w[i][c][1]), hv, one[1], 0, 0, 0);
-                    }
-                if (mine[s] == d) acc[s][0] = one[0], acc[s][1] = one[1];
-            }
-        }
-    };
-    struct Base {
-        Piece p[NT][PIECES];
-    };
-    const auto fetch_base = [&](Base& b, int step) {
+    if (rank) rows.fetch(a, d, first);
+    if (first < whole) fetch_base(first);
+    for (int step = first; step < whole; ++step) {
+        if constexpr (NT * RC > 4) asm volatile("" ::: "memory");  // h is read from LDS where it is used: it does not fit registers
+        // nor are addresses kept from step to step: they would take 32 registers
 #pragma unroll
         for (int s = 0; s < NT; ++s)
 #pragma unroll
-            for (int h = 0; h < PIECES; ++h) {
-                b.p[s][h] = Piece{};
-                if constexpr (BASE) b.p[s][h] = *reinterpret_cast<const Loose*>(bp[s] + 32 * step + place(h));
-            }
-    };
-    Rows rows;
-    Base base;
-    if (n_ad) fetch_rows(rows, 0, first);
-    if (first < whole) fetch_base(base, first);
-    for (int step = first; step < whole; ++step) {
-        if constexpr (NT * RC > 4) asm volatile("" ::: "memory");  // h is read from LDS where it is used: it does not fit registers
-        v4f acc[NT][2] = {};
-        if (n_ad) multiply(rows, 0, acc);
-        for (int i0 = AT; i0 < n_ad; i0 += AT) {
-            Rows more;
-            fetch_rows(more, i0, step);
-            multiply(more, i0, acc);
-        }
-        const Base b = base;
-        if (n_ad) fetch_rows(rows, 0, min(step + 1, last - 1));
-        fetch_base(base, min(step + 1, whole - 1));
+            for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(tok[s][i]));
+        v4f acc[NT][4] = {};
+        if (rank) multiply(acc);
+        typename O::Piece b[NT][4];
 #pragma unroll
-        for (int s = 0; s < NT; ++s) {
-            if constexpr (YD == MOE_X_F32) {
+        for (int s = 0; s < NT; ++s)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) *reinterpret_cast<Loose*>(yp[s] + 32 * step + place(h)) = acc[s][h] + b.p[s][h];
-            } else {
-                bf16x8 o;
+            for (int i = 0; i < 4; ++i) b[s][i] = base[s][i];
+        if (rank) rows.fetch(a, d, min(step + 1, last - 1));
+        fetch_base(min(step + 1, whole - 1));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t w = b.p[s][0][i >> 1];
-                    o[i] = (__bf16)((i & 1 ? moe::bf16_hi(w) : moe::bf16_lo(w)) + acc[s][i >> 2][i & 3]);
-                }
-                *reinterpret_cast<Loose*>(yp[s] + 32 * step + place(0)) = __builtin_bit_cast(v4u, o);
-            }
-        }
+        for (int s = 0; s < NT; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (used(s, i))
+                    O::put(a.y, tok[s][i] * a.ldy + (STEP * step + 4 * m), b[s][i], v4f{acc[s][0][i], acc[s][1][i], acc[s][2][i], acc[s][3][i]});
     }
     if (whole >= last) return;
-    // the last rows, fewer than 32
-    v4f acc[NT][2] = {};
-    if (n_ad) multiply(rows, 0, acc);
-    for (int i0 = AT; i0 < n_ad; i0 += AT) {
-        Rows more;
-        fetch_rows(more, i0, whole);
-        multiply(more, i0, acc);
-    }
+    // the last rows, fewer than STEP
+    v4f acc[NT][4] = {};
+    if (rank) multiply(acc);
 #pragma unroll
-    for (int s = 0; s < NT; ++s) {
-        if (from[s] != 16 * (sub + s) + m) continue;
+    for (int s = 0; s < NT; ++s)
 #pragma unroll
-        for (int h = 0; h < PIECES; ++h)
+        for (int i = 0; i < 4; ++i) {
+            if (16 * s + 4 * i + q >= cnt) continue;
 #pragma unroll
-            for (int i = 0; i < WIDE; ++i) {
-                const int n = 32 * whole + place(h) + i;
-                if (n >= a.N) continue;
-                const float v = acc[s][YD == MOE_X_F32 ? h : i >> 2][i & 3];
-                yp[s][n] = (Out)(BASE ? (float)bp[s][n] + v : v);
+            for (int h = 0; h < 4; ++h) {
+                const int n = STEP * whole + 4 * m + h;
+                if (n < a.N) O::put_one(a.y, tok[s][i] * a.ldy + n, BASE ? a.base : nullptr, tok[s][i] * a.ldb + n, acc[s][h][i]);
             }
+        }
+}
+
+// A workgroup takes a tile of tokens, some of its adapters (those without one are one
+// more) and some steps.  h of an adapter's tokens, added up, scaled and cut, lies in
+// LDS as the products want it; of 64 tokens two waves share the steps, each with its
+// half of them.
+template <int YD, int TM, int RC, bool BASE>
+__global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) k_lora_up(LoraArgs a) {
+    constexpr int HALVES = TM == 64 ? 2 : 1, NT = TM / 16 / HALVES;
+    __shared__ __align__(16) v4u hs[HALVES][NT][RC][3][64];
+    __shared__ int s_tok[TM];
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, half = wid % HALVES;
+    const int at_tile = blockIdx.x / a.parts, wave = (blockIdx.x - at_tile * a.parts) * ((blockDim.x >> 6) / HALVES) + wid / HALVES;
+    const int first = wave * a.steps, last = min(first + a.steps, (a.N + STEP - 1) / STEP);
+    int tok, ad;
+    member<TM>(a, at_tile, lane, tok, ad);
+    if (threadIdx.x < TM) s_tok[lane] = tok;
+    int group = 0;
+    for (unsigned long long rest = __ballot(tok >= 0 && lane < TM); rest; ++group) {
+        const int at = __builtin_ctzll(rest), d = __builtin_amdgcn_readlane(ad, at);
+        const unsigned long long here = rest & __ballot(ad == d);  // neighbours: the tile is in order of its adapters
+        rest &= ~here;
+        if (group % gridDim.y != blockIdx.y) continue;
+        const int cnt = __builtin_popcountll(here), rank = rank_of(a, d);
+        if (rank == 0 && BASE && a.base == a.y) continue;
+        __syncthreads();  // the tokens are there, and the last adapter's h is read
+        for (int i = threadIdx.x; i < cnt * RC * 4 && rank; i += blockDim.x) {
+            const int k = i / (RC * 4), j = i % (RC * 4) * 8, t = s_tok[at + k];
+            float v[8] = {};
+            if (j < rank) {
+                v4f part[MAX_SPLITS][2];  // on their way together
+#pragma unroll
+                for (int sp = 0; sp < MAX_SPLITS; ++sp) {
+                    const v4f* p = reinterpret_cast<const v4f*>(a.h + ((int64_t)min(sp, a.splits - 1) * a.T + t) * a.r + j);
+                    part[sp][0] = p[0], part[sp][1] = p[1];
+                }
+#pragma unroll
+                for (int sp = 0; sp < MAX_SPLITS; ++sp)
+                    if (sp < a.splits)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] += part[sp][e >> 2][e & 3];
+                const float f = a.scale ? a.scale[d] : 1.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = j + e < rank ? f * v[e] : 0.0f;
+            }
+            bf16x8 w[3];
+            cut8(v, w);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                hs[k / (16 * NT)][k / 16 % NT][j >> 5][p][4 * (k & 3) + (k >> 2 & 3) + 16 * (j >> 3 & 3)] = __builtin_bit_cast(v4u, w[p]);
+        }
+        __syncthreads();
+        const int mine = min(cnt - 16 * NT * half, 16 * NT);
+        if (mine <= 0 || first >= last) continue;
+        const int* list = s_tok + at + 16 * NT * half;
+        if (mine == 16 * NT) up_steps<YD, RC, NT, BASE, true>(a, hs[half], list, mine, d, rank, first, last);
+        else up_steps<YD, RC, NT, BASE, false>(a, hs[half], list, mine, d, rank, first, last);
     }
 }
 
@@ -466,13 +484,8 @@ void launch_down(const LoraArgs& g, int tiles, int spread, hipStream_t stream) {
 
 template <int YD, int TM, int RC>
 void launch_up(const LoraArgs& g, const dim3& grid, const dim3& block, hipStream_t stream) {
-    // four adapters at a time where a tile has several: where tokens that share one are few
-    constexpr int AT = TM == 16 && RC <= 2 ? 4 : 1;
-    const bool several = AT > 1 && g.n > 1 && (int64_t)g.T < 16 * (int64_t)g.n;
-    if (several && g.base) hipLaunchKernelGGL((k_lora_up<YD, TM, RC, AT, true>), grid, block, 0, stream, g);
-    else if (several) hipLaunchKernelGGL((k_lora_up<YD, TM, RC, AT, false>), grid, block, 0, stream, g);
-    else if (g.base) hipLaunchKernelGGL((k_lora_up<YD, TM, RC, 1, true>), grid, block, 0, stream, g);
-    else hipLaunchKernelGGL((k_lora_up<YD, TM, RC, 1, false>), grid, block, 0, stream, g);
+    if (g.base) hipLaunchKernelGGL((k_lora_up<YD, TM, RC, true>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_lora_up<YD, TM, RC, false>), grid, block, 0, stream, g);
 }
 
 template <int YD, int TM>
@@ -515,7 +528,7 @@ int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const v
                 ws_bytes, moe_lora_workspace_bytes(T, K, r));
     if (T == 0) return moe_ok();
     LoraArgs g{x, ldx, reinterpret_cast<const uint16_t*>(a), reinterpret_cast<const uint16_t*>(b), ranks, scale, ids, n, r,
-               T, N, K, base, ldb, y, ldy, reinterpret_cast<float*>(ws), nullptr, down_splits(T, K), 1};
+               T, N, K, base, ldb, y, ldy, reinterpret_cast<float*>(ws), nullptr, down_splits(T, K), 1, 1};
     if (T > WAVE_TOKENS) {
         g.order = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(ws) + h_bytes(T, K, r));
         hipLaunchKernelGGL(k_lora_order, dim3((T + 63) / 64), dim3(256), 0, stream, g);
@@ -523,7 +536,9 @@ int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const v
     }
     const int tm = tile_tokens(T), tiles = (T + tm - 1) / tm;
     const int most = n < tm ? n : tm;  // adapters of a tile
-    const int spread = tm == 16 ? most : most < 4 ? most : 4;
+    // workgroups that share a tile's adapters; a tile of 16 has seldom more than 8 (257 tokens of 64 adapters: first pass
+    // 13.1 us by 16, 10.4 by 8, 11.1 by 4), one of 64 of a prompt one or two
+    const int spread = most < (tm == 16 ? 8 : 4) ? most : tm == 16 ? 8 : 4;
     if (x_dtype == MOE_X_F32) {
         if (tm == 16) launch_down<MOE_X_F32, 1>(g, tiles, spread, stream);
         else launch_down<MOE_X_F32, 4>(g, tiles, spread, stream);
@@ -532,12 +547,19 @@ int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const v
         else launch_down<MOE_X_BF16, 4>(g, tiles, spread, stream);
     }
     if (int rc = moe_check_launch("moe_lora_add/down")) return rc;
-    // steps a wave: as many as leave 16 waves a CU, up to 8
-    const int steps = (N + 31) / 32;
-    while (g.steps < 8 && (int64_t)tiles * steps / (2 * g.steps) >= 256 * 16) g.steps *= 2;
+    // steps a wave: so many that the workgroups are in flight all at once (of 64 tokens two a CU, pairs of waves for a
+    // step; of 16 three): what comes before the first step takes as long as some steps
+    const int groups = n + 1 < tm ? n + 1 : tm, up_spread = groups < (tm == 16 ? 8 : 2) ? groups : tm == 16 ? 8 : 2;
+    const int steps = (N + STEP - 1) / STEP;
+    const int64_t at_once = 256 * (tm == 64 ? 2 * 2 : 3 * 4);
+    // adapters of a tile, as far as the numbers tell
+    const int64_t units = tm == 64 ? tiles : (int64_t)tiles + (n < T ? n : T - 1);
+    g.steps = (int)((units * steps + at_once - 1) / at_once);
+    if (g.steps > steps) g.steps = steps;
     const int need = (steps + g.steps - 1) / g.steps;  // waves a tile
-    const int per = tm == 64 ? 2 : (int64_t)need * tiles <= 1024 ? 1 : 4;  // waves a workgroup (of 64 tokens: pairs)
-    const dim3 grid((need + per - 1) / per, tiles), block(tm == 64 ? 256 : 64 * per);
+    const int per = tm == 64 ? 2 : units * need <= 1024 ? 1 : 4;  // waves a workgroup (of 64 tokens: pairs)
+    g.parts = (need + per - 1) / per;
+    const dim3 grid(g.parts * tiles, up_spread), block(tm == 64 ? 256 : 64 * per);
     if (y_dtype == MOE_X_F32) {
         if (tm == 16) launch_up<MOE_X_F32, 16>(g, grid, block, stream);
         else launch_up<MOE_X_F32, 64>(g, grid, block, stream);
