@@ -4,14 +4,12 @@
 // + B (scale h).
 //
 // Both run on the matrix cores, v_mfma_f32_16x16x32_bf16, 16 rows of A or B
-// against 16 tokens.  Tokens that share an adapter share its rows: the tokens are
-// taken in order of their adapters (of 16 at most as they come, of 64 sorted inside
-// each wave, else by k_lora_order, in windows of 1024), in tiles of 16, or of 64
-// where there are more than 1024.  A tile that holds several adapters takes them one
-// after the other, and of each product every token keeps the columns of its own
-// adapter alone: nothing of one adapter, an infinity or a NaN, reaches another's
-// tokens.  fp32 x and h are cut into three bf16 planes (8 + 8 + 8 bits, exact) and
-// take three products: A x keeps its 24 bits, and the products are no bound.
+// against 16 tokens.  Tokens that share an adapter share its rows: they are taken in
+// order of their adapters (up to 64 sorted inside each wave, more by k_lora_order, in
+// windows of 1024), in tiles of 16, or of 64 where there are many.  The adapters of a
+// tile are taken each by itself: nothing of one, an infinity or a NaN, reaches
+// another's tokens.  fp32 x and h are cut into three bf16 planes (8 + 8 + 8 bits,
+// exact) and take three products: A x keeps its 24 bits, and the products are no bound.
 //
 // The inputs of A x are split over waves and workgroups; the partial sums (one of
 // each split in the workspace) are added in a fixed order.
@@ -31,7 +29,10 @@ typedef v2u v2u_loose __attribute__((aligned(2)));
 
 constexpr int WINDOW = 1024;     // tokens sorted together
 constexpr int WAVE_TOKENS = 64;  // up to so many are sorted in a wave
-constexpr int MANY = 1024;       // tokens from which tiles are of 64
+// More tokens than this go in tiles of 64.  Tiles of 16 and of 64, us, 4096 x 4096, bf16: 512 tokens of one adapter of
+// rank 16 15.6 and 17.7, of 8 in a row 22.7 and 17.3, of 64 in no order 24.5 and 40.4; 1024 tokens, rank 64, one 27.1
+// and 31.9, 8 in a row 35.0 and 31.1, 64 in no order 51.9 and 55.1; 257 tokens of 64 adapters 20 and 55.
+constexpr int MANY = 1024;
 constexpr int DOWN_WAVES = 4;    // of a workgroup of the first pass
 constexpr int MAX_SPLITS = 4;
 constexpr int STEP = 64;         // rows of B of a step of the second pass
@@ -356,6 +357,13 @@ __device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[NT][
         for (int s = 0; s < NT; ++s)
             if (s == 0 || used(s, 0)) rows.multiply(hs[own[s] >> 6], (own[s] & 63) + 16 * q, acc[s]);
     };
+    const auto start = [&](v4f (&acc)[NT][4]) {
+        const float zero = rank ? 0.0f : -0.0f;  // of base plus -0 the bits are base's
+#pragma unroll
+        for (int s = 0; s < NT; ++s)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) acc[s][h] = v4f{zero, zero, zero, zero};
+    };
     if (rank) rows.fetch(a, d, first);
     if (first < whole) fetch_base(first);
     for (int step = first; step < whole; ++step) {
@@ -365,7 +373,8 @@ __device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[NT][
         for (int s = 0; s < NT; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(tok[s][i]));
-        v4f acc[NT][4] = {};
+        v4f acc[NT][4];
+        start(acc);
         if (rank) multiply(acc);
         typename O::Piece b[NT][4];
 #pragma unroll
@@ -383,7 +392,8 @@ __device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[NT][
     }
     if (whole >= last) return;
     // the last rows, fewer than STEP
-    v4f acc[NT][4] = {};
+    v4f acc[NT][4];
+    start(acc);
     if (rank) multiply(acc);
 #pragma unroll
     for (int s = 0; s < NT; ++s)

@@ -484,6 +484,44 @@ def test_lora_random(m, T, N, K, n, r, xt, yt, kind):
         assert np.linalg.norm(got - want) <= (np.sqrt(K) + np.sqrt(3 * r) + 4) * 2.0 ** -23 * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("kind", ["mixed", "runs", "one"])
+@pytest.mark.parametrize("xt,yt", [("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("T,N,K,n,r", [(1025, 130, 136, 3, 40), (1100, 70, 264, 5, 72), (1500, 200, 96, 2, 128), (2100, 67, 72, 9, 256),
+                                       (1030, 1, 8, 2, 136), (1200, 64, 256, 1200, 8), (1090, 129, 512, 70, 64)])
+def test_lora_many_tokens_of_large_ranks(m, T, N, K, n, r, xt, yt, kind):
+    """Tiles of 64 tokens at every size of h, whole and in part, adapters of every rank."""
+    g = gen(T + r)
+    a, b = pool(n, r, K, N, g, whole=True)
+    x = torch.randint(-2, 3, (T, K), device="cuda", generator=g).to(DT[xt])
+    ids = some_ids(T, n, kind, g)
+    ranks = torch.randint(0, r + 1, (n,), device="cuda", generator=g).to(torch.int32) if T % 4 else None
+    base = torch.randint(-64, 65, (T, N), device="cuda", generator=g).float()
+    args = (host64(x), host64(a), host64(b), ids.cpu().numpy(), None if ranks is None else ranks.cpu().numpy())
+    for given in (base, None):
+        want, size = ref.lora(*args, None, None if given is None else host64(given))
+        exact = size < 2 ** 23
+        assert exact.mean() > 0.5
+        got = host64(run_lora(m, x, a, b, ids, ranks, None, given, "f32", pad=(8, 1, 2)))
+        np.testing.assert_array_equal(got[exact], want[exact])
+        if given is not None:
+            got = host64(run_lora(m, x, a, b, ids, ranks, None, given.to(DT[yt]), yt, in_place=True))
+            np.testing.assert_array_equal(got[exact], host64(torch.from_numpy(want).float().to(DT[yt]))[exact])
+
+
+def test_lora_leaves_the_base_of_others_as_it_is(m):
+    """Without an adapter y is base bit for bit: negative zeros, infinities, numbers below the normal range."""
+    for yt, T in (("f32", 5), ("bf16", 70), ("f32", 1200)):
+        a, b = pool(2, 16, 64, 200, gen(1))
+        base = torch.randn(T, 200, device="cuda", generator=gen(2)).to(DT[yt])
+        base[:, ::5], base[:, 1::5], base[:, 2::7] = -0.0, float("inf"), 1e-40
+        ids = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+        ids[::3] = 1
+        ranks = torch.tensor([16, 0], dtype=torch.int32, device="cuda")
+        got = run_lora(m, torch.randn(T, 64, device="cuda").bfloat16(), a, b, ids, ranks, None, base, yt)
+        kind = torch.int32 if yt == "f32" else torch.int16
+        assert torch.equal(got.contiguous().view(kind), base.view(kind))
+
+
 @pytest.mark.parametrize("xt", ["bf16", "f32"])
 def test_lora_every_weight_by_itself(m, xt):
     """One input of a token, one row of A and one column of B: the product of three, with all 24 bits of an fp32 x."""
