@@ -621,8 +621,9 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
             }
         } else {
             double c, rest, share = rcp64((double)my_sum);
+            float top = my_m;  // what was taken off the logits under `share`
             for (bool exact = sigmoid;; exact = true) {
-                const double p = !live ? 0.0 : sigmoid ? sigmoid64(zc, rest) : soft64(zc, my_m) * share;
+                const double p = !live ? 0.0 : sigmoid ? sigmoid64(zc, rest) : soft64(zc, top) * share;
                 c = live ? p + (double)a.bias[id] : -INFINITY;
                 rank = 0;
                 for (int x = 0; x < seg; x += 16) {
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
                     const int i = __builtin_ctzll(near) / seg;
                     float m;
                     const double s = softmax64<ZD>(a, t0 + i, m);
-                    if (mine == i) share = s;
+                    if (mine == i) share = s, top = m;
                     near &= ~__ballot(mine == i);
                 }
                 wave_sync();

@@ -192,6 +192,26 @@ def test_select_choices_closer_than_fp32(m, E, k, score):
     check_select(m, z, k, dict(score=score), bias)
 
 
+@pytest.mark.parametrize("shift", [0.0, 3.0, -20.0, 300.0])
+@pytest.mark.parametrize("zt", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups", [(64, 6, 1), (288, 8, 1), (512, 10, 1), (1500, 12, 1), (288, 8, 8)])
+def test_select_pairs_closer_than_fp32(m, E, k, groups, score, zt, shift):
+    """Of every two of the best, the second's bias makes up for its logit but for some 1e-9; the others lie far off."""
+    g = gen(E + k)
+    z = logits(1, E, E, zt).expand(24, E).contiguous()
+    z = (z.float() + (shift if score == "softmax" else 0.0)).to(DT[zt])
+    z[20:] = logits(4, E, E + 1, zt)  # and tokens that the biases are not made for
+    s = ref.scores(host64(z[:1]), score)[0]
+    order = np.argsort(-s, kind="stable")
+    bias = np.zeros(E, np.float32)
+    for i in range(0, 2 * (k // 2) + 2, 2):
+        bias[order[i + 1]] = np.float32(s[order[i]] - s[order[i + 1]])
+    bias = torch.from_numpy(bias).cuda()
+    check_select(m, z, k, dict(score=score, groups=groups, groups_kept=max(1, groups // 2), group_top=2), bias)
+    check_select(m, z, k, dict(score=score, groups=groups, groups_kept=max(1, groups // 2), renorm=False), bias)
+
+
 def special_rows(E, g):
     inf, nan = float("inf"), float("nan")
     z = torch.randn(12, E, device="cuda", generator=g)
