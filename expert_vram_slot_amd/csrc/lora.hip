@@ -158,15 +158,19 @@ struct Piece {
 // where there are any and change nothing but h of those rows, which the second
 // pass does not use.
 template <int XD, int NT, int RB>
-__global__ void __launch_bounds__(64 * DOWN_WAVES) k_lora_down(LoraArgs a) {
-    constexpr int U = NT == 1 ? 4 : XD == MOE_X_BF16 ? 2 : 1;  // products of 32 inputs loaded together
+__global__ void __launch_bounds__(64 * DOWN_WAVES, 2) k_lora_down(LoraArgs a) {
+    // products of 32 inputs loaded together: as many as leave room for two waves a SIMD
+    constexpr int U = NT == 1 ? (XD == MOE_X_F32 && RB == 4 ? 2 : 4) : XD == MOE_X_BF16 ? 2 : 1;
     constexpr int XB = XD == MOE_X_F32 ? 4 : 2;
     __shared__ __align__(16) v4f red[DOWN_WAVES][NT * RB][64];
     __shared__ int s_tok[16 * NT], s_ad[16 * NT];
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, m = lane & 15, q = lane >> 4;
-    const int split = blockIdx.z % a.splits, row0 = blockIdx.z / a.splits * RANKS;
+    // workgroups go to the eight dies in turn: those of a tile, with other rows of A, go to one, where its inputs then are
+    const int parts = a.splits * ((a.r + RANKS - 1) / RANKS), part = (blockIdx.x >> 3) % parts;
+    const int at_tile = (blockIdx.x >> 3) / parts * 8 + (blockIdx.x & 7), split = part % a.splits, row0 = part / a.splits * RANKS;
+    if ((int64_t)at_tile * 16 * NT >= a.T) return;
     int tok, ad;
-    member<16 * NT>(a, blockIdx.x, lane, tok, ad);
+    member<16 * NT>(a, at_tile, lane, tok, ad);
     if (wid == 0 && lane < 16 * NT) s_tok[lane] = tok, s_ad[lane] = ad;
     const int units = (a.K + 31) / 32, waves = a.splits * DOWN_WAVES, wi = split * DOWN_WAVES + wid;
     const int u0 = (int)((int64_t)units * wi / waves), u1 = (int)((int64_t)units * (wi + 1) / waves);
@@ -318,6 +322,8 @@ struct Rows {
     }
 };
 
+constexpr int up_sharing(int tm, int rc) { return tm == 16 ? 1 : rc <= 2 ? 2 : 4; }  // waves that share a step
+
 // Up to 16 NT tokens of one adapter, list[0 .. cnt), and their y; rank 0: y = base.
 // Token j of a product's 16 stands in row 4 (j % 4) + j / 4 of h, so that outputs i of
 // the lanes are tokens 4i..4i + 3: with few tokens most loads and stores are left out
@@ -410,11 +416,11 @@ __device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[NT][
 
 // A workgroup takes a tile of tokens, some of its adapters (those without one are one
 // more) and some steps.  h of an adapter's tokens, added up, scaled and cut, lies in
-// LDS as the products want it; of 64 tokens two waves share the steps, each with its
-// half of them.
+// LDS as the products want it; of 64 tokens two or four waves share the steps, each
+// with its part of them.
 template <int YD, int TM, int RC, bool BASE>
-__global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) k_lora_up(LoraArgs a) {
-    constexpr int HALVES = TM == 64 ? 2 : 1, NT = TM / 16 / HALVES;
+__global__ void __launch_bounds__(256, RC <= 4 ? 2 : 1) k_lora_up(LoraArgs a) {
+    constexpr int HALVES = up_sharing(TM, RC), NT = TM / 16 / HALVES;
     __shared__ __align__(16) v4u hs[HALVES][NT][RC][3][64];
     __shared__ int s_tok[TM];
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, half = wid % HALVES;
@@ -486,7 +492,7 @@ size_t h_bytes(int T, int K, int r) { return (size_t)down_splits(T, K) * (T > 0 
 
 template <int XD, int NT>
 void launch_down(const LoraArgs& g, int tiles, int spread, hipStream_t stream) {
-    const dim3 grid(tiles, spread, g.splits * ((g.r + RANKS - 1) / RANKS)), block(64 * DOWN_WAVES);
+    const dim3 grid((tiles + 7) / 8 * 8 * g.splits * ((g.r + RANKS - 1) / RANKS), spread), block(64 * DOWN_WAVES);
     if (g.r <= 16) hipLaunchKernelGGL((k_lora_down<XD, NT, 1>), grid, block, 0, stream, g);
     else if (g.r <= 32) hipLaunchKernelGGL((k_lora_down<XD, NT, 2>), grid, block, 0, stream, g);
     else hipLaunchKernelGGL((k_lora_down<XD, NT, 4>), grid, block, 0, stream, g);
@@ -557,17 +563,25 @@ int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const v
         else launch_down<MOE_X_BF16, 4>(g, tiles, spread, stream);
     }
     if (int rc = moe_check_launch("moe_lora_add/down")) return rc;
-    // steps a wave: so many that the workgroups are in flight all at once (of 64 tokens two a CU, pairs of waves for a
-    // step; of 16 three): what comes before the first step takes as long as some steps
     const int groups = n + 1 < tm ? n + 1 : tm, up_spread = groups < (tm == 16 ? 8 : 2) ? groups : tm == 16 ? 8 : 2;
-    const int steps = (N + STEP - 1) / STEP;
-    const int64_t at_once = 256 * (tm == 64 ? 2 * 2 : 3 * 4);
+    const int rc = r <= 32 ? 1 : r <= 64 ? 2 : r <= 128 ? 4 : 8, sharing = up_sharing(tm, rc);
+    const int resident = rc == 8 ? 1 : tm == 64 || rc == 4 ? 2 : 3;  // waves a SIMD
+    const int64_t at_once = 256 * 4 * resident / sharing;
     // adapters of a tile, as far as the numbers tell
     const int64_t units = tm == 64 ? tiles : (int64_t)tiles + (n < T ? n : T - 1);
-    g.steps = (int)((units * steps + at_once - 1) / at_once);
-    if (g.steps > steps) g.steps = steps;
-    const int need = (steps + g.steps - 1) / g.steps;  // waves a tile
-    const int per = tm == 64 ? 2 : units * need <= 1024 ? 1 : 4;  // waves a workgroup (of 64 tokens: pairs)
+    // waves a tile (those that share as one): as many as fill the card a whole number of times, what comes before a
+    // wave's first step being as long as START steps
+    constexpr int START = 3;
+    const int steps = (N + STEP - 1) / STEP;
+    int need = 1;
+    int64_t best = INT64_MAX;
+    for (int rounds = 1; rounds <= 8; ++rounds) {
+        int64_t w = at_once * rounds / units;
+        w = w < 1 ? 1 : w > steps ? steps : w;
+        const int64_t each = (steps + w - 1) / w, long_ = (units * ((steps + each - 1) / each) + at_once - 1) / at_once * (each + START);
+        if (long_ < best) best = long_, need = (int)((steps + each - 1) / each), g.steps = (int)each;
+    }
+    const int per = tm == 64 ? 4 / sharing : units * need <= 1024 ? 1 : 4;  // waves a workgroup (those that share as one)
     g.parts = (need + per - 1) / per;
     const dim3 grid(g.parts * tiles, up_spread), block(tm == 64 ? 256 : 64 * per);
     if (y_dtype == MOE_X_F32) {
