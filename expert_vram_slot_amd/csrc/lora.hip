@@ -280,6 +280,13 @@ struct Outputs {
     }
 };
 
+// Columns j.. of a row of B; those past the rank may hold anything.
+__device__ __forceinline__ v4u within(v4u w, int j, int rank) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] &= (j + 2 * k < rank ? 0xFFFFu : 0u) | (j + 2 * k + 1 < rank ? 0xFFFF0000u : 0u);
+    return w;
+}
+
 // Rows 4m + h of step `step` of adapter d, columns 32c + 8q..
 template <int RC>
 struct Rows {
@@ -293,19 +300,13 @@ struct Rows {
                 w[c][h] = *reinterpret_cast<const v4u*>(a.b + ((int64_t)d * a.N + min(STEP * step + 4 * m + h, a.N - 1)) * a.r +
                                                         min(32 * c + 8 * q, a.r - 8));
     }
-    // columns past the rank may hold anything
     __device__ __forceinline__ void cut(int rank) {
         const int q = (threadIdx.x & 63) >> 4;
 #pragma unroll
         for (int c = 0; c < RC; ++c) {
             if (32 * c + 32 <= rank) continue;
-            const int j = 32 * c + 8 * q;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t keep = (j + 2 * k < rank ? 0xFFFFu : 0u) | (j + 2 * k + 1 < rank ? 0xFFFF0000u : 0u);
-#pragma unroll
-                for (int h = 0; h < 4; ++h) w[c][h][k] &= keep;
-            }
+            for (int h = 0; h < 4; ++h) w[c][h] = within(w[c][h], 32 * c + 8 * q, rank);
         }
     }
     // sum += rows times h, as it lies in LDS
@@ -322,109 +323,142 @@ struct Rows {
     }
 };
 
-constexpr int up_sharing(int tm, int rc) { return tm == 16 ? 1 : rc <= 2 ? 2 : 4; }  // waves that share a step
-
-// Up to 16 NT tokens of one adapter, list[0 .. cnt), and their y; rank 0: y = base.
-// Token j of a product's 16 stands in row 4 (j % 4) + j / 4 of h, so that outputs i of
-// the lanes are tokens 4i..4i + 3: with few tokens most loads and stores are left out
-// whole.  The next step's rows and base are on their way before this one's y is stored:
-// loads and stores count as one, and a wait for loads behind stores would wait for those
-// too.  For the same reason no lane is without a token: the places behind the last are
-// the first's.  FULL: no place is.
-template <int YD, int RC, int NT, bool BASE, bool FULL>
-__device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[NT][RC][3][64], const int* list, int cnt, int d,
-                                         int rank, int first, int last) {
-    using O = Outputs<YD>;
-    const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4, whole = min(last, a.N / STEP);
-    int own[NT], tok[NT][4];
+// The same for four waves that share a step: each brings one of the four rows, and all
+// read them from LDS.
+template <int RC>
+struct SharedRows {
+    v4u w[RC];
+    __device__ __forceinline__ void fetch(const LoraArgs& a, int d, int step) {
+        const int lane = threadIdx.x & 63, h = threadIdx.x >> 6, m = lane & 15, q = lane >> 4;
 #pragma unroll
-    for (int s = 0; s < NT; ++s) {
-        own[s] = 16 * s + 4 * (m & 3) + (m >> 2) < cnt ? 64 * s + m : 0;
+        for (int c = 0; c < RC; ++c)
+            w[c] = *reinterpret_cast<const v4u*>(a.b + ((int64_t)d * a.N + min(STEP * step + 4 * m + h, a.N - 1)) * a.r +
+                                                 min(32 * c + 8 * q, a.r - 8));
+    }
+    __device__ __forceinline__ void share(int rank, v4u (&rows)[RC][4][64]) {
+        const int lane = threadIdx.x & 63, h = threadIdx.x >> 6, q = lane >> 4;
+        __syncthreads();  // the last step's are read
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = 16 * s + 4 * i + q;
-            tok[s][i] = list[j < cnt ? j : 0];
+        for (int c = 0; c < RC; ++c) {
+            v4u v = w[c];
+            if (32 * c + 32 > rank) v = within(v, 32 * c + 8 * q, rank);
+            rows[c][h][lane] = v;
+        }
+        __syncthreads();
+    }
+    static __device__ __forceinline__ void multiply(const v4u (&rows)[RC][4][64], const v4u (&hs)[RC][3][64], int at, v4f (&sum)[4]) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int c = 0; c < RC; ++c) {
+            bf16x8 w[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) w[h] = __builtin_bit_cast(bf16x8, rows[c][h][lane]);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                const bf16x8 hv = __builtin_bit_cast(bf16x8, hs[c][p][at]);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) sum[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv, w[h], sum[h], 0, 0, 0);
+            }
         }
     }
-    const auto used = [&](int s, int i) { return FULL || 16 * s + 4 * i < cnt; };
-    Rows<RC> rows;
-    typename O::Piece base[NT][4] = {};
+};
+
+// Up to 16 tokens of one adapter, list[0 .. cnt), and their y; rank 0: y = base.
+// Token j stands in row 4 (j % 4) + j / 4 of h, so that outputs i of the lanes are
+// tokens 4i..4i + 3: with few tokens most loads and stores are left out whole.  The next
+// step's rows and base are on their way before this one's y is stored: loads and stores
+// count as one, and a wait for loads behind stores would wait for those too.  For the
+// same reason no lane is without a token: the places behind the last are the first's.
+// FULL: no place is.  SHARED: the workgroup's waves go through the steps together, also
+// those that are left without a token.
+template <int YD, int RC, bool BASE, bool FULL, bool SHARED>
+__device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[RC][3][64], v4u (*shared)[RC][4][64], const int* list,
+                                         int cnt, int d, int rank, int first, int last) {
+    using O = Outputs<YD>;
+    const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4, whole = min(last, a.N / STEP);
+    const int own = (4 * (m & 3) + (m >> 2) < cnt ? m : 0) + 16 * q;
+    int tok[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tok[i] = list[4 * i + q < cnt ? 4 * i + q : 0];
+    // (a wave by itself has a token: known, so that the loop's waits count on its load)
+    const auto used = [&](int i) { return FULL || (!SHARED && i == 0) || 4 * i < cnt; };
+    std::conditional_t<SHARED, SharedRows<RC>, Rows<RC>> rows;
+    typename O::Piece base[4] = {};
     const auto fetch_base = [&](int step) {
         if constexpr (BASE)
 #pragma unroll
-            for (int s = 0; s < NT; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (used(s, i)) base[s][i] = O::get(a.base, tok[s][i] * a.ldb + (STEP * step + 4 * m));
+            for (int i = 0; i < 4; ++i)
+                if (used(i)) base[i] = O::get(a.base, tok[i] * a.ldb + (STEP * step + 4 * m));
     };
-    const auto multiply = [&](v4f (&acc)[NT][4]) {
-        rows.cut(rank);
-#pragma unroll
-        for (int s = 0; s < NT; ++s)
-            if (s == 0 || used(s, 0)) rows.multiply(hs[own[s] >> 6], (own[s] & 63) + 16 * q, acc[s]);
-    };
-    const auto start = [&](v4f (&acc)[NT][4]) {
+    const auto start = [&](v4f (&acc)[4]) {
         const float zero = rank ? 0.0f : -0.0f;  // of base plus -0 the bits are base's
 #pragma unroll
-        for (int s = 0; s < NT; ++s)
-#pragma unroll
-            for (int h = 0; h < 4; ++h) acc[s][h] = v4f{zero, zero, zero, zero};
+        for (int h = 0; h < 4; ++h) acc[h] = v4f{zero, zero, zero, zero};
+    };
+    const auto multiply = [&](v4f (&acc)[4]) {
+        if constexpr (SHARED) {
+            rows.share(rank, *shared);
+            if (used(0)) rows.multiply(*shared, hs, own, acc);
+        } else {
+            rows.cut(rank);
+            rows.multiply(hs, own, acc);
+        }
     };
     if (rank) rows.fetch(a, d, first);
     if (first < whole) fetch_base(first);
     for (int step = first; step < whole; ++step) {
-        if constexpr (NT * RC > 4) asm volatile("" ::: "memory");  // h is read from LDS where it is used: it does not fit registers
-        // nor are addresses kept from step to step: they would take 32 registers
+        if constexpr (RC >= (SHARED ? 2 : 4)) asm volatile("" ::: "memory");  // h is read from LDS where it is used: it does not fit registers
+        // nor are addresses kept from step to step
 #pragma unroll
-        for (int s = 0; s < NT; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(tok[s][i]));
-        v4f acc[NT][4];
+        for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(tok[i]));
+        v4f acc[4];
         start(acc);
         if (rank) multiply(acc);
-        typename O::Piece b[NT][4];
+        typename O::Piece b[4];
 #pragma unroll
-        for (int s = 0; s < NT; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[s][i] = base[s][i];
+        for (int i = 0; i < 4; ++i) b[i] = base[i];
         if (rank) rows.fetch(a, d, min(step + 1, last - 1));
         fetch_base(min(step + 1, whole - 1));
 #pragma unroll
-        for (int s = 0; s < NT; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (used(s, i))
-                    O::put(a.y, tok[s][i] * a.ldy + (STEP * step + 4 * m), b[s][i], v4f{acc[s][0][i], acc[s][1][i], acc[s][2][i], acc[s][3][i]});
+        for (int i = 0; i < 4; ++i)
+            if (used(i))
+                O::put(a.y, tok[i] * a.ldy + (STEP * step + 4 * m), b[i], v4f{acc[0][i], acc[1][i], acc[2][i], acc[3][i]});
     }
     if (whole >= last) return;
     // the last rows, fewer than STEP
-    v4f acc[NT][4];
+    v4f acc[4];
     start(acc);
     if (rank) multiply(acc);
 #pragma unroll
-    for (int s = 0; s < NT; ++s)
+    for (int i = 0; i < 4; ++i) {
+        if (4 * i + q >= cnt) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (16 * s + 4 * i + q >= cnt) continue;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const int n = STEP * whole + 4 * m + h;
-                if (n < a.N) O::put_one(a.y, tok[s][i] * a.ldy + n, BASE ? a.base : nullptr, tok[s][i] * a.ldb + n, acc[s][h][i]);
-            }
+        for (int h = 0; h < 4; ++h) {
+            const int n = STEP * whole + 4 * m + h;
+            if (n < a.N) O::put_one(a.y, tok[i] * a.ldy + n, BASE ? a.base : nullptr, tok[i] * a.ldb + n, acc[h][i]);
         }
+    }
 }
+
+// Waves a SIMD: as many as LDS (64) and registers (16) have room for.  Tiles of 64 by
+// four, three and two, us: 16384 x 4096 x 4096 of rank 64 112, 112 and 124, of rank 16
+// 97, 99 and 117.
+constexpr int up_resident(int tm, int rc) { return rc == 8 ? 1 : rc == 4 ? 2 : tm == 64 ? 4 : rc == 1 ? 3 : 2; }
 
 // A workgroup takes a tile of tokens, some of its adapters (those without one are one
 // more) and some steps.  h of an adapter's tokens, added up, scaled and cut, lies in
-// LDS as the products want it; of 64 tokens two or four waves share the steps, each
-// with its part of them.
+// LDS as the products want it.  Of 16 tokens each wave takes steps of its own; of 64
+// the four waves share theirs, each with 16 of the tokens, and B passes through LDS once
+// for all (16384 x 4096 x 4096 of rank 64: 121 us where two pairs of waves took steps of
+// their own and B from the caches; 4096 x 4096 x 4096 of rank 128 80 and 61).
 template <int YD, int TM, int RC, bool BASE>
-__global__ void __launch_bounds__(256, RC <= 4 ? 2 : 1) k_lora_up(LoraArgs a) {
-    constexpr int HALVES = up_sharing(TM, RC), NT = TM / 16 / HALVES;
-    __shared__ __align__(16) v4u hs[HALVES][NT][RC][3][64];
+__global__ void __launch_bounds__(256, up_resident(TM, RC)) k_lora_up(LoraArgs a) {
+    constexpr bool SHARED = TM == 64;
+    __shared__ __align__(16) v4u hs[TM / 16][RC][3][64];
+    __shared__ __align__(16) v4u shared[SHARED ? RC : 1][4][64];
     __shared__ int s_tok[TM];
-    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, half = wid % HALVES;
-    const int at_tile = blockIdx.x / a.parts, wave = (blockIdx.x - at_tile * a.parts) * ((blockDim.x >> 6) / HALVES) + wid / HALVES;
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, quarter = SHARED ? wid : 0;
+    const int at_tile = blockIdx.x / a.parts, part = blockIdx.x - at_tile * a.parts, wave = SHARED ? part : part * (blockDim.x >> 6) + wid;
     const int first = wave * a.steps, last = min(first + a.steps, (a.N + STEP - 1) / STEP);
     int tok, ad;
     member<TM>(a, at_tile, lane, tok, ad);
@@ -461,14 +495,19 @@ __global__ void __launch_bounds__(256, RC <= 4 ? 2 : 1) k_lora_up(LoraArgs a) {
             cut8(v, w);
 #pragma unroll
             for (int p = 0; p < 3; ++p)
-                hs[k / (16 * NT)][k / 16 % NT][j >> 5][p][4 * (k & 3) + (k >> 2 & 3) + 16 * (j >> 3 & 3)] = __builtin_bit_cast(v4u, w[p]);
+                hs[k >> 4][j >> 5][p][4 * (k & 3) + (k >> 2 & 3) + 16 * (j >> 3 & 3)] = __builtin_bit_cast(v4u, w[p]);
         }
         __syncthreads();
-        const int mine = min(cnt - 16 * NT * half, 16 * NT);
-        if (mine <= 0 || first >= last) continue;
-        const int* list = s_tok + at + 16 * NT * half;
-        if (mine == 16 * NT) up_steps<YD, RC, NT, BASE, true>(a, hs[half], list, mine, d, rank, first, last);
-        else up_steps<YD, RC, NT, BASE, false>(a, hs[half], list, mine, d, rank, first, last);
+        const int mine = max(0, min(cnt - 16 * quarter, 16));
+        if (first >= last) continue;
+        const int* list = s_tok + at + (mine ? 16 * quarter : 0);
+        if constexpr (SHARED) {
+            if (cnt == TM) up_steps<YD, RC, BASE, true, true>(a, hs[quarter], &shared, list, 16, d, rank, first, last);
+            else up_steps<YD, RC, BASE, false, true>(a, hs[quarter], &shared, list, mine, d, rank, first, last);
+        } else {
+            if (mine == 16) up_steps<YD, RC, BASE, true, false>(a, hs[0], nullptr, list, mine, d, rank, first, last);
+            else up_steps<YD, RC, BASE, false, false>(a, hs[0], nullptr, list, mine, d, rank, first, last);
+        }
     }
 }
 
@@ -564,12 +603,11 @@ int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const v
     }
     if (int rc = moe_check_launch("moe_lora_add/down")) return rc;
     const int groups = n + 1 < tm ? n + 1 : tm, up_spread = groups < (tm == 16 ? 8 : 2) ? groups : tm == 16 ? 8 : 2;
-    const int rc = r <= 32 ? 1 : r <= 64 ? 2 : r <= 128 ? 4 : 8, sharing = up_sharing(tm, rc);
-    const int resident = rc == 8 ? 1 : tm == 64 || rc == 4 ? 2 : 3;  // waves a SIMD
-    const int64_t at_once = 256 * 4 * resident / sharing;
+    const int resident = up_resident(tm, r <= 32 ? 1 : r <= 64 ? 2 : r <= 128 ? 4 : 8);
+    const int64_t at_once = 256 * resident * (tm == 64 ? 1 : 4);
     // adapters of a tile, as far as the numbers tell
     const int64_t units = tm == 64 ? tiles : (int64_t)tiles + (n < T ? n : T - 1);
-    // waves a tile (those that share as one): as many as fill the card a whole number of times, what comes before a
+    // waves a tile (the four that share as one): as many as fill the card a whole number of times, what comes before a
     // wave's first step being as long as START steps
     constexpr int START = 3;
     const int steps = (N + STEP - 1) / STEP;
@@ -581,7 +619,7 @@ int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const v
         const int64_t each = (steps + w - 1) / w, long_ = (units * ((steps + each - 1) / each) + at_once - 1) / at_once * (each + START);
         if (long_ < best) best = long_, need = (int)((steps + each - 1) / each), g.steps = (int)each;
     }
-    const int per = tm == 64 ? 4 / sharing : units * need <= 1024 ? 1 : 4;  // waves a workgroup (those that share as one)
+    const int per = tm == 64 || units * need <= 1024 ? 1 : 4;  // waves a workgroup (those that share as one)
     g.parts = (need + per - 1) / per;
     const dim3 grid(g.parts * tiles, up_spread), block(tm == 64 ? 256 : 64 * per);
     if (y_dtype == MOE_X_F32) {
