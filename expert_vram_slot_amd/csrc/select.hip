@@ -522,8 +522,11 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
             };
             reach(bound);
             if (C > seg) {
-                // lanes with several, or equals: the same search over every key
-                for (++hi; hi - lo > 1 && C > seg;) {
+                // lanes with several, or equals: the same search over every key.  Fewer than k reach hi: a signalling NaN
+                // may have hidden a lane's best from the largest of all, then it is what lies above +inf
+                reach(of_code(++hi));
+                if (C >= k) hi = 0xFF800001u;
+                for (C = seg + 1; hi - lo > 1 && C > seg;) {
                     const uint32_t mid = lo + (hi - lo) / 2;
                     const float kth = fmaxf(of_code(mid), -3.402823466e38f);
                     reach(kth);

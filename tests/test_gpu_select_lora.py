@@ -122,7 +122,10 @@ def check_grad(m, z, ids, dw, rule, add=None, into=None):
         top = np.where(np.isfinite(zh), zh, -np.inf).max(axis=1, keepdims=True)
         far = np.abs(np.nan_to_num(np.where(np.isfinite(zh), zh - top, 0)))
     own = (1.5 * np.minimum(far, 200) + 4) * 2.0 ** -23 if r["score"] == "softmax" and not r["renorm"] else 0.0
-    tol = (3 * DS(E) + own) * size + 2.0 ** -23 * (np.abs(ah) + np.abs(part)) + HALF[zt] * np.abs(want) * (1 + 2.0 ** -8) + 1.2e-38
+    # numbers below 2^-126 = 1.1755e-38 are as good as 0: one of dz, and one of p, which goes into dz times h - sum h p, of a
+    # magnitude of 2 max |h| at most (sum p <= 1): off by 2^-126 (1 + 2 max |h|) together
+    h = r["scale"] * np.abs(np.nan_to_num(np.where(ih >= 0, host64(dw), 0))).max(axis=1, keepdims=True)
+    tol = (3 * DS(E) + own) * size + 2.0 ** -23 * (np.abs(ah) + np.abs(part)) + HALF[zt] * np.abs(want) * (1 + 2.0 ** -8) + 1.2e-38 * (1 + 2 * h)
     assert np.all(np.abs(got - want) <= tol), (np.abs(got - want) - tol).max()
     return into
 
@@ -248,6 +251,27 @@ def test_select_masked_and_special_rows(m, E, k, groups, kept, rule):
         mask = torch.tensor([1, 0, 1, 1, 0, 1, 0, 1, 1, 2, 1, 0], dtype=torch.uint8, device="cuda")
         check_select(m, z, k, rule, bias, mask)
         check_select(m, z, k, rule, torch.full((E,), -float("inf"), device="cuda"))  # no expert open at all
+
+
+@pytest.mark.parametrize("rule", RULES, ids=lambda r: f"{r['score']}{'' if r.get('renorm', True) else '_raw'}")
+@pytest.mark.parametrize("E,k,groups", [(64, 6, 1), (300, 8, 1), (512, 10, 1), (512, 4, 8), (1024, 32, 1), (4096, 8, 1)])
+def test_select_signalling_nans(m, E, k, groups, rule):
+    """Neither an expert whose logit is a signalling NaN nor one that is looked at next to it is lost or found by that."""
+    z = logits(70, E, 17 * E + k)
+    z[20:40] = 8.0 * z[20:40] + 20.0
+    z[40:50] = torch.floor(z[40:50])
+    g = gen(5)
+    holes = torch.rand(70, E, device="cuda", generator=g) < 0.4
+    holes[:10], holes[10:20] = False, False
+    holes[:60, E - E // 8:] |= True  # the last that each lane holds
+    rule = dict(rule, groups=groups, group_top=2)
+    for zt, bits, ints in (("f32", 0x7F800001, torch.int32), ("bf16", 0x7F81, torch.int16)):
+        zz = z.to(DT[zt]).clone()
+        zz.view(ints)[holes] = bits
+        assert torch.equal(torch.isnan(zz), holes)
+        ids, _ = check_select(m, zz, k, rule)
+        check_grad(m, zz, ids, torch.randn(70, k, device="cuda", generator=g), rule)
+        check_select(m, zz, k, rule, torch.randn(E, device="cuda", generator=g))
 
 
 def test_select_biases_without_end(m):
