@@ -28,13 +28,16 @@ typedef v4f v4f_loose __attribute__((aligned(4)));
 typedef v2u v2u_loose __attribute__((aligned(2)));
 
 constexpr int WINDOW = 1024;     // tokens sorted together
-constexpr int WAVE_TOKENS = 64;  // up to so many are sorted in a wave
+// Up to so many are sorted in a wave, without a kernel for it (4096 x 4096, us with and without: 64 tokens of 32
+// adapters 17.7 and 15.7, 40 of 16 14.5 and 13.9).
+constexpr int WAVE_TOKENS = 64;
 // More tokens than this go in tiles of 64.  Tiles of 16 and of 64, us, 4096 x 4096, bf16: 512 tokens of one adapter of
-// rank 16 15.6 and 17.7, of 8 in a row 22.7 and 17.3, of 64 in no order 24.5 and 40.4; 1024 tokens, rank 64, one 27.1
-// and 31.9, 8 in a row 35.0 and 31.1, 64 in no order 51.9 and 55.1; 257 tokens of 64 adapters 20 and 55.
+// rank 16 16.5 and 17.1, of 64 in no order 21.9 and 36.9; 1024 of rank 64, of one 30.8 and 31.2, of 8 in a row 32.9 and
+// 30.2, of 64 in no order 46.0 and 51.1; 2048 of rank 16, of one 27.9 and 26.0, of 8 in a row 31.7 and 25.9, of 64 in no
+// order 41.5 and 53.7, of rank 64 of 8 62.8 and 41.4.
 constexpr int MANY = 1024;
 constexpr int DOWN_WAVES = 4;    // of a workgroup of the first pass
-constexpr int MAX_SPLITS = 4;
+constexpr int MAX_SPLITS = 4;    // of the inputs, between workgroups
 constexpr int STEP = 64;         // rows of B of a step of the second pass
 constexpr int RANKS = 64;        // rows of A that a workgroup of the first pass takes
 
@@ -92,7 +95,9 @@ __device__ __forceinline__ void member(const LoraArgs& a, int tile, int lane, in
 
 // Places of the tokens of a window in order of their adapters, then of their
 // numbers: each counts the window's smaller keys.  One workgroup for 64 tokens,
-// four threads a token.
+// four threads a token: no workgroup waits for another, and nothing depends on the
+// order of atomics.  3.5 us for 257 tokens, 6 for 16384: a launch, the ids, and 64
+// reads of LDS a thread.
 __global__ void __launch_bounds__(256) k_lora_order(LoraArgs a) {
     __shared__ __align__(16) uint32_t key[WINDOW];
     __shared__ int part[4][64];
@@ -157,6 +162,12 @@ struct Piece {
 // token m, and holds h of rows 4q.. of token m.  Rows of A past the rank are read
 // where there are any and change nothing but h of those rows, which the second
 // pass does not use.
+//
+// What bounds it: the way of x and A to the registers.  16384 tokens of 4096 inputs,
+// rank 64: 48 us, x alone (134 MB) takes 37-41 so, A alone (512 KB a workgroup, from the
+// caches) 22, the products with no loads 13.  Two groups of loads on their way, not one
+// (63 us); of few tokens it is waiting: 257 tokens of 4096 inputs, rank 32, 10 us, one
+// token of 2048 3 us.
 template <int XD, int NT, int RB>
 __global__ void __launch_bounds__(64 * DOWN_WAVES, 2) k_lora_down(LoraArgs a) {
     // products of 32 inputs loaded together: as many as leave room for two waves a SIMD
@@ -252,7 +263,8 @@ __global__ void __launch_bounds__(64 * DOWN_WAVES, 2) k_lora_down(LoraArgs a) {
     }
 }
 
-// The second pass takes a tile of tokens by 64 rows of B a step, in four products:
+// The second pass takes a tile of tokens by 64 rows of B a step, in four products (times
+// three planes of h):
 // lane (m, q) brings columns 8q.. of rows 4m.., a row a product, and of token m's h,
 // and holds outputs 4m.. of tokens 4q.., so that a load of the base or a store takes
 // 256 bytes of fp32 or 128 of bf16 in a row.
@@ -451,6 +463,12 @@ constexpr int up_resident(int tm, int rc) { return rc == 8 ? 1 : rc == 4 ? 2 : t
 // the four waves share theirs, each with 16 of the tokens, and B passes through LDS once
 // for all (16384 x 4096 x 4096 of rank 64: 121 us where two pairs of waves took steps of
 // their own and B from the caches; 4096 x 4096 x 4096 of rank 128 80 and 61).
+//
+// What bounds it: base, y and B.  16384 tokens of 4096 outputs, bf16, rank 64: 62 us,
+// 268 MB are 52 at a large copy's rate (92 us where a store took 64 bytes of a row, not
+// 128; loads and stores past the caches 99-108).  64 tokens of 131072 outputs, fp32, 16
+// adapters of rank 16: 37 us, 134 MB are 26; the base is loaded a step ahead, and at the
+// ends of a wave's steps there is nothing else to do.
 template <int YD, int TM, int RC, bool BASE>
 __global__ void __launch_bounds__(256, up_resident(TM, RC)) k_lora_up(LoraArgs a) {
     constexpr bool SHARED = TM == 64;
@@ -518,7 +536,8 @@ bool on_elements(const void* p, int dtype) {
 int tile_tokens(int T) { return T > MANY ? 64 : 16; }
 
 // Parts that the inputs are split in between workgroups: enough for one a CU where
-// every token has the same adapter, none shorter than 256 inputs.
+// every token has the same adapter, none shorter than 256 inputs.  Four at most and
+// none, us: 512 x 4096 x 4096 of rank 16 16.5 and 20.2, 8 x 4096 x 8192 12.4 and 19.4.
 int down_splits(int T, int K) {
     const int tm = tile_tokens(T), tiles = (T + tm - 1) / tm;
     int s = 256 / (tiles > 0 ? tiles : 1);
@@ -591,8 +610,9 @@ int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const v
     }
     const int tm = tile_tokens(T), tiles = (T + tm - 1) / tm;
     const int most = n < tm ? n : tm;  // adapters of a tile
-    // workgroups that share a tile's adapters; a tile of 16 has seldom more than 8 (257 tokens of 64 adapters: first pass
-    // 13.1 us by 16, 10.4 by 8, 11.1 by 4), one of 64 of a prompt one or two
+    // workgroups that share a tile's adapters.  A tile of 16 has seldom more than 8 (first pass, 257 tokens of 64 adapters:
+    // 13.1 us by 16, 10.4 by 8, 11.1 by 4; both passes, 40 tokens of 16: 13.9 by 8, 26.0 by one); one of 64 of a prompt
+    // has one or two (2048 tokens of 64 adapters in no order 53.7 us by 4, 68.9 by one; 16384 of 8 in a row 117 either way)
     const int spread = most < (tm == 16 ? 8 : 4) ? most : tm == 16 ? 8 : 4;
     if (x_dtype == MOE_X_F32) {
         if (tm == 16) launch_down<MOE_X_F32, 1>(g, tiles, spread, stream);
