@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
     unsigned long long todo = __ballot(lane < n && (!a.mask || a.mask[t0 + lane]));
 
     // The biases stay in registers, and the next token's logits are read while this one's are looked at, where registers
-    // are left: 16384 tokens of 2048 bf16 logits 59 us so and 70 without.
+    // are left: 16384 tokens of 2048 fp32 logits 59 us so and 70 without.
     constexpr bool KEEP = NE <= 32;
     float bias[HOW != PLAIN && KEEP ? NE : 1];
     const auto bias_at = [&](int j) { return j / VEC < own ? (a.bias ? a.bias[at(j)] : 0.0f) : -INFINITY; };
@@ -729,7 +729,7 @@ struct SelBwdArgs {
 //
 // What bounds it: the rows.  65537 tokens of 512 bf16 logits, dense: 31 us, 134 MB are
 // 26 at a large copy's rate (203 vector instructions a token); 16384 of 288 in fp32, the
-// picks alone: 9 us, 19 MB written, most of it the wait for the picks and their logits.
+// picks alone and another gradient added: 9 us, 38 MB are 7.
 template <int ZD, int VEC, int NE, bool DENSE>
 __global__ void __launch_bounds__(64 * SEL_WAVES) k_select_bwd(SelBwdArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select_bwd(SelBwdArgs a) {
             }
         }
     };
-    constexpr bool AHEAD = NE <= 32;  // the next token's rows while this one's are looked at (2048 bf16 logits: 45 us, 47 without)
+    constexpr bool AHEAD = NE <= 32;  // the next token's rows while this one's are looked at (16384 x 2048 fp32: 45 us, 47 without)
     float zn[DENSE ? NE : 1], an[NE];
     if (AHEAD) {
         if constexpr (DENSE) load(a.z, t0, zn, -INFINITY);
