@@ -538,15 +538,28 @@ int tile_tokens(int T) { return T > MANY ? 64 : 16; }
 // Parts that the inputs are split in between workgroups: enough for one a CU where
 // every token has the same adapter, none shorter than 256 inputs.  Four at most and
 // none, us: 512 x 4096 x 4096 of rank 16 16.5 and 20.2, 8 x 4096 x 8192 12.4 and 19.4.
+int most_splits(int K) {
+    const int s = K / 256;
+    return s < 1 ? 1 : s > MAX_SPLITS ? MAX_SPLITS : s;
+}
+
 int down_splits(int T, int K) {
-    const int tm = tile_tokens(T), tiles = (T + tm - 1) / tm;
-    int s = 256 / (tiles > 0 ? tiles : 1);
-    if (s > K / 256) s = K / 256;
-    if (s > MAX_SPLITS) s = MAX_SPLITS;
-    return s < 1 ? 1 : s;
+    const int tm = tile_tokens(T), tiles = (T + tm - 1) / tm, most = most_splits(K);
+    const int s = 256 / (tiles > 0 ? tiles : 1);
+    return s < 1 ? 1 : s > most ? most : s;
 }
 
 size_t h_bytes(int T, int K, int r) { return (size_t)down_splits(T, K) * (T > 0 ? T : 1) * r * 4; }
+
+// The most that up to T tokens need: s parts where they are at most 256 / s tiles.
+size_t h_bytes_to(int T, int K, int r) {
+    int64_t rows = 1;
+    for (int s = 1; s <= most_splits(K); ++s) {
+        const int64_t to = s == 1 ? T : 64 * (256 / s), n = (T < to ? T : to) * s;
+        if (n > rows) rows = n;
+    }
+    return (size_t)rows * r * 4;
+}
 
 template <int XD, int NT>
 void launch_down(const LoraArgs& g, int tiles, int spread, hipStream_t stream) {
@@ -576,7 +589,7 @@ extern "C" {
 
 size_t moe_lora_workspace_bytes(int T, int K, int r) {
     if (T < 0 || T > MOE_LINEAR_MAX_T || K < 8 || K > MOE_LINEAR_MAX_NK || r < 8 || r > MOE_LORA_MAX_R) return 0;
-    return h_bytes(T, K, r) + (T > WAVE_TOKENS ? (size_t)T * 4 : 0);
+    return h_bytes_to(T, K, r) + (T > WAVE_TOKENS ? (size_t)T * 4 : 0);
 }
 
 int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const void* b, const int32_t* ranks,

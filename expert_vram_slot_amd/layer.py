@@ -434,7 +434,7 @@ class Adapters:
     """A pool of low-rank adapters beside one product (moe_lora_add), a
     request's each: a: device bf16 [n][r][K], b: device bf16 [n][N][r], ranks:
     device int32 [n] or None, scale: device float32 [n] or None.  x_dtype and
-    y_dtype are the product's.
+    y_dtype are the product's.  Its calls share a workspace: one at a time.
     """
 
     def __init__(self, *, a, b, T_max, ranks=None, scale=None, x_dtype=MOE_X_BF16, y_dtype=MOE_X_F32):
@@ -460,6 +460,7 @@ class Adapters:
         ldx = _row_stride("x", x, T, self.K, X_TYPES[self.x_dtype], dev)
         ldy = _row_stride("y", y, T, self.N, X_TYPES[self.y_dtype], dev)
         _check_given("ids", ids, T, (torch.int32,), dev)
+        assert dev.type == "cuda", f"the adapters are on {dev}"
         with torch.cuda.device(dev):
             moe_lora_add(x, self.x_dtype, ldx, self.a, self.b, self.ranks, self.scale, ids, self.n, self.r, T, self.N,
                          self.K, y, ldy, y, self.y_dtype, ldy, self.ws, self.ws_bytes, torch.cuda.current_stream())
@@ -472,8 +473,9 @@ class DecodeHead:
 
     wq: device uint8 [V][H/2], scales: device fp16 [V][H/group] (the layout of
     moe_linear_q4); bias: device float [V] or None.  x_dtype is the stack's
-    activation format.  adapters: an Adapters of [V] outputs or None.  What a call brings has to be of the types given here
-    and on the head's device (AssertionError otherwise, before any launch).
+    activation format.  adapters: an Adapters of [V] outputs or None.  What a
+    call brings has to be of the types given here and on the head's device
+    (AssertionError otherwise, before any launch).
     """
 
     def __init__(self, *, H, V, wq, scales, group, T_max, x_dtype=MOE_X_BF16, bias=None, device="cuda",

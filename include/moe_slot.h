@@ -628,8 +628,9 @@ int moe_bias_balance(const int32_t* counts, const float* bias, int L, int E, flo
  *   y      device [T][ldy] in y_dtype out; may be base (ldb = ldy then), must
  *          not overlap the inputs otherwise.  Columns from N to ldy are left as
  *          they are
- *   ws     device workspace of >= moe_lora_workspace_bytes(T, K, r) bytes;
- *          need not be cleared; calls that may overlap need one each
+ *   ws     device workspace of >= moe_lora_workspace_bytes(T, K, r) bytes
+ *          (enough for fewer tokens, too); need not be cleared; calls that
+ *          may overlap need one each
  * Both products are summed in fp32; A x keeps its 24 bits (below 2^-100 in
  * magnitude the last of them are lost, as those of fp32 x), y is rounded once.
  * An infinity or a NaN of a token or an adapter makes outputs of that token or

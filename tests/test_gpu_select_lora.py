@@ -687,6 +687,27 @@ def test_lora_prompts(m, T, N, K, n, r):
 # ------------------------------------------- together, streams and graphs
 
 
+def test_adapters_take_fewer_tokens_than_they_were_made_for(m):
+    """The most tokens at once are not those that need the largest workspace: 4160 are split in fewer parts than 4096."""
+    from expert_vram_slot_amd.layer import Adapters
+    g = gen(41)
+    N, K, n, r = 24, 1024, 3, 16
+    a = torch.randn(n, r, K, device="cuda", generator=g).bfloat16()
+    b = torch.randn(n, N, r, device="cuda", generator=g).bfloat16()
+    pool = Adapters(a=a, b=b, T_max=4160)
+    for T in (4160, 4096, 1025, 1024, 65, 1):
+        x = torch.randn(T, K, device="cuda", generator=g).bfloat16()
+        ids = torch.randint(-1, n, (T,), device="cuda", generator=g, dtype=torch.int32)
+        base = torch.randn(T, N, device="cuda", generator=g)
+        y = pool.add(x, T, ids, base.clone())
+        h = torch.einsum("tk,trk->tr", x.double(), a.double()[ids.clamp(min=0).long()])
+        size = torch.einsum("tk,trk->tr", x.double().abs(), a.double()[ids.clamp(min=0).long()].abs())
+        bb = b.double()[ids.clamp(min=0).long()] * (ids >= 0)[:, None, None]
+        want = base.double() + torch.einsum("tr,tnr->tn", h, bb)
+        bound = (K + r + 8) * 2.0 ** -23 * (base.double().abs() + torch.einsum("tr,tnr->tn", size, bb.abs()))
+        assert torch.all((y.double() - want).abs() <= bound)
+
+
 def test_a_decode_step_of_many_tenants(m):
     """Two 4-bit layers under a selection rule, the head with each request's adapter, a draw; then the router's training
     step: counts, bias and the gradient of both losses.  Each against its reference on what it was given."""

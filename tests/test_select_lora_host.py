@@ -135,6 +135,14 @@ def test_lora_of_no_tokens_and_workspace(mlib):
         assert mlib.moe_lora_workspace_bytes(*bad) == 0
 
 
+@pytest.mark.parametrize("K", [8, 256, 520, 1000, 1024, 8192])
+def test_a_workspace_is_enough_for_fewer_tokens(mlib, K):
+    """A caller makes it once, for the most tokens."""
+    sizes = [mlib.moe_lora_workspace_bytes(T, K, 24) for T in [*range(0, 200), *range(1000, 18000, 8), 1 << 17, 1 << 20]]
+    assert all(x <= y for x, y in zip(sizes, sizes[1:]))
+
+
+
 def test_binding_raises_with_the_reason(mlib):
     with pytest.raises(mlib.MoeError) as e:
         mlib.moe_route_select(16, 0, None, None, None, 1, 10, 2, mlib.select_rule(groups=4), 16, 16, stream=0)
@@ -387,3 +395,9 @@ def test_reference_lora_by_loops():
                     for i in range(K):
                         want += scale[ids[t]] * b[ids[t], o, j] * a[ids[t], j, i] * x[t, i]
             assert y[t, o] == pytest.approx(want) and abs(y[t, o]) <= size[t, o] + 1e-12
+
+
+def test_adapters_off_the_gpu_refuse_to_add(mlib):
+    torch = pytest.importorskip("torch")
+    with pytest.raises(AssertionError, match="on cpu"):
+        _pool().add(torch.zeros(2, 64, dtype=torch.bfloat16), 2, torch.zeros(2, dtype=torch.int32), torch.zeros(2, 8))
