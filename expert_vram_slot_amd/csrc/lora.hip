@@ -407,13 +407,16 @@ __device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[RC][
 #pragma unroll
         for (int h = 0; h < 4; ++h) acc[h] = v4f{zero, zero, zero, zero};
     };
-    const auto multiply = [&](v4f (&acc)[4]) {
+    // sums of a step; the next one's rows are on their way as soon as this one's are out of their registers
+    const auto multiply = [&](v4f (&acc)[4], int next) {
         if constexpr (SHARED) {
             rows.share(rank, *shared);
+            rows.fetch(a, d, next);
             if (used(0)) rows.multiply(*shared, hs, own, acc);
         } else {
             rows.cut(rank);
             rows.multiply(hs, own, acc);
+            rows.fetch(a, d, next);
         }
     };
     if (rank) rows.fetch(a, d, first);
@@ -425,11 +428,10 @@ __device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[RC][
         for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(tok[i]));
         v4f acc[4];
         start(acc);
-        if (rank) multiply(acc);
+        if (rank) multiply(acc, min(step + 1, last - 1));
         typename O::Piece b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) b[i] = base[i];
-        if (rank) rows.fetch(a, d, min(step + 1, last - 1));
         fetch_base(min(step + 1, whole - 1));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -440,7 +442,7 @@ __device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[RC][
     // the last rows, fewer than STEP
     v4f acc[4];
     start(acc);
-    if (rank) multiply(acc);
+    if (rank) multiply(acc, last - 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (4 * i + q >= cnt) continue;
