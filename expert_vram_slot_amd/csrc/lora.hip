@@ -455,7 +455,7 @@ __device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[RC][
 }
 
 // Waves a SIMD: as many as LDS (64) and registers (16) have room for.  Tiles of 64 by
-// four, three and two, us: 16384 x 4096 x 4096 of rank 64 112, 112 and 124, of rank 16
+// four, three and two, us: 16384 x 4096 x 4096 of rank 64 112, 112 and 124 (now 109 by four), of rank 16
 // 97, 99 and 117.
 constexpr int up_resident(int tm, int rc) { return rc == 8 ? 1 : rc == 4 ? 2 : tm == 64 ? 4 : rc == 1 ? 3 : 2; }
 
@@ -466,7 +466,7 @@ constexpr int up_resident(int tm, int rc) { return rc == 8 ? 1 : rc == 4 ? 2 : t
 // for all (16384 x 4096 x 4096 of rank 64: 121 us where two pairs of waves took steps of
 // their own and B from the caches; 4096 x 4096 x 4096 of rank 128 80 and 61).
 //
-// What bounds it: base, y and B.  16384 tokens of 4096 outputs, bf16, rank 64: 62 us,
+// What bounds it: base, y and B.  16384 tokens of 4096 outputs, bf16, rank 64: 61 us,
 // 268 MB are 52 at a large copy's rate (92 us where a store took 64 bytes of a row, not
 // 128; loads and stores past the caches 99-108).  64 tokens of 131072 outputs, fp32, 16
 // adapters of rank 16: 37 us, 134 MB are 26; the base is loaded a step ahead, and at the
