@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(64 * DOWN_WAVES, 2) k_lora_down(LoraArgs a) {
     __shared__ int s_tok[16 * NT], s_ad[16 * NT];
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, m = lane & 15, q = lane >> 4;
     // workgroups go to the eight dies in turn: those of a tile, with other rows of A, go to one, where its inputs then are
+    // (257 x 8192 x 4096 of rank 64 23 us so, 27 in the tiles' own order)
     const int parts = a.splits * ((a.r + RANKS - 1) / RANKS), part = (blockIdx.x >> 3) % parts;
     const int at_tile = (blockIdx.x >> 3) / parts * 8 + (blockIdx.x & 7), split = part % a.splits, row0 = part / a.splits * RANKS;
     if ((int64_t)at_tile * 16 * NT >= a.T) return;
