@@ -197,7 +197,7 @@ __host__ __device__ __forceinline__ int lanes_per_group(int G) {
     return per;
 }
 
-// 1 / the sum of a softmax, in double, and the largest logit.
+// The sum of a softmax, in double, and the largest logit.
 template <int ZD>
 __device__ __forceinline__ double softmax64(const SelArgs& a, int64_t t, float& m) {
     const int lane = threadIdx.x & 63;
@@ -209,7 +209,7 @@ __device__ __forceinline__ double softmax64(const SelArgs& a, int64_t t, float& 
         const float z = load_z<ZD>(a.z, t * a.E + e);
         sum += z > -INFINITY ? soft64(z, m) : 0.0;
     }
-    return rcp64(moe::wave_all_sum(sum));
+    return moe::wave_all_sum(sum);
 }
 
 // A token's choices in double, an expert at a time.
@@ -220,7 +220,7 @@ struct Choice64 {
     float m = 0.0f;
     double r = 1.0;
     __device__ __forceinline__ Choice64(const SelArgs& args, int64_t t) : a(args), row(t * args.E) {
-        if (a.rule.score == MOE_SCORE_SOFTMAX) r = softmax64<ZD>(a, t, m);
+        if (a.rule.score == MOE_SCORE_SOFTMAX) r = rcp64(softmax64<ZD>(a, t, m));
     }
     __device__ __forceinline__ double operator()(int e, float& z) const {
         z = load_z<ZD>(a.z, row + e);
@@ -415,6 +415,11 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
             if (KEEP && todo) load(t0 + __builtin_ctzll(todo));
             if (HOW == GROUPED && NE == 64 && gs > NE * per) {  // more than registers
                 slow |= 1u << i;
+                if (sums && !a.rule.renorm) {  // choose64 makes a sum of its own for the picks; the weights take this one
+                    float m;
+                    const double s = softmax64<ZD>(a, t, m);
+                    if (mine == i) my_m = m, my_sum = (float)s;
+                }
                 continue;
             }
             float key[NE], m = 0.0f, sum = 1.0f;
@@ -672,7 +677,7 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
                 while (near) {
                     const int i = __builtin_ctzll(near) / seg;
                     float m;
-                    const double s = softmax64<ZD>(a, t0 + i, m);
+                    const double s = rcp64(softmax64<ZD>(a, t0 + i, m));
                     if (mine == i) share = s, top = m;
                     near &= ~__ballot(mine == i);
                 }

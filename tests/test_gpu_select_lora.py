@@ -883,3 +883,40 @@ def test_two_streams_with_workspaces_of_their_own(m):
     for (_, _, outputs), w in zip(paths, want):
         for a, b in zip(w, outputs):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------- groups larger than a wave's registers
+
+
+LARGE_GROUPS = [  # T, E, k, groups, kept, top: more than 64 experts a lane, and 64
+    (5, 2145, 8, 33, 5, 2), (9, 4095, 8, 3, 2, 2), (7, 4000, 10, 10, 4, 1), (3, 2565, 3, 5, 5, 2), (4, 2210, 32, 34, 20, 1),
+    (2, 4080, 17, 48, 1, 2), (5, 2112, 8, 33, 5, 2)]
+
+
+@pytest.mark.parametrize("zt", ["f32", "bf16"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("rule", RULES, ids=lambda r: f"{r['score']}{'' if r.get('renorm', True) else '_raw'}")
+@pytest.mark.parametrize("T,E,k,groups,kept,top", LARGE_GROUPS)
+def test_select_large_groups(m, T, E, k, groups, kept, top, rule, with_bias, zt):
+    """Ordinary logits, far ones (700 and more is beyond what exp takes without the maximum off), nothing open, padding."""
+    rule = dict(rule, groups=groups, groups_kept=kept, group_top=top)
+    g = gen(E + k)
+    z = torch.cat([logits(T, E, T * E + k), 4.0 * logits(2, E, 1) + 800.0, logits(1, E, 2) - 900.0, special_rows(E, g)]).to(DT[zt])
+    bias = 0.001 * torch.randint(-80, 81, (E,), device="cuda", generator=g).float() if with_bias else None
+    ids, _ = check_select(m, z, k, rule, bias)
+    check_grad(m, z, ids, torch.randn(*ids.shape, device="cuda", generator=g), rule)
+    check_select(m, z, k, rule, bias, (torch.arange(len(z), device="cuda") % 3 != 1).to(torch.uint8))
+
+
+@pytest.mark.parametrize("rule", RULES, ids=lambda r: f"{r['score']}{'' if r.get('renorm', True) else '_raw'}")
+@pytest.mark.parametrize("E,k,groups", [(2145, 8, 33), (4095, 20, 3)])
+def test_select_large_groups_of_many_tokens(m, E, k, groups, rule):
+    """A wave takes several tokens: each gets its own sum and picks.  Tokens are copies of some, which are checked."""
+    rule = dict(rule, groups=groups, groups_kept=2, group_top=2)
+    g = gen(E)
+    some = logits(37, E, 5)
+    at = torch.randint(0, 37, (16500,), device="cuda", generator=g)
+    bias = 0.001 * torch.randint(-80, 81, (E,), device="cuda", generator=g).float()
+    want_ids, want_w = check_select(m, some, k, rule, bias)
+    ids, w = run_select(m, some[at], k, rule, bias)
+    assert torch.equal(ids, want_ids[at]) and torch.equal(w, want_w[at])
