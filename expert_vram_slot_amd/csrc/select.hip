@@ -144,16 +144,19 @@ __device__ __forceinline__ SelLds sel_parts(unsigned char* p) {
 }
 
 // Which lanes hold experts of a kept group: every one of the `per` lanes of a group
-// has that group's value.  unsure: values are off by up to err, and that may matter.
+// has that group's value.  some: the group has an open expert (two of the lowest biases
+// add up to an fp32 -inf all the same; err is inf then).  unsure: values are off by up to
+// err, and that may matter.
 template <typename T>
-__device__ __forceinline__ unsigned long long keep_groups(T value, T err, int G, int kept, int per, T* sorted, bool& unsure) {
+__device__ __forceinline__ unsigned long long keep_groups(T value, bool some, T err, int G, int kept, int per, T* sorted,
+                                                          bool& unsure) {
     const int lane = threadIdx.x & 63, g = lane / per;
     int rank = 0;
     for (int o = 0; o < G; ++o) {
         const T v = lane_of(value, o * per);
         rank += v > value || (v == value && o < g);
     }
-    const bool open = g < G && value > (T)-INFINITY;
+    const bool open = g < G && some;
     unsure = false;
     if (err > 0 && kept < G) {
         if (g < G) sorted[rank] = value;
@@ -174,9 +177,10 @@ __device__ __forceinline__ void top2(T v, T& best, T& second) {
 }
 
 // A group's value from the two largest choices of each of its lanes (per: a power
-// of two, neighbours).  size: the magnitudes of what was added.
+// of two, neighbours), of which best and second become the group's.  size: the
+// magnitudes of what was added.
 template <typename T>
-__device__ __forceinline__ T group_value(T best, T second, int per, int top, T& size) {
+__device__ __forceinline__ T group_value(T& best, T& second, int per, int top, T& size) {
     const auto join = [&](T b, T c) {
         top2(b, best, second);
         top2(c, best, second);
@@ -242,7 +246,7 @@ __device__ __forceinline__ unsigned long long groups64(const SelArgs& a, const C
 #pragma unroll 1
         for (int i = lane % per; i < gs; i += per) top2(choice(g * gs + i, z), best, second);
     const double value = group_value<double>(best, second, per, a.rule.group_top, size);
-    return keep_groups<double>(value, 0.0, G, a.rule.groups_kept, per, sorted, unsure);
+    return keep_groups<double>(value, best > -INFINITY, 0.0, G, a.rule.groups_kept, per, sorted, unsure);
 }
 
 // A token's picks, round by round, each the best behind the one before: where more
@@ -484,7 +488,8 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
                 const float value = group_value<float>(best, second, per, a.rule.group_top, size);
                 // a choice is off by the slack and a rounding, a sum of two by a rounding more
                 bool unsure;
-                in_kept = keep_groups<float>(value, 2.0f * slack + size * 0x1p-22f, G, a.rule.groups_kept, per, l.ordz, unsure);
+                in_kept = keep_groups<float>(value, best > -INFINITY, 2.0f * slack + size * 0x1p-22f, G, a.rule.groups_kept, per,
+                                             l.ordz, unsure);
                 if (exact) {
                     in_kept = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)l.kept[2 * i]) |
                               ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)l.kept[2 * i + 1]) << 32);

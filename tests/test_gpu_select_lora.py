@@ -920,3 +920,25 @@ def test_select_large_groups_of_many_tokens(m, E, k, groups, rule):
     want_ids, want_w = check_select(m, some, k, rule, bias)
     ids, w = run_select(m, some[at], k, rule, bias)
     assert torch.equal(ids, want_ids[at]) and torch.equal(w, want_w[at])
+
+
+@pytest.mark.parametrize("zt", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,kept", [(8, 8, 4, 4), (8, 3, 4, 3), (96, 6, 3, 2), (288, 8, 8, 4), (288, 32, 8, 8), (2145, 8, 33, 30)])
+def test_select_groups_of_lowest_biases(m, E, k, groups, kept, score, zt):
+    """Two biases of the type's lowest value add up to more than fp32 holds; their group is open all the same, and stands
+    behind the others, before those with nothing open."""
+    g, gs, low = gen(E + k), E // groups, torch.finfo(torch.float32).min
+    z = logits(6, E, E, zt)
+    z[5] = 0
+    for group_top in (1, 2):
+        rule = dict(score=score, groups=groups, groups_kept=kept, group_top=group_top)
+        for masked in ([0], [0, groups - 1], range(groups), range(1, groups), range(groups - 1)):
+            for value in (low, -2e38, -low):
+                bias = 0.001 * torch.randint(-80, 81, (E,), device="cuda", generator=g).float()
+                for i in masked:
+                    bias[i * gs:(i + 1) * gs] = value
+                check_select(m, z, k, rule, bias)
+                bias[gs:2 * gs] = -float("inf")  # one group is closed
+                bias[gs * (groups - 1)] = low    # and one has a single expert as low as this
+                check_select(m, z, k, rule, bias)
