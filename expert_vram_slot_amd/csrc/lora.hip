@@ -404,7 +404,7 @@ __device__ __forceinline__ void up_steps(const LoraArgs& a, const v4u (&hs)[RC][
                 if (used(i)) base[i] = O::get(a.base, tok[i] * a.ldb + (STEP * step + 4 * m));
     };
     const auto start = [&](v4f (&acc)[4]) {
-        const float zero = rank ? 0.0f : -0.0f;  // of base plus -0 the bits are base's
+        const float zero = rank || !BASE ? 0.0f : -0.0f;  // of base plus -0 the bits are base's
 #pragma unroll
         for (int h = 0; h < 4; ++h) acc[h] = v4f{zero, zero, zero, zero};
     };

@@ -942,3 +942,15 @@ def test_select_groups_of_lowest_biases(m, E, k, groups, kept, score, zt):
                 bias[gs:2 * gs] = -float("inf")  # one group is closed
                 bias[gs * (groups - 1)] = low    # and one has a single expert as low as this
                 check_select(m, z, k, rule, bias)
+
+
+@pytest.mark.parametrize("T", [1, 70, 1200])
+@pytest.mark.parametrize("yt", ["f32", "bf16"])
+def test_lora_without_base_or_adapter_is_zero(m, T, yt):
+    """No base is a base of zeros, of a positive sign in every column."""
+    a, b = pool(2, 16, 64, 200, gen(1))
+    ids = (torch.arange(T, device="cuda") % 3 - 1).to(torch.int32)
+    ranks = torch.tensor([16, 0], dtype=torch.int32, device="cuda")
+    got = run_lora(m, torch.randn(T, 64, device="cuda").bfloat16(), a, b, ids, ranks, None, None, yt)
+    without = got[ids != 0].contiguous()
+    assert not torch.any(without.view(torch.int32 if yt == "f32" else torch.int16))
