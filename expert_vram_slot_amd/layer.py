@@ -67,6 +67,9 @@ class SlotLayer:
     which moe_route_select then takes the picks and weights (bias goes on the
     scores); None: moe_route's rule."""
 
+    bound = 0                                # the layer of a SlotStack whose weights and bias are bound
+    step_layer, balanced_layer = None, None  # the layers of the last step, and of the counts of the last balance()
+
     def __init__(self, *, E, k, H, I, S, w_type, T_max, policy, host_store, slot_store, G, bias=None,
                  n_threads=None, device="cuda", select=None):
         dev = torch.device(device)
@@ -163,7 +166,7 @@ class SlotLayer:
             moe_route_logits(x, self.x_dtype, self.G, T, self.H, self.E, self.logits, cur)
             moe_route_select(self.logits, MOE_X_F32, self.bias, mask, given, T, self.E, self.k, self.select, self.ids,
                              self.w, cur)
-        self.steps, self.step_T = self.steps + 1, T
+        self.steps, self.step_T, self.step_layer = self.steps + 1, T, self.bound
         self.captured |= torch.cuda.is_current_stream_capturing()
         ids = self.ids
         # 2. cache step: victims, miss list, remap
@@ -232,7 +235,7 @@ class SlotLayer:
             moe_balance_loss(self.logits, MOE_X_F32, self.ids, mask, T, self.E, self.k, o["counts"], o["totals"],
                              o["share"], o["lse"], o["loss"], o["ws"], o["ws_bytes"], torch.cuda.current_stream())
             self.captured |= torch.cuda.is_current_stream_capturing()
-        self.balanced = (self.steps, T)
+        self.balanced, self.balanced_layer = (self.steps, T), self.step_layer
         return dict(counts=o["counts"], totals=o["totals"], share=o["share"], lse=o["lse"][:T], loss=o["loss"])
 
     def balance_grad(self, T, dloss, mask=None):
@@ -272,10 +275,16 @@ class SlotLayer:
 
     def balance_bias(self, rate):
         """One step of the layer's bias, in place, by the last balance()'s counts
-        (moe_bias_balance): experts picked less than the mean move up by rate."""
+        (moe_bias_balance): experts picked less than the mean move up by rate.
+        The counts have to be the last step's, and of a SlotStack's layers those
+        of the one whose bias is bound: there, balance() and this go into
+        on_layer."""
         o = self.stats_out
         assert self.bias is not None and o is not None, "a bias and a balance() come first"
         _check_given("bias", self.bias, self.E, (torch.float32,), self.ids.device)
+        assert self.captured or (self.balanced is not None and self.balanced[0] == self.steps), "balance() of the last step comes first"
+        assert self.captured or self.balanced_layer == self.bound, \
+            f"the counts are layer {self.balanced_layer}'s, the bias is layer {self.bound}'s"
         with torch.cuda.device(self.ids.device):
             moe_bias_balance(o["counts"], self.bias, 1, self.E, rate, self.bias, torch.cuda.current_stream())
 
@@ -316,7 +325,7 @@ class SlotStack:
         """Point the shared step machinery at layer l."""
         L, spec = self.layer, self.layers[l]
         L.host_store, L.slot_store, L.G, L.bias = spec["host_store"], spec["slot_store"], spec["G"], spec.get("bias")
-        L.st = self.states[l][0]
+        L.st, L.bound = self.states[l][0], l
         return L
 
     def step(self, x, T, host_pass=True, trace=None, on_layer=None, ffn_events=None):

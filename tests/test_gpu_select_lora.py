@@ -954,3 +954,30 @@ def test_lora_without_base_or_adapter_is_zero(m, T, yt):
     got = run_lora(m, torch.randn(T, 64, device="cuda").bfloat16(), a, b, ids, ranks, None, None, yt)
     without = got[ids != 0].contiguous()
     assert not torch.any(without.view(torch.int32 if yt == "f32" else torch.int16))
+
+
+def test_a_stack_keeps_its_layers_counts_apart(m):
+    """A bias moves by its own layer's counts of the last step, or not at all."""
+    import synth
+    from expert_vram_slot_amd.layer import SlotStack
+    E, k, H, I, T = 16, 4, 256, 128, 5
+    base = synth.config_seed("c4")
+    layers = []
+    for n in range(2):
+        store = synth.slabs(synth.W_Q4B32, base, n, 0, E, H, I, 0.05)
+        pinned = torch.empty(store.shape, dtype=torch.uint8, pin_memory=True)
+        pinned.copy_(torch.from_numpy(store))
+        G = synth.normal(synth.key(base, synth.TAG_G, n, 0), (E, H), 0.5, synth.X_BF16)
+        layers.append(dict(host_store=pinned, slot_store=torch.from_numpy(store).cuda(), bias=torch.zeros(E, device="cuda"),
+                           G=torch.from_numpy(G.view(np.int16)).cuda(), resident=torch.arange(E, dtype=torch.int32, device="cuda")))
+    stack = SlotStack(E=E, k=k, H=H, I=I, S=E, w_type=synth.W_Q4B32, T_max=8, layers=layers, n_threads=1, select=m.select_rule())
+    x = torch.randn(T, H, device="cuda", generator=gen(6)).bfloat16()
+    stack.step(x, T, host_pass=False, on_layer=lambda l, L, x_l, y_l: L.balance(T) if l == 0 else None)
+    with pytest.raises(AssertionError, match="last step"):  # layer 1's step came behind the counts
+        stack.layer.balance_bias(0.01)
+    counts = stack.layer.balance(T)["counts"].cpu().numpy()
+    with pytest.raises(AssertionError, match="layer 1's, the bias is layer 0's"):
+        stack.bind(0).balance_bias(0.01)
+    stack.bind(1).balance_bias(0.01)
+    assert not torch.any(layers[0]["bias"])
+    np.testing.assert_array_equal(layers[1]["bias"].cpu().numpy(), ref.bias_balance(counts[None], np.zeros((1, E), np.float32), 0.01)[0])

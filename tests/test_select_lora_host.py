@@ -401,3 +401,59 @@ def test_adapters_off_the_gpu_refuse_to_add(mlib):
     torch = pytest.importorskip("torch")
     with pytest.raises(AssertionError, match="on cpu"):
         _pool().add(torch.zeros(2, 64, dtype=torch.bfloat16), 2, torch.zeros(2, dtype=torch.int32), torch.zeros(2, 8))
+
+
+class _Launched(Exception):
+    pass
+
+
+def _balanced(mlib, monkeypatch):
+    """A layer behind a step and its balance(), on the CPU; the launch itself says that it was reached."""
+    import contextlib
+
+    import torch
+
+    from expert_vram_slot_amd import layer as layer_py
+
+    def launch(*a):
+        raise _Launched
+    monkeypatch.setattr(layer_py, "moe_bias_balance", launch)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: 0)
+    L = _layer_after_a_step(2, mlib)
+    L.stats_out = dict(counts=torch.zeros(8, dtype=torch.int32))
+    L.step_layer = L.bound
+    L.balanced, L.balanced_layer = (L.steps, 2), L.step_layer
+    return L
+
+
+def test_layer_balance_bias_takes_the_last_steps_counts_alone(mlib, monkeypatch):
+    pytest.importorskip("torch")
+    L = _balanced(mlib, monkeypatch)
+    with pytest.raises(_Launched):
+        L.balance_bias(0.001)
+    L.steps += 1  # another step, whose counts nobody took
+    with pytest.raises(AssertionError, match="last step"):
+        L.balance_bias(0.001)
+    L.captured = True  # replayed steps are not counted
+    with pytest.raises(_Launched):
+        L.balance_bias(0.001)
+
+
+def test_stack_moves_no_bias_by_another_layers_counts(mlib, monkeypatch):
+    """Layers of a SlotStack share one SlotLayer: bound anew, its counts are still the last layer's."""
+    torch = pytest.importorskip("torch")
+    from expert_vram_slot_amd.layer import SlotStack
+    stack = SlotStack.__new__(SlotStack)
+    stack.layer = L = _balanced(mlib, monkeypatch)
+    spec = dict(host_store=None, slot_store=None, G=None)
+    stack.layers = [dict(spec, bias=torch.zeros(8)) for _ in range(3)]
+    stack.states = [(None,)] * 3
+    for l in (0, 2, 0):
+        stack.bind(l)
+        if l == 0:
+            with pytest.raises(_Launched):
+                L.balance_bias(0.001)
+        else:
+            with pytest.raises(AssertionError, match="layer 0's, the bias is layer 2's"):
+                L.balance_bias(0.001)
