@@ -222,9 +222,9 @@ struct Choice64 {
     const SelArgs& a;
     int64_t row;
     float m = 0.0f;
-    double r = 1.0;
+    double sum = 1.0, r = 1.0;
     __device__ __forceinline__ Choice64(const SelArgs& args, int64_t t) : a(args), row(t * args.E) {
-        if (a.rule.score == MOE_SCORE_SOFTMAX) r = rcp64(softmax64<ZD>(a, t, m));
+        if (a.rule.score == MOE_SCORE_SOFTMAX) sum = softmax64<ZD>(a, t, m), r = rcp64(sum);
     }
     __device__ __forceinline__ double operator()(int e, float& z) const {
         z = load_z<ZD>(a.z, row + e);
@@ -251,12 +251,14 @@ __device__ __forceinline__ unsigned long long groups64(const SelArgs& a, const C
 
 // A token's picks, round by round, each the best behind the one before: where more
 // candidates than lanes are nearly equal, or a group is larger than the registers.
-// Picks go to places `to` and up.
+// Picks go to places `to` and up.  m, sum: the softmax's largest logit and its sum, for
+// the weights.
 template <int ZD>
-__device__ __forceinline__ void choose64(const SelArgs& a, int64_t t, const SelLds& l, int to) {
+__device__ __forceinline__ void choose64(const SelArgs& a, int64_t t, const SelLds& l, int to, float& m, float& sum) {
     const int lane = threadIdx.x & 63, E = a.E, G = a.rule.groups, gs = E / G, per = lanes_per_group(G);
     const int first = lane / per * gs + lane % per, end = lane / per < G ? (lane / per + 1) * gs : 0;
     const Choice64<ZD> choice(a, t);
+    m = choice.m, sum = (float)choice.sum;
     const bool kept = G == 1 || (groups64<ZD>(a, choice, l.ord) >> lane) & 1;
     double pc = INFINITY;
     float pz = INFINITY;
@@ -419,11 +421,6 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
             if (KEEP && todo) load(t0 + __builtin_ctzll(todo));
             if (HOW == GROUPED && NE == 64 && gs > NE * per) {  // more than registers
                 slow |= 1u << i;
-                if (sums && !a.rule.renorm) {  // choose64 makes a sum of its own for the picks; the weights take this one
-                    float m;
-                    const double s = softmax64<ZD>(a, t, m);
-                    if (mine == i) my_m = m, my_sum = (float)s;
-                }
                 continue;
             }
             float key[NE], m = 0.0f, sum = 1.0f;
@@ -693,7 +690,9 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
         wave_sync();
         for (; slow && HOW != PLAIN; slow &= slow - 1) {
             const int i = __builtin_ctz(slow);
-            choose64<ZD>(a, t0 + i, l, i * seg);
+            float m, sum;
+            choose64<ZD>(a, t0 + i, l, i * seg, m, sum);
+            if (mine == i) my_m = m, my_sum = sum;
         }
     }
     // the weights
