@@ -669,11 +669,13 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
                 }
                 if (exact) break;
                 // the sum of the softmax is an fp32 one: where neighbours are so close that it may have put them the wrong
-                // way round, one in double
+                // way round, one in double.  Equal logits have equal scores, and their order stands; behind the last pick's
+                // equals the next neighbour counts
                 wave_sync();
                 if (live) l.ord[mine * seg + rank] = c, l.ordz[mine * seg + rank] = zc, l.candz[mine * seg + rank] = (float)p * share_error(E);
                 wave_sync();
-                unsigned long long near = __ballot(r < k && r + 1 < my_c && l.ordz[lane] != l.ordz[lane + 1] &&
+                const bool counts = r < k || l.ordz[lane] == l.ordz[mine * seg + k - 1];  // picks, and the last one's equals
+                unsigned long long near = __ballot(counts && r + 1 < my_c && l.ordz[lane] != l.ordz[lane + 1] &&
                                                    l.ord[lane] - l.ord[lane + 1] <= (double)(l.candz[lane] + l.candz[(lane + 1) & 63]));
                 if (!near) break;
                 while (near) {

@@ -981,3 +981,25 @@ def test_a_stack_keeps_its_layers_counts_apart(m):
     stack.bind(1).balance_bias(0.01)
     assert not torch.any(layers[0]["bias"])
     np.testing.assert_array_equal(layers[1]["bias"].cpu().numpy(), ref.bias_balance(counts[None], np.zeros((1, E), np.float32), 0.01)[0])
+
+
+@pytest.mark.parametrize("zt", ["f32", "bf16"])
+@pytest.mark.parametrize("E,groups", [(8, 1), (8, 4), (64, 1), (288, 1), (288, 8), (512, 16)])
+def test_select_border_among_equals_near_others(m, E, groups, zt):
+    """The last pick lies among experts of one logit and one choice, and others, less than the fp32 sum's error away, on
+    either side of them: whether a sum in double is needed is not decided by the equals alone."""
+    g, borders = gen(E + groups), 0
+    for equals in (torch.finfo(torch.float32).min, -60.0, 0.25, 2.0):
+        for turn in range(6):
+            z = logits(1, E, 7 * E + turn, zt)
+            order = torch.randperm(E, device="cuda", generator=g).cpu().numpy()
+            same, others = order[:min(E // 2, 8)], order[min(E // 2, 8):min(E, 24)]
+            z[0, torch.from_numpy(same).cuda()] = equals
+            s = ref.scores(host64(z), "softmax")[0]
+            bias = np.full(E, -2.0, np.float32)  # the rest are far behind
+            bias[same], bias[others] = (0.5 - s[same]).astype(np.float32), (0.5 - s[others]).astype(np.float32)
+            ahead = int((s[others] + bias[others] > s[same[0]] + np.float64(bias[same[0]])).sum())
+            for k in sorted({1, ahead + 1, ahead + len(same) // 2}):
+                borders += len(others) > ahead
+                check_select(m, z, k, dict(score="softmax", groups=groups, renorm=turn % 2 == 0), torch.from_numpy(bias).cuda())
+    assert borders > 20
