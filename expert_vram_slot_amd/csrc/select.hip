@@ -668,15 +668,16 @@ __global__ void __launch_bounds__(64 * SEL_WAVES) k_select(SelArgs a) {
                     }
                 }
                 if (exact) break;
-                // the sum of the softmax is an fp32 one: where neighbours are so close that it may have put them the wrong
-                // way round, one in double.  Equal logits have equal scores, and their order stands; behind the last pick's
-                // equals the next neighbour counts
+                // the sum of the softmax is an fp32 one: where two are so close that it may have put them the wrong way round,
+                // one in double.  Each pick against the next (what holds for neighbours adds up for others), and the last one
+                // against every candidate behind it: of these a near one may stand behind others that are far enough.  Equal
+                // logits have equal scores, and their order stands
                 wave_sync();
                 if (live) l.ord[mine * seg + rank] = c, l.ordz[mine * seg + rank] = zc, l.candz[mine * seg + rank] = (float)p * share_error(E);
                 wave_sync();
-                const bool counts = r < k || l.ordz[lane] == l.ordz[mine * seg + k - 1];  // picks, and the last one's equals
-                unsigned long long near = __ballot(counts && r + 1 < my_c && l.ordz[lane] != l.ordz[lane + 1] &&
-                                                   l.ord[lane] - l.ord[lane + 1] <= (double)(l.candz[lane] + l.candz[(lane + 1) & 63]));
+                const int o = r < k - 1 ? lane + 1 : mine * seg + k - 1;
+                unsigned long long near = __ballot(r != k - 1 && (r < k - 1 ? r + 1 : r) < my_c && l.ordz[lane] != l.ordz[o] &&
+                                                   fabs(l.ord[lane] - l.ord[o]) <= (double)(l.candz[lane] + l.candz[o]));
                 if (!near) break;
                 while (near) {
                     const int i = __builtin_ctzll(near) / seg;

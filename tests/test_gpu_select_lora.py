@@ -1003,3 +1003,25 @@ def test_select_border_among_equals_near_others(m, E, groups, zt):
                 borders += len(others) > ahead
                 check_select(m, z, k, dict(score="softmax", groups=groups, renorm=turn % 2 == 0), torch.from_numpy(bias).cuda())
     assert borders > 20
+
+
+@pytest.mark.parametrize("zt", ["f32", "bf16"])
+@pytest.mark.parametrize("E,groups", [(8, 1), (8, 4), (64, 1), (288, 1), (288, 8), (512, 16)])
+def test_select_border_before_experts_of_large_scores(m, E, groups, zt):
+    """Experts of small scores, that a sum's error hardly moves, stand at the border next to one another; behind them, by
+    places, but within that error, stand some of large scores."""
+    g, behind = gen(E + groups), 0
+    for turn in range(40):
+        z = logits(1, E, 9 * E + turn, zt) - 9.0
+        order = torch.randperm(E, device="cuda", generator=g).cpu().numpy()
+        large, small = order[:2], order[2:min(E, 24)]
+        z[0, torch.from_numpy(large).cuda()] = logits(1, 2, 5 * E + turn, zt)[0]
+        s = ref.scores(host64(z), "softmax")[0]
+        bias = np.full(E, -2.0, np.float32)
+        bias[large], bias[small] = (0.5 - s[large]).astype(np.float32), (0.5 - s[small]).astype(np.float32)
+        c = s + bias.astype(np.float64)
+        places = np.nonzero(np.isin(np.argsort(-c), large))[0]  # of the two of large scores
+        for k in sorted({1, int(places[0]) + 1, int(places[1]) + 1, max(1, int(places[1]) - 1)}):
+            behind += 0 <= places[0] - k <= 8
+            check_select(m, z, k, dict(score="softmax", groups=groups, renorm=turn % 2 == 0), torch.from_numpy(bias).cuda())
+    assert behind > 5
