@@ -166,7 +166,7 @@ struct Piece {
 // What bounds it: the way of x and A to the registers.  16384 tokens of 4096 inputs,
 // rank 64: 48 us, x alone (134 MB) takes 37-41 so, A alone (512 KB a workgroup, from the
 // caches) 22, the products with no loads 13.  Two groups of loads on their way, not one
-// (63 us); of few tokens it is waiting: 257 tokens of 4096 inputs, rank 32, 10 us, one
+// (63 us); of few tokens it is waiting: 257 tokens of 4096 inputs, rank 32, 12 us, one
 // token of 2048 3 us.
 template <int XD, int NT, int RB>
 __global__ void __launch_bounds__(64 * DOWN_WAVES, 2) k_lora_down(LoraArgs a) {
@@ -470,7 +470,7 @@ constexpr int up_resident(int tm, int rc) { return rc == 8 ? 1 : rc == 4 ? 2 : t
 // What bounds it: base, y and B.  16384 tokens of 4096 outputs, bf16, rank 64: 61 us,
 // 268 MB are 52 at a large copy's rate (92 us where a store took 64 bytes of a row, not
 // 128; loads and stores past the caches 99-108).  64 tokens of 131072 outputs, fp32, 16
-// adapters of rank 16: 37 us, 134 MB are 26; the base is loaded a step ahead, and at the
+// adapters of rank 16: 38 us, 134 MB are 26; the base is loaded a step ahead, and at the
 // ends of a wave's steps there is nothing else to do.
 template <int YD, int TM, int RC, bool BASE>
 __global__ void __launch_bounds__(256, up_resident(TM, RC)) k_lora_up(LoraArgs a) {
@@ -638,13 +638,18 @@ int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const v
         else launch_down<MOE_X_BF16, 4>(g, tiles, spread, stream);
     }
     if (int rc = moe_check_launch("moe_lora_add/down")) return rc;
+    // Of a tile of 64 the second pass shares out adapters by two: no difference where a tile has one or two (16384 tokens of
+    // 8 in a row 111 us by one, two and four; 2048 35.8, 34.9 and 36.7), more where it has many (1200 x 30000 x 1024 of 64
+    // in no order 300, 225 and 183 us; 1025 x 7337 x 2936 of 31 in a row 44, 40 and 40), and by four large ranks lose (4096 x
+    // 4096 x 4096 of rank 128 60.6, 60.6 and 62.3)
     const int groups = n + 1 < tm ? n + 1 : tm, up_spread = groups < (tm == 16 ? 8 : 2) ? groups : tm == 16 ? 8 : 2;
     const int resident = up_resident(tm, r <= 32 ? 1 : r <= 64 ? 2 : r <= 128 ? 4 : 8);
     const int64_t at_once = 256 * resident * (tm == 64 ? 1 : 4);
     // adapters of a tile, as far as the numbers tell
     const int64_t units = tm == 64 ? tiles : (int64_t)tiles + (n < T ? n : T - 1);
     // waves a tile (the four that share as one): as many as fill the card a whole number of times, what comes before a
-    // wave's first step being as long as START steps
+    // wave's first step being as long as START steps.  1, 3 and 6 are alike to 2 %; 0 makes short waves of prompts (3000 x
+    // 4096 x 4096 of rank 16 47 us, 41 with 3) and more of them of long rows (1388 x 51862 x 1464 of rank 128 in fp32 221 us, 271)
     constexpr int START = 3;
     const int steps = (N + STEP - 1) / STEP;
     int need = 1;
@@ -655,7 +660,10 @@ int moe_lora_add(const void* x, int x_dtype, int64_t ldx, const void* a, const v
         const int64_t each = (steps + w - 1) / w, long_ = (units * ((steps + each - 1) / each) + at_once - 1) / at_once * (each + START);
         if (long_ < best) best = long_, need = (int)((steps + each - 1) / each), g.steps = (int)each;
     }
-    const int per = tm == 64 || units * need <= 1024 ? 1 : 4;  // waves a workgroup (those that share as one)
+    // waves a workgroup (those that share as one).  Few stand alone, to lie on more CUs (16 x 8192 x 4096 10.8 us, by four
+    // 12.6; 7 x 5001 x 1536 10.7 and 12.3); of many, four share a workgroup's start, the adding up and cutting
+    // of h: as fast as alone (512 x 4096 x 4096 19.6 us both ways) or up to 6 % slower (64 x 131072 x 4096 43.6 and 41.0)
+    const int per = tm == 64 || units * need <= 1024 ? 1 : 4;
     g.parts = (need + per - 1) / per;
     const dim3 grid(g.parts * tiles, up_spread), block(tm == 64 ? 256 : 64 * per);
     if (y_dtype == MOE_X_F32) {

@@ -44,7 +44,8 @@ __device__ __forceinline__ float load_z(const void* z, int64_t i) {
     else return moe::bf16_to_f32(reinterpret_cast<const uint16_t*>(z)[i]);
 }
 
-// 1 / v to a double's last bits, v in [1, 2^30]: the hardware's estimate and two Newton steps
+// 1 / v to a double's last bits, v and 1 / v far inside the normal range (here 1 + exp and sums of 2^-8 to 2^16): the
+// hardware's estimate and two Newton steps
 __device__ __forceinline__ double rcp64(double v) {
     double r = __builtin_amdgcn_rcp(v);
     r = fma(fma(-v, r, 1.0), r, r);
@@ -902,8 +903,9 @@ __global__ void __launch_bounds__(256) k_bias_balance(const int32_t* __restrict_
 
 // Calls go with the number of experts a lane holds (64: what is more is taken in
 // double from the start); bf16 rows of an even length are read in pairs.  Five and six
-// have kernels of their own, 8 for 5 costs as much again: 65536 tokens of 288 experts in
-// groups 68 us and 90, 16384 of 320 in a row 10.6 and 11.3.
+// have kernels of their own, where 8 instead costs most in groups: 65536 tokens of 288
+// experts 67 us and 88, of 384 71 and 90, in a row 27.5 and 30.  Three and seven have
+// none, they would gain 4 %: of 192 experts 56 us and 53.5, of 448 91 and 87.
 template <typename Go>
 void by_count(int ne, const Go& go) {
     using std::integral_constant;
@@ -955,12 +957,18 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 int seg_of(int k) { return k <= 8 ? 8 : k <= 16 ? 16 : 32; }
 // Lanes of a token's candidates: k, some equal ones and a few for the bound's sake.  The
-// fewer, the more tokens side by side: 65537 tokens of 512, k 10, 48 us by 16 and 86 by 64.
+// fewer, the more tokens side by side, and the sooner equal logits have to be searched
+// for one by one.  65537 tokens of 512 bf16 logits, us by 16, 32 and 64 lanes, a bias and
+// logits that differ: k 10 50, 61 and 94, k 12 52, 61 and 95, k 14 96, 62 and 97, k 22 by
+// 32 72 and by 64 108, k 28 88 and 112.  No bias, logits in steps of a quarter (many
+// equals): k 8 50 and 40 by 32, k 10 74 and 43, k 12 107 and 45, k 22 by 32 85 and by 64 70,
+// k 28 164 and 71.  The cuts lie where both kinds are well served.
 int cand_of(int k) { return k <= 10 ? 16 : k <= 22 ? 32 : 64; }
 
 // Tokens a wave: as many as leave 16 waves a CU, and as have their picks side by side.
-// Several at a time save the second half of the work (65537 tokens of 512: 48 us by four
-// and 74 one by one), one at a time fills the card (4096 tokens: 7.5 us, 10.2 by four).
+// Several at a time save the second half of the work (65537 tokens of 512: 50 us by four
+// and 75 one by one; 8192 12.4 by two, 14.4 one by one, 15.0 by four), one at a time fills
+// the card (4096 tokens: 9.7 us, 13.1 by four; 1024 7.6 and 12.0).
 int batch_of(int T, int seg) {
     int n = 1;
     while (n < 64 / seg && T / (2 * n) >= 256 * 16) n *= 2;

@@ -571,9 +571,13 @@ typedef struct {
  *           then by rising id; -1 where there are no more.  Not written if
  *           ids_in is given
  *   w       device float[T][k] out: scale * s of each pick, or scale * s / sum
- *           of s over the token's picks; 0 for a pick of -1 and a masked token
- * Choice scores are taken in double.  Their ids do not depend on the other
- * tokens.  T = 0 does nothing.
+ *           of s over the token's picks; 0 for a pick of -1 and a masked token.
+ *           Taken in double and rounded once, but for the softmax's sum over the
+ *           experts (renorm 0), an fp32 one: that is off by a factor of
+ *           1 + (E / 64 + 2 ln E + 32) 2^-23 at most
+ * Choice scores are taken in double (exponentials below e^-708 are 0 there):
+ * experts or groups whose values differ by less than a double's rounding may
+ * change places.  Ids do not depend on the other tokens.  T = 0 does nothing.
  * Errors: ARG (null, sizes, score, group_top or scale out of range), DTYPE,
  * SHAPE (E > MOE_MAX_E, k > MOE_MAX_K, groups that do not divide E or are over
  * MOE_SELECT_MAX_GROUPS, k more than the kept groups hold, T beyond the limit),
@@ -594,7 +598,9 @@ int moe_route_select(const void* z, int z_dtype, const float* bias, const uint8_
  *            gradient (moe_balance_loss_bwd's)
  *   dz       device [T][E] in z_dtype out: dz_add + sum over i of dw_i dw_i/dz;
  *            may be z or dz_add
- * In fp32, rounded once at the end.  T = 0 does nothing.
+ * In fp32, rounded once at the end (of a raw softmax the exponential of a
+ * logit d below the largest is good to some (1.5 d + 4) 2^-23 of itself, and
+ * scores below 2^-118 may count as 0).  T = 0 does nothing.
  * Errors: as moe_route_select; ALIGN (z, dz_add and dz on 16 bytes). */
 int moe_route_select_bwd(const void* z, int z_dtype, const int32_t* ids, const float* dw, int T, int E, int k,
                          const moe_select_rule* rule, const void* dz_add, void* dz, hipStream_t stream);
